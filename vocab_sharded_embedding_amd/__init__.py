@@ -8,7 +8,9 @@ computation runs in the library's HIP kernels; there is no fallback path, and
 loading fails loudly when the library is missing or cannot be loaded.
 
 Names follow the C ABI: ``vpe_shard_range``, ``vpe_embed``,
-``vpe_sum_partials``, ``vpe_last_token_select``, ``vpe_lmhead``.
+``vpe_sum_partials``, ``vpe_last_token_select``, ``vpe_lmhead``.  The training
+calls live in ``training.py`` and the beam-search calls in ``beam.py``, and are
+re-exported here.
 """
 from __future__ import annotations
 
@@ -34,6 +36,15 @@ EXPORTED_SYMBOLS = ("vpe_shard_range", "vpe_embed", "vpe_sum_partials",
                     "vpe_lmhead_logsumexp_workspace", "vpe_lmhead_logsumexp",
                     "vpe_lmhead_prefill_logsumexp", "vpe_logsumexp_combine",
                     "vpe_lmhead_logsumexp_noalloc", "vpe_status_string")
+# include/vpe_train.h and include/vpe_beam.h
+TRAIN_SYMBOLS = ("vpe_embed_scaled", "vpe_embed_grad_workspace", "vpe_embed_grad",
+                 "vpe_distill_workspace", "vpe_distill_shard", "vpe_distill_loss",
+                 "vpe_distill_grad")
+BEAM_SYMBOLS = ("vpe_beam_select_workspace", "vpe_beam_select", "vpe_beam_merge",
+                "vpe_beam_reorder")
+VPE_MAX_TEACHER_ENTRIES = 1024
+VPE_MAX_DISTILL_ROWS = 1 << 21
+VPE_MAX_BEAMS = VPE_MAX_BEAM_PICKS = 64
 
 
 class VpeError(RuntimeError):
@@ -102,7 +113,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                  i64, vp, vp, i64, vp]
     lib.vpe_logsumexp_combine.argtypes = [ctypes.POINTER(vp), i32, i64, vp, vp]
     lib.vpe_lmhead_logsumexp_noalloc.argtypes = [vp, i64, i64, vp, i64, ci, vp, i64, i64, vp, vp]
-    for name in EXPORTED_SYMBOLS[:-1]:
+    f32, pi64, pvp = ctypes.c_float, ctypes.POINTER(i64), ctypes.POINTER(vp)
+    lib.vpe_embed_scaled.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, f32, vp, vp]
+    lib.vpe_embed_grad_workspace.argtypes = [i64, i64, i64, pi64]
+    lib.vpe_embed_grad.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, f32, vp, ci, i32, vp, i64,
+                                   vp]
+    lib.vpe_distill_workspace.argtypes = [i64, i64, pi64]
+    lib.vpe_distill_shard.argtypes = [vp, i64, i64, i64, i64, ci, i64, i64, f32, vp, ci, vp, ci,
+                                      i32, vp, vp, vp, vp, i64, vp]
+    lib.vpe_distill_loss.argtypes = [pvp, pvp, i32, i64, i64, f32, vp, ci, vp, ci, i32, vp, vp,
+                                     vp, vp]
+    lib.vpe_distill_grad.argtypes = [vp, i64, i64, i64, i64, ci, i64, i64, f32, vp, ci, vp, ci,
+                                     i32, vp, vp, vp, vp, i64, i64, vp]
+    lib.vpe_beam_select_workspace.argtypes = [i64, i32, i64, i32, pi64]
+    lib.vpe_beam_select.argtypes = [vp, i64, i64, ci, i64, i32, i64, i64, i64, vp, vp, i32, vp,
+                                    vp, i64, vp]
+    lib.vpe_beam_merge.argtypes = [pvp, i32, i64, i32, i64, vp, vp, vp, vp]
+    lib.vpe_beam_reorder.argtypes = [vp, i64, i64, i32, i64, vp, i64, i32, vp, vp]
+    for name in EXPORTED_SYMBOLS[:-1] + TRAIN_SYMBOLS + BEAM_SYMBOLS:
         getattr(lib, name).restype = ci
     lib.vpe_status_string.argtypes = [ci]
     lib.vpe_status_string.restype = ctypes.c_char_p
@@ -551,6 +579,11 @@ def vpe_logsumexp_combine(shard_lse: Sequence, out=None):
     return out
 
 
+from .training import (vpe_distill_grad, vpe_distill_loss, vpe_distill_shard,  # noqa: E402
+                       vpe_distill_workspace, vpe_embed_grad, vpe_embed_grad_workspace,
+                       vpe_embed_scaled)
+from .beam import (vpe_beam_merge, vpe_beam_reorder, vpe_beam_select,  # noqa: E402
+                   vpe_beam_select_workspace)
 from .layers import ParallelLMHead, VocabParallelEmbedding  # noqa: E402
 
 __all__ = [
@@ -561,4 +594,7 @@ __all__ = [
     "vpe_logsumexp_combine",
     "vpe_lmhead_logsumexp_noalloc", "VocabParallelEmbedding", "ParallelLMHead", "VpeError", "StaleLibraryError", "load_library",
     "check_library_current", "LIB_PATH",
+    "vpe_embed_scaled", "vpe_embed_grad_workspace", "vpe_embed_grad", "vpe_distill_workspace",
+    "vpe_distill_shard", "vpe_distill_loss", "vpe_distill_grad", "vpe_beam_select_workspace",
+    "vpe_beam_select", "vpe_beam_merge", "vpe_beam_reorder",
 ]

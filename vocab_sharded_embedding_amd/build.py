@@ -20,8 +20,8 @@ OBJDIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["gather.hip", "lmhead.hip"]
-CXX_SOURCES = ["vpe_api.cpp"]
+HIP_SOURCES = ["gather.hip", "lmhead.hip", "embed_train.hip", "distill.hip", "beam.hip"]
+CXX_SOURCES = ["vpe_api.cpp", "vpe_train_api.cpp", "vpe_beam_api.cpp"]
 
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17", "-Wall",
@@ -34,11 +34,11 @@ CXX_FLAGS = ["-O2", "-fPIC", "-std=c++17", "-Wall", "-Wextra", "-I", INCLUDE, "-
 
 def source_files() -> List[str]:
     """Every file the library is built from: kernels, the C-ABI layer, the
-    internal headers, the public header and build.py itself."""
+    internal headers, the public headers and build.py itself."""
     names = sorted(f for f in os.listdir(CSRC)
                    if f.endswith((".hip", ".cpp", ".h")))
-    return [os.path.join(CSRC, f) for f in names] + [os.path.join(INCLUDE, "vpe.h"),
-                                                     os.path.abspath(__file__)]
+    headers = [os.path.join(INCLUDE, h) for h in ("vpe.h", "vpe_train.h", "vpe_beam.h")]
+    return [os.path.join(CSRC, f) for f in names] + headers + [os.path.abspath(__file__)]
 
 
 def source_digest() -> str:

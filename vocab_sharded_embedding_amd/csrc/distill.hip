@@ -1,0 +1,530 @@
+// Distillation from a teacher's top logits for gfx950: per-shard statistics,
+// the loss, and the gradient of the logits.
+//
+// All of it is bound by HBM: the statistics read a rank's logits once, the
+// gradient reads them once and writes once; a row's teacher entries (at most
+// 1024) are small beside its columns.
+//  - Statistics: one pass with a running maximum and sum per thread, in base 2
+//    (x = z log2(e) / T, one fma and one v_exp_f32 per logit), joined over the
+//    block.  The maximum is moved once per batch of vectors, not per logit.
+//    Few rows are cut into column slices, one workgroup each, whose pairs a
+//    second kernel joins.
+//  - Gradient: P exp(z/T - lse) for every column, and for the entries' columns
+//    the entries' probabilities taken off.  Those columns are read before the
+//    dense pass (the gradient may overwrite the logits) and written again
+//    after it.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "vpe_device.h"
+#include "vpe_train_launch.h"
+
+namespace vpe {
+namespace {
+
+using namespace dev;
+
+constexpr int kBlock = 256;
+constexpr int kWaves = kBlock / 64;
+constexpr int kMaxEntries = 1024;
+constexpr int kEntriesPerThread = kMaxEntries / kBlock;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_huge_valf(); }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Block-wide maximum and sum, the same in every thread.
+__device__ __forceinline__ float block_max(float v, float *lds) {
+  v = wave_max(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[wave_in_block()] = v;
+  __syncthreads();
+  float r = lds[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) r = fmaxf(r, lds[w]);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T *lds) {
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[wave_in_block()] = v;
+  __syncthreads();
+  T r = lds[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) r += lds[w];
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// a row's teacher entries
+// ---------------------------------------------------------------------------
+struct TeacherArgs {
+  const void *ids, *logits;
+  const float *lse;
+  int itype, dtype, k;
+  int64_t vocab;
+  float temperature;
+  float inv_t;   // 1 / T
+  float to_log2; // log2(e) / T, rounded; ...
+  double unit;   // ... and what a power 2^x of it stands for: ln(2) times the
+                 // exact log2(e) / T over the rounded one
+};
+
+// Entry e of the row: its scaled logit t_e / T, or -inf (p_e = 0) for padding.
+__device__ __forceinline__ float entry(const TeacherArgs &t, int64_t row, int e, int64_t &id) {
+  const int64_t i = row * t.k + e;
+  id = t.itype == 0 ? static_cast<const int32_t *>(t.ids)[i]
+                    : static_cast<const int64_t *>(t.ids)[i];
+  if (static_cast<uint64_t>(id) >= static_cast<uint64_t>(t.vocab)) return neg_inf();
+  const float v = t.dtype == 0
+                      ? static_cast<const float *>(t.logits)[i]
+                      : __uint_as_float(static_cast<uint32_t>(
+                            static_cast<const uint16_t *>(t.logits)[i]) << 16);
+  return v / t.temperature;
+}
+
+// p_e of the thread's entries e = threadIdx.x + kBlock * i, their columns in
+// the shard [start, start + cols) (-1: elsewhere, or p_e = 0); returns P.
+__device__ __forceinline__ float teacher_row(const TeacherArgs &t, int64_t row, int64_t start,
+                                             int64_t cols, float (&p)[kEntriesPerThread],
+                                             int (&col)[kEntriesPerThread], float *lds) {
+  float mx = neg_inf();
+#pragma unroll
+  for (int i = 0; i < kEntriesPerThread; ++i) {
+    const int e = threadIdx.x + kBlock * i;
+    p[i] = neg_inf();
+    col[i] = -1;
+    if (e < t.k) {
+      int64_t id;
+      p[i] = entry(t, row, e, id);
+      const uint64_t local = static_cast<uint64_t>(id) - static_cast<uint64_t>(start);
+      if (local < static_cast<uint64_t>(cols)) col[i] = static_cast<int>(local);
+    }
+    mx = fmaxf(mx, p[i]);
+  }
+  float sum = 0.f;
+  if (t.lse != nullptr) {
+    const float l = t.lse[row];
+#pragma unroll
+    for (int i = 0; i < kEntriesPerThread; ++i) {
+      p[i] = p[i] == neg_inf() ? 0.f : expf(p[i] - l);
+      sum += p[i];
+    }
+    sum = block_sum(sum, lds);
+  } else {
+    mx = block_max(mx, lds);
+    if (mx == neg_inf()) mx = 0.f;  // no entry counts (NaN ones stay NaN)
+#pragma unroll
+    for (int i = 0; i < kEntriesPerThread; ++i) p[i] = expf(p[i] - mx), sum += p[i];
+    sum = block_sum(sum, lds);
+    if (sum != 0.f) {
+#pragma unroll
+      for (int i = 0; i < kEntriesPerThread; ++i) p[i] /= sum;
+      sum = sum != sum ? sum : 1.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kEntriesPerThread; ++i)
+    if (p[i] == 0.f) col[i] = -1;
+  return sum;
+}
+
+// ---------------------------------------------------------------------------
+// student rows
+// ---------------------------------------------------------------------------
+// Rows begin at any element, so vectors are only element-aligned.
+template <bool BF16> struct Row;
+template <> struct Row<true> {
+  static constexpr int kEpv = 8;
+  typedef u32x4 __attribute__((aligned(2))) loose;
+  static __device__ __forceinline__ float one(const void *base, int64_t i) {
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(base)[i]) << 16);
+  }
+  static __device__ __forceinline__ void put(void *base, int64_t i, float v) {
+    static_cast<uint16_t *>(base)[i] = one_bf16(v);
+  }
+};
+template <> struct Row<false> {
+  static constexpr int kEpv = 4;
+  typedef u32x4 __attribute__((aligned(4))) loose;
+  static __device__ __forceinline__ float one(const void *base, int64_t i) {
+    return static_cast<const float *>(base)[i];
+  }
+  static __device__ __forceinline__ void put(void *base, int64_t i, float v) {
+    static_cast<float *>(base)[i] = v;
+  }
+};
+
+// log2 of a sum of powers of two kept as (largest exponent, sum of
+// 2^(x - largest)).
+struct Pair {
+  float mx, sum;
+};
+__device__ __forceinline__ Pair join(Pair a, Pair b) {
+  const float m = fmaxf(a.mx, b.mx);
+  // (-inf) - (-inf) would be NaN: an empty side adds nothing
+  const float sa = a.mx == neg_inf() ? a.sum : a.sum * exp2_fast(a.mx - m);
+  const float sb = b.mx == neg_inf() ? b.sum : b.sum * exp2_fast(b.mx - m);
+  return Pair{m, sa + sb};
+}
+// In 64 bits (one value per row).  The largest exponent carries the rounding of
+// to_log2, which `unit` takes back: what remains is that rounding times the
+// others' distance from the largest.
+__device__ __forceinline__ float natural_log(Pair p, double unit) {
+  return static_cast<float>(static_cast<double>(p.mx) * unit +
+                            log2(static_cast<double>(p.sum)) * kLn2);
+}
+
+__device__ __forceinline__ Pair wave_join(Pair p) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) p = join(p, Pair{__shfl_xor(p.mx, d), __shfl_xor(p.sum, d)});
+  return p;
+}
+
+struct ShardArgs {
+  const char *base;  // first column of row 0
+  int64_t ld_bytes;
+  int64_t cols, vocab_start;
+  int slices;        // workgroups per row that reduce it
+  int64_t slice;     // columns of each, a multiple of the vector length
+};
+
+// blockIdx.x = row * per_row + s: slice s of the row, or (s == slices) its
+// dot product; with one slice, the workgroup does both.
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void distill_stats(ShardArgs z, TeacherArgs t, int per_row,
+                                                       float *__restrict__ shard_lse,
+                                                       float *__restrict__ shard_dot,
+                                                       Pair *__restrict__ pairs) {
+  typedef Row<BF16> R;
+  constexpr int kEpv = R::kEpv, kUnroll = 4;
+  __shared__ float red[kWaves];
+  __shared__ double red_d[kWaves];
+  __shared__ Pair red2[kWaves];
+  const int64_t row = blockIdx.x / static_cast<unsigned>(per_row);
+  const int s = static_cast<int>(blockIdx.x - row * per_row);
+  const char *base = z.base + row * z.ld_bytes;
+  const int tid = threadIdx.x;
+
+  if (s < z.slices && shard_lse != nullptr) {
+    const int64_t c0 = s * z.slice;
+    const int64_t n = c0 + z.slice < z.cols ? z.slice : z.cols - c0;
+    const char *p = base + c0 * (BF16 ? 2 : 4);
+    const float c = t.to_log2;
+    const int64_t nv = n / kEpv;
+    Pair acc{neg_inf(), 0.f};
+    for (int64_t i = tid; i < nv; i += kBlock * kUnroll) {
+      float v[kUnroll][kEpv];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t j = i + u * kBlock;
+        u32x4 r = BF16 ? u32x4(0xff80ff80u) : u32x4(0xff800000u);  // -inf: adds nothing
+        if (j < nv) r = reinterpret_cast<const typename R::loose *>(p)[j];
+        Vec<BF16, kEpv>::widen(r, v[u]);
+      }
+      float mx = neg_inf();
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int e = 0; e < kEpv; ++e) mx = fmaxf(mx, v[u][e]);
+      const float m2 = fmaxf(acc.mx, mx * c);
+      if (acc.mx != m2) acc = Pair{m2, acc.mx == neg_inf() ? acc.sum : acc.sum * exp2_fast(acc.mx - m2)};
+      const float off = m2 == neg_inf() ? 0.f : m2;
+      float sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int e = 0; e < kEpv; ++e) sum += exp2_fast(fmaf(v[u][e], c, -off));
+      acc.sum += sum;
+    }
+    for (int64_t i = nv * kEpv + tid; i < n; i += kBlock) {
+      const float x = R::one(p, i);
+      const float m2 = fmaxf(acc.mx, x * c);
+      if (acc.mx != m2) acc = Pair{m2, acc.mx == neg_inf() ? acc.sum : acc.sum * exp2_fast(acc.mx - m2)};
+      acc.sum += exp2_fast(fmaf(x, c, m2 == neg_inf() ? 0.f : -m2));
+    }
+    acc = wave_join(acc);
+    if ((tid & 63) == 0) red2[wave_in_block()] = acc;
+    __syncthreads();
+    if (tid == 0) {
+      Pair a = red2[0];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) a = join(a, red2[w]);
+      if (z.slices == 1) shard_lse[row] = natural_log(a, t.unit);
+      else pairs[row * z.slices + s] = a;
+    }
+  }
+  if (s == per_row - 1) {
+    float p[kEntriesPerThread];
+    int col[kEntriesPerThread];
+    teacher_row(t, row, z.vocab_start, z.cols, p, col, red);
+    // in 64 bits: the loss is a small difference of this and the log-sum-exp
+    double dot = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEntriesPerThread; ++i)
+      if (col[i] >= 0) dot += static_cast<double>(p[i]) * static_cast<double>(R::one(base, col[i]));
+    dot = block_sum(dot, red_d);
+    if (tid == 0) shard_dot[row] = static_cast<float>(dot / static_cast<double>(t.temperature));
+  }
+}
+
+// One wave per row: the slices' pairs joined.
+__global__ __launch_bounds__(kBlock) void distill_join(const Pair *__restrict__ pairs, int64_t m,
+                                                      int slices, double unit,
+                                                      float *__restrict__ shard_lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
+  if (row >= m) return;
+  Pair a{neg_inf(), 0.f};
+  for (int s = lane; s < slices; s += 64) a = join(a, pairs[row * slices + s]);
+  a = wave_join(a);
+  if (lane == 0) shard_lse[row] = natural_log(a, unit);
+}
+
+struct Parts {
+  const float *lse[64];
+  const float *dot[64];
+};
+
+// One wave per row.  Sums of a few tens of near-cancelling terms per row: the
+// row's scalars are joined in 64 bits and rounded once.
+__global__ __launch_bounds__(kBlock) void distill_loss_rows(Parts parts, int n_parts, int64_t m,
+                                                           TeacherArgs t, float *loss,
+                                                           float *lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
+  if (row >= m) return;
+  double dot = 0.0;
+  float top = neg_inf();
+  for (int r = 0; r < n_parts; ++r) {
+    dot += static_cast<double>(parts.dot[r][row]);
+    top = fmaxf(top, parts.lse[r][row]);
+  }
+  const float shift = top == neg_inf() ? 0.f : top;
+  double total = 0.0;
+  for (int r = 0; r < n_parts; ++r)
+    total += exp(static_cast<double>(parts.lse[r][row]) - static_cast<double>(shift));
+  const double l = static_cast<double>(shift) + log(total);
+
+  int64_t id;
+  float mx = neg_inf();
+  if (t.lse != nullptr) {
+    mx = t.lse[row];
+  } else {
+    for (int e = lane; e < t.k; e += 64) mx = fmaxf(mx, entry(t, row, e, id));
+    mx = wave_max(mx);
+    if (mx == neg_inf()) mx = 0.f;
+  }
+  // w = exp(x), x = t / T - mx: sums of w and of w x
+  double w_sum = 0.0, wx_sum = 0.0;
+  for (int e = lane; e < t.k; e += 64) {
+    const float v = entry(t, row, e, id), x = v - mx;
+    const float w = v == neg_inf() ? 0.f : expf(x);
+    w_sum += static_cast<double>(w);
+    if (w != 0.f) wx_sum += static_cast<double>(w) * static_cast<double>(x);
+  }
+  w_sum = wave_sum(w_sum);
+  wx_sum = wave_sum(wx_sum);
+  if (lane != 0) return;
+  double out = 0.0;
+  if (w_sum != 0.0) {
+    // given log-sum-exp: p = w; else p = w / sum w, log p = x - log(sum w)
+    if (t.lse != nullptr) out = wx_sum - dot + w_sum * l;
+    else out = wx_sum / w_sum - log(w_sum) - dot + l;
+  }
+  loss[row] = static_cast<float>(out);
+  lse[row] = static_cast<float>(l);
+}
+
+// ---------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------
+constexpr int kHashBits = 8192;
+
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, TeacherArgs t,
+                                                           const float *__restrict__ lse,
+                                                           const float *__restrict__ grad_loss,
+                                                           char *out_base, int64_t out_ld_bytes) {
+  typedef Row<BF16> R;
+  constexpr int kEpv = R::kEpv, kUnroll = 4, kSize = BF16 ? 2 : 4;
+  __shared__ float red[kWaves];
+  __shared__ float sp[kMaxEntries];
+  __shared__ int scol[kMaxEntries];
+  __shared__ uint32_t seen[kHashBits / 32], twice[kHashBits / 32];
+  const int64_t row = blockIdx.x / static_cast<unsigned>(z.slices);
+  const int s = static_cast<int>(blockIdx.x - row * z.slices);
+  const int tid = threadIdx.x;
+  const int64_t c0 = s * z.slice;
+  const int64_t n = c0 + z.slice < z.cols ? z.slice : z.cols - c0;
+  const char *src = z.base + row * z.ld_bytes + c0 * kSize;
+  char *dst = out_base + row * out_ld_bytes + c0 * kSize;
+  const int64_t nv = n / kEpv;
+
+  float p[kEntriesPerThread];
+  int col[kEntriesPerThread];
+  const float g = grad_loss[row] * t.inv_t;
+  float mass = 0.f;
+  if (grad_loss[row] != 0.f) mass = teacher_row(t, row, z.vocab_start + c0, n, p, col, red);
+  if (grad_loss[row] == 0.f || mass == 0.f) {
+    for (int64_t i = tid; i < nv; i += kBlock)
+      reinterpret_cast<typename R::loose *>(dst)[i] = u32x4(0);
+    for (int64_t i = nv * kEpv + tid; i < n; i += kBlock) R::put(dst, i, 0.f);
+    return;
+  }
+
+  // the entries' columns: logits before they may be overwritten, and the
+  // probabilities of ids that occur more than once added at the first of them
+  for (int i = tid; i < kHashBits / 32; i += kBlock) seen[i] = 0, twice[i] = 0;
+#pragma unroll
+  for (int i = 0; i < kEntriesPerThread; ++i) {
+    sp[tid + kBlock * i] = p[i];
+    scol[tid + kBlock * i] = col[i];
+  }
+  __syncthreads();
+  float zk[kEntriesPerThread];
+#pragma unroll
+  for (int i = 0; i < kEntriesPerThread; ++i) {
+    zk[i] = 0.f;
+    if (col[i] >= 0) {
+      zk[i] = R::one(src, col[i]);
+      const uint32_t h = static_cast<uint32_t>(col[i]) % kHashBits, bit = 1u << (h & 31);
+      if (atomicOr(&seen[h / 32], bit) & bit) atomicOr(&twice[h / 32], bit);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEntriesPerThread; ++i) {
+    if (col[i] >= 0) {
+      const uint32_t h = static_cast<uint32_t>(col[i]) % kHashBits;
+      if ((twice[h / 32] >> (h & 31)) & 1u) {
+        const int e = tid + kBlock * i;
+        bool first = true;
+        for (int j = 0; j < e; ++j) first = first && scol[j] != col[i];
+        float sum = 0.f;
+        for (int j = e; j < t.k; ++j) sum += scol[j] == col[i] ? sp[j] : 0.f;
+        p[i] = sum;
+        if (!first) col[i] = -1;
+      }
+    }
+  }
+
+  const float c = t.to_log2;
+  const float off = -lse[row] * kLog2e;
+  const float a = g * mass;
+  for (int64_t i = tid; i < nv; i += kBlock * kUnroll) {
+    u32x4 r[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t j = i + u * kBlock;
+      r[u] = u32x4(0);
+      if (j < nv) r[u] = reinterpret_cast<const typename R::loose *>(src)[j];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t j = i + u * kBlock;
+      float v[kEpv];
+      Vec<BF16, kEpv>::widen(r[u], v);
+#pragma unroll
+      for (int e = 0; e < kEpv; ++e) v[e] = a * exp2_fast(fmaf(v[e], c, off));
+      if (j < nv) reinterpret_cast<typename R::loose *>(dst)[j] = Vec<BF16, kEpv>::narrow(v);
+    }
+  }
+  for (int64_t i = nv * kEpv + tid; i < n; i += kBlock)
+    R::put(dst, i, a * exp2_fast(fmaf(R::one(src, i), c, off)));
+  __syncthreads();  // the dense pass's stores come before the entries'
+#pragma unroll
+  for (int i = 0; i < kEntriesPerThread; ++i)
+    if (col[i] >= 0)
+      R::put(dst, col[i], g * (mass * exp2_fast(fmaf(zk[i], c, off)) - p[i]));
+}
+
+TeacherArgs args_of(const Teacher &t) {
+  const double c = 1.4426950408889634 / static_cast<double>(t.temperature);
+  const float to_log2 = static_cast<float>(c);
+  return TeacherArgs{t.ids, t.logits, t.lse, t.itype, t.dtype, t.k, t.vocab, t.temperature,
+                     1.f / t.temperature, to_log2, kLn2 * (c / static_cast<double>(to_log2))};
+}
+
+ShardArgs args_of(const LogitsShard &z, int64_t slices) {
+  const int epv = z.dtype == 1 ? 8 : 4;
+  const int64_t slice = ((z.cols + slices - 1) / slices + epv - 1) / epv * epv;
+  return ShardArgs{static_cast<const char *>(z.base), z.ld * (z.dtype == 1 ? 2 : 4), z.cols,
+                   z.vocab_start, static_cast<int>((z.cols + slice - 1) / slice), slice};
+}
+
+}  // namespace
+
+// Enough workgroups to fill the chip when there are few rows, slices of at
+// least 8192 columns.
+int64_t distill_slices(int64_t m, int64_t cols) {
+  const int64_t want = (2048 + m - 1) / m;
+  return std::max<int64_t>(1, std::min(want, cols / 8192));
+}
+
+int launch_distill_shard(const LogitsShard &z, const Teacher &t, float *shard_lse,
+                         float *shard_dot, float *pairs, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();  // clear a stale error so the status returned is this launch's
+  const ShardArgs a = args_of(z, shard_lse ? distill_slices(z.m, z.cols) : 1);
+  const int per_row = a.slices > 1 ? a.slices + 1 : 1;
+  const dim3 grid(static_cast<unsigned>(z.m * per_row));
+  Pair *pr = reinterpret_cast<Pair *>(pairs);
+  if (z.dtype == 1)
+    hipLaunchKernelGGL((distill_stats<true>), grid, dim3(kBlock), 0, st, a, args_of(t), per_row,
+                       shard_lse, shard_dot, pr);
+  else
+    hipLaunchKernelGGL((distill_stats<false>), grid, dim3(kBlock), 0, st, a, args_of(t), per_row,
+                       shard_lse, shard_dot, pr);
+  if (shard_lse && a.slices > 1)
+    hipLaunchKernelGGL(distill_join, dim3(static_cast<unsigned>((z.m + kWaves - 1) / kWaves)),
+                       dim3(kBlock), 0, st, pr, z.m, a.slices, args_of(t).unit, shard_lse);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_distill_loss(const float *const *shard_lse, const float *const *shard_dot, int n_parts,
+                        int64_t m, const Teacher &t, float *loss, float *lse, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  Parts parts{};
+  for (int r = 0; r < n_parts; ++r) parts.lse[r] = shard_lse[r], parts.dot[r] = shard_dot[r];
+  hipLaunchKernelGGL(distill_loss_rows, dim3(static_cast<unsigned>((m + kWaves - 1) / kWaves)),
+                     dim3(kBlock), 0, st, parts, n_parts, m, args_of(t), loss, lse);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_distill_grad(const LogitsShard &z, const Teacher &t, const float *lse,
+                        const float *grad_loss, void *grad_base, int64_t ld_grad, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  const ShardArgs a = args_of(z, distill_slices(z.m, z.cols));
+  const dim3 grid(static_cast<unsigned>(z.m * a.slices));
+  const int64_t ld_bytes = ld_grad * (z.dtype == 1 ? 2 : 4);
+  char *out = static_cast<char *>(grad_base);
+  if (z.dtype == 1)
+    hipLaunchKernelGGL((distill_grad_rows<true>), grid, dim3(kBlock), 0, st, a, args_of(t), lse,
+                       grad_loss, out, ld_bytes);
+  else
+    hipLaunchKernelGGL((distill_grad_rows<false>), grid, dim3(kBlock), 0, st, a, args_of(t), lse,
+                       grad_loss, out, ld_bytes);
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace vpe

@@ -20,6 +20,9 @@ import torch
 from . import (vpe_embed, vpe_lmhead, vpe_lmhead_argmax, vpe_lmhead_logsumexp, vpe_lmhead_prefill,
                vpe_lmhead_prefill_argmax, vpe_lmhead_prefill_logsumexp, vpe_load_shard,
                vpe_logsumexp_combine, vpe_shard_range, vpe_sum_partials)
+from .beam import vpe_beam_merge, vpe_beam_reorder, vpe_beam_select
+from .training import (vpe_distill_grad, vpe_distill_loss, vpe_distill_shard, vpe_embed_grad,
+                       vpe_embed_scaled)
 
 
 class VocabParallelEmbedding(torch.nn.Module):
@@ -60,9 +63,25 @@ class VocabParallelEmbedding(torch.nn.Module):
                              f"shard {tuple(param.data.shape)}")
         param.data.copy_(piece)
 
-    def forward(self, ids: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """This rank's partial embedding (zero rows for ids it does not own)."""
+    def forward(self, ids: torch.Tensor, out: Optional[torch.Tensor] = None,
+                scale: Optional[float] = None) -> torch.Tensor:
+        """This rank's partial embedding (zero rows for ids it does not own),
+        times ``scale`` when one is given."""
+        if scale is not None:
+            return vpe_embed_scaled(ids, self.weight, self.vocab_start_idx, scale, out=out)
         return vpe_embed(ids, self.weight, self.vocab_start_idx, out=out)
+
+    def weight_grad(self, ids: torch.Tensor, grad_out: torch.Tensor, scale: float = 1.0,
+                    grad_weight: Optional[torch.Tensor] = None, accumulate: bool = False,
+                    dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+        """Gradient of this rank's shard from the gradient of the (scaled)
+        embedding: the same ``grad_out`` serves every rank, as the sum of the
+        partials passes it on unchanged.  Written to ``grad_weight`` (added to
+        it with ``accumulate``: a tied head's part may be there already), or to
+        a new tensor of ``dtype``."""
+        return vpe_embed_grad(ids, grad_out, self.vocab_start_idx,
+                              self.num_embeddings_per_partition, scale, grad_weight=grad_weight,
+                              accumulate=accumulate, dtype=dtype)
 
     @staticmethod
     def sum_partials(partials: Sequence[torch.Tensor],
@@ -140,3 +159,65 @@ class ParallelLMHead(VocabParallelEmbedding):
         """The ranks' per-row values combined into the log-sum-exp of the full
         vocabulary rows (the exchange step, on one device)."""
         return vpe_logsumexp_combine(shard_lse, out=out)
+
+    def _columns(self, logits: torch.Tensor):
+        """Where this rank's columns lie in its [M, V/tp] buffer or the full [M, V] one."""
+        if logits.dim() == 2 and logits.shape[1] == self.num_embeddings_per_partition:
+            return dict(shard_rows=self.num_embeddings_per_partition, col_offset=0)
+        if logits.dim() == 2 and logits.shape[1] == self.num_embeddings:
+            return dict(shard_rows=self.num_embeddings_per_partition,
+                        col_offset=self.vocab_start_idx)
+        raise ValueError("logits must be [M, V/tp] (one shard) or [M, V] (all shards)")
+
+    def distill_shard(self, logits: torch.Tensor, teacher_ids: torch.Tensor,
+                      teacher: torch.Tensor, temperature: float = 1.0,
+                      teacher_lse: Optional[torch.Tensor] = None, with_lse: bool = True):
+        """This rank's (shard_lse, shard_dot) of the distillation loss against the
+        teacher's top logits ``teacher`` [M, k] with vocabulary ids
+        ``teacher_ids``; the ranks' values go to ``distill_loss``.  With
+        ``with_lse`` False (temperature 1) ``logsumexp``'s value serves as
+        shard_lse."""
+        return vpe_distill_shard(logits, teacher_ids, teacher, self.vocab_start_idx,
+                                 self.num_embeddings, temperature=temperature,
+                                 teacher_lse=teacher_lse, with_lse=with_lse,
+                                 **self._columns(logits))
+
+    def distill_loss(self, shard_lse: Sequence[torch.Tensor], shard_dot: Sequence[torch.Tensor],
+                     teacher_ids: torch.Tensor, teacher: torch.Tensor, temperature: float = 1.0,
+                     teacher_lse: Optional[torch.Tensor] = None):
+        """(loss, lse) per row from the ranks' parts (the exchange step, on one device)."""
+        return vpe_distill_loss(shard_lse, shard_dot, teacher_ids, teacher, self.num_embeddings,
+                                temperature=temperature, teacher_lse=teacher_lse)
+
+    def distill_grad(self, logits: torch.Tensor, lse: torch.Tensor, grad_loss: torch.Tensor,
+                     teacher_ids: torch.Tensor, teacher: torch.Tensor, temperature: float = 1.0,
+                     teacher_lse: Optional[torch.Tensor] = None,
+                     grad_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Gradient of sum(grad_loss * loss) with respect to this rank's logits, as
+        a new [M, V/tp] tensor or into ``grad_logits`` ([M, V/tp] or [M, V],
+        ``logits`` itself allowed)."""
+        to = {}
+        if grad_logits is not None:
+            to = dict(grad_logits=grad_logits,
+                      grad_col_offset=self._columns(grad_logits)["col_offset"])
+        return vpe_distill_grad(logits, lse, grad_loss, teacher_ids, teacher,
+                                self.vocab_start_idx, self.num_embeddings,
+                                temperature=temperature, teacher_lse=teacher_lse,
+                                **self._columns(logits), **to)
+
+    def beam_select(self, logits: torch.Tensor, lse: torch.Tensor, scores: torch.Tensor,
+                    beams: int, picks: int) -> torch.Tensor:
+        """This rank's best ``picks`` (beam, token) candidates of every sequence, as
+        keys for ``merge_beams``; ``lse`` is the combined log-sum-exp of the rows."""
+        return vpe_beam_select(logits, lse, scores, beams, picks, self.vocab_start_idx,
+                               self.num_embeddings, **self._columns(logits))
+
+    def merge_beams(self, keys: Sequence[torch.Tensor]):
+        """(scores, parents, tokens) [n_seqs, picks], best first, from the ranks' keys."""
+        return vpe_beam_merge(keys, self.num_embeddings)
+
+    @staticmethod
+    def reorder_beams(state: torch.Tensor, parents: torch.Tensor, beams: int, dim: int = 0,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """A per-beam state (rows along ``dim``) with its rows taken from the parents'."""
+        return vpe_beam_reorder(state, parents, beams, dim=dim, out=out)
