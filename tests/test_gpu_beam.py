@@ -142,6 +142,22 @@ def test_masked_infinite_and_nan(dtype):
     _check(logits, lse, scores, beams, 3)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_infinite_logits_of_rows_that_end_at_minus_infinity(dtype):
+    # +inf - inf and +inf + -inf are NaN, the row's other scores are -inf
+    n, beams, v = 1, 3, 20000
+    logits, lse, scores, g = _case(12, n, beams, v, dtype)
+    logits[:, ::7] = INF
+    lse[0] = INF
+    scores[1] = -INF
+    scores[2] = -INF
+    lse[2] = INF
+    for picks in (1, 10, 64):
+        _check(logits, lse, scores, beams, picks, 2)
+    logits[:] = INF
+    _check(logits, lse, scores, beams, 20)
+
+
 @pytest.mark.parametrize("col,extra", [(0, 0), (1, 0), (5, 3), (8, 1)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_strided_rows(col, extra, dtype):

@@ -9,9 +9,10 @@ import ctypes
 import math
 from typing import Optional, Sequence
 
-from . import (_check, _dtype_code, _need_device, _same_device, _stream_handle, _torch,
-               load_library)
-from .training import _float_rows, _nbytes, logits_shard, on_device, workspace_for
+import torch
+
+from . import _check, _dtype_code, _need_device, _same_device, load_library
+from .training import _float_rows, _nbytes, enqueue, logits_shard, workspace_for
 
 
 def vpe_beam_select_workspace(n_seqs: int, beams: int, shard_rows: int, picks: int) -> int:
@@ -33,7 +34,6 @@ def vpe_beam_select(logits, lse, scores, beams: int, picks: int, vocab_start: in
     row, the log-sum-exp over the whole vocabulary and the beam's accumulated
     log-probability.
     """
-    torch = _torch()
     m, rows = logits_shard("logits", logits, shard_rows, col_offset)
     if beams < 1 or m % beams != 0:
         raise ValueError("logits must have `beams` rows per sequence")
@@ -47,21 +47,17 @@ def vpe_beam_select(logits, lse, scores, beams: int, picks: int, vocab_start: in
     _need_device("keys", keys)
     if keys.dtype != torch.int64 or keys.numel() != n * picks:
         raise ValueError("keys must be an int64 tensor [n_seqs, picks] (uint64 keys)")
-    workspace = workspace_for("workspace", need, workspace, logits.device)
+    workspace = workspace_for(need, workspace, logits.device)
     _same_device(logits, lse, scores, keys, workspace)
-    with on_device(logits.device):
-        _check("vpe_beam_select", load_library().vpe_beam_select(
-            logits.data_ptr(), logits.shape[1], int(col_offset), dt, n, beams, rows,
-            int(vocab_start), int(vocab), lse.data_ptr(), scores.data_ptr(), picks,
-            keys.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-            _stream_handle(logits.device)))
+    enqueue("vpe_beam_select", logits.device, logits.data_ptr(), logits.shape[1], int(col_offset),
+            dt, n, beams, rows, int(vocab_start), int(vocab), lse.data_ptr(), scores.data_ptr(),
+            picks, keys.data_ptr(), workspace.data_ptr(), _nbytes(workspace))
     return keys
 
 
 def vpe_beam_merge(keys: Sequence, vocab: int):
     """(scores float32, parents int64, tokens int64), each [n_seqs, picks], best
     first: the shards' picks merged."""
-    torch = _torch()
     parts = list(keys)
     if not parts:
         raise ValueError("need at least one shard's keys")
@@ -76,10 +72,8 @@ def vpe_beam_merge(keys: Sequence, vocab: int):
     parent = torch.empty((n, picks), dtype=torch.int64, device=device)
     token = torch.empty((n, picks), dtype=torch.int64, device=device)
     arr = (ctypes.c_void_p * len(parts))(*[t.data_ptr() for t in parts])
-    with on_device(device):
-        _check("vpe_beam_merge", load_library().vpe_beam_merge(
-            arr, len(parts), n, picks, int(vocab), score.data_ptr(), parent.data_ptr(),
-            token.data_ptr(), _stream_handle(device)))
+    enqueue("vpe_beam_merge", device, arr, len(parts), n, picks, int(vocab), score.data_ptr(),
+            parent.data_ptr(), token.data_ptr())
     return score, parent, token
 
 
@@ -91,7 +85,6 @@ def vpe_beam_reorder(state, parents, beams: int, dim: int = 0, out=None):
     vpe_beam_merge's) names each new beam's old one.  The result has n_seqs *
     beams_out rows there; a parent outside [0, beams) gives zeros.
     """
-    torch = _torch()
     _need_device("state", state)
     if not parents.is_cuda:
         raise ValueError(f"parents must be a HIP device tensor, got device {parents.device}")
@@ -118,8 +111,6 @@ def vpe_beam_reorder(state, parents, beams: int, dim: int = 0, out=None):
     _same_device(state, parents, out)
     if row_bytes == 0:
         return out
-    with on_device(state.device):
-        _check("vpe_beam_reorder", load_library().vpe_beam_reorder(
-            state.data_ptr(), outer, n, beams, row_bytes, parents.data_ptr(), ld, beams_out,
-            out.data_ptr(), _stream_handle(state.device)))
+    enqueue("vpe_beam_reorder", state.device, state.data_ptr(), outer, n, beams, row_bytes,
+            parents.data_ptr(), ld, beams_out, out.data_ptr())
     return out

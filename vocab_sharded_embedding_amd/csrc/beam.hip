@@ -5,15 +5,19 @@
 // Selection reads every logit once; its picks are a few keys.  A candidate is
 // a 64-bit key (order of the score, then the lower place), and all keys of a
 // sequence are distinct, so "the k best" is one definite set.
-//  - A workgroup holds a chunk of a row in registers, kItems scores per
-//    thread.  The k-th largest of the threads' best keys is a bound that at
-//    least k keys reach, and only the k threads at or above it hold any that
-//    do: at most k * kItems candidates, usually little more than k.  Those go
-//    to LDS, where each finds its rank by counting.
-//  - A row is cut into slices, one workgroup each; a second kernel joins the
-//    slices' sorted lists of all beams of a sequence.  With L lists the k-th
-//    largest of the lists' heads is such a bound again: at most k lists reach
-//    it, so at most k * k candidates.
+//  - A first kernel leaves the largest logit of every group of 64 vectors of a
+//    row: a widening and half a maximum per logit, no branches, bound by HBM.
+//    The score rises with the logit, so the group's best score follows from it.
+//  - A second kernel, one workgroup per sequence, orders the groups of all
+//    beams by (best score, lower place).  A candidate outside the k best groups
+//    is beaten by k candidates, one in each, so only about k groups are read
+//    again, and of those only the scores at the k-th group's best and above are
+//    looked at: usually little more than k.
+//  - The k-th largest of many keys is found by their digits of 11 bits from the
+//    top, counted in LDS: two rounds for scores that differ.  A selection by
+//    single bits (ballots in one wave) took 150 to 400 cycles a bit, 14000 a
+//    selection, and a selection per row slice 32 us for [256, 75968] logits.
+//  - Few candidates (kDirect) are ordered by the second kernel alone.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,9 +33,13 @@ using namespace dev;
 
 constexpr int kBlock = 256;
 constexpr int kMaxPicks = 64;
-constexpr int kItems = 32;                  // scores per thread and chunk
-constexpr int kChunk = kBlock * kItems;     // columns per chunk
-constexpr int kMaxSlices = 32;              // lists per row
+constexpr int kGroupsPerWave = 4;        // vectors in flight per lane
+constexpr int64_t kDirect = 16384;       // candidates a workgroup orders by itself
+constexpr int kThreads = 1024;           // of that workgroup
+constexpr int kDigitBits = 11;
+constexpr int kBins = 1 << kDigitBits;
+constexpr int kCap = 2048;               // keys collected
+constexpr int kFew = 256;                // keys ordered by counting
 
 // Unsigned integers ordered like the scores, NaN below all.
 __device__ __forceinline__ uint32_t order_of(float c) {
@@ -60,220 +68,362 @@ template <> struct Row<false> {
   }
 };
 
-// The rank of `mine` among keys[0, n): how many are larger, or equal with a
-// lower index (keys of different candidates differ; key 0 may repeat).
-__device__ __forceinline__ int rank_among(const uint64_t *keys, int n, uint64_t mine, int index) {
-  int rank = 0;
-  for (int j = 0; j < n; ++j) rank += keys[j] > mine || (keys[j] == mine && j < index);
-  return rank;
-}
-
 struct BeamArgs {
   const char *base;
   int64_t ld_bytes;
   int64_t cols, vocab_start, vocab;
   const float *lse, *scores;
-  int beams, picks, slices;
-  int64_t slice;  // columns per slice, a multiple of the vector length
+  int beams, picks;
+  int64_t groups;  // per row
 };
 
-// blockIdx.x = row * slices + s: the slice's best keys, descending, 0 beyond.
-template <bool BF16>
-__global__ __launch_bounds__(kBlock) void beam_slice(BeamArgs a, uint64_t *__restrict__ out) {
-  typedef Row<BF16> R;
-  constexpr int kEpv = R::kEpv, kVecs = kItems / kEpv;
-  __shared__ __attribute__((aligned(16))) uint64_t top[kBlock];
-  __shared__ __attribute__((aligned(16))) uint64_t cand[kMaxPicks * kItems + kMaxPicks];
-  __shared__ uint64_t best[kMaxPicks];
-  __shared__ uint64_t bound;
-  __shared__ int n_cand;
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x / static_cast<unsigned>(a.slices);
-  const int s = static_cast<int>(blockIdx.x - row * a.slices);
-  const int64_t c0 = s * a.slice;
-  const int64_t n = c0 + a.slice < a.cols ? a.slice : a.cols - c0;
-  const char *p = a.base + row * a.ld_bytes + c0 * (BF16 ? 2 : 4);
-  const float lse = a.lse[row], score = a.scores[row];
-  // places count down from the beam's first token, as the low key half does
-  const uint32_t low0 = 0xFFFFFFFFu - static_cast<uint32_t>((row % a.beams) * a.vocab +
-                                                            a.vocab_start + c0);
-  const int k = a.picks;
+// Maximum over the wave's lanes (NaN is passed over), in lane 63: DPP moves
+// within rows of 16 lanes, then from row to row.
+template <int CTRL>
+__device__ __forceinline__ float max_from(float v) {
+  const int i = __float_as_int(v);
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false)));
+}
+__device__ __forceinline__ float wave_max_last(float v) {
+  v = max_from<0x111>(v);  // row_shr:1
+  v = max_from<0x112>(v);  // row_shr:2
+  v = max_from<0x114>(v);  // row_shr:4
+  v = max_from<0x118>(v);  // row_shr:8
+  v = max_from<0x142>(v);  // row_bcast:15
+  return max_from<0x143>(v);  // row_bcast:31
+}
 
-  if (tid < k) best[tid] = 0;
-  __syncthreads();
-  for (int64_t at = 0; at < n; at += kChunk) {
-    uint32_t ord[kItems];
-    uint32_t low[kVecs];
-    uint64_t mine = 0;
+// best[row * groups + g] = the largest logit of columns [g, g + 1) * 64 vectors
+// of the row, NaN if there is none.
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t units_per_row,
+                                                     int64_t units, float *__restrict__ best) {
+  typedef Row<BF16> R;
+  constexpr int kEpv = R::kEpv, kSize = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kBlock / 64) + wave_in_block();
+  if (unit >= units) return;
+  const int64_t row = unit / units_per_row;
+  const int64_t g0 = (unit - row * units_per_row) * kGroupsPerWave;
+  const char *p = a.base + row * a.ld_bytes;
+  const uint32_t none = BF16 ? 0x7fc07fc0u : 0x7fc00000u;
+  u32x4 raw[kGroupsPerWave];
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int64_t j = at + static_cast<int64_t>(u * kBlock + tid) * kEpv;
-      low[u] = low0 - static_cast<uint32_t>(j);
+  for (int u = 0; u < kGroupsPerWave; ++u) {
+    const int64_t j = ((g0 + u) * 64 + lane) * kEpv;
+    raw[u] = u32x4(none);
+    if (j + kEpv <= a.cols) raw[u] = *reinterpret_cast<const typename R::loose *>(p + j * kSize);
+  }
+  // where +inf has a NaN score (a row whose log-sum-exp is +inf, a beam at
+  // -inf) the others of its group come before it
+  const float inf = __builtin_huge_valf();
+  const float top = (inf - a.lse[row]) + a.scores[row];
+  const bool no_inf = top != top;
+  float mx[kGroupsPerWave];
+#pragma unroll
+  for (int u = 0; u < kGroupsPerWave; ++u) {
+    float v[kEpv];
+    Vec<BF16, kEpv>::widen(raw[u], v);
+    if (no_inf) {
+#pragma unroll
+      for (int e = 0; e < kEpv; ++e) v[e] = v[e] == inf ? __uint_as_float(0x7fc00000u) : v[e];
+    }
+    mx[u] = v[0];
+#pragma unroll
+    for (int e = 1; e < kEpv; ++e) mx[u] = fmaxf(mx[u], v[e]);
+    // the row's last columns where they do not fill a vector
+    const int64_t j = ((g0 + u) * 64 + lane) * kEpv;
+    if (j < a.cols && j + kEpv > a.cols) {
+#pragma nounroll
+      for (int64_t i = j; i < a.cols; ++i) {
+        const float x = R::one(p, i);
+        if (!(no_inf && x == inf)) mx[u] = fmaxf(mx[u], x);
+      }
+    }
+  }
+  float mine = 0.f;
+#pragma unroll
+  for (int u = 0; u < kGroupsPerWave; ++u) {
+    const float m = __int_as_float(
+        __builtin_amdgcn_readlane(__float_as_int(wave_max_last(mx[u])), 63));
+    if (lane == u) mine = m;
+  }
+  if (lane < kGroupsPerWave && g0 + lane < a.groups) best[row * a.groups + g0 + lane] = mine;
+}
+
+// ---------------------------------------------------------------------------
+// selection by one workgroup of kThreads
+// ---------------------------------------------------------------------------
+struct SelectLds {
+  uint32_t bins[kBins];
+  uint32_t sums[kThreads / 64];
+  uint64_t cand[kCap];
+  uint64_t few[kFew];
+  float lse[kMaxPicks], score[kMaxPicks];  // of the sequence's beams
+  uint32_t group[kFew];                    // groups read again
+  int n;                                   // keys collected
+  uint32_t digit, above, reach;
+};
+
+// A bound that at least k of the keys (key 0 stands for none) reach, and at
+// most k + slack unless they are copies of one key; 1 where there are fewer.
+template <class Keys>
+__device__ __forceinline__ uint64_t bound_of(const Keys &keys, int n, int k, int slack,
+                                             SelectLds &s) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
+  uint64_t prefix = 0;
+  int need = k;  // keys still to be found among those of the prefix
+#pragma nounroll
+  for (int open = 64; open > 0;) {  // low bits not decided yet
+    const int bits = open < kDigitBits ? open : kDigitBits;
+    const int shift = open - bits;
+    for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
+    if (tid == 0) s.reach = 0;
+    __syncthreads();
+#pragma nounroll
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t key = keys(i);
+      if (key != 0 && (open == 64 || key >> open == prefix))
+        atomicAdd(&s.bins[(key >> shift) & ((1 << bits) - 1)], 1u);
+    }
+    __syncthreads();
+    // thread t: digits kBins - 1 - 2t and the one below; `above`: keys of larger ones
+    static_assert(kBins == 2 * kThreads, "two digits per thread");
+    const uint32_t hi = s.bins[kBins - 1 - 2 * tid], lo = s.bins[kBins - 2 - 2 * tid];
+    uint32_t above = hi + lo;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const uint32_t up = __shfl_up(above, d);
+      if (lane >= d) above += up;
+    }
+    if (lane == 63) s.sums[wave] = above;
+    __syncthreads();
+    above -= hi + lo;
+#pragma nounroll
+    for (int w = 0; w < wave; ++w) above += s.sums[w];
+    const uint32_t want = static_cast<uint32_t>(need);
+    if (above < want && above + hi + lo >= want) {
+      const bool upper = above + hi >= want;
+      s.digit = upper ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
+      s.above = upper ? above : above + hi;
+      s.reach = upper ? above + hi : above + hi + lo;
+    }
+    __syncthreads();
+    const int reach = static_cast<int>(s.reach);  // keys of the digit and larger ones
+    if (reach == 0) return 1;
+    prefix = (prefix << bits) | s.digit;
+    const int total = k - need + reach;
+    need -= static_cast<int>(s.above);
+    open = shift;
+    __syncthreads();  // read before the next round (or call) clears it
+    if (total <= k + slack || open == 0) return prefix << open;
+  }
+  return 1;  // not reached
+}
+
+// out[0 .. s.n) = value(i) of the keys that reach the bound, in any order;
+// s.n counts those past cap too.
+template <class Keys, class Value, typename T>
+__device__ __forceinline__ void collect(const Keys &keys, const Value &value, int n, uint64_t bound,
+                                        T *out, int cap, SelectLds &s) {
+  if (threadIdx.x == 0) s.n = 0;
+  __syncthreads();
+#pragma nounroll
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t key = keys(i);
+    if (key != 0 && key >= bound) {
+      const int at = atomicAdd(&s.n, 1);
+      if (at < cap) out[at] = value(i, key);
+    }
+  }
+  __syncthreads();
+}
+
+// The k best of s.few[0, n), best first, to thread t < k (0 beyond them).
+__device__ __forceinline__ uint64_t best_of_few(int n, int k, SelectLds &s) {
+  const int tid = threadIdx.x;
+  if (n > kFew) n = kFew;  // copies of one key
+  if (tid < k) s.cand[tid] = 0;
+  __syncthreads();
+  if (tid < n) {
+    const uint64_t mine = s.few[tid];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j)
+      rank += s.few[j] > mine || (s.few[j] == mine && j < tid);
+    if (rank < k) s.cand[rank] = mine;
+  }
+  __syncthreads();
+  return tid < k ? s.cand[tid] : 0;
+}
+
+struct TheKey {
+  __device__ __forceinline__ uint64_t operator()(int, uint64_t key) const { return key; }
+};
+struct TheIndex {
+  __device__ __forceinline__ uint32_t operator()(int i, uint64_t) const {
+    return static_cast<uint32_t>(i);
+  }
+};
+struct LdsKeys {
+  const uint64_t *keys;
+  __device__ __forceinline__ uint64_t operator()(int i) const { return keys[i]; }
+};
+
+// A sequence's candidates.
+template <bool BF16>
+struct Candidates {
+  const BeamArgs &a;
+  const SelectLds &s;
+  const char *base;  // the sequence's first row
+  const float *best; // its groups' largest logits
+  static constexpr int kGroupCols = 64 * Row<BF16>::kEpv;
+
+  __device__ __forceinline__ uint64_t key(int beam, uint32_t col, float z) const {
+    const float c = ((z - s.lse[beam]) + s.score[beam]) + 0.f;  // -0 becomes +0
+    const uint32_t place = static_cast<uint32_t>(beam * a.vocab + a.vocab_start) + col;
+    return (static_cast<uint64_t>(order_of(c)) << 32) | (0xFFFFFFFFu - place);
+  }
+  __device__ __forceinline__ uint64_t at(int beam, uint32_t col) const {
+    return key(beam, col, Row<BF16>::one(base + beam * a.ld_bytes, col));
+  }
+};
+// all of them, one by one
+template <bool BF16>
+struct AllKeys {
+  const Candidates<BF16> &c;
+  __device__ __forceinline__ uint64_t operator()(int i) const {
+    const uint32_t cols = static_cast<uint32_t>(c.a.cols), beam = static_cast<uint32_t>(i) / cols;
+    return c.at(static_cast<int>(beam), static_cast<uint32_t>(i) - beam * cols);
+  }
+};
+// group i's best, as if it were the group's first column
+template <bool BF16>
+struct GroupKeys {
+  const Candidates<BF16> &c;
+  __device__ __forceinline__ uint64_t operator()(int i) const {
+    const uint32_t groups = static_cast<uint32_t>(c.a.groups);
+    const uint32_t beam = static_cast<uint32_t>(i) / groups;
+    return c.key(static_cast<int>(beam), (static_cast<uint32_t>(i) - beam * groups) * c.kGroupCols,
+                 c.best[i]);
+  }
+};
+// those of the groups listed in s.group
+template <bool BF16>
+struct ListedKeys {
+  const Candidates<BF16> &c;
+  __device__ __forceinline__ uint64_t operator()(int i) const {
+    const uint32_t group = c.s.group[i / c.kGroupCols];
+    const uint32_t groups = static_cast<uint32_t>(c.a.groups), beam = group / groups;
+    const uint32_t col = (group - beam * groups) * c.kGroupCols + i % c.kGroupCols;
+    return col < c.a.cols ? c.at(static_cast<int>(beam), col) : 0;
+  }
+};
+
+// One workgroup per sequence: its `picks` best keys, descending, 0 beyond.
+// best == nullptr: few candidates, ordered one by one.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void beam_pick(BeamArgs a, const float *__restrict__ best,
+                                                     uint64_t *__restrict__ keys) {
+  __shared__ SelectLds s;
+  const int64_t seq = blockIdx.x;
+  const int tid = threadIdx.x, k = a.picks;
+  if (tid < a.beams) {
+    s.lse[tid] = a.lse[seq * a.beams + tid];
+    s.score[tid] = a.scores[seq * a.beams + tid];
+  }
+  __syncthreads();
+  const Candidates<BF16> c{a, s, a.base + seq * a.beams * a.ld_bytes,
+                           best ? best + seq * a.beams * a.groups : nullptr};
+  if (best == nullptr) {
+    const int n = static_cast<int>(a.beams * a.cols);
+    const AllKeys<BF16> all{c};
+    collect(all, TheKey{}, n, n <= kFew ? 1 : bound_of(all, n, k, kFew - k, s), s.few, kFew, s);
+  } else {
+    // the k best groups (up to as many again where that saves a round)
+    const GroupKeys<BF16> groups{c};
+    const int n = static_cast<int>(a.beams * a.groups);
+    const uint64_t bound = bound_of(groups, n, k, k, s);
+    collect(groups, TheIndex{}, n, bound, s.group, kFew, s);
+    const int listed = s.n;
+    __syncthreads();
+    // their scores at the bound and above
+    typedef Row<BF16> R;
+    constexpr int kEpv = R::kEpv;
+    if (tid == 0) s.n = 0;
+    __syncthreads();
+    const uint32_t least = static_cast<uint32_t>(bound >> 32);
+    for (int i = wave_in_block(); i < listed; i += kThreads / 64) {
+      const uint32_t group = s.group[i], ng = static_cast<uint32_t>(a.groups);
+      const uint32_t beam = group / ng;
+      const int64_t j = (static_cast<int64_t>(group - beam * ng) * 64 + (tid & 63)) * kEpv;
+      const char *p = c.base + beam * a.ld_bytes;
       float v[kEpv];
-      const int left = n - j < kEpv ? static_cast<int>(n - j) : kEpv;
-      if (left == kEpv) {
-        Vec<BF16, kEpv>::widen(*reinterpret_cast<const typename R::loose *>(p + j * (BF16 ? 2 : 4)), v);
+      if (j + kEpv <= a.cols) {
+        Vec<BF16, kEpv>::widen(
+            *reinterpret_cast<const typename R::loose *>(p + j * (BF16 ? 2 : 4)), v);
       } else {
 #pragma unroll
-        for (int e = 0; e < kEpv; ++e) v[e] = e < left ? R::one(p, j + e) : 0.f;
+        for (int e = 0; e < kEpv; ++e) v[e] = j + e < a.cols ? R::one(p, j + e) : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < kEpv; ++e) {
-        const float c = ((v[e] - lse) + score) + 0.f;  // -0 becomes +0
-        ord[u * kEpv + e] = order_of(c);
-        const uint64_t key = (static_cast<uint64_t>(ord[u * kEpv + e]) << 32) | (low[u] - e);
-        if (e < left && key > mine) mine = key;
-      }
-    }
-    const uint64_t floor_key = best[k - 1];
-    top[tid] = mine;
-    if (tid == 0) bound = 0, n_cand = 0;
-    __syncthreads();
-    if (rank_among(top, kBlock, mine, tid) == k - 1) bound = mine;
-    __syncthreads();
-    const uint64_t least = bound > floor_key ? bound : floor_key;
-    if (mine != 0 && mine >= least) {
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) {
-        const int64_t j = at + static_cast<int64_t>(u * kBlock + tid) * kEpv;
-#pragma unroll
-        for (int e = 0; e < kEpv; ++e) {
-          const uint64_t key = (static_cast<uint64_t>(ord[u * kEpv + e]) << 32) | (low[u] - e);
-          if (j + e < n && key >= least) cand[atomicAdd(&n_cand, 1)] = key;
+        const uint64_t key = c.key(static_cast<int>(beam), static_cast<uint32_t>(j) + e, v[e]);
+        if (j + e < a.cols && static_cast<uint32_t>(key >> 32) >= least) {
+          const int at = atomicAdd(&s.n, 1);
+          if (at < kCap) s.cand[at] = key;
         }
       }
     }
-    if (tid < k && best[tid] != 0) cand[atomicAdd(&n_cand, 1)] = best[tid];
     __syncthreads();
-    const int nc = n_cand;
-    if (tid < k) best[tid] = 0;
+    const int n_cand = s.n;
     __syncthreads();
-    for (int i = tid; i < nc; i += kBlock) {
-      const uint64_t key = cand[i];
-      const int r = rank_among(cand, nc, key, i);
-      if (r < k) best[r] = key;
+    if (n_cand <= kCap) {
+      const LdsKeys some{s.cand};
+      collect(some, TheKey{}, n_cand, n_cand <= kFew ? 1 : bound_of(some, n_cand, k, kFew - k, s),
+              s.few, kFew, s);
+    } else {  // many equal scores
+      const ListedKeys<BF16> some{c};
+      const int n_some = listed * c.kGroupCols;
+      collect(some, TheKey{}, n_some, bound_of(some, n_some, k, kFew - k, s), s.few, kFew, s);
     }
-    __syncthreads();
   }
-  if (tid < k) out[static_cast<int64_t>(blockIdx.x) * k + tid] = best[tid];
+  const uint64_t key = best_of_few(s.n, k, s);
+  if (tid < k) keys[seq * k + tid] = key;
 }
 
-// ---------------------------------------------------------------------------
-// sorted lists of k keys joined: lists l < n_lists of block `seq`
-// ---------------------------------------------------------------------------
-struct Adjacent {  // the slices of a sequence's beams follow each other
-  const uint64_t *keys;
-  int64_t n_lists;
-  int k;
-  __device__ __forceinline__ const uint64_t *list(int64_t seq, int l) const {
-    return keys + (seq * n_lists + l) * k;
-  }
-};
-struct PerPart {  // one array per shard
+struct PartKeys {  // one array per shard
   const uint64_t *part[64];
+};
+struct SeqParts {
+  const PartKeys &parts;
+  int64_t at;
   int k;
-  __device__ __forceinline__ const uint64_t *list(int64_t seq, int l) const {
-    return part[l] + seq * k;
+  __device__ __forceinline__ uint64_t operator()(int i) const {
+    const int part = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(k));
+    return parts.part[part][at + i - part * k];
   }
 };
 
-// best[0, k) (LDS) = the k largest keys of the lists, descending, 0 beyond.
-template <class Lists>
-__device__ __forceinline__ void join_lists(const Lists &lists, int64_t seq, int n_lists, int k,
-                                           uint64_t *top, uint64_t *cand, int cap, uint64_t *best,
-                                           uint64_t *bound, int *n_cand) {
-  const int tid = threadIdx.x;
-  // a bound that k heads reach: the k-th largest of the threads' best heads,
-  uint64_t mine = 0;
-  for (int l = tid; l < n_lists; l += kBlock) {
-    const uint64_t h = lists.list(seq, l)[0];
-    if (h > mine) mine = h;
-  }
-  top[tid] = mine;
-  if (tid == 0) *bound = 0, *n_cand = 0;
-  if (tid < k) best[tid] = 0;
-  __syncthreads();
-  if (rank_among(top, kBlock, mine, tid) == k - 1) *bound = mine;
-  __syncthreads();
-  uint64_t least = *bound;
-  if (n_lists > kBlock) {
-    // then exactly the k-th largest head, among the heads that reach it
-    for (int l = tid; l < n_lists; l += kBlock) {
-      const uint64_t h = lists.list(seq, l)[0];
-      if (h != 0 && h >= least) {
-        const int i = atomicAdd(n_cand, 1);
-        if (i < cap) cand[i] = h;
-      }
-    }
-    __syncthreads();
-    const int nh = *n_cand < cap ? *n_cand : cap;
-    for (int i = tid; i < nh; i += kBlock)
-      if (rank_among(cand, nh, cand[i], i) == k - 1) *bound = cand[i];
-    __syncthreads();
-    least = *bound;
-    if (tid == 0) *n_cand = 0;
-    __syncthreads();
-  }
-  for (int l = tid; l < n_lists; l += kBlock) {
-    const uint64_t *list = lists.list(seq, l);
-    for (int i = 0; i < k; ++i) {
-      const uint64_t key = list[i];
-      if (key == 0 || key < least) break;
-      const int at = atomicAdd(n_cand, 1);
-      if (at < cap) cand[at] = key;
-    }
-  }
-  __syncthreads();
-  const int nc = *n_cand < cap ? *n_cand : cap;
-  for (int i = tid; i < nc; i += kBlock) {
-    const uint64_t key = cand[i];
-    const int r = rank_among(cand, nc, key, i);
-    if (r < k) best[r] = key;
-  }
-  __syncthreads();
-}
-
-// k lists of k keys reach the bound at most; at most kMaxSlices * 64 / kBlock
-// heads per thread do (fewer).
-constexpr int kListCap = kMaxPicks * kMaxPicks;
-
-#define VPE_JOIN_LDS                                                    \
-  __shared__ __attribute__((aligned(16))) uint64_t top[kBlock];         \
-  __shared__ __attribute__((aligned(16))) uint64_t cand[kListCap];      \
-  __shared__ uint64_t best[kMaxPicks];                                  \
-  __shared__ uint64_t bound;                                            \
-  __shared__ int n_cand
-
-__global__ __launch_bounds__(kBlock) void beam_join(Adjacent lists, uint64_t *__restrict__ keys) {
-  VPE_JOIN_LDS;
+// One workgroup per sequence.
+__global__ __launch_bounds__(kThreads) void beam_merge_rows(PartKeys parts, int n_parts, int k,
+                                                           int64_t vocab,
+                                                           float *__restrict__ score,
+                                                           int64_t *__restrict__ parent,
+                                                           int64_t *__restrict__ token) {
+  __shared__ SelectLds s;
   const int64_t seq = blockIdx.x;
-  join_lists(lists, seq, static_cast<int>(lists.n_lists), lists.k, top, cand, kListCap, best,
-             &bound, &n_cand);
-  if (static_cast<int>(threadIdx.x) < lists.k) keys[seq * lists.k + threadIdx.x] = best[threadIdx.x];
-}
-
-__global__ __launch_bounds__(kBlock) void beam_merge_rows(PerPart lists, int n_parts, int64_t vocab,
-                                                         float *__restrict__ score,
-                                                         int64_t *__restrict__ parent,
-                                                         int64_t *__restrict__ token) {
-  VPE_JOIN_LDS;
-  const int64_t seq = blockIdx.x;
-  const int k = lists.k, tid = threadIdx.x;
-  uint64_t key = 0;
-  if (n_parts == 1) {
-    if (tid < k) key = lists.part[0][seq * k + tid];
-  } else {
-    join_lists(lists, seq, n_parts, k, top, cand, kListCap, best, &bound, &n_cand);
-    if (tid < k) key = best[tid];
-  }
-  if (tid < k) {
-    const int64_t i = seq * k + tid;
-    const uint64_t place = 0xFFFFFFFFull - (key & 0xFFFFFFFFull);
-    const uint64_t b = place / static_cast<uint64_t>(vocab);
-    score[i] = key == 0 ? -__builtin_huge_valf() : score_of(static_cast<uint32_t>(key >> 32));
-    parent[i] = key == 0 ? -1 : static_cast<int64_t>(b);
-    token[i] = key == 0 ? -1 : static_cast<int64_t>(place - b * static_cast<uint64_t>(vocab));
-  }
+  const int tid = threadIdx.x, n = n_parts * k;
+  const SeqParts all{parts, seq * k, k};
+  collect(all, TheKey{}, n, n <= kFew ? 1 : bound_of(all, n, k, kFew - k, s), s.few, kFew, s);
+  const uint64_t key = best_of_few(s.n, k, s);
+  if (tid >= k) return;
+  const int64_t i = seq * k + tid;
+  const uint64_t place = 0xFFFFFFFFull - (key & 0xFFFFFFFFull);
+  const uint64_t b = place / static_cast<uint64_t>(vocab);
+  score[i] = key == 0 ? -__builtin_huge_valf() : score_of(static_cast<uint32_t>(key >> 32));
+  parent[i] = key == 0 ? -1 : static_cast<int64_t>(b);
+  token[i] = key == 0 ? -1 : static_cast<int64_t>(place - b * static_cast<uint64_t>(vocab));
 }
 
 // ---------------------------------------------------------------------------
@@ -343,31 +493,38 @@ int launch_reorder(const void *src, int64_t outer, int64_t n_seqs, int beams_in,
 
 }  // namespace
 
-int64_t beam_slices(int64_t rows, int64_t cols) {
-  (void)rows;
-  const int64_t slices = (cols + kChunk - 1) / kChunk;
-  return std::min<int64_t>(slices, kMaxSlices);
+int64_t beam_groups_per_row(int64_t cols, int dtype) {
+  const int64_t group = 64 * (dtype == 1 ? Row<true>::kEpv : Row<false>::kEpv);
+  return (cols + group - 1) / group;
 }
 
 int launch_beam_select(const void *base, int64_t ld, int dtype, int64_t n_seqs, int beams,
                        int64_t cols, int64_t vocab_start, int64_t vocab, const float *lse,
-                       const float *scores, int picks, uint64_t *keys, uint64_t *slice_keys,
+                       const float *scores, int picks, uint64_t *keys, float *group_best,
                        void *stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();  // clear a stale error so the status returned is this launch's
-  const int64_t want = beam_slices(n_seqs * beams, cols);
-  const int64_t slice = ((cols + want - 1) / want + 7) / 8 * 8;
-  const int slices = static_cast<int>((cols + slice - 1) / slice);
+  const int64_t groups = beam_groups_per_row(cols, dtype);
   const BeamArgs a{static_cast<const char *>(base), ld * (dtype == 1 ? 2 : 4), cols, vocab_start,
-                   vocab, lse, scores, beams, picks, slices, slice};
-  const dim3 grid(static_cast<unsigned>(n_seqs * beams * slices));
+                   vocab, lse, scores, beams, picks, groups};
+  const bool direct = beams * cols <= kDirect;
+  if (!direct) {
+    const int64_t per_row = (groups + kGroupsPerWave - 1) / kGroupsPerWave;
+    const int64_t units = n_seqs * beams * per_row;
+    const dim3 grid(static_cast<unsigned>((units + kBlock / 64 - 1) / (kBlock / 64)));
+    if (dtype == 1)
+      hipLaunchKernelGGL((beam_groups<true>), grid, dim3(kBlock), 0, st, a, per_row, units,
+                         group_best);
+    else
+      hipLaunchKernelGGL((beam_groups<false>), grid, dim3(kBlock), 0, st, a, per_row, units,
+                         group_best);
+  }
+  const float *best = direct ? nullptr : group_best;
+  const dim3 seqs(static_cast<unsigned>(n_seqs));
   if (dtype == 1)
-    hipLaunchKernelGGL((beam_slice<true>), grid, dim3(kBlock), 0, st, a, slice_keys);
+    hipLaunchKernelGGL((beam_pick<true>), seqs, dim3(kThreads), 0, st, a, best, keys);
   else
-    hipLaunchKernelGGL((beam_slice<false>), grid, dim3(kBlock), 0, st, a, slice_keys);
-  const Adjacent lists{slice_keys, static_cast<int64_t>(beams) * slices, picks};
-  hipLaunchKernelGGL(beam_join, dim3(static_cast<unsigned>(n_seqs)), dim3(kBlock), 0, st, lists,
-                     keys);
+    hipLaunchKernelGGL((beam_pick<false>), seqs, dim3(kThreads), 0, st, a, best, keys);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -375,11 +532,10 @@ int launch_beam_merge(const uint64_t *const *keys, int n_parts, int64_t n_seqs, 
                       int64_t vocab, float *score, int64_t *parent, int64_t *token, void *stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  PerPart lists{};
-  for (int r = 0; r < n_parts; ++r) lists.part[r] = keys[r];
-  lists.k = picks;
-  hipLaunchKernelGGL(beam_merge_rows, dim3(static_cast<unsigned>(n_seqs)), dim3(kBlock), 0, st,
-                     lists, n_parts, vocab, score, parent, token);
+  PartKeys parts{};
+  for (int r = 0; r < n_parts; ++r) parts.part[r] = keys[r];
+  hipLaunchKernelGGL(beam_merge_rows, dim3(static_cast<unsigned>(n_seqs)), dim3(kThreads), 0, st, parts,
+                     n_parts, picks, vocab, score, parent, token);
   return static_cast<int>(hipGetLastError());
 }
 

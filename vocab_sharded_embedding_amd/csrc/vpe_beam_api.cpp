@@ -32,7 +32,7 @@ vpe_status vpe_beam_select_workspace(int64_t n_seqs, int32_t beams, int64_t shar
                                      int32_t picks, int64_t *bytes) {
   if (!bytes) return VPE_ERR_NULL;
   if (!beam_shape_ok(n_seqs, beams, shard_rows, picks)) return VPE_ERR_SHAPE;
-  *bytes = n_seqs * beams * vpe::beam_slices(n_seqs * beams, shard_rows) * picks * 8;
+  *bytes = n_seqs * beams * vpe::beam_groups_per_row(shard_rows, 0) * 4;
   return VPE_OK;
 }
 
@@ -62,7 +62,7 @@ vpe_status vpe_beam_select(const void *logits, int64_t ld, int64_t col_offset, v
   return launched(vpe::launch_beam_select(
       static_cast<const char *>(logits) + col_offset * size, ld, dt == VPE_BF16 ? 1 : 0, n_seqs,
       beams, shard_rows, vocab_start, vocab, lse, scores, picks, keys,
-      static_cast<uint64_t *>(workspace), stream));
+      static_cast<float *>(workspace), stream));
 }
 
 vpe_status vpe_beam_merge(const uint64_t *const *keys, int32_t n_parts, int64_t n_seqs,

@@ -101,12 +101,13 @@ int launch_distill_grad(const LogitsShard &z, const Teacher &t, const float *lse
 // ---------------------------------------------------------------------------
 // beam search
 // ---------------------------------------------------------------------------
-// Column slices a row is cut into; each leaves `picks` keys in the workspace.
-int64_t beam_slices(int64_t rows, int64_t cols);
+// Groups of columns of a row, whose largest logits (one float each) the
+// workspace holds; the most for f32.
+int64_t beam_groups_per_row(int64_t cols, int dtype);
 
 int launch_beam_select(const void *base, int64_t ld, int dtype, int64_t n_seqs, int beams,
                        int64_t cols, int64_t vocab_start, int64_t vocab, const float *lse,
-                       const float *scores, int picks, uint64_t *keys, uint64_t *slice_keys,
+                       const float *scores, int picks, uint64_t *keys, float *group_best,
                        void *stream);
 int launch_beam_merge(const uint64_t *const *keys, int n_parts, int64_t n_seqs, int picks,
                       int64_t vocab, float *score, int64_t *parent, int64_t *token, void *stream);

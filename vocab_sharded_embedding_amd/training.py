@@ -12,18 +12,32 @@ from __future__ import annotations
 import ctypes
 from typing import Optional, Sequence
 
-from . import (_check, _dtype_code, _itype_code, _need_device, _same_device, _stream_handle,
-               _torch, load_library)
+import torch
+
+from . import _check, _dtype_code, _itype_code, _need_device, _same_device, load_library
+
+# The current stream's handle by device index, without a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:  # pragma: no cover
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
-def on_device(device):
-    """Context in which `device` is current: kernels are enqueued there."""
-    return _torch().cuda.device(device)
+def enqueue(name: str, device, *args) -> None:
+    """Call `name` of the library with `args` and the device's current stream, the
+    device being the current one meanwhile (kernels are enqueued there)."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device.index))
+    if status:
+        _check(name, status)
 
 
-def workspace_for(name: str, need: int, workspace, device):
-    """The caller's workspace (checked by the library against `need`), or a new one."""
-    torch = _torch()
+def workspace_for(need: int, workspace, device):
+    """The caller's workspace (its size is checked by the library), or a new one."""
     if workspace is None:
         return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     _need_device("workspace", workspace)
@@ -36,7 +50,6 @@ def _nbytes(t) -> int:
 
 def vpe_embed_scaled(ids, weight, vocab_start: int, scale: float, out=None):
     """vpe_embed with every owned row times `scale` (fp32 product, one rounding)."""
-    torch = _torch()
     _need_device("ids", ids)
     _need_device("weight", weight)
     if weight.dim() != 2:
@@ -49,11 +62,9 @@ def vpe_embed_scaled(ids, weight, vocab_start: int, scale: float, out=None):
     if out.dtype != weight.dtype or out.numel() != ids.numel() * dim:
         raise ValueError("out must have the weight's dtype and ids.numel() * dim elements")
     _same_device(ids, weight, out)
-    with on_device(weight.device):
-        _check("vpe_embed_scaled", load_library().vpe_embed_scaled(
-            ids.data_ptr(), _itype_code(ids), ids.numel(), weight.data_ptr(), _dtype_code(weight),
-            rows, dim, int(vocab_start), float(scale), out.data_ptr(),
-            _stream_handle(weight.device)))
+    enqueue("vpe_embed_scaled", weight.device, ids.data_ptr(), _itype_code(ids), ids.numel(),
+            weight.data_ptr(), _dtype_code(weight), rows, dim, int(vocab_start), float(scale),
+            out.data_ptr())
     return out
 
 
@@ -74,7 +85,6 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
     or to a new tensor of `dtype` (grad_out's when None).  Rows of positions
     whose id lies outside the shard add nothing.
     """
-    torch = _torch()
     _need_device("ids", ids)
     _need_device("grad_out", grad_out)
     if grad_out.dim() < 1 or tuple(grad_out.shape[:-1]) != tuple(ids.shape):
@@ -93,13 +103,11 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
             raise ValueError("grad_weight must be [shard_rows, dim]")
     itype, dt, gdt = _itype_code(ids), _dtype_code(grad_out), _dtype_code(grad_weight)
     need = vpe_embed_grad_workspace(n, shard_rows, dim)
-    workspace = workspace_for("workspace", need, workspace, grad_out.device)
+    workspace = workspace_for(need, workspace, grad_out.device)
     _same_device(ids, grad_out, grad_weight, workspace)
-    with on_device(grad_out.device):
-        _check("vpe_embed_grad", load_library().vpe_embed_grad(
-            ids.data_ptr(), itype, n, grad_out.data_ptr(), dt, dim, int(vocab_start), shard_rows,
-            float(scale), grad_weight.data_ptr(), gdt, int(accumulate), workspace.data_ptr(),
-            _nbytes(workspace), _stream_handle(grad_out.device)))
+    enqueue("vpe_embed_grad", grad_out.device, ids.data_ptr(), itype, n, grad_out.data_ptr(), dt,
+            dim, int(vocab_start), shard_rows, float(scale), grad_weight.data_ptr(), gdt,
+            int(accumulate), workspace.data_ptr(), _nbytes(workspace))
     return grad_weight
 
 
@@ -108,7 +116,7 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
 # ---------------------------------------------------------------------------
 def _float_rows(name: str, t, m: int):
     _need_device(name, t)
-    if t.dtype != _torch().float32 or t.numel() != m:
+    if t.dtype != torch.float32 or t.numel() != m:
         raise ValueError(f"{name} must be a float32 tensor with one value per row")
     return t
 
@@ -158,7 +166,6 @@ def vpe_distill_shard(logits, teacher_ids, teacher, vocab_start: int, vocab: int
     logits are read and shard_lse is None (temperature 1 after
     vpe_lmhead_logsumexp, which gives the same shard_lse).
     """
-    torch = _torch()
     m, rows = logits_shard("logits", logits, shard_rows, col_offset)
     _, k, itype, tdt = _teacher(teacher_ids, teacher, teacher_lse, m)
     dt = _dtype_code(logits)
@@ -171,25 +178,22 @@ def vpe_distill_shard(logits, teacher_ids, teacher, vocab_start: int, vocab: int
         _float_rows("shard_lse", shard_lse, m)
         need = vpe_distill_workspace(m, rows)
         if workspace is not None or need > 0:
-            workspace = workspace_for("workspace", need, workspace, logits.device)
+            workspace = workspace_for(need, workspace, logits.device)
     elif shard_lse is not None:
         raise ValueError("shard_lse given with with_lse=False")
     _same_device(*(t for t in (logits, teacher, shard_dot, shard_lse, workspace) if t is not None))
-    with on_device(logits.device):
-        _check("vpe_distill_shard", load_library().vpe_distill_shard(
-            logits.data_ptr(), logits.shape[1], int(col_offset), m, rows, dt, int(vocab_start),
-            int(vocab), float(temperature), teacher_ids.data_ptr(), itype, teacher.data_ptr(), tdt,
-            k, None if teacher_lse is None else teacher_lse.data_ptr(),
-            None if shard_lse is None else shard_lse.data_ptr(), shard_dot.data_ptr(),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else _nbytes(workspace), _stream_handle(logits.device)))
+    enqueue("vpe_distill_shard", logits.device, logits.data_ptr(), logits.shape[1], int(col_offset),
+            m, rows, dt, int(vocab_start), int(vocab), float(temperature), teacher_ids.data_ptr(),
+            itype, teacher.data_ptr(), tdt, k, None if teacher_lse is None else
+            teacher_lse.data_ptr(), None if shard_lse is None else shard_lse.data_ptr(),
+            shard_dot.data_ptr(), None if workspace is None else workspace.data_ptr(), 0 if
+            workspace is None else _nbytes(workspace))
     return shard_lse, shard_dot
 
 
 def vpe_distill_loss(shard_lse: Sequence, shard_dot: Sequence, teacher_ids, teacher, vocab: int,
                      temperature: float = 1.0, teacher_lse=None, loss=None, lse=None):
     """(loss, lse) per row, float32 [m], from the shards' parts in shard order."""
-    torch = _torch()
     lses, dots = list(shard_lse), list(shard_dot)
     if not lses or len(lses) != len(dots):
         raise ValueError("need one shard_lse and one shard_dot per shard")
@@ -207,11 +211,9 @@ def vpe_distill_loss(shard_lse: Sequence, shard_dot: Sequence, teacher_ids, teac
     n = len(lses)
     lp = (ctypes.c_void_p * n)(*[t.data_ptr() for t in lses])
     dp = (ctypes.c_void_p * n)(*[t.data_ptr() for t in dots])
-    with on_device(teacher.device):
-        _check("vpe_distill_loss", load_library().vpe_distill_loss(
-            lp, dp, n, m, int(vocab), float(temperature), teacher_ids.data_ptr(), itype,
-            teacher.data_ptr(), tdt, k, None if teacher_lse is None else teacher_lse.data_ptr(),
-            loss.data_ptr(), lse.data_ptr(), _stream_handle(teacher.device)))
+    enqueue("vpe_distill_loss", teacher.device, lp, dp, n, m, int(vocab), float(temperature),
+            teacher_ids.data_ptr(), itype, teacher.data_ptr(), tdt, k, None if teacher_lse is None
+            else teacher_lse.data_ptr(), loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
 
@@ -226,7 +228,6 @@ def vpe_distill_grad(logits, lse, grad_loss, teacher_ids, teacher, vocab_start: 
     None) of grad_logits [m, ld], which may be the logits themselves, or to a
     new [m, shard_rows] tensor.
     """
-    torch = _torch()
     m, rows = logits_shard("logits", logits, shard_rows, col_offset)
     _, k, itype, tdt = _teacher(teacher_ids, teacher, teacher_lse, m)
     dt = _dtype_code(logits)
@@ -244,11 +245,9 @@ def vpe_distill_grad(logits, lse, grad_loss, teacher_ids, teacher, vocab_start: 
             raise ValueError("grad_logits must be [m, ld] of the logits' dtype")
         grad_col_offset = col_offset if grad_col_offset is None else grad_col_offset
     _same_device(logits, lse, grad_loss, teacher, grad_logits)
-    with on_device(logits.device):
-        _check("vpe_distill_grad", load_library().vpe_distill_grad(
-            logits.data_ptr(), logits.shape[1], int(col_offset), m, rows, dt, int(vocab_start),
-            int(vocab), float(temperature), teacher_ids.data_ptr(), itype, teacher.data_ptr(), tdt,
-            k, None if teacher_lse is None else teacher_lse.data_ptr(), lse.data_ptr(),
-            grad_loss.data_ptr(), grad_logits.data_ptr(), grad_logits.shape[1],
-            int(grad_col_offset), _stream_handle(logits.device)))
+    enqueue("vpe_distill_grad", logits.device, logits.data_ptr(), logits.shape[1], int(col_offset),
+            m, rows, dt, int(vocab_start), int(vocab), float(temperature), teacher_ids.data_ptr(),
+            itype, teacher.data_ptr(), tdt, k, None if teacher_lse is None else
+            teacher_lse.data_ptr(), lse.data_ptr(), grad_loss.data_ptr(), grad_logits.data_ptr(),
+            grad_logits.shape[1], int(grad_col_offset))
     return grad_logits
