@@ -34,8 +34,9 @@ vpe_status vpe_embed_scaled(const void *ids, vpe_itype itype, int64_t n, const v
                             vpe_dtype dt, int64_t shard_rows, int64_t dim, int64_t vocab_start,
                             float scale, void *out, void *stream);
 
-/* Bytes of workspace vpe_embed_grad needs.  Host-only.  Errors: VPE_ERR_NULL,
- * VPE_ERR_SHAPE (as vpe_embed_grad). */
+/* Bytes of workspace vpe_embed_grad needs for n ids; as much serves any smaller
+ * number.  Host-only.  Errors: VPE_ERR_NULL, VPE_ERR_SHAPE (as
+ * vpe_embed_grad). */
 vpe_status vpe_embed_grad_workspace(int64_t n, int64_t shard_rows, int64_t dim, int64_t *bytes);
 
 /*

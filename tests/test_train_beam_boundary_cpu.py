@@ -108,9 +108,9 @@ def test_embed_grad_workspace():
                 (10, 10, 2 ** 39)):
         assert f(*bad, ctypes.byref(b)) == vpe.VPE_ERR_SHAPE, bad
     last = 0
-    for n in (0, 1, 32, 33, 8192, 8193, 10 ** 6):
+    for n in [*range(0, 70), *range(4000, 140000, 997), 10 ** 6, 2 * 10 ** 8]:
         need = vpe.vpe_embed_grad_workspace(n, 1000, 64)
-        assert need >= last and need % 16 == 0 and need >= 1000
+        assert need >= last and need % 16 == 0
         last = need
 
 

@@ -14,10 +14,10 @@
 //    in LDS in a single launch; more ids take two launches per pass (digit
 //    counts per workgroup, then ranks and scatter).  Ids outside the shard
 //    are dropped in the first pass.
-//  - Sum: runs are cut into pieces at every multiple of kGradPiece sorted
-//    positions, so that a token with thousands of positions (natural text) is
-//    spread over the chip; pieces that are not a whole run leave fp32 partial
-//    sums, which a second kernel joins in the order of the pieces.
+//  - Sum: the sorted positions are cut into chunks of up to 32, one wave each
+//    (and per block of columns), so that a token with thousands of positions
+//    (natural text) is spread over the chip; the parts of a run that crosses
+//    chunks leave fp32 partial sums, which a second kernel joins in order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -37,16 +37,15 @@ constexpr int kWaves = kBlock / 64;
 // ---------------------------------------------------------------------------
 // scaled lookup
 // ---------------------------------------------------------------------------
-// LOG2G lanes (a power of two, at most 64) serve one row; each covers VPL
-// vectors per sweep, issued before any store.
-template <bool BF16, int EPV, int VPL, typename IdT>
+// 2^log2g lanes (at most 64) serve one row; each covers VPL vectors per sweep,
+// loaded before any is stored.
+template <bool BF16, int VPL, typename IdT>
 __global__ __launch_bounds__(kBlock) void scaled_rows(const IdT *__restrict__ ids, int64_t n,
-                                                     const void *__restrict__ weight,
+                                                     const char *__restrict__ weight,
                                                      uint64_t start, uint64_t rows, int64_t dim,
                                                      float scale, int log2g,
-                                                     void *__restrict__ out) {
-  typedef Vec<BF16, EPV> V;
-  typedef typename V::raw raw;
+                                                     char *__restrict__ out) {
+  constexpr int kEpv = BF16 ? 8 : 4;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
   const int64_t row = t >> log2g;
   if (row >= n) return;
@@ -55,29 +54,33 @@ __global__ __launch_bounds__(kBlock) void scaled_rows(const IdT *__restrict__ id
   // one unsigned compare covers both ends (a wrapped difference is >= rows)
   const uint64_t local = static_cast<uint64_t>(static_cast<int64_t>(ids[row])) - start;
   const bool owned = local < rows;
-  const int64_t vr = dim / EPV;
-  const raw *src = static_cast<const raw *>(weight) + static_cast<int64_t>(owned ? local : 0) * vr;
-  raw *dst = static_cast<raw *>(out) + row * vr;
-  for (int64_t c0 = lane; c0 < vr; c0 += static_cast<int64_t>(VPL) * group) {
-    raw r[VPL];
+  const int64_t row_bytes = dim * (BF16 ? 2 : 4);
+  const char *src = weight + static_cast<int64_t>(owned ? local : 0) * row_bytes;
+  char *dst = out + row * row_bytes;
+  typedef Vec<BF16, kEpv> V;
+  const typename V::loose *src_v = reinterpret_cast<const typename V::loose *>(src);
+  typename V::loose *dst_v = reinterpret_cast<typename V::loose *>(dst);
+  const int64_t whole = dim / kEpv;
+  for (int64_t c0 = lane; c0 < whole; c0 += VPL * group) {
+    typename V::raw r[VPL];
 #pragma unroll
     for (int c = 0; c < VPL; ++c) {
-      const int64_t col = c0 + c * group;
-      r[c] = raw(0);
-      if (owned && col < vr) r[c] = src[col];
+      r[c] = typename V::raw(0);
+      if (owned && c0 + c * group < whole) r[c] = src_v[c0 + c * group];
     }
 #pragma unroll
     for (int c = 0; c < VPL; ++c) {
-      const int64_t col = c0 + c * group;
-      float v[EPV];
+      float v[kEpv];
       V::widen(r[c], v);
 #pragma unroll
-      for (int e = 0; e < EPV; ++e) v[e] *= scale;
-      raw o = V::narrow(v);
-      if (!owned) o = raw(0);  // +0.0, also for a negative factor
-      if (col < vr) __builtin_nontemporal_store(o, dst + col);
+      for (int e = 0; e < kEpv; ++e) v[e] *= scale;
+      typename V::raw o = V::narrow(v);
+      if (!owned) o = typename V::raw(0);  // +0, also for a negative factor
+      if (c0 + c * group < whole) __builtin_nontemporal_store(o, dst_v + c0 + c * group);
     }
   }
+  for (int64_t i = whole * kEpv + lane; i < dim; i += group)
+    store_one<BF16>(dst, i, owned ? load_one<BF16>(src, i) * scale : 0.f);
 }
 
 int ceil_log2(int64_t v) {
@@ -89,19 +92,20 @@ int ceil_log2(int64_t v) {
 // Rows per launch: keeps every grid inside the 32-bit work-item range.
 constexpr int64_t kRowsPerLaunch = int64_t(1) << 24;
 
-template <bool BF16, int EPV, typename IdT>
-int scaled_launch(const IdT *ids, int64_t n, const void *weight, int64_t rows, int64_t dim,
-                  int64_t start, float scale, void *out, hipStream_t st) {
-  const int64_t vr = dim / EPV;
+template <bool BF16, typename IdT>
+int scaled_any(const IdT *ids, int64_t n, const void *weight, int64_t rows, int64_t dim,
+               int64_t start, float scale, void *out, hipStream_t st) {
+  const int64_t vr = (dim + (BF16 ? 7 : 3)) / (BF16 ? 8 : 4);  // vectors per row
   const int log2g = std::min(6, ceil_log2(vr));
   for (int64_t r0 = 0; r0 < n; r0 += kRowsPerLaunch) {
     const int64_t nr = std::min(n - r0, kRowsPerLaunch);
     const unsigned blocks = static_cast<unsigned>(((nr << log2g) + kBlock - 1) / kBlock);
-    void *o = static_cast<char *>(out) + r0 * dim * (BF16 ? 2 : 4);
-#define VPE_SCALED(VPL)                                                                        \
-  hipLaunchKernelGGL((scaled_rows<BF16, EPV, VPL, IdT>), dim3(blocks), dim3(kBlock), 0, st,    \
-                     ids + r0, nr, weight, static_cast<uint64_t>(start),                       \
-                     static_cast<uint64_t>(rows), dim, scale, log2g, o)
+    char *o = static_cast<char *>(out) + r0 * dim * (BF16 ? 2 : 4);
+#define VPE_SCALED(VPL)                                                                     \
+  hipLaunchKernelGGL((scaled_rows<BF16, VPL, IdT>), dim3(blocks), dim3(kBlock), 0, st,      \
+                     ids + r0, nr, static_cast<const char *>(weight),                       \
+                     static_cast<uint64_t>(start), static_cast<uint64_t>(rows), dim, scale, \
+                     log2g, o)
     if (vr <= 64) VPE_SCALED(1);
     else if (vr <= 128) VPE_SCALED(2);
     else if (vr <= 256) VPE_SCALED(4);
@@ -111,46 +115,27 @@ int scaled_launch(const IdT *ids, int64_t n, const void *weight, int64_t rows, i
   return static_cast<int>(hipGetLastError());
 }
 
-// Most elements per vector that divide the row and keep every base aligned
-// (`low`: the bases' addresses or-ed together, in bytes).
-int pick_epv(bool bf16, int64_t dim, uint64_t low) {
-  const int size = bf16 ? 2 : 4;
-  for (int epv = 16 / size; epv > 1; epv /= 2)
-    if (dim % epv == 0 && low % (static_cast<uint64_t>(epv) * size) == 0) return epv;
-  return 1;
-}
-
-template <typename IdT>
-int scaled_any(const IdT *ids, int64_t n, const void *weight, int dtype, int64_t rows, int64_t dim,
-               int64_t start, float scale, void *out, hipStream_t st) {
-  const int epv = pick_epv(dtype == 1, dim,
-                           reinterpret_cast<uint64_t>(weight) | reinterpret_cast<uint64_t>(out));
-  if (dtype == 1) {
-    switch (epv) {
-      case 8: return scaled_launch<true, 8>(ids, n, weight, rows, dim, start, scale, out, st);
-      case 4: return scaled_launch<true, 4>(ids, n, weight, rows, dim, start, scale, out, st);
-      case 2: return scaled_launch<true, 2>(ids, n, weight, rows, dim, start, scale, out, st);
-      default: return scaled_launch<true, 1>(ids, n, weight, rows, dim, start, scale, out, st);
-    }
-  }
-  switch (epv) {
-    case 4: return scaled_launch<false, 4>(ids, n, weight, rows, dim, start, scale, out, st);
-    case 2: return scaled_launch<false, 2>(ids, n, weight, rows, dim, start, scale, out, st);
-    default: return scaled_launch<false, 1>(ids, n, weight, rows, dim, start, scale, out, st);
-  }
-}
-
 // ---------------------------------------------------------------------------
 // stable sort of the owned positions by token
 // ---------------------------------------------------------------------------
+constexpr int kDigitBits = 9;
+constexpr int kDigits = static_cast<int>(kSortDigits);
+static_assert(kDigits == 1 << kDigitBits, "digit values");
+
 // Lanes of the wave whose digit equals this lane's, among lanes with `valid`.
-__device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits, bool valid) {
-  uint64_t mask = __ballot(valid);
-  for (int b = 0; b < bits; ++b) {
-    const uint64_t one = __ballot((digit >> b) & 1u);
-    mask &= ((digit >> b) & 1u) ? one : ~one;
+// All kDigitBits bits, unrolled: a rolled loop pays more for its branch than
+// for a bit.
+__device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool valid) {
+  const uint64_t mask = __ballot(valid);
+  uint32_t lo = static_cast<uint32_t>(mask), hi = static_cast<uint32_t>(mask >> 32);
+#pragma unroll
+  for (int b = 0; b < kDigitBits; ++b) {
+    const uint32_t bit = (digit >> b) & 1u, set = 0u - bit;
+    const uint64_t one = __ballot(bit != 0);
+    lo &= ~(static_cast<uint32_t>(one) ^ set);
+    hi &= ~(static_cast<uint32_t>(one >> 32) ^ set);
   }
-  return mask;
+  return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
 __device__ __forceinline__ int below(uint64_t mask) {  // set lanes below this one
@@ -169,113 +154,121 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   return v;
 }
 
-constexpr int kOneThreads = 1024;
-constexpr int kOneWaves = kOneThreads / 64;
-constexpr int kOneItems = static_cast<int>(kGradOneBlockIds / kOneThreads);
-constexpr int kDigits = static_cast<int>(kSortDigits);
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
 
-// Every owned id of at most kGradOneBlockIds, sorted in LDS.  Wave w takes the
-// w-th run of items; a digit's items are ranked by (wave, round, lane), which
-// is their order, so the sort is stable.
+// Workgroups of zeros that ride along with the sort, which leaves most of the
+// chip idle: rows [row0, row1) of the gradient, `blocks` workgroups after the
+// sort's own.  flags == nullptr: all of them; else those without an id.
+struct ZeroRows {
+  char *dw;
+  int64_t row_bytes;
+  int64_t row0, row1;
+  const uint8_t *flags;
+  unsigned blocks;
+};
+
+// `block` of z.blocks workgroups of `threads` threads.
+__device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int threads) {
+  const int64_t share = (z.row1 - z.row0 + z.blocks - 1) / z.blocks;
+  const int64_t r0 = z.row0 + block * share, r1 = r0 + share < z.row1 ? r0 + share : z.row1;
+  if (r0 >= r1) return;
+  if (z.flags == nullptr) {
+    zero_bytes(z.dw + r0 * z.row_bytes, (r1 - r0) * z.row_bytes, threadIdx.x, threads);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = r0 + wave_in_block() * 64; r < r1; r += threads) {
+    uint64_t empty = __ballot(r + lane < r1 && z.flags[r + lane < r1 ? r + lane : r0] == 0);
+    while (empty) {
+      const int64_t row = r + __builtin_ctzll(empty);
+      empty &= empty - 1;
+      zero_bytes(z.dw + row * z.row_bytes, z.row_bytes, lane, 64);
+    }
+  }
+}
+
+// Every owned id of at most kGradOneBlockIds, sorted in LDS by workgroup 0.
+// Wave w takes the w-th run of items in every pass; an item's place is behind
+// the smaller digits, behind its digit's items of the waves and rounds before
+// and of the lanes before, so the sort is stable.
 template <typename IdT>
-__global__ __launch_bounds__(kOneThreads) void sort_one_block(
+__global__ __launch_bounds__(kSortThreads) void sort_one_block(
     const IdT *__restrict__ ids, int n, uint64_t start, uint64_t rows, int bits, int passes,
     uint32_t *__restrict__ key_out, uint32_t *__restrict__ pos_out,
-    uint32_t *__restrict__ count_out, uint8_t *flags) {
-  __shared__ uint32_t skey[kGradOneBlockIds];
-  __shared__ uint16_t spos[kGradOneBlockIds];
-  __shared__ uint16_t cnt_[kOneWaves][kDigits];
+    uint32_t *__restrict__ count_out, ZeroRows zero) {
+  constexpr uint32_t kNone = 0xffffffffu;  // an id of another shard (rows < 2^31)
+  __shared__ uint32_t skey[2][kGradOneBlockIds];
+  __shared__ uint16_t spos[2][kGradOneBlockIds];
+  __shared__ uint32_t at_[kSortWaves][kDigits];
   __shared__ uint32_t sums[kDigits / 64];
+  if (blockIdx.x > 0) return zero_rows(zero, blockIdx.x - 1, kSortThreads);
   // a wave reads and updates its own counters in program order
-  volatile uint16_t(*cnt)[kDigits] = cnt_;
+  volatile uint32_t(*at)[kDigits] = at_;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
-
-  if (flags != nullptr) {
-    u32x4 *f = reinterpret_cast<u32x4 *>(flags);
-    const int64_t nf = static_cast<int64_t>((rows + 15) / 16);
-    for (int64_t i = tid; i < nf; i += kOneThreads) f[i] = u32x4(0);
+#pragma unroll 4
+  for (int i = tid; i < n; i += kSortThreads) {
+    const uint64_t local = static_cast<uint64_t>(static_cast<int64_t>(ids[i])) - start;
+    skey[0][i] = local < rows ? static_cast<uint32_t>(local) : kNone;
+    spos[0][i] = static_cast<uint16_t>(i);
   }
-
-  uint32_t key[kOneItems], pos[kOneItems], rank[kOneItems];
-  bool have[kOneItems];
+  const uint32_t low = (1u << bits) - 1;
   int m = n;
-  int rounds = (m + kOneThreads - 1) / kOneThreads;
-#pragma unroll
-  for (int r = 0; r < kOneItems; ++r) {
-    const int i = (wave * rounds + r) * 64 + lane;
-    have[r] = false, key[r] = 0, pos[r] = 0, rank[r] = 0;
-    if (r < rounds && i < m) {
-      const uint64_t local = static_cast<uint64_t>(static_cast<int64_t>(ids[i])) - start;
-      have[r] = local < rows;
-      key[r] = static_cast<uint32_t>(local);
-      pos[r] = static_cast<uint32_t>(i);
-    }
-  }
   for (int pass = 0; pass < passes; ++pass) {
+    const uint32_t *from = skey[pass & 1];
+    const uint16_t *from_pos = spos[pass & 1];
+    uint32_t *to_key = skey[1 - (pass & 1)];
+    uint16_t *to_pos = spos[1 - (pass & 1)];
     const int shift = pass * bits;
-    const uint32_t low = (1u << bits) - 1;
-    for (int d = tid; d < kOneWaves * kDigits / 2; d += kOneThreads)
-      reinterpret_cast<uint32_t *>(cnt_)[d] = 0;
-    __syncthreads();
+    const int share = (m + kSortThreads - 1) / kSortThreads * 64;
+    const int i0 = wave * share, i1 = i0 + share < m ? i0 + share : m;
 #pragma unroll
-    for (int r = 0; r < kOneItems; ++r) {
-      if (r < rounds) {
-        const uint32_t d = (key[r] >> shift) & low;
-        const uint64_t same = same_digit(d, bits, have[r]);
-        if (have[r]) {
-          const uint32_t seen = cnt[wave][d];
-          rank[r] = seen + below(same);
-          if (below(same) == 0) cnt[wave][d] = static_cast<uint16_t>(seen + __popcll(same));
-        }
-      }
-    }
+    for (int d = 0; d < kSortWaves * kDigits; d += kSortThreads)
+      reinterpret_cast<uint32_t *>(at_)[d + tid] = 0;
+    __syncthreads();
+    for (int i = i0 + lane; i < i1; i += 64)
+      if (from[i] != kNone) atomicAdd(&at_[wave][(from[i] >> shift) & low], 1u);
     __syncthreads();
     // exclusive sums over (digit, wave)
-    uint32_t total = 0, incl = 0;
+    uint32_t c[kSortWaves], total = 0, incl = 0;
     if (tid < kDigits) {
-      for (int w = 0; w < kOneWaves; ++w) total += cnt_[w][tid];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) c[w] = at_[w][tid], total += c[w];
       incl = wave_scan(total);
       if (lane == 63) sums[wave] = incl;
     }
     __syncthreads();
+    uint32_t all = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kDigits / 64; ++w) {
+      before += w < wave ? sums[w] : 0;
+      all += sums[w];
+    }
     if (tid < kDigits) {
-      uint32_t at = incl - total;
-      for (int w = 0; w < wave; ++w) at += sums[w];
-      for (int w = 0; w < kOneWaves; ++w) {
-        const uint32_t c = cnt_[w][tid];
-        cnt_[w][tid] = static_cast<uint16_t>(at);
-        at += c;
-      }
-    }
-    uint32_t all = 0;
-    for (int w = 0; w < kDigits / 64; ++w) all += sums[w];
-    __syncthreads();
+      uint32_t to = before + incl - total;
 #pragma unroll
-    for (int r = 0; r < kOneItems; ++r) {
-      if (r < rounds && have[r]) {
-        const uint32_t to = cnt_[wave][(key[r] >> shift) & low] + rank[r];
-        skey[to] = key[r];
-        spos[to] = static_cast<uint16_t>(pos[r]);
-      }
+      for (int w = 0; w < kSortWaves; ++w) at_[w][tid] = to, to += c[w];
     }
     __syncthreads();
+    for (int r = i0; r < i1; r += 64) {
+      const int i = r + lane;
+      const uint32_t key = i < i1 ? from[i] : kNone;
+      const uint32_t d = (key >> shift) & low;
+      const uint64_t same = same_digit(d, key != kNone);
+      if (key != kNone) {
+        const uint32_t seen = at[wave][d];
+        const int ahead = below(same);
+        if (ahead == 0) at[wave][d] = seen + __popcll(same);
+        to_key[seen + ahead] = key;
+        to_pos[seen + ahead] = from_pos[i];
+      }
+    }
     m = static_cast<int>(all);
-    rounds = (m + kOneThreads - 1) / kOneThreads;
-#pragma unroll
-    for (int r = 0; r < kOneItems; ++r) {
-      const int i = (wave * rounds + r) * 64 + lane;
-      have[r] = r < rounds && i < m;
-      if (have[r]) key[r] = skey[i], pos[r] = spos[i];
-    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int r = 0; r < kOneItems; ++r) {
-    const int i = (wave * rounds + r) * 64 + lane;
-    if (have[r]) {
-      key_out[i] = key[r];
-      pos_out[i] = pos[r];
-      if (flags != nullptr) flags[key[r]] = 1;
-    }
+  for (int i = tid; i < m; i += kSortThreads) {
+    key_out[i] = skey[passes & 1][i];
+    pos_out[i] = spos[passes & 1][i];
   }
   if (tid == 0) *count_out = static_cast<uint32_t>(m);
 }
@@ -298,101 +291,130 @@ struct SortItems {
     }
   }
 };
+struct SortPass {
+  int64_t n;       // ids
+  int64_t tile;    // items per workgroup, a multiple of kSortThreads
+  unsigned blocks;
+  int shift, bits;
+};
 
+// hist[b][d] = items of digit d in workgroup b's tile.  The first pass also
+// clears the rows' flags.
 template <bool FIRST, typename IdT>
-__global__ __launch_bounds__(kBlock) void sort_counts(SortItems<FIRST, IdT> items, int64_t n,
-                                                     const uint32_t *count, int64_t tile,
-                                                     int shift, int bits, uint32_t *hist,
-                                                     uint8_t *flags) {
+__global__ __launch_bounds__(kSortThreads) void sort_counts(SortItems<FIRST, IdT> items,
+                                                           SortPass pass, const uint32_t *count,
+                                                           uint32_t *hist, uint8_t *flags,
+                                                           ZeroRows zero) {
   __shared__ uint32_t h[kDigits];
+  if (blockIdx.x >= pass.blocks) return zero_rows(zero, blockIdx.x - pass.blocks, kSortThreads);
   const int tid = threadIdx.x;
   if (FIRST && flags != nullptr) {
     u32x4 *f = reinterpret_cast<u32x4 *>(flags);
     const int64_t nf = static_cast<int64_t>((items.rows + 15) / 16);
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kBlock + tid; i < nf;
-         i += static_cast<int64_t>(gridDim.x) * kBlock)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; i < nf;
+         i += static_cast<int64_t>(pass.blocks) * kSortThreads)
       f[i] = u32x4(0);
   }
-  for (int d = tid; d < kDigits; d += kBlock) h[d] = 0;
+  if (tid < kDigits) h[tid] = 0;
   __syncthreads();
-  const int64_t m = FIRST ? n : static_cast<int64_t>(*count);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * tile;
-  const int64_t i1 = i0 + tile < m ? i0 + tile : m;
-  const uint32_t low = (1u << bits) - 1;
-  for (int64_t i = i0 + tid; i < i1; i += kBlock) {
+  const int64_t m = FIRST ? pass.n : static_cast<int64_t>(*count);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * pass.tile;
+  const int64_t i1 = i0 + pass.tile < pass.n ? i0 + pass.tile : pass.n;
+  const uint32_t low = (1u << pass.bits) - 1;
+  // keys past m are read and dropped: they lie inside the buffer, and waiting
+  // for m first costs a latency
+#pragma unroll 2
+  for (int64_t i = i0 + tid; i < i1; i += kSortThreads) {
     uint32_t key;
-    if (items.get(i, key)) atomicAdd(&h[(key >> shift) & low], 1u);
+    if (items.get(i, key) && i < m) atomicAdd(&h[(key >> pass.shift) & low], 1u);
   }
   __syncthreads();
-  for (int d = tid; d < kDigits; d += kBlock)
-    hist[static_cast<int64_t>(blockIdx.x) * kDigits + d] = h[d];
+  if (tid < kDigits) hist[static_cast<int64_t>(blockIdx.x) * kDigits + tid] = h[tid];
 }
 
+// Every item to its place: behind the smaller digits, behind its digit's items
+// in the workgroups, waves and rounds before, behind the lanes before.
 template <bool FIRST, typename IdT>
-__global__ __launch_bounds__(kBlock) void sort_scatter(SortItems<FIRST, IdT> items, int64_t n,
-                                                      uint32_t *count, int64_t tile, int shift,
-                                                      int bits, const uint32_t *__restrict__ hist,
-                                                      uint32_t *__restrict__ key_out,
-                                                      uint32_t *__restrict__ pos_out,
-                                                      uint8_t *flags) {
-  __shared__ uint32_t at_[kWaves][kDigits];
+__global__ __launch_bounds__(kSortThreads) void sort_scatter(
+    SortItems<FIRST, IdT> items, SortPass pass, uint32_t *count, const uint32_t *__restrict__ hist,
+    uint32_t *__restrict__ key_out, uint32_t *__restrict__ pos_out, uint8_t *flags,
+    ZeroRows zero) {
+  constexpr int kParts = kSortThreads / (kDigits / 2);  // threads that share a pair of digits
+  __shared__ uint32_t at_[kSortWaves][kDigits];
+  __shared__ u32x2 part_before[kParts][kDigits / 2], part_total[kParts][kDigits / 2];
   __shared__ uint32_t base[kDigits];
-  __shared__ uint32_t sums[kWaves];
+  __shared__ uint32_t sums[kDigits / 128];
+  if (blockIdx.x >= pass.blocks) return zero_rows(zero, blockIdx.x - pass.blocks, kSortThreads);
+  // a wave reads and updates its own counters in program order
   volatile uint32_t(*at)[kDigits] = at_;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
-  const int64_t m = FIRST ? n : static_cast<int64_t>(*count);
+  const int64_t m = FIRST ? pass.n : static_cast<int64_t>(*count);
+  const uint32_t low = (1u << pass.bits) - 1;
 
-  // where this workgroup's items of each digit go: the digits below, and the
-  // same digit of the workgroups before (thread t: digits 2t and 2t + 1)
-  uint32_t before0 = 0, before1 = 0, total0 = 0, total1 = 0;
+  // the workgroups' counts: pair of digits `pair`, every kParts-th workgroup
+  const int pair = tid % (kDigits / 2), part = tid / (kDigits / 2);
+  u32x2 before = u32x2(0), total = u32x2(0);
   const u32x2 *h2 = reinterpret_cast<const u32x2 *>(hist);
 #pragma unroll 8
-  for (unsigned b = 0; b < gridDim.x; ++b) {
-    const u32x2 c = h2[b * (kDigits / 2) + tid];
-    if (b < blockIdx.x) before0 += c[0], before1 += c[1];
-    total0 += c[0], total1 += c[1];
+  for (unsigned b = part; b < pass.blocks; b += kParts) {
+    const u32x2 c = h2[b * (kDigits / 2) + pair];
+    if (b < blockIdx.x) before += c;
+    total += c;
   }
-  const uint32_t incl = wave_scan(total0 + total1);
-  if (lane == 63) sums[wave] = incl;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) at_[w][2 * tid] = 0, at_[w][2 * tid + 1] = 0;
+  // counts of every wave's part of the tile
+  for (int d = tid; d < kSortWaves * kDigits; d += kSortThreads)
+    reinterpret_cast<uint32_t *>(at_)[d] = 0;
   __syncthreads();
-  uint32_t first = incl - total0 - total1;
-  for (int w = 0; w < wave; ++w) first += sums[w];
-  base[2 * tid] = first + before0;
-  base[2 * tid + 1] = first + total0 + before1;
-  if (FIRST && blockIdx.x == 0 && tid == kBlock - 1) *count = first + total0 + total1;
-
-  // counts of each wave's quarter of the tile
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * tile + wave * (tile / kWaves);
-  const int64_t i1 = i0 + tile / kWaves < m ? i0 + tile / kWaves : m;
-  const uint32_t low = (1u << bits) - 1;
+  const int64_t per_wave = pass.tile / kSortWaves;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * pass.tile + wave * per_wave;
+  const int64_t i1 = i0 + per_wave < pass.n ? i0 + per_wave : pass.n;
+#pragma unroll 2
   for (int64_t i = i0 + lane; i < i1; i += 64) {
     uint32_t key;
-    if (items.get(i, key)) atomicAdd(&at_[wave][(key >> shift) & low], 1u);
+    if (items.get(i, key) && i < m) atomicAdd(&at_[wave][(key >> pass.shift) & low], 1u);
+  }
+  part_before[part][pair] = before;
+  part_total[part][pair] = total;
+  __syncthreads();
+  uint32_t incl = 0;
+  if (part == 0) {
+#pragma unroll
+    for (int q = 1; q < kParts; ++q) before += part_before[q][pair], total += part_total[q][pair];
+    incl = wave_scan(total[0] + total[1]);
+    if (lane == 63) sums[wave] = incl;
   }
   __syncthreads();
-  for (int d = tid; d < kDigits; d += kBlock) {
-    uint32_t to = base[d];
-    for (int w = 0; w < kWaves; ++w) {
-      const uint32_t c = at_[w][d];
-      at_[w][d] = to;
-      to += c;
-    }
+  if (part == 0) {
+    uint32_t first = incl - total[0] - total[1];
+#pragma unroll
+    for (int w = 0; w < kDigits / 128; ++w) first += w < wave ? sums[w] : 0;
+    base[2 * pair] = first + before[0];
+    base[2 * pair + 1] = first + total[0] + before[1];
+    if (FIRST && blockIdx.x == 0 && pair == kDigits / 2 - 1) *count = first + total[0] + total[1];
+  }
+  __syncthreads();
+  if (tid < kDigits) {
+    uint32_t c[kSortWaves], to = base[tid];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = at_[w][tid];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) at_[w][tid] = to, to += c[w];
   }
   __syncthreads();
   for (int64_t r = i0; r < i1; r += 64) {
     const int64_t i = r + lane;
-    uint32_t key = 0;
-    const bool have = i < i1 && items.get(i, key);
-    const uint32_t d = (key >> shift) & low;
-    const uint64_t same = same_digit(d, bits, have);
+    uint32_t key = 0, from = static_cast<uint32_t>(i);
+    bool have = i < i1 && items.get(i, key);
+    if (!FIRST && i < i1) from = items.pos_in[i];
+    have = have && i < m;
+    const uint32_t d = (key >> pass.shift) & low;
+    const uint64_t same = same_digit(d, have);
     if (have) {
       const uint32_t seen = at[wave][d];
       const uint32_t to = seen + below(same);
       if (below(same) == 0) at[wave][d] = seen + __popcll(same);
       key_out[to] = key;
-      pos_out[to] = FIRST ? static_cast<uint32_t>(i) : items.pos_in[i];
+      pos_out[to] = from;
       if (FIRST && flags != nullptr) flags[key] = 1;
     }
   }
@@ -403,139 +425,137 @@ __global__ __launch_bounds__(kBlock) void sort_scatter(SortItems<FIRST, IdT> ite
 // ---------------------------------------------------------------------------
 struct GradArgs {
   const uint32_t *key, *pos, *count;
-  const void *dy;
+  const char *dy;
   int64_t dim;
   float scale;
-  void *dw;
+  char *dw;
   bool accumulate;
-  float *partial;      // [2 * pieces][dim]
-  const uint8_t *flags;
-  int64_t rows;
-  int col_blocks;      // waves per row
+  float *partial;      // [2 * chunks][partial_ld]
+  int64_t partial_ld;
+  int chunk;           // sorted positions per wave, a power of two up to 32
+  int col_blocks;      // waves per chunk
 };
 
-constexpr int kPiece = static_cast<int>(kGradPiece);
-constexpr int kZeroRowsPerWave = 16;
-
 template <bool OUT16, int EPV>
-__device__ __forceinline__ void write_row(const GradArgs &a, int64_t elem, const float (&sum)[EPV]) {
+__device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64_t col,
+                                          const float (&sum)[EPV]) {
+  char *dw = a.dw + static_cast<int64_t>(row) * a.dim * (OUT16 ? 2 : 4);
   float v[EPV];
   if (a.accumulate) {
-    load_vec<OUT16, EPV>(a.dw, elem, v);
+    load_vec<OUT16, EPV>(dw, col, a.dim, v);
 #pragma unroll
     for (int e = 0; e < EPV; ++e) v[e] = v[e] + a.scale * sum[e];
   } else {
 #pragma unroll
     for (int e = 0; e < EPV; ++e) v[e] = a.scale * sum[e];
   }
-  store_vec_nt<OUT16, EPV>(a.dw, elem, v);
+  store_vec_nt<OUT16, EPV>(dw, col, a.dim, v);
 }
 
-// Waves [0, positions * col_blocks) take one sorted position and column block
-// each: the wave whose position begins a piece sums it, the others end at
-// once.  The waves after them write the zero rows, kZeroRowsPerWave each.
-template <bool IN16, bool OUT16, int EPV, int VPL>
-__global__ __launch_bounds__(kBlock) void grad_pieces(GradArgs a, int64_t p0, int64_t n_pos,
-                                                     int64_t pos_blocks, int64_t zero_row0) {
+// One wave per chunk of sorted positions and block of 64 vectors of columns: it
+// walks the chunk's rows, kDeep of them in flight, and leaves each run of equal
+// tokens when it ends.  A run that began before the chunk or goes on behind it
+// leaves a partial sum: slot 2c if it holds the chunk's first position, slot
+// 2c + 1 if it begins inside.  Workgroups after them write zero rows.
+template <bool IN16, bool OUT16, int EPV>
+__global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0, int64_t n_chunks,
+                                                     unsigned chunk_blocks, ZeroRows zero) {
+  if (blockIdx.x >= chunk_blocks) return zero_rows(zero, blockIdx.x - chunk_blocks, kBlock);
+  typedef Vec<IN16, EPV> V;
+  constexpr int kDeep = 8;
   const int lane = threadIdx.x & 63;
-  const int64_t vr = a.dim / EPV;
-  if (static_cast<int64_t>(blockIdx.x) >= pos_blocks) {
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) - pos_blocks) * kWaves + wave_in_block();
-    const int64_t r0 = zero_row0 + w * kZeroRowsPerWave;
-    const bool here = lane < kZeroRowsPerWave && r0 + lane < a.rows;
-    uint64_t empty = __ballot(here && a.flags[here ? r0 + lane : 0] == 0);
-    float zero[EPV];
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) zero[e] = 0.f;
-    while (empty) {
-      const int64_t row = r0 + __builtin_ctzll(empty);
-      empty &= empty - 1;
-      for (int64_t c = lane; c < vr; c += 64)
-        store_vec_nt<OUT16, EPV>(a.dw, row * a.dim + c * EPV, zero);
-    }
-    return;
-  }
   const int64_t wave = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
   const int64_t rel = wave / a.col_blocks;
-  if (rel >= n_pos) return;
-  const int64_t p = p0 + rel;
-  const int64_t n = *a.count;
-  if (p >= n) return;
-  const int64_t col0 = (wave - rel * a.col_blocks) * (64 * VPL);
-  const uint32_t token = a.key[p];
-  const bool head = p == 0 || a.key[p - 1] != token;
-  if (!head && p % kPiece != 0) return;
-  const int64_t limit = (p / kPiece + 1) * kPiece < n ? (p / kPiece + 1) * kPiece : n;
-  const bool mine = lane < kPiece && p + lane < limit && a.key[p + lane] == token;
-  const uint32_t src = mine ? a.pos[p + lane] : 0;
-  const int len = __popcll(__ballot(mine));
-  const bool whole = head && !(p + len == limit && limit < n && a.key[limit] == token);
+  if (rel >= n_chunks) return;
+  const int64_t c = chunk0 + rel;
+  const int64_t n = *a.count, p0 = c * a.chunk;
+  if (p0 >= n) return;
+  const int len = n - p0 < a.chunk ? static_cast<int>(n - p0) : a.chunk;
+  // lane l < len: position p0 + l; lane len: the position behind the chunk
+  const uint32_t key = p0 + lane < n ? a.key[p0 + lane] : 0;
+  const uint32_t before = p0 > 0 ? a.key[p0 - 1] : 0;
+  const uint32_t pos = lane < len ? a.pos[p0 + lane] : 0;
+  // ends: bit l is set where the run of position l ends with it
+  const uint32_t next = __shfl_down(key, 1);
+  const uint64_t ends = __ballot(lane < len && (p0 + lane + 1 >= n || next != key));
+  const bool begun = p0 > 0 && before == static_cast<uint32_t>(
+                                             __builtin_amdgcn_readfirstlane(static_cast<int>(key)));
 
-  float sum[VPL][EPV];
+  const int64_t col = ((wave - rel * a.col_blocks) * 64 + lane) * EPV;
+  const bool whole = col + EPV <= a.dim;
+  const bool ragged = __ballot(!whole && col < a.dim) != 0;  // a row's end inside a vector
+  const int64_t in_bytes = a.dim * V::kSize;
+  float sum[EPV];
 #pragma unroll
-  for (int c = 0; c < VPL; ++c)
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) sum[c][e] = 0.f;
-  constexpr int kDeep = 4;  // rows in flight
-  for (int i = 0; i < len; i += kDeep) {
-    float v[kDeep][VPL][EPV];
+  for (int e = 0; e < EPV; ++e) sum[e] = 0.f;
+  bool inside = !begun;  // the run began in this chunk, at its first position or later
+  int first = 0;         // the run's first position in the chunk
+  for (int i0 = 0; i0 < len; i0 += kDeep) {
+    typename V::raw r[kDeep];
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
-      const uint32_t s = static_cast<uint32_t>(
-          __builtin_amdgcn_readlane(static_cast<int>(src), i + u < len ? i + u : 0));
-      const int64_t at = static_cast<int64_t>(s) * a.dim;
-#pragma unroll
-      for (int c = 0; c < VPL; ++c) {
-        const int64_t col = col0 + c * 64 + lane;
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) v[u][c][e] = 0.f;
-        if (i + u < len && col < vr) load_vec<IN16, EPV>(a.dy, at + col * EPV, v[u][c]);
-      }
+      const int64_t s = static_cast<uint32_t>(
+          __builtin_amdgcn_readlane(static_cast<int>(pos), i0 + u < len ? i0 + u : i0));
+      r[u] = typename V::raw(0);
+      if (whole && i0 + u < len)
+        r[u] = *reinterpret_cast<const typename V::loose *>(a.dy + s * in_bytes + col * V::kSize);
     }
 #pragma unroll
-    for (int u = 0; u < kDeep; ++u)
+    for (int u = 0; u < kDeep; ++u) {
+      const int i = i0 + u;
+      if (i >= len) break;
+      float v[EPV];
+      V::widen(r[u], v);
+      if (ragged) {
+        const int64_t s = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(pos), i));
+        if (!whole) load_vec<IN16, EPV>(a.dy + s * in_bytes, col, a.dim, v);
+      }
 #pragma unroll
-      for (int c = 0; c < VPL; ++c)
+      for (int e = 0; e < EPV; ++e) sum[e] += v[e];
+      const bool end = (ends >> i) & 1;
+      if (end || i == len - 1) {
+        if (col < a.dim) {
+          if (inside && end) {
+            const uint32_t token =
+                static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), i));
+            write_row<OUT16, EPV>(a, token, col, sum);
+          } else {
+            f32x4 *o = reinterpret_cast<f32x4 *>(a.partial + (2 * c + (first > 0)) * a.partial_ld +
+                                                 col);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) sum[c][e] += v[u][c][e];
-  }
+            for (int e = 0; e < EPV; e += 4)
+              o[e / 4] = f32x4{sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
+          }
+        }
 #pragma unroll
-  for (int c = 0; c < VPL; ++c) {
-    const int64_t col = col0 + c * 64 + lane;
-    if (col >= vr) continue;
-    if (whole) {
-      write_row<OUT16, EPV>(a, static_cast<int64_t>(token) * a.dim + col * EPV, sum[c]);
-    } else {
-      // slot 2c: the piece that begins with chunk c; 2c + 1: the one inside it
-      const int64_t slot = 2 * (p / kPiece) + (p % kPiece != 0);
-      float *o = a.partial + slot * a.dim + col * EPV;
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) o[e] = sum[c][e];
+        for (int e = 0; e < EPV; ++e) sum[e] = 0.f;
+        inside = true;
+        first = i + 1;
+      }
     }
   }
 }
 
-// One wave per chunk of kPiece positions and column block: the run that leaves
-// the chunk having begun in it is joined from its pieces, in order.
-template <bool OUT16, int EPV>
-__global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int64_t n_chunks) {
-  const int lane = threadIdx.x & 63;
-  const int64_t vr = a.dim / EPV;
-  const int64_t blocks = (vr + 63) / 64;
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
-  const int64_t rel = wave / blocks;
+// One workgroup per chunk and block of 256 columns: the run that leaves the
+// chunk having begun in it is joined from its partial sums, a quarter of them
+// per wave, in order.
+template <bool OUT16>
+__global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int col_blocks) {
+  __shared__ f32x4 part[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = wave_in_block();
+  const int64_t rel = blockIdx.x / static_cast<unsigned>(col_blocks);
   const int64_t c = chunk0 + rel;
   const int64_t n = *a.count;
-  const int64_t next = (c + 1) * kPiece;
-  if (rel >= n_chunks || next >= n) return;
+  const int64_t next = (c + 1) * a.chunk;
+  if (next >= n) return;
   const uint32_t token = a.key[next];
   if (a.key[next - 1] != token) return;
-  const bool whole_chunk = a.key[next - kPiece] == token;
-  if (whole_chunk && c > 0 && a.key[next - kPiece - 1] == token) return;  // began before
+  const bool whole_chunk = a.key[next - a.chunk] == token;
+  if (whole_chunk && c > 0 && a.key[next - a.chunk - 1] == token) return;  // began before
   // chunks after c that begin with the token
   int64_t more = 1;
   for (;;) {
-    const int64_t q = (c + 1 + more + lane) * kPiece;
+    const int64_t q = (c + 1 + more + lane) * a.chunk;
     const uint64_t on = __ballot(q < n && a.key[q < n ? q : 0] == token);
     if (on != ~0ull) {
       more += __builtin_ctzll(~on);
@@ -543,123 +563,135 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
     }
     more += 64;
   }
-  const int64_t col = (wave - rel * blocks) * 64 + lane;
-  if (col >= vr) return;
-  float sum[EPV];
-  load_vec<false, EPV>(a.partial + (2 * c + (whole_chunk ? 0 : 1)) * a.dim, col * EPV, sum);
+  const int64_t col = ((blockIdx.x - rel * col_blocks) * 64 + lane) * 4;
+  // pieces 0 (in chunk c) .. more; partial rows are padded past dim
+  const int64_t share = (more + kWaves) / kWaves;
+  const int64_t i0 = wave * share, i1 = i0 + share <= more ? i0 + share : more + 1;
+  f32x4 sum = f32x4(0.f);
+  if (col < a.dim) {
 #pragma unroll 8
-  for (int64_t i = 1; i <= more; ++i) {
-    float v[EPV];
-    load_vec<false, EPV>(a.partial + 2 * (c + i) * a.dim, col * EPV, v);
-#pragma unroll
-    for (int e = 0; e < EPV; ++e) sum[e] += v[e];
-  }
-  write_row<OUT16, EPV>(a, static_cast<int64_t>(token) * a.dim + col * EPV, sum);
-}
-
-template <bool IN16, bool OUT16, int EPV, int VPL>
-void launch_pieces(GradArgs a, int64_t n, hipStream_t st) {
-  const int64_t vr = a.dim / EPV;
-  const int64_t blocks = (vr + 64 * VPL - 1) / (64 * VPL);
-  a.col_blocks = static_cast<int>(blocks);
-  // positions and zero rows per launch: grids stay inside the 32-bit range
-  const int64_t pos_step = std::max<int64_t>(1, (int64_t(1) << 24) / blocks);
-  const int64_t zero_step = (int64_t(1) << 24) * kZeroRowsPerWave;
-  const int64_t zero_rows = a.accumulate ? 0 : a.rows;
-  for (int64_t p = 0, z = 0; p < n || z < zero_rows; p += pos_step, z += zero_step) {
-    const int64_t np = std::max<int64_t>(0, std::min(pos_step, n - p));
-    const int64_t nz = std::max<int64_t>(0, std::min(zero_step, zero_rows - z));
-    const int64_t pb = (np * blocks + kWaves - 1) / kWaves;
-    const int64_t zb = (nz + kZeroRowsPerWave * kWaves - 1) / (kZeroRowsPerWave * kWaves);
-    hipLaunchKernelGGL((grad_pieces<IN16, OUT16, EPV, VPL>), dim3(static_cast<unsigned>(pb + zb)),
-                       dim3(kBlock), 0, st, a, p, np, pb, z);
-  }
-}
-
-template <bool IN16, bool OUT16, int EPV>
-int launch_sums(const GradArgs &a, int64_t n, hipStream_t st) {
-  if (a.dim / EPV <= 64) launch_pieces<IN16, OUT16, EPV, 1>(a, n, st);
-  else launch_pieces<IN16, OUT16, EPV, 2>(a, n, st);
-  if (n > kPiece) {
-    const int64_t chunks = (n + kPiece - 1) / kPiece;
-    const int64_t blocks = (a.dim / EPV + 63) / 64;
-    const int64_t step = std::max<int64_t>(1, (int64_t(1) << 24) / blocks);
-    for (int64_t c = 0; c < chunks; c += step) {
-      const int64_t nc = std::min(step, chunks - c);
-      hipLaunchKernelGGL((grad_join<OUT16, EPV>),
-                         dim3(static_cast<unsigned>((nc * blocks + kWaves - 1) / kWaves)),
-                         dim3(kBlock), 0, st, a, c, nc);
+    for (int64_t i = i0; i < i1; ++i) {
+      const int64_t slot = i == 0 ? 2 * c + (whole_chunk ? 0 : 1) : 2 * (c + i);
+      sum += *reinterpret_cast<const f32x4 *>(a.partial + slot * a.partial_ld + col);
     }
+  }
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (wave != 0 || col >= a.dim) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) sum += part[w][lane];
+  const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+  write_row<OUT16, 4>(a, token, col, v);
+}
+
+// Workgroups of `threads` threads for `rows` rows of zeros: about 64 KB each.
+unsigned zero_blocks(int64_t rows, int64_t row_bytes) {
+  if (rows <= 0) return 0;
+  const double bytes = static_cast<double>(rows) * static_cast<double>(row_bytes);
+  return static_cast<unsigned>(std::max(1.0, std::min(bytes / 65536.0, 65536.0)));
+}
+
+template <bool IN16, bool OUT16>
+int launch_sums(GradArgs a, int64_t n, ZeroRows zero, hipStream_t st) {
+  // 16-byte vectors on the wider side
+  constexpr int kEpv = IN16 && OUT16 ? 8 : 4;
+  const int64_t chunks = (n + a.chunk - 1) / a.chunk;
+  const int64_t blocks = (a.dim + 64 * kEpv - 1) / (64 * kEpv);
+  a.col_blocks = static_cast<int>(blocks);
+  // chunks per launch: grids stay inside the 32-bit range
+  const int64_t step = std::max<int64_t>(1, (int64_t(1) << 24) / blocks);
+  for (int64_t c = 0; c < chunks || zero.blocks > 0; c += step) {
+    const int64_t nc = std::max<int64_t>(0, std::min(step, chunks - c));
+    const unsigned cb = static_cast<unsigned>((nc * blocks + kWaves - 1) / kWaves);
+    hipLaunchKernelGGL((grad_chunks<IN16, OUT16, kEpv>), dim3(cb + zero.blocks), dim3(kBlock), 0,
+                       st, a, c, nc, cb, zero);
+    zero.blocks = 0;
+  }
+  if (chunks > 1) {
+    const int64_t join_blocks = (a.dim + 255) / 256;
+    const int64_t join_step = std::max<int64_t>(1, (int64_t(1) << 22) / join_blocks);
+    for (int64_t c = 0; c < chunks - 1; c += join_step)
+      hipLaunchKernelGGL(
+          (grad_join<OUT16>),
+          dim3(static_cast<unsigned>(std::min(join_step, chunks - 1 - c) * join_blocks)),
+          dim3(kBlock), 0, st, a, c, static_cast<int>(join_blocks));
   }
   return static_cast<int>(hipGetLastError());
 }
 
-template <bool IN16, bool OUT16>
-int launch_sums_any(const GradArgs &a, int64_t n, hipStream_t st) {
-  // vectors of the same elements on both sides, at most 16 bytes of the input
-  const uint64_t dy = reinterpret_cast<uint64_t>(a.dy), dw = reinterpret_cast<uint64_t>(a.dw);
-  const int epv = std::min(pick_epv(IN16, a.dim, dy), OUT16 ? pick_epv(true, a.dim, dw)
-                                                      : a.dim % 8 == 0 && dw % 16 == 0
-                                                          ? 8
-                                                          : pick_epv(false, a.dim, dw));
-  if constexpr (IN16) {
-    if (epv == 8) return launch_sums<IN16, OUT16, 8>(a, n, st);
-  }
-  if (epv >= 4) return launch_sums<IN16, OUT16, 4>(a, n, st);
-  if (epv == 2) return launch_sums<IN16, OUT16, 2>(a, n, st);
-  return launch_sums<IN16, OUT16, 1>(a, n, st);
-}
-
 template <typename IdT>
-int grad_any(const IdT *ids, int64_t n, GradArgs a, int dtype, int gdtype, uint64_t start,
-             char *ws, hipStream_t st) {
-  const EmbedGradLayout l = embed_grad_layout(n, a.rows, a.dim);
+int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int gdtype,
+             uint64_t start, char *ws, hipStream_t st) {
+  const EmbedGradLayout l = embed_grad_layout(n, rows, a.dim);
   uint32_t *key[2] = {reinterpret_cast<uint32_t *>(ws + l.key[0]),
                       reinterpret_cast<uint32_t *>(ws + l.key[1])};
   uint32_t *pos[2] = {reinterpret_cast<uint32_t *>(ws + l.pos[0]),
                       reinterpret_cast<uint32_t *>(ws + l.pos[1])};
   uint32_t *count = reinterpret_cast<uint32_t *>(ws + l.count);
   uint32_t *hist = reinterpret_cast<uint32_t *>(ws + l.hist);
-  uint8_t *flags = a.accumulate ? nullptr : reinterpret_cast<uint8_t *>(ws + l.flags);
-  const uint64_t rows = static_cast<uint64_t>(a.rows);
-  const int key_bits = std::max(1, ceil_log2(a.rows));
+  const int key_bits = std::max(1, ceil_log2(rows));
   const int passes = (key_bits + 8) / 9;
   const int bits = (key_bits + passes - 1) / passes;
+  const uint64_t urows = static_cast<uint64_t>(rows);
+  const int64_t zero_to = a.accumulate ? 0 : rows;
+  ZeroRows zero{a.dw, a.dim * (gdtype == 1 ? 2 : 4), 0, 0, nullptr, 0};
   int last = 0;
   if (n <= kGradOneBlockIds) {
-    hipLaunchKernelGGL((sort_one_block<IdT>), dim3(1), dim3(kOneThreads), 0, st, ids,
-                       static_cast<int>(n), start, rows, bits, passes, key[0], pos[0], count,
-                       flags);
+    // few rows have an id: all are cleared while they are sorted, and those
+    // written again
+    zero.row1 = zero_to;
+    zero.blocks = zero_blocks(zero.row1, zero.row_bytes);
+    hipLaunchKernelGGL((sort_one_block<IdT>), dim3(1 + zero.blocks), dim3(kSortThreads), 0, st,
+                       ids, static_cast<int>(n), start, urows, bits, passes, key[0], pos[0], count,
+                       zero);
+    zero.blocks = 0;
   } else {
     // at least kSortTile items per workgroup, at most kSortMaxBlocks workgroups
     const int64_t unit = kSortTile * kSortMaxBlocks;
-    const int64_t tile = kSortTile * ((n + unit - 1) / unit);
-    const unsigned blocks = static_cast<unsigned>((n + tile - 1) / tile);
+    SortPass ps{n, kSortTile * ((n + unit - 1) / unit), 0, 0, bits};
+    ps.blocks = static_cast<unsigned>((n + ps.tile - 1) / ps.tile);
+    uint8_t *flags = a.accumulate ? nullptr : reinterpret_cast<uint8_t *>(ws + l.flags);
+    zero.flags = flags;
+    // the flags are complete after the first pass: each later launch of the
+    // sort clears an equal part of half the rows without an id
+    const int riders = 2 * passes - 2;
+    auto ride = [&]() {
+      zero.row0 = zero.row1;
+      zero.row1 = std::min(zero_to, zero.row0 + (zero_to / 2 + riders - 1) / riders);
+      zero.blocks = zero_blocks(zero.row1 - zero.row0, zero.row_bytes);
+    };
     for (int pass = 0; pass < passes; ++pass) {
       last = pass & 1;
-      const int shift = pass * bits;
+      ps.shift = pass * bits;
       if (pass == 0) {
-        SortItems<true, IdT> it{ids, nullptr, nullptr, start, rows};
-        hipLaunchKernelGGL((sort_counts<true, IdT>), dim3(blocks), dim3(kBlock), 0, st, it, n,
-                           count, tile, shift, bits, hist, flags);
-        hipLaunchKernelGGL((sort_scatter<true, IdT>), dim3(blocks), dim3(kBlock), 0, st, it, n,
-                           count, tile, shift, bits, hist, key[0], pos[0], flags);
+        SortItems<true, IdT> it{ids, nullptr, nullptr, start, urows};
+        hipLaunchKernelGGL((sort_counts<true, IdT>), dim3(ps.blocks), dim3(kSortThreads), 0, st,
+                           it, ps, count, hist, flags, zero);
+        hipLaunchKernelGGL((sort_scatter<true, IdT>), dim3(ps.blocks), dim3(kSortThreads), 0, st,
+                           it, ps, count, hist, key[0], pos[0], flags, zero);
       } else {
-        SortItems<false, IdT> it{nullptr, key[1 - last], pos[1 - last], start, rows};
-        hipLaunchKernelGGL((sort_counts<false, IdT>), dim3(blocks), dim3(kBlock), 0, st, it, n,
-                           count, tile, shift, bits, hist, flags);
-        hipLaunchKernelGGL((sort_scatter<false, IdT>), dim3(blocks), dim3(kBlock), 0, st, it, n,
-                           count, tile, shift, bits, hist, key[last], pos[last], flags);
+        SortItems<false, IdT> it{nullptr, key[1 - last], pos[1 - last], start, urows};
+        ride();
+        hipLaunchKernelGGL((sort_counts<false, IdT>), dim3(ps.blocks + zero.blocks),
+                           dim3(kSortThreads), 0, st, it, ps, count, hist, flags, zero);
+        ride();
+        hipLaunchKernelGGL((sort_scatter<false, IdT>), dim3(ps.blocks + zero.blocks),
+                           dim3(kSortThreads), 0, st, it, ps, count, hist, key[last], pos[last],
+                           flags, zero);
       }
     }
+    zero.row0 = zero.row1, zero.row1 = zero_to;
+    zero.blocks = zero_blocks(zero.row1 - zero.row0, zero.row_bytes);
   }
-  a.key = key[last], a.pos = pos[last], a.count = count, a.flags = flags;
+  a.key = key[last], a.pos = pos[last], a.count = count;
   a.partial = reinterpret_cast<float *>(ws + l.partial);
+  a.partial_ld = l.partial_ld;
+  a.chunk = static_cast<int>(l.chunk);
   if (dtype == 1)
-    return gdtype == 1 ? launch_sums_any<true, true>(a, n, st)
-                       : launch_sums_any<true, false>(a, n, st);
-  return gdtype == 1 ? launch_sums_any<false, true>(a, n, st)
-                     : launch_sums_any<false, false>(a, n, st);
+    return gdtype == 1 ? launch_sums<true, true>(a, n, zero, st)
+                       : launch_sums<true, false>(a, n, zero, st);
+  return gdtype == 1 ? launch_sums<false, true>(a, n, zero, st)
+                     : launch_sums<false, false>(a, n, zero, st);
 }
 
 }  // namespace
@@ -669,11 +701,12 @@ int launch_embed_scaled(const void *ids, int itype, int64_t n, const void *weigh
                         void *out, void *stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();  // clear a stale error so the status returned is this launch's
-  if (itype == 0)
-    return scaled_any(static_cast<const int32_t *>(ids), n, weight, dtype, shard_rows, dim,
-                      vocab_start, scale, out, st);
-  return scaled_any(static_cast<const int64_t *>(ids), n, weight, dtype, shard_rows, dim,
-                    vocab_start, scale, out, st);
+#define VPE_SCALED_ANY(BF16, IdT)                                                              \
+  scaled_any<BF16>(static_cast<const IdT *>(ids), n, weight, shard_rows, dim, vocab_start,     \
+                   scale, out, st)
+  if (itype == 0) return dtype == 1 ? VPE_SCALED_ANY(true, int32_t) : VPE_SCALED_ANY(false, int32_t);
+  return dtype == 1 ? VPE_SCALED_ANY(true, int64_t) : VPE_SCALED_ANY(false, int64_t);
+#undef VPE_SCALED_ANY
 }
 
 int launch_embed_grad(const void *ids, int itype, int64_t n, const void *grad_out, int dtype,
@@ -683,13 +716,15 @@ int launch_embed_grad(const void *ids, int itype, int64_t n, const void *grad_ou
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   GradArgs a{};
-  a.dy = grad_out, a.dim = dim, a.scale = scale, a.dw = grad_weight, a.accumulate = accumulate;
-  a.rows = shard_rows;
+  a.dy = static_cast<const char *>(grad_out), a.dim = dim, a.scale = scale;
+  a.dw = static_cast<char *>(grad_weight), a.accumulate = accumulate;
   char *ws = static_cast<char *>(workspace);
   const uint64_t start = static_cast<uint64_t>(vocab_start);
   if (itype == 0)
-    return grad_any(static_cast<const int32_t *>(ids), n, a, dtype, gdtype, start, ws, st);
-  return grad_any(static_cast<const int64_t *>(ids), n, a, dtype, gdtype, start, ws, st);
+    return grad_any(static_cast<const int32_t *>(ids), n, a, shard_rows, dtype, gdtype, start, ws,
+                    st);
+  return grad_any(static_cast<const int64_t *>(ids), n, a, shard_rows, dtype, gdtype, start, ws,
+                  st);
 }
 
 }  // namespace vpe

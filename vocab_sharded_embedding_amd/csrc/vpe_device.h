@@ -1,5 +1,5 @@
 // Device helpers shared by the training and beam-search kernels: fp32 and
-// bf16 elements in vectors of up to 16 bytes, widened to fp32 registers.
+// bf16 elements in vectors of 8 or 16 bytes, widened to fp32 registers.
 #ifndef VPE_DEVICE_H
 #define VPE_DEVICE_H
 
@@ -30,88 +30,97 @@ __device__ __forceinline__ uint16_t one_bf16(float a) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(a));
 }
 
+// EPV elements (2 or 4 bytes each) moved as one vector of 8 or 16 bytes.  Rows
+// may begin at any element, so the types only ask for the element's alignment
+// (global accesses of any width may: the hardware splits what crosses).
 template <int BYTES> struct Raw;
-template <> struct Raw<16> { typedef u32x4 type; };
-template <> struct Raw<8> { typedef u32x2 type; };
-template <> struct Raw<4> { typedef uint32_t type; };
-template <> struct Raw<2> { typedef uint16_t type; };
+template <> struct Raw<16> {
+  typedef u32x4 type;
+  typedef u32x4 __attribute__((aligned(2))) loose;
+};
+template <> struct Raw<8> {
+  typedef u32x2 type;
+  typedef u32x2 __attribute__((aligned(2))) loose;
+};
 
-// EPV elements (2 or 4 bytes each) moved as one vector.
 template <bool BF16, int EPV>
 struct Vec {
-  static constexpr int kBytes = EPV * (BF16 ? 2 : 4);
-  typedef typename Raw<kBytes>::type raw;
+  static constexpr int kSize = BF16 ? 2 : 4;
+  typedef typename Raw<EPV * kSize>::type raw;
+  typedef typename Raw<EPV * kSize>::loose loose;
 
   static __device__ __forceinline__ void widen(raw r, float (&v)[EPV]) {
     if constexpr (!BF16) {
-      if constexpr (EPV == 1) {
-        v[0] = __uint_as_float(r);
-      } else {
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) v[e] = __uint_as_float(r[e]);
-      }
-    } else if constexpr (EPV == 1) {
-      v[0] = __uint_as_float(static_cast<uint32_t>(r) << 16);
-    } else if constexpr (EPV == 2) {
-      v[0] = bf16_lo(r), v[1] = bf16_hi(r);
+      for (int e = 0; e < EPV; ++e) v[e] = __uint_as_float(r[e]);
     } else {
 #pragma unroll
       for (int e = 0; e < EPV / 2; ++e) v[2 * e] = bf16_lo(r[e]), v[2 * e + 1] = bf16_hi(r[e]);
     }
   }
-
   static __device__ __forceinline__ raw narrow(const float (&v)[EPV]) {
+    raw r;
     if constexpr (!BF16) {
-      if constexpr (EPV == 1) {
-        return __float_as_uint(v[0]);
-      } else {
-        raw r;
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) r[e] = __float_as_uint(v[e]);
-        return r;
-      }
-    } else if constexpr (EPV == 1) {
-      return one_bf16(v[0]);
-    } else if constexpr (EPV == 2) {
-      return pack_bf16(v[0], v[1]);
+      for (int e = 0; e < EPV; ++e) r[e] = __float_as_uint(v[e]);
     } else {
-      raw r;
 #pragma unroll
       for (int e = 0; e < EPV / 2; ++e) r[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-      return r;
     }
+    return r;
   }
 };
 
-// Vectors of EPV elements, EPV * element size possibly 32 bytes (fp32 beside
-// bf16 vectors of 8): loaded and stored in 16-byte halves.
+template <bool BF16>
+__device__ __forceinline__ float load_one(const void *base, int64_t i) {
+  if constexpr (BF16)
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(base)[i]) << 16);
+  return static_cast<const float *>(base)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ void store_one(void *base, int64_t i, float v) {
+  if constexpr (BF16) static_cast<uint16_t *>(base)[i] = one_bf16(v);
+  else static_cast<float *>(base)[i] = v;
+}
+
+// Elements [i, i + EPV) of a row of n, 0 past its end.
 template <bool BF16, int EPV>
-__device__ __forceinline__ void load_vec(const void *base, int64_t elem, float (&v)[EPV]) {
-  if constexpr (!BF16 && EPV == 8) {
-    float a[4], b[4];
-    load_vec<false, 4>(base, elem, a);
-    load_vec<false, 4>(base, elem + 4, b);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+__device__ __forceinline__ void load_vec(const void *row, int64_t i, int64_t n, float (&v)[EPV]) {
+  typedef Vec<BF16, EPV> V;
+  if (i + EPV <= n) {
+    const char *p = static_cast<const char *>(row) + i * V::kSize;
+    V::widen(*reinterpret_cast<const typename V::loose *>(p), v);
   } else {
-    typedef Vec<BF16, EPV> V;
-    const char *p = static_cast<const char *>(base) + elem * (BF16 ? 2 : 4);
-    V::widen(*reinterpret_cast<const typename V::raw *>(p), v);
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) v[e] = i + e < n ? load_one<BF16>(row, i + e) : 0.f;
+  }
+}
+template <bool BF16, int EPV>
+__device__ __forceinline__ void store_vec_nt(void *row, int64_t i, int64_t n,
+                                             const float (&v)[EPV]) {
+  typedef Vec<BF16, EPV> V;
+  if (i + EPV <= n) {
+    char *p = static_cast<char *>(row) + i * V::kSize;
+    __builtin_nontemporal_store(V::narrow(v), reinterpret_cast<typename V::loose *>(p));
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPV; ++e)
+      if (i + e < n) store_one<BF16>(row, i + e, v[e]);
   }
 }
 
-template <bool BF16, int EPV>
-__device__ __forceinline__ void store_vec_nt(void *base, int64_t elem, const float (&v)[EPV]) {
-  if constexpr (!BF16 && EPV == 8) {
-    float a[4], b[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = v[e], b[e] = v[4 + e];
-    store_vec_nt<false, 4>(base, elem, a);
-    store_vec_nt<false, 4>(base, elem + 4, b);
-  } else {
-    typedef Vec<BF16, EPV> V;
-    char *p = static_cast<char *>(base) + elem * (BF16 ? 2 : 4);
-    __builtin_nontemporal_store(V::narrow(v), reinterpret_cast<typename V::raw *>(p));
+// `bytes` (even) zero bytes at p (even), by `lanes` lanes: whole 16-byte words
+// where they are aligned.
+__device__ __forceinline__ void zero_bytes(char *p, int64_t bytes, int64_t lane, int64_t lanes) {
+  int64_t head = static_cast<int64_t>(-reinterpret_cast<uintptr_t>(p) & 15);
+  if (head > bytes) head = bytes;
+  const int64_t words = (bytes - head) / 16;
+  u32x4 *w = reinterpret_cast<u32x4 *>(p + head);
+  for (int64_t i = lane; i < words; i += lanes) __builtin_nontemporal_store(u32x4(0), w + i);
+  if (head != 0 || (bytes & 15) != 0) {
+    for (int64_t i = lane * 2; i < head; i += lanes * 2) *reinterpret_cast<uint16_t *>(p + i) = 0;
+    for (int64_t i = head + words * 16 + lane * 2; i < bytes; i += lanes * 2)
+      *reinterpret_cast<uint16_t *>(p + i) = 0;
   }
 }
 

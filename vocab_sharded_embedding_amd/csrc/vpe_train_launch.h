@@ -18,11 +18,15 @@ int launch_embed_scaled(const void *ids, int itype, int64_t n, const void *weigh
                         int64_t shard_rows, int64_t dim, int64_t vocab_start, float scale,
                         void *out, void *stream);
 
-// Sorted positions are summed in pieces that end at multiples of this.
-constexpr int64_t kGradPiece = 32;
+// Sorted positions are summed in chunks of a power of two up to this, each by
+// one wave per block of columns: fewer while there are few ids, so that the
+// waves fill the chip.
+constexpr int64_t kGradChunk = 32;
+constexpr int64_t kGradFillChunks = 2048;
 // Up to this many ids are sorted by one workgroup.
 constexpr int64_t kGradOneBlockIds = 8192;
-// Workgroups and digit values of one pass of the sort of more ids.
+// Workgroups, ids per workgroup (at least) and digit values of one pass of the
+// sort of more ids.
 constexpr int64_t kSortMaxBlocks = 128;
 constexpr int64_t kSortTile = 2048;
 constexpr int64_t kSortDigits = 512;
@@ -30,11 +34,13 @@ constexpr int64_t kSortDigits = 512;
 // Byte offsets of the gradient's workspace (all 16-byte aligned).
 struct EmbedGradLayout {
   int64_t count;    // uint32: owned ids
-  int64_t hist;     // uint32 [2][kSortMaxBlocks][kSortDigits]
+  int64_t hist;     // uint32 [kSortMaxBlocks][kSortDigits]
   int64_t flags;    // uint8 [shard_rows]: the row has an id
   int64_t key[2];   // uint32 [n]
   int64_t pos[2];   // uint32 [n]
-  int64_t partial;  // float [2 * pieces][dim]
+  int64_t partial;  // float [2 * chunks][partial_ld]
+  int64_t partial_ld;
+  int64_t chunk;    // sorted positions per chunk
   int64_t bytes;
 };
 
@@ -42,16 +48,24 @@ constexpr int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
 inline EmbedGradLayout embed_grad_layout(int64_t n, int64_t shard_rows, int64_t dim) {
   EmbedGradLayout l{};
+  const bool passes = n > kGradOneBlockIds;
   int64_t at = 0;
   l.count = at, at += 16;
-  l.hist = at, at += n > kGradOneBlockIds ? 2 * kSortMaxBlocks * kSortDigits * 4 : 0;
-  l.flags = at, at += round16(shard_rows);
+  l.hist = at, at += passes ? kSortMaxBlocks * kSortDigits * 4 : 0;
+  l.flags = at, at += passes ? round16(shard_rows) : 0;
   for (int b = 0; b < 2; ++b) {
-    l.key[b] = at, at += round16(n * 4);
-    l.pos[b] = at, at += round16(n * 4);
+    l.key[b] = at, at += b == 0 || passes ? round16(n * 4) : 0;
+    l.pos[b] = at, at += b == 0 || passes ? round16(n * 4) : 0;
   }
-  // at most one piece that starts and one that continues per piece boundary
-  l.partial = at, at += n > kGradPiece ? 2 * ((n + kGradPiece - 1) / kGradPiece) * dim * 4 : 0;
+  l.partial_ld = (dim + 7) / 8 * 8;
+  l.chunk = kGradChunk;
+  while (l.chunk > 4 && (n + l.chunk - 1) / l.chunk < kGradFillChunks) l.chunk /= 2;
+  // at most one run that enters a chunk and one that leaves it having begun in
+  // it; the most chunks of any number of ids up to n, so that a workspace for
+  // more ids serves fewer
+  const int64_t small = (n + 3) / 4, full = (n + kGradChunk - 1) / kGradChunk;
+  const int64_t most = full > 2 * kGradFillChunks ? full : 2 * kGradFillChunks;
+  l.partial = at, at += n > 1 ? 2 * (small < most ? small : most) * l.partial_ld * 4 : 0;
   l.bytes = round16(at);
   return l;
 }
