@@ -56,7 +56,7 @@ vpe_status vpe_beam_select_workspace(int64_t n_seqs, int32_t beams, int64_t shar
  * keys    device uint64 [n_seqs, picks], written.
  * workspace  device, at least vpe_beam_select_workspace(...) bytes, 8-byte
  *         aligned; needs no initialisation, not shared by calls that may run
- *         at the same time; may be NULL where that is 0.
+ *         at the same time.
  * n_seqs == 0 is a no-op.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (n_seqs <
  * 0, n_seqs * beams > 2^21, beams outside [1, VPE_MAX_BEAMS], picks outside

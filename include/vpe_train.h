@@ -123,8 +123,7 @@ vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes);
  * shard_dot    device float [m].
  * workspace    device, at least vpe_distill_workspace(m, shard_rows) bytes,
  *              8-byte aligned; needs no initialisation, not shared by calls
- *              that may run at the same time; may be NULL where that is 0 or
- *              shard_lse is NULL.
+ *              that may run at the same time; may be NULL where shard_lse is.
  * m == 0 is a no-op.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (m < 0 or
  * > VPE_MAX_DISTILL_ROWS, shard_rows < 1 or >= 2^31, k outside [1,

@@ -34,6 +34,7 @@ using namespace dev;
 constexpr int kBlock = 256;
 constexpr int kMaxPicks = 64;
 constexpr int kGroupsPerWave = 4;        // vectors in flight per lane
+constexpr int64_t kRowsPerGrid = 32768;
 constexpr int64_t kDirect = 16384;       // candidates a workgroup orders by itself
 constexpr int kThreads = 1024;           // of that workgroup
 constexpr int kDigitBits = 11;
@@ -52,20 +53,9 @@ __device__ __forceinline__ float score_of(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
 }
 
-template <bool BF16> struct Row;
-template <> struct Row<true> {
-  static constexpr int kEpv = 8;
-  typedef u32x4 __attribute__((aligned(2))) loose;
-  static __device__ __forceinline__ float one(const void *base, int64_t i) {
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(base)[i]) << 16);
-  }
-};
-template <> struct Row<false> {
-  static constexpr int kEpv = 4;
-  typedef u32x4 __attribute__((aligned(4))) loose;
-  static __device__ __forceinline__ float one(const void *base, int64_t i) {
-    return static_cast<const float *>(base)[i];
-  }
+template <bool BF16>
+struct Row : Vec<BF16, BF16 ? 8 : 4> {
+  static constexpr int kEpv = BF16 ? 8 : 4;
 };
 
 struct BeamArgs {
@@ -77,34 +67,18 @@ struct BeamArgs {
   int64_t groups;  // per row
 };
 
-// Maximum over the wave's lanes (NaN is passed over), in lane 63: DPP moves
-// within rows of 16 lanes, then from row to row.
-template <int CTRL>
-__device__ __forceinline__ float max_from(float v) {
-  const int i = __float_as_int(v);
-  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xf, 0xf, false)));
-}
-__device__ __forceinline__ float wave_max_last(float v) {
-  v = max_from<0x111>(v);  // row_shr:1
-  v = max_from<0x112>(v);  // row_shr:2
-  v = max_from<0x114>(v);  // row_shr:4
-  v = max_from<0x118>(v);  // row_shr:8
-  v = max_from<0x142>(v);  // row_bcast:15
-  return max_from<0x143>(v);  // row_bcast:31
-}
-
 // best[row * groups + g] = the largest logit of columns [g, g + 1) * 64 vectors
-// of the row, NaN if there is none.
+// of the row, NaN if there is none (grid: groups / 16, rows).
 template <bool BF16>
-__global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t units_per_row,
-                                                     int64_t units, float *__restrict__ best) {
+__global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t row0,
+                                                     float *__restrict__ best) {
   typedef Row<BF16> R;
   constexpr int kEpv = R::kEpv, kSize = BF16 ? 2 : 4;
   const int lane = threadIdx.x & 63;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kBlock / 64) + wave_in_block();
-  if (unit >= units) return;
-  const int64_t row = unit / units_per_row;
-  const int64_t g0 = (unit - row * units_per_row) * kGroupsPerWave;
+  const int64_t row = row0 + blockIdx.y;
+  const int64_t g0 =
+      (static_cast<int64_t>(blockIdx.x) * (kBlock / 64) + wave_in_block()) * kGroupsPerWave;
+  if (g0 >= a.groups) return;
   const char *p = a.base + row * a.ld_bytes;
   const uint32_t none = BF16 ? 0x7fc07fc0u : 0x7fc00000u;
   u32x4 raw[kGroupsPerWave];
@@ -136,7 +110,7 @@ __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t units_
     if (j < a.cols && j + kEpv > a.cols) {
 #pragma nounroll
       for (int64_t i = j; i < a.cols; ++i) {
-        const float x = R::one(p, i);
+        const float x = load_one<BF16>(p, i);
         if (!(no_inf && x == inf)) mx[u] = fmaxf(mx[u], x);
       }
     }
@@ -144,8 +118,7 @@ __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t units_
   float mine = 0.f;
 #pragma unroll
   for (int u = 0; u < kGroupsPerWave; ++u) {
-    const float m = __int_as_float(
-        __builtin_amdgcn_readlane(__float_as_int(wave_max_last(mx[u])), 63));
+    const float m = wave_max(mx[u]);
     if (lane == u) mine = m;
   }
   if (lane < kGroupsPerWave && g0 + lane < a.groups) best[row * a.groups + g0 + lane] = mine;
@@ -285,7 +258,7 @@ struct Candidates {
     return (static_cast<uint64_t>(order_of(c)) << 32) | (0xFFFFFFFFu - place);
   }
   __device__ __forceinline__ uint64_t at(int beam, uint32_t col) const {
-    return key(beam, col, Row<BF16>::one(base + beam * a.ld_bytes, col));
+    return key(beam, col, load_one<BF16>(base + beam * a.ld_bytes, col));
   }
 };
 // all of them, one by one
@@ -364,7 +337,7 @@ __global__ __launch_bounds__(kThreads) void beam_pick(BeamArgs a, const float *_
             *reinterpret_cast<const typename R::loose *>(p + j * (BF16 ? 2 : 4)), v);
       } else {
 #pragma unroll
-        for (int e = 0; e < kEpv; ++e) v[e] = j + e < a.cols ? R::one(p, j + e) : 0.f;
+        for (int e = 0; e < kEpv; ++e) v[e] = j + e < a.cols ? load_one<BF16>(p, j + e) : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < kEpv; ++e) {
@@ -429,34 +402,42 @@ __global__ __launch_bounds__(kThreads) void beam_merge_rows(PartKeys parts, int 
 // ---------------------------------------------------------------------------
 // reordering of states
 // ---------------------------------------------------------------------------
-// 2^log2g lanes serve a unit: `span` vectors (of V) of one destination row.
+// 2^log2g lanes serve a unit: `span` vectors (of V) of one destination row,
+// rows row0 .. row0 + n_rows - 1 in units_per_row units each.
 template <typename V>
 __global__ __launch_bounds__(kBlock) void reorder_rows(const V *__restrict__ src, int64_t row0,
-                                                      int64_t n_rows, int64_t rows_per_outer,
+                                                      uint32_t n_rows, int64_t rows_per_outer,
                                                       int beams_in, int beams_out, int64_t n_seqs,
-                                                      int64_t vr, int64_t units_per_row,
+                                                      int64_t vr, uint32_t units_per_row,
                                                       int64_t span, int log2g,
                                                       const int64_t *__restrict__ parent,
                                                       int64_t ld_parent, V *__restrict__ dst) {
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
-  const int64_t unit = t >> log2g;
-  const int64_t rel = unit / units_per_row;
+  const uint32_t t = blockIdx.x * kBlock + threadIdx.x;
+  const uint32_t unit = t >> log2g, rel = unit / units_per_row;
   if (rel >= n_rows) return;
   const int group = 1 << log2g;
-  const int64_t v0 = (unit - rel * units_per_row) * span + (t & (group - 1));
-  const int64_t v1 = (unit - rel * units_per_row + 1) * span < vr
-                         ? (unit - rel * units_per_row + 1) * span
-                         : vr;
+  const int64_t begin = (unit - rel * units_per_row) * span;
+  const int64_t v1 = begin + span < vr ? begin + span : vr;
   const int64_t row = row0 + rel;
-  const int64_t o = row / rows_per_outer;
-  const int64_t in = row - o * rows_per_outer;  // s * beams_out + b
-  const int64_t s = in / beams_out;
-  const int64_t from = parent[s * ld_parent + (in - s * beams_out)];
+  // 64-bit divisions cost more than the rest of a short row's work
+  int64_t o, s;
+  int b;
+  if (row < 0x7fffffff && rows_per_outer < 0x7fffffff) {
+    const uint32_t r = static_cast<uint32_t>(row), per = static_cast<uint32_t>(rows_per_outer);
+    const uint32_t q = r / per, in = r - q * per, sq = in / static_cast<uint32_t>(beams_out);
+    o = q, s = sq, b = static_cast<int>(in - sq * beams_out);
+  } else {
+    o = row / rows_per_outer;
+    const int64_t in = row - o * rows_per_outer;
+    s = in / beams_out;
+    b = static_cast<int>(in - s * beams_out);
+  }
+  const int64_t from = parent[s * ld_parent + b];
   const bool valid = static_cast<uint64_t>(from) < static_cast<uint64_t>(beams_in);
   const V *from_row = src + ((o * n_seqs + s) * beams_in + (valid ? from : 0)) * vr;
   V *to_row = dst + row * vr;
   constexpr int kDeep = 4;
-  for (int64_t v = v0; v < v1; v += kDeep * group) {
+  for (int64_t v = begin + (t & (group - 1)); v < v1; v += kDeep * group) {
     V r[kDeep];
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
@@ -484,9 +465,10 @@ int launch_reorder(const void *src, int64_t outer, int64_t n_seqs, int beams_in,
     const int64_t nr = std::min(step, rows - r);
     const int64_t threads = (nr * units) << log2g;
     hipLaunchKernelGGL((reorder_rows<V>), dim3(static_cast<unsigned>((threads + kBlock - 1) / kBlock)),
-                       dim3(kBlock), 0, st, static_cast<const V *>(src), r, nr,
-                       n_seqs * beams_out, beams_in, beams_out, n_seqs, vr, units, span, log2g,
-                       parent, ld_parent, static_cast<V *>(dst));
+                       dim3(kBlock), 0, st, static_cast<const V *>(src), r,
+                       static_cast<uint32_t>(nr), n_seqs * beams_out, beams_in, beams_out, n_seqs,
+                       vr, static_cast<uint32_t>(units), span, log2g, parent, ld_parent,
+                       static_cast<V *>(dst));
   }
   return static_cast<int>(hipGetLastError());
 }
@@ -509,15 +491,16 @@ int launch_beam_select(const void *base, int64_t ld, int dtype, int64_t n_seqs, 
                    vocab, lse, scores, beams, picks, groups};
   const bool direct = beams * cols <= kDirect;
   if (!direct) {
-    const int64_t per_row = (groups + kGroupsPerWave - 1) / kGroupsPerWave;
-    const int64_t units = n_seqs * beams * per_row;
-    const dim3 grid(static_cast<unsigned>((units + kBlock / 64 - 1) / (kBlock / 64)));
-    if (dtype == 1)
-      hipLaunchKernelGGL((beam_groups<true>), grid, dim3(kBlock), 0, st, a, per_row, units,
-                         group_best);
-    else
-      hipLaunchKernelGGL((beam_groups<false>), grid, dim3(kBlock), 0, st, a, per_row, units,
-                         group_best);
+    constexpr int64_t kPerBlock = kGroupsPerWave * (kBlock / 64);
+    const unsigned gx = static_cast<unsigned>((groups + kPerBlock - 1) / kPerBlock);
+    const int64_t rows = n_seqs * beams;
+    for (int64_t r = 0; r < rows; r += kRowsPerGrid) {
+      const dim3 grid(gx, static_cast<unsigned>(std::min(kRowsPerGrid, rows - r)));
+      if (dtype == 1)
+        hipLaunchKernelGGL((beam_groups<true>), grid, dim3(kBlock), 0, st, a, r, group_best);
+      else
+        hipLaunchKernelGGL((beam_groups<false>), grid, dim3(kBlock), 0, st, a, r, group_best);
+    }
   }
   const float *best = direct ? nullptr : group_best;
   const dim3 seqs(static_cast<unsigned>(n_seqs));

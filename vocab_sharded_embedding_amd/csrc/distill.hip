@@ -4,11 +4,10 @@
 // All of it is bound by HBM: the statistics read a rank's logits once, the
 // gradient reads them once and writes once; a row's teacher entries (at most
 // 1024) are small beside its columns.
-//  - Statistics: one pass with a running maximum and sum per thread, in base 2
-//    (x = z log2(e) / T, one fma and one v_exp_f32 per logit), joined over the
-//    block.  The maximum is moved once per batch of vectors, not per logit.
-//    Few rows are cut into column slices, one workgroup each, whose pairs a
-//    second kernel joins.
+//  - Statistics: one wave per 256 vectors of a row, in base 2 (x = z log2(e) /
+//    T): their maximum first, then one fma and one v_exp_f32 per logit, so no
+//    sum is ever rescaled; a second kernel joins a row's (maximum, sum) pairs
+//    and takes the products with the teacher's entries, one wave per row.
 //  - Gradient: P exp(z/T - lse) for every column, and for the entries' columns
 //    the entries' probabilities taken off.  Those columns are read before the
 //    dense pass (the gradient may overwrite the logits) and written again
@@ -36,18 +35,6 @@ constexpr double kLn2 = 0.6931471805599453;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_huge_valf(); }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
-  return v;
-}
 
 // Block-wide maximum and sum, the same in every thread.
 __device__ __forceinline__ float block_max(float v, float *lds) {
@@ -149,27 +136,9 @@ __device__ __forceinline__ float teacher_row(const TeacherArgs &t, int64_t row, 
 // ---------------------------------------------------------------------------
 // student rows
 // ---------------------------------------------------------------------------
-// Rows begin at any element, so vectors are only element-aligned.
-template <bool BF16> struct Row;
-template <> struct Row<true> {
-  static constexpr int kEpv = 8;
-  typedef u32x4 __attribute__((aligned(2))) loose;
-  static __device__ __forceinline__ float one(const void *base, int64_t i) {
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(base)[i]) << 16);
-  }
-  static __device__ __forceinline__ void put(void *base, int64_t i, float v) {
-    static_cast<uint16_t *>(base)[i] = one_bf16(v);
-  }
-};
-template <> struct Row<false> {
-  static constexpr int kEpv = 4;
-  typedef u32x4 __attribute__((aligned(4))) loose;
-  static __device__ __forceinline__ float one(const void *base, int64_t i) {
-    return static_cast<const float *>(base)[i];
-  }
-  static __device__ __forceinline__ void put(void *base, int64_t i, float v) {
-    static_cast<float *>(base)[i] = v;
-  }
+template <bool BF16>
+struct Row : Vec<BF16, BF16 ? 8 : 4> {
+  static constexpr int kEpv = BF16 ? 8 : 4;
 };
 
 // log2 of a sum of powers of two kept as (largest exponent, sum of
@@ -202,100 +171,115 @@ struct ShardArgs {
   const char *base;  // first column of row 0
   int64_t ld_bytes;
   int64_t cols, vocab_start;
-  int slices;        // workgroups per row that reduce it
+  int slices;        // pieces a row is cut into
   int64_t slice;     // columns of each, a multiple of the vector length
 };
 
-// blockIdx.x = row * per_row + s: slice s of the row, or (s == slices) its
-// dot product; with one slice, the workgroup does both.
+constexpr int kPairVecs = 4;  // vectors per lane and pair
+constexpr int64_t kRowsPerGrid = 32768;
+
+// One wave per pair of a row (grid: pairs / kWaves, rows): the maximum and the
+// sum of its columns.
 template <bool BF16>
-__global__ __launch_bounds__(kBlock) void distill_stats(ShardArgs z, TeacherArgs t, int per_row,
-                                                       float *__restrict__ shard_lse,
-                                                       float *__restrict__ shard_dot,
+__global__ __launch_bounds__(kBlock) void distill_pairs(ShardArgs z, float to_log2, int64_t row0,
                                                        Pair *__restrict__ pairs) {
   typedef Row<BF16> R;
-  constexpr int kEpv = R::kEpv, kUnroll = 4;
-  __shared__ float red[kWaves];
-  __shared__ double red_d[kWaves];
-  __shared__ Pair red2[kWaves];
-  const int64_t row = blockIdx.x / static_cast<unsigned>(per_row);
-  const int s = static_cast<int>(blockIdx.x - row * per_row);
-  const char *base = z.base + row * z.ld_bytes;
-  const int tid = threadIdx.x;
-
-  if (s < z.slices && shard_lse != nullptr) {
-    const int64_t c0 = s * z.slice;
-    const int64_t n = c0 + z.slice < z.cols ? z.slice : z.cols - c0;
-    const char *p = base + c0 * (BF16 ? 2 : 4);
-    const float c = t.to_log2;
-    const int64_t nv = n / kEpv;
-    Pair acc{neg_inf(), 0.f};
-    for (int64_t i = tid; i < nv; i += kBlock * kUnroll) {
-      float v[kUnroll][kEpv];
+  constexpr int kEpv = R::kEpv, kSize = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = row0 + blockIdx.y;
+  const int64_t s = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
+  if (s >= z.slices) return;
+  const char *p = z.base + row * z.ld_bytes;
+  const int64_t j0 = s * z.slice + lane * kEpv;
+  u32x4 raw[kPairVecs];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int64_t j = i + u * kBlock;
-        u32x4 r = BF16 ? u32x4(0xff80ff80u) : u32x4(0xff800000u);  // -inf: adds nothing
-        if (j < nv) r = reinterpret_cast<const typename R::loose *>(p)[j];
-        Vec<BF16, kEpv>::widen(r, v[u]);
-      }
-      float mx = neg_inf();
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int e = 0; e < kEpv; ++e) mx = fmaxf(mx, v[u][e]);
-      const float m2 = fmaxf(acc.mx, mx * c);
-      if (acc.mx != m2) acc = Pair{m2, acc.mx == neg_inf() ? acc.sum : acc.sum * exp2_fast(acc.mx - m2)};
-      const float off = m2 == neg_inf() ? 0.f : m2;
-      float sum = 0.f;
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int e = 0; e < kEpv; ++e) sum += exp2_fast(fmaf(v[u][e], c, -off));
-      acc.sum += sum;
-    }
-    for (int64_t i = nv * kEpv + tid; i < n; i += kBlock) {
-      const float x = R::one(p, i);
-      const float m2 = fmaxf(acc.mx, x * c);
-      if (acc.mx != m2) acc = Pair{m2, acc.mx == neg_inf() ? acc.sum : acc.sum * exp2_fast(acc.mx - m2)};
-      acc.sum += exp2_fast(fmaf(x, c, m2 == neg_inf() ? 0.f : -m2));
-    }
-    acc = wave_join(acc);
-    if ((tid & 63) == 0) red2[wave_in_block()] = acc;
-    __syncthreads();
-    if (tid == 0) {
-      Pair a = red2[0];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) a = join(a, red2[w]);
-      if (z.slices == 1) shard_lse[row] = natural_log(a, t.unit);
-      else pairs[row * z.slices + s] = a;
-    }
+  for (int u = 0; u < kPairVecs; ++u) {
+    const int64_t j = j0 + u * (64 * kEpv);
+    raw[u] = BF16 ? u32x4(0xff80ff80u) : u32x4(0xff800000u);  // -inf: adds nothing
+    if (j + kEpv <= z.cols) raw[u] = *reinterpret_cast<const typename R::loose *>(p + j * kSize);
   }
-  if (s == per_row - 1) {
-    float p[kEntriesPerThread];
-    int col[kEntriesPerThread];
-    teacher_row(t, row, z.vocab_start, z.cols, p, col, red);
-    // in 64 bits: the loss is a small difference of this and the log-sum-exp
-    double dot = 0.0;
+  // the row's last columns where they do not fill a vector: one lane's
+  const int64_t tail = z.cols - z.cols % kEpv;
+  const bool ragged = tail < z.cols && j0 <= tail && (tail - j0) % (64 * kEpv) == 0 &&
+                      tail - j0 < kPairVecs * 64 * kEpv;
+  float mx = neg_inf();
 #pragma unroll
-    for (int i = 0; i < kEntriesPerThread; ++i)
-      if (col[i] >= 0) dot += static_cast<double>(p[i]) * static_cast<double>(R::one(base, col[i]));
-    dot = block_sum(dot, red_d);
-    if (tid == 0) shard_dot[row] = static_cast<float>(dot / static_cast<double>(t.temperature));
+  for (int u = 0; u < kPairVecs; ++u) {
+    float v[kEpv];
+    Vec<BF16, kEpv>::widen(raw[u], v);
+#pragma unroll
+    for (int e = 0; e < kEpv; ++e) mx = fmaxf(mx, v[e]);
   }
+  if (ragged) {
+#pragma nounroll
+    for (int64_t i = tail; i < z.cols; ++i) mx = fmaxf(mx, load_one<BF16>(p, i));
+  }
+  mx = wave_max(mx) * to_log2;
+  const float off = mx == neg_inf() ? 0.f : mx;
+  float sum = 0.f;
+#pragma unroll
+  for (int u = 0; u < kPairVecs; ++u) {
+    float v[kEpv];
+    Vec<BF16, kEpv>::widen(raw[u], v);
+#pragma unroll
+    for (int e = 0; e < kEpv; ++e) sum += exp2_fast(fmaf(v[e], to_log2, -off));
+  }
+  if (ragged) {
+#pragma nounroll
+    for (int64_t i = tail; i < z.cols; ++i)
+      sum += exp2_fast(fmaf(load_one<BF16>(p, i), to_log2, -off));
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) pairs[row * z.slices + s] = Pair{mx, sum};
 }
 
-// One wave per row: the slices' pairs joined.
-__global__ __launch_bounds__(kBlock) void distill_join(const Pair *__restrict__ pairs, int64_t m,
-                                                      int slices, double unit,
-                                                      float *__restrict__ shard_lse) {
+// A row's entries by one wave: the largest t_e / T (or the given
+// log-sum-exp), that the powers are taken from.
+__device__ __forceinline__ float entries_shift(const TeacherArgs &t, int64_t row) {
+  if (t.lse != nullptr) return t.lse[row];
+  float mx = neg_inf();
+  int64_t id;
+  for (int e = threadIdx.x & 63; e < t.k; e += 64) mx = fmaxf(mx, entry(t, row, e, id));
+  mx = wave_max(mx);
+  return mx == neg_inf() ? 0.f : mx;  // no entry counts (NaN ones stay NaN)
+}
+
+// One wave per row: the pairs joined (shard_lse != nullptr), and the entries'
+// product with the shard's logits.
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void distill_rows(ShardArgs z, TeacherArgs t, int64_t m,
+                                                      const Pair *__restrict__ pairs,
+                                                      float *__restrict__ shard_lse,
+                                                      float *__restrict__ shard_dot) {
   const int lane = threadIdx.x & 63;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
   if (row >= m) return;
-  Pair a{neg_inf(), 0.f};
-  for (int s = lane; s < slices; s += 64) a = join(a, pairs[row * slices + s]);
-  a = wave_join(a);
-  if (lane == 0) shard_lse[row] = natural_log(a, unit);
+  const char *p = z.base + row * z.ld_bytes;
+  const float shift = entries_shift(t, row);
+  // in 64 bits: the loss is a small difference of this and the log-sum-exp
+  double dot = 0.0, total = 0.0;
+  for (int e = lane; e < t.k; e += 64) {
+    int64_t id;
+    const float v = entry(t, row, e, id);
+    const float w = v == neg_inf() ? 0.f : expf(v - shift);
+    total += static_cast<double>(w);
+    const uint64_t local = static_cast<uint64_t>(id) - static_cast<uint64_t>(z.vocab_start);
+    if (w != 0.f && local < static_cast<uint64_t>(z.cols))
+      dot += static_cast<double>(w) *
+             static_cast<double>(load_one<BF16>(p, static_cast<int64_t>(local)));
+  }
+  if (shard_lse != nullptr) {
+    Pair a{neg_inf(), 0.f};
+    for (int s = lane; s < z.slices; s += 64) a = join(a, pairs[row * z.slices + s]);
+    a = wave_join(a);
+    if (lane == 0) shard_lse[row] = natural_log(a, t.unit);
+  }
+  dot = wave_sum(dot);
+  total = t.lse != nullptr ? 1.0 : wave_sum(total);
+  if (lane == 0)
+    shard_dot[row] =
+        total == 0.0 ? 0.f
+                     : static_cast<float>(dot / total / static_cast<double>(t.temperature));
 }
 
 struct Parts {
@@ -324,14 +308,7 @@ __global__ __launch_bounds__(kBlock) void distill_loss_rows(Parts parts, int n_p
   const double l = static_cast<double>(shift) + log(total);
 
   int64_t id;
-  float mx = neg_inf();
-  if (t.lse != nullptr) {
-    mx = t.lse[row];
-  } else {
-    for (int e = lane; e < t.k; e += 64) mx = fmaxf(mx, entry(t, row, e, id));
-    mx = wave_max(mx);
-    if (mx == neg_inf()) mx = 0.f;
-  }
+  const float mx = entries_shift(t, row);
   // w = exp(x), x = t / T - mx: sums of w and of w x
   double w_sum = 0.0, wx_sum = 0.0;
   for (int e = lane; e < t.k; e += 64) {
@@ -357,8 +334,11 @@ __global__ __launch_bounds__(kBlock) void distill_loss_rows(Parts parts, int n_p
 // gradient
 // ---------------------------------------------------------------------------
 constexpr int kHashBits = 8192;
+constexpr int64_t kGradFill = 32768;
+constexpr int64_t kGradCols = 4096;
+constexpr int64_t kGradStream = int64_t(128) << 20;
 
-template <bool BF16>
+template <bool BF16, bool STREAM>
 __global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, TeacherArgs t,
                                                            const float *__restrict__ lse,
                                                            const float *__restrict__ grad_loss,
@@ -386,7 +366,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, Teacher
   if (grad_loss[row] == 0.f || mass == 0.f) {
     for (int64_t i = tid; i < nv; i += kBlock)
       reinterpret_cast<typename R::loose *>(dst)[i] = u32x4(0);
-    for (int64_t i = nv * kEpv + tid; i < n; i += kBlock) R::put(dst, i, 0.f);
+    for (int64_t i = nv * kEpv + tid; i < n; i += kBlock) store_one<BF16>(dst, i, 0.f);
     return;
   }
 
@@ -404,7 +384,7 @@ __global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, Teacher
   for (int i = 0; i < kEntriesPerThread; ++i) {
     zk[i] = 0.f;
     if (col[i] >= 0) {
-      zk[i] = R::one(src, col[i]);
+      zk[i] = load_one<BF16>(src, col[i]);
       const uint32_t h = static_cast<uint32_t>(col[i]) % kHashBits, bit = 1u << (h & 31);
       if (atomicOr(&seen[h / 32], bit) & bit) atomicOr(&twice[h / 32], bit);
     }
@@ -435,7 +415,8 @@ __global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, Teacher
     for (int u = 0; u < kUnroll; ++u) {
       const int64_t j = i + u * kBlock;
       r[u] = u32x4(0);
-      if (j < nv) r[u] = reinterpret_cast<const typename R::loose *>(src)[j];
+      const typename R::loose *from = reinterpret_cast<const typename R::loose *>(src) + j;
+      if (j < nv) r[u] = STREAM ? __builtin_nontemporal_load(from) : *from;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -444,16 +425,18 @@ __global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, Teacher
       Vec<BF16, kEpv>::widen(r[u], v);
 #pragma unroll
       for (int e = 0; e < kEpv; ++e) v[e] = a * exp2_fast(fmaf(v[e], c, off));
-      if (j < nv) reinterpret_cast<typename R::loose *>(dst)[j] = Vec<BF16, kEpv>::narrow(v);
+      if (j < nv)
+        __builtin_nontemporal_store(Vec<BF16, kEpv>::narrow(v),
+                                    reinterpret_cast<typename R::loose *>(dst) + j);
     }
   }
   for (int64_t i = nv * kEpv + tid; i < n; i += kBlock)
-    R::put(dst, i, a * exp2_fast(fmaf(R::one(src, i), c, off)));
+    store_one<BF16>(dst, i, a * exp2_fast(fmaf(load_one<BF16>(src, i), c, off)));
   __syncthreads();  // the dense pass's stores come before the entries'
 #pragma unroll
   for (int i = 0; i < kEntriesPerThread; ++i)
     if (col[i] >= 0)
-      R::put(dst, col[i], g * (mass * exp2_fast(fmaf(zk[i], c, off)) - p[i]));
+      store_one<BF16>(dst, col[i], g * (mass * exp2_fast(fmaf(zk[i], c, off)) - p[i]));
 }
 
 TeacherArgs args_of(const Teacher &t) {
@@ -463,39 +446,43 @@ TeacherArgs args_of(const Teacher &t) {
                      1.f / t.temperature, to_log2, kLn2 * (c / static_cast<double>(to_log2))};
 }
 
-ShardArgs args_of(const LogitsShard &z, int64_t slices) {
-  const int epv = z.dtype == 1 ? 8 : 4;
-  const int64_t slice = ((z.cols + slices - 1) / slices + epv - 1) / epv * epv;
+ShardArgs args_of(const LogitsShard &z, int64_t slice) {
   return ShardArgs{static_cast<const char *>(z.base), z.ld * (z.dtype == 1 ? 2 : 4), z.cols,
                    z.vocab_start, static_cast<int>((z.cols + slice - 1) / slice), slice};
 }
 
+int64_t pair_cols(int dtype) { return kPairVecs * 64 * (dtype == 1 ? 8 : 4); }
+
 }  // namespace
 
-// Enough workgroups to fill the chip when there are few rows, slices of at
-// least 8192 columns.
-int64_t distill_slices(int64_t m, int64_t cols) {
-  const int64_t want = (2048 + m - 1) / m;
-  return std::max<int64_t>(1, std::min(want, cols / 8192));
+int64_t distill_pairs_per_row(int64_t cols, int dtype) {
+  return (cols + pair_cols(dtype) - 1) / pair_cols(dtype);
 }
 
 int launch_distill_shard(const LogitsShard &z, const Teacher &t, float *shard_lse,
                          float *shard_dot, float *pairs, void *stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();  // clear a stale error so the status returned is this launch's
-  const ShardArgs a = args_of(z, shard_lse ? distill_slices(z.m, z.cols) : 1);
-  const int per_row = a.slices > 1 ? a.slices + 1 : 1;
-  const dim3 grid(static_cast<unsigned>(z.m * per_row));
+  const ShardArgs a = args_of(z, pair_cols(z.dtype));
+  const TeacherArgs ta = args_of(t);
   Pair *pr = reinterpret_cast<Pair *>(pairs);
+  if (shard_lse) {
+    const unsigned gx = static_cast<unsigned>((a.slices + kWaves - 1) / kWaves);
+    for (int64_t r = 0; r < z.m; r += kRowsPerGrid) {
+      const dim3 grid(gx, static_cast<unsigned>(std::min(kRowsPerGrid, z.m - r)));
+      if (z.dtype == 1)
+        hipLaunchKernelGGL((distill_pairs<true>), grid, dim3(kBlock), 0, st, a, ta.to_log2, r, pr);
+      else
+        hipLaunchKernelGGL((distill_pairs<false>), grid, dim3(kBlock), 0, st, a, ta.to_log2, r, pr);
+    }
+  }
+  const dim3 rows(static_cast<unsigned>((z.m + kWaves - 1) / kWaves));
   if (z.dtype == 1)
-    hipLaunchKernelGGL((distill_stats<true>), grid, dim3(kBlock), 0, st, a, args_of(t), per_row,
-                       shard_lse, shard_dot, pr);
+    hipLaunchKernelGGL((distill_rows<true>), rows, dim3(kBlock), 0, st, a, ta, z.m, pr, shard_lse,
+                       shard_dot);
   else
-    hipLaunchKernelGGL((distill_stats<false>), grid, dim3(kBlock), 0, st, a, args_of(t), per_row,
-                       shard_lse, shard_dot, pr);
-  if (shard_lse && a.slices > 1)
-    hipLaunchKernelGGL(distill_join, dim3(static_cast<unsigned>((z.m + kWaves - 1) / kWaves)),
-                       dim3(kBlock), 0, st, pr, z.m, a.slices, args_of(t).unit, shard_lse);
+    hipLaunchKernelGGL((distill_rows<false>), rows, dim3(kBlock), 0, st, a, ta, z.m, pr, shard_lse,
+                       shard_dot);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -514,16 +501,26 @@ int launch_distill_grad(const LogitsShard &z, const Teacher &t, const float *lse
                         const float *grad_loss, void *grad_base, int64_t ld_grad, void *stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  const ShardArgs a = args_of(z, distill_slices(z.m, z.cols));
+  // one workgroup per row, or more where there are few rows, for at least
+  // kGradCols columns each
+  const int64_t want = std::max<int64_t>(1, std::min((kGradFill + z.m - 1) / z.m, z.cols / kGradCols));
+  const ShardArgs a = args_of(z, ((z.cols + want - 1) / want + 7) / 8 * 8);
   const dim3 grid(static_cast<unsigned>(z.m * a.slices));
   const int64_t ld_bytes = ld_grad * (z.dtype == 1 ? 2 : 4);
   char *out = static_cast<char *>(grad_base);
-  if (z.dtype == 1)
-    hipLaunchKernelGGL((distill_grad_rows<true>), grid, dim3(kBlock), 0, st, a, args_of(t), lse,
-                       grad_loss, out, ld_bytes);
-  else
-    hipLaunchKernelGGL((distill_grad_rows<false>), grid, dim3(kBlock), 0, st, a, args_of(t), lse,
-                       grad_loss, out, ld_bytes);
+  // logits that the last-level cache cannot hold are read past it, which leaves
+  // room for what is still to be written: [1024, 151936] in two shards 202 ->
+  // 195 us a step, [4096, 37984] 126 -> 122 us; 38 MB ([251, 75968]) are still
+  // there from their producer, and read past it 17.2 instead of 15.7 us
+  const bool streamed = z.m * z.cols * (z.dtype == 1 ? 2 : 4) > kGradStream;
+#define VPE_GRAD(BF16, STREAM)                                                               \
+  hipLaunchKernelGGL((distill_grad_rows<BF16, STREAM>), grid, dim3(kBlock), 0, st, a,         \
+                     args_of(t), lse, grad_loss, out, ld_bytes)
+  if (z.dtype == 1 && streamed) VPE_GRAD(true, true);
+  else if (z.dtype == 1) VPE_GRAD(true, false);
+  else if (streamed) VPE_GRAD(false, true);
+  else VPE_GRAD(false, false);
+#undef VPE_GRAD
   return static_cast<int>(hipGetLastError());
 }
 

@@ -464,8 +464,8 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
   typedef Vec<IN16, EPV> V;
   constexpr int kDeep = 8;
   const int lane = threadIdx.x & 63;
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
-  const int64_t rel = wave / a.col_blocks;
+  const uint32_t wave = blockIdx.x * kWaves + wave_in_block();
+  const uint32_t rel = wave / static_cast<uint32_t>(a.col_blocks);
   if (rel >= n_chunks) return;
   const int64_t c = chunk0 + rel;
   const int64_t n = *a.count, p0 = c * a.chunk;
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
   const bool begun = p0 > 0 && before == static_cast<uint32_t>(
                                              __builtin_amdgcn_readfirstlane(static_cast<int>(key)));
 
-  const int64_t col = ((wave - rel * a.col_blocks) * 64 + lane) * EPV;
+  const int64_t col = (static_cast<int64_t>(wave - rel * a.col_blocks) * 64 + lane) * EPV;
   const bool whole = col + EPV <= a.dim;
   const bool ragged = __ballot(!whole && col < a.dim) != 0;  // a row's end inside a vector
   const int64_t in_bytes = a.dim * V::kSize;
@@ -543,7 +543,7 @@ template <bool OUT16>
 __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int col_blocks) {
   __shared__ f32x4 part[kWaves][64];
   const int lane = threadIdx.x & 63, wave = wave_in_block();
-  const int64_t rel = blockIdx.x / static_cast<unsigned>(col_blocks);
+  const unsigned rel = blockIdx.x / static_cast<unsigned>(col_blocks);
   const int64_t c = chunk0 + rel;
   const int64_t n = *a.count;
   const int64_t next = (c + 1) * a.chunk;
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
     }
     more += 64;
   }
-  const int64_t col = ((blockIdx.x - rel * col_blocks) * 64 + lane) * 4;
+  const int64_t col = (static_cast<int64_t>(blockIdx.x - rel * col_blocks) * 64 + lane) * 4;
   // pieces 0 (in chunk c) .. more; partial rows are padded past dim
   const int64_t share = (more + kWaves) / kWaves;
   const int64_t i0 = wave * share, i1 = i0 + share <= more ? i0 + share : more + 1;

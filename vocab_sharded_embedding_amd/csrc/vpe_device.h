@@ -124,6 +124,39 @@ __device__ __forceinline__ void zero_bytes(char *p, int64_t bytes, int64_t lane,
   }
 }
 
+// Reductions over the wave's 64 lanes by DPP moves, within rows of 16 lanes
+// (row_shr 1, 2, 4, 8) and from row to row (row_bcast 15 and 31): lane 63 ends
+// with the whole, and all lanes read it there.  The order is fixed.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL,
+                                                    ROWS, 0xf, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float wave_max(float v) {  // NaN is passed over
+  v = fmaxf(v, dpp<0x111, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x112, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x114, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x118, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x142, 0xf>(v, v));
+  return last_lane(fmaxf(v, dpp<0x143, 0xf>(v, v)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x111, 0xf>(0.f, v);
+  v += dpp<0x112, 0xf>(0.f, v);
+  v += dpp<0x114, 0xf>(0.f, v);
+  v += dpp<0x118, 0xf>(0.f, v);
+  v += dpp<0x142, 0xa>(0.f, v);
+  return last_lane(v + dpp<0x143, 0xc>(0.f, v));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
 __device__ __forceinline__ int wave_in_block() {
   return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
 }

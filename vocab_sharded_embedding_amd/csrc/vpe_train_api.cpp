@@ -130,8 +130,7 @@ vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes) 
   if (!bytes) return VPE_ERR_NULL;
   if (m < 0 || m > VPE_MAX_DISTILL_ROWS || shard_rows < 1 || shard_rows > kMax31)
     return VPE_ERR_SHAPE;
-  const int64_t slices = m == 0 ? 1 : vpe::distill_slices(m, shard_rows);
-  *bytes = slices > 1 ? m * slices * 8 : 0;
+  *bytes = m * vpe::distill_pairs_per_row(shard_rows, 0) * 8;
   return VPE_OK;
 }
 
@@ -157,7 +156,7 @@ vpe_status vpe_distill_shard(const void *logits, int64_t ld, int64_t col_offset,
     int64_t need = 0;
     rs = vpe_distill_workspace(m, shard_rows, &need);
     if (rs != VPE_OK) return rs;
-    if (need > 0 && !workspace) return VPE_ERR_NULL;
+    if (!workspace) return VPE_ERR_NULL;
     if (workspace_bytes < need) return VPE_ERR_WORKSPACE;
   }
   return launched(vpe::launch_distill_shard(

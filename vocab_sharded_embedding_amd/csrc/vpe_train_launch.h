@@ -101,9 +101,9 @@ struct LogitsShard {
   int dtype;
 };
 
-// Column slices a row is cut into when there are few rows, for the pass that
-// reduces it: (maximum, sum) pairs [m][slices] in the workspace.
-int64_t distill_slices(int64_t m, int64_t cols);
+// (maximum, sum) pairs of 8 bytes per row that the workspace holds; the most
+// for f32.
+int64_t distill_pairs_per_row(int64_t cols, int dtype);
 
 int launch_distill_shard(const LogitsShard &z, const Teacher &t, float *shard_lse,
                          float *shard_dot, float *pairs, void *stream);

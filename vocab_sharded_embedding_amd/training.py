@@ -16,6 +16,9 @@ import torch
 
 from . import _check, _dtype_code, _itype_code, _need_device, _same_device, load_library
 
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+_ITYPES = {torch.int32: 0, torch.int64: 1}
+
 # The current stream's handle by device index, without a Stream object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 if _raw_stream is None:  # pragma: no cover
@@ -23,53 +26,71 @@ if _raw_stream is None:  # pragma: no cover
         return torch.cuda.current_stream(index).cuda_stream
 
 
-def enqueue(name: str, device, *args) -> None:
-    """Call `name` of the library with `args` and the device's current stream, the
-    device being the current one meanwhile (kernels are enqueued there)."""
+def enqueue(name: str, index: int, *args) -> None:
+    """Call `name` of the library with `args` and device `index`'s current stream,
+    that device being the current one meanwhile (kernels are enqueued there)."""
     fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(device.index))
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(device.index))
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
     if status:
         _check(name, status)
 
 
-def workspace_for(need: int, workspace, device):
-    """The caller's workspace (its size is checked by the library), or a new one."""
-    if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    _need_device("workspace", workspace)
-    return workspace
+def placed(names: str, *tensors) -> int:
+    """The index of the one HIP device all `tensors` (contiguous) are on; `names`
+    are theirs, for the error."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if index < 0 or t.get_device() != index or not t.is_contiguous():
+            for name, each in zip(names.split(), tensors):
+                _need_device(name, each)
+            _same_device(*tensors)
+    return index
 
 
-def _nbytes(t) -> int:
+def dtype_code(t) -> int:
+    code = _DTYPES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
+def itype_code(t) -> int:
+    code = _ITYPES.get(t.dtype)
+    return _itype_code(t) if code is None else code
+
+
+def float_rows(name: str, t, m: int) -> None:
+    if t.dtype != torch.float32 or t.numel() != m:
+        raise ValueError(f"{name} must be a float32 tensor with one value per row")
+
+
+def new_workspace(need: int, device):
+    return torch.empty(need if need > 16 else 16, dtype=torch.uint8, device=device)
+
+
+def nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
 def vpe_embed_scaled(ids, weight, vocab_start: int, scale: float, out=None):
     """vpe_embed with every owned row times `scale` (fp32 product, one rounding)."""
-    _need_device("ids", ids)
-    _need_device("weight", weight)
     if weight.dim() != 2:
         raise ValueError("weight must be [shard_rows, dim]")
     rows, dim = weight.shape
     if out is None:
         out = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=weight.device)
-    else:
-        _need_device("out", out)
-    if out.dtype != weight.dtype or out.numel() != ids.numel() * dim:
+    elif out.dtype != weight.dtype or out.numel() != ids.numel() * dim:
         raise ValueError("out must have the weight's dtype and ids.numel() * dim elements")
-    _same_device(ids, weight, out)
-    enqueue("vpe_embed_scaled", weight.device, ids.data_ptr(), _itype_code(ids), ids.numel(),
-            weight.data_ptr(), _dtype_code(weight), rows, dim, int(vocab_start), float(scale),
-            out.data_ptr())
+    index = placed("ids weight out", ids, weight, out)
+    enqueue("vpe_embed_scaled", index, ids.data_ptr(), itype_code(ids), ids.numel(),
+            weight.data_ptr(), dtype_code(weight), rows, dim, vocab_start, scale, out.data_ptr())
     return out
 
 
 def vpe_embed_grad_workspace(n: int, shard_rows: int, dim: int) -> int:
-    """Bytes of workspace vpe_embed_grad needs for n ids."""
+    """Bytes of workspace vpe_embed_grad needs for n ids; as much serves fewer."""
     b = ctypes.c_int64()
     _check("vpe_embed_grad_workspace", load_library().vpe_embed_grad_workspace(
         n, shard_rows, dim, ctypes.byref(b)))
@@ -85,9 +106,7 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
     or to a new tensor of `dtype` (grad_out's when None).  Rows of positions
     whose id lies outside the shard add nothing.
     """
-    _need_device("ids", ids)
-    _need_device("grad_out", grad_out)
-    if grad_out.dim() < 1 or tuple(grad_out.shape[:-1]) != tuple(ids.shape):
+    if grad_out.dim() < 1 or grad_out.shape[:-1] != ids.shape:
         raise ValueError("grad_out must be [*ids.shape, dim]")
     dim, n = grad_out.shape[-1], ids.numel()
     if grad_weight is None:
@@ -96,57 +115,49 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
         grad_weight = torch.empty((shard_rows, dim), dtype=dtype or grad_out.dtype,
                                   device=grad_out.device)
     else:
-        _need_device("grad_weight", grad_weight)
         if dtype is not None and dtype != grad_weight.dtype:
             raise ValueError("dtype differs from grad_weight's")
-        if tuple(grad_weight.shape) != (shard_rows, dim):
+        if grad_weight.shape != (shard_rows, dim):
             raise ValueError("grad_weight must be [shard_rows, dim]")
-    itype, dt, gdt = _itype_code(ids), _dtype_code(grad_out), _dtype_code(grad_weight)
-    need = vpe_embed_grad_workspace(n, shard_rows, dim)
-    workspace = workspace_for(need, workspace, grad_out.device)
-    _same_device(ids, grad_out, grad_weight, workspace)
-    enqueue("vpe_embed_grad", grad_out.device, ids.data_ptr(), itype, n, grad_out.data_ptr(), dt,
-            dim, int(vocab_start), shard_rows, float(scale), grad_weight.data_ptr(), gdt,
-            int(accumulate), workspace.data_ptr(), _nbytes(workspace))
+    if workspace is None:
+        workspace = new_workspace(vpe_embed_grad_workspace(n, shard_rows, dim), grad_out.device)
+    index = placed("ids grad_out grad_weight workspace", ids, grad_out, grad_weight, workspace)
+    enqueue("vpe_embed_grad", index, ids.data_ptr(), itype_code(ids), n, grad_out.data_ptr(),
+            dtype_code(grad_out), dim, vocab_start, shard_rows, scale, grad_weight.data_ptr(),
+            dtype_code(grad_weight), bool(accumulate), workspace.data_ptr(), nbytes(workspace))
     return grad_weight
 
 
 # ---------------------------------------------------------------------------
 # distillation
 # ---------------------------------------------------------------------------
-def _float_rows(name: str, t, m: int):
-    _need_device(name, t)
-    if t.dtype != torch.float32 or t.numel() != m:
-        raise ValueError(f"{name} must be a float32 tensor with one value per row")
-    return t
-
-
 def _teacher(teacher_ids, teacher, teacher_lse, m: Optional[int]):
-    """Checked (rows, k, itype, dtype) of a batch of teacher entries."""
-    _need_device("teacher_ids", teacher_ids)
-    _need_device("teacher", teacher)
+    """Checked (ids, itype, teacher, dtype, k, teacher_lse) arguments, and the rows."""
     if teacher_ids.dim() != 2 or teacher_ids.shape != teacher.shape:
         raise ValueError("teacher_ids and teacher must both be [m, k]")
-    if m is not None and teacher_ids.shape[0] != m:
+    rows, k = teacher_ids.shape
+    if m is not None and rows != m:
         raise ValueError("the teacher's entries must have one row per row of logits")
+    lse = None
     if teacher_lse is not None:
-        _float_rows("teacher_lse", teacher_lse, teacher_ids.shape[0])
-        _same_device(teacher_ids, teacher_lse)
-    _same_device(teacher_ids, teacher)
-    return (*teacher_ids.shape, _itype_code(teacher_ids), _dtype_code(teacher))
+        float_rows("teacher_lse", teacher_lse, rows)
+        placed("teacher_ids teacher_lse", teacher_ids, teacher_lse)
+        lse = teacher_lse.data_ptr()
+    return (teacher_ids.data_ptr(), itype_code(teacher_ids), teacher.data_ptr(),
+            dtype_code(teacher), k, lse), rows
 
 
 def logits_shard(name: str, logits, shard_rows: Optional[int], col_offset: int):
-    """(rows, columns of the shard) of a [m, ld] buffer; all columns from
+    """(rows, ld, columns of the shard) of a [m, ld] buffer; all columns from
     col_offset on when shard_rows is None."""
-    _need_device(name, logits)
     if logits.dim() != 2:
         raise ValueError(f"{name} must be [m, ld]")
-    return logits.shape[0], logits.shape[1] - col_offset if shard_rows is None else shard_rows
+    m, ld = logits.shape
+    return m, ld, ld - col_offset if shard_rows is None else shard_rows
 
 
 def vpe_distill_workspace(m: int, shard_rows: int) -> int:
-    """Bytes of workspace vpe_distill_shard needs (may be 0)."""
+    """Bytes of workspace vpe_distill_shard needs (unless with_lse is False)."""
     b = ctypes.c_int64()
     _check("vpe_distill_workspace", load_library().vpe_distill_workspace(
         m, shard_rows, ctypes.byref(b)))
@@ -166,54 +177,53 @@ def vpe_distill_shard(logits, teacher_ids, teacher, vocab_start: int, vocab: int
     logits are read and shard_lse is None (temperature 1 after
     vpe_lmhead_logsumexp, which gives the same shard_lse).
     """
-    m, rows = logits_shard("logits", logits, shard_rows, col_offset)
-    _, k, itype, tdt = _teacher(teacher_ids, teacher, teacher_lse, m)
-    dt = _dtype_code(logits)
+    m, ld, rows = logits_shard("logits", logits, shard_rows, col_offset)
+    entries, _ = _teacher(teacher_ids, teacher, teacher_lse, m)
     if shard_dot is None:
         shard_dot = torch.empty(m, dtype=torch.float32, device=logits.device)
-    _float_rows("shard_dot", shard_dot, m)
+    else:
+        float_rows("shard_dot", shard_dot, m)
     if with_lse:
         if shard_lse is None:
-            shard_lse = torch.empty(m, dtype=torch.float32, device=logits.device)
-        _float_rows("shard_lse", shard_lse, m)
-        need = vpe_distill_workspace(m, rows)
-        if workspace is not None or need > 0:
-            workspace = workspace_for(need, workspace, logits.device)
+            shard_lse = torch.empty_like(shard_dot)
+        else:
+            float_rows("shard_lse", shard_lse, m)
+        if workspace is None:
+            workspace = new_workspace(vpe_distill_workspace(m, rows), logits.device)
+        index = placed("logits teacher_ids teacher shard_dot shard_lse workspace", logits,
+                       teacher_ids, teacher, shard_dot, shard_lse, workspace)
+        tail = (shard_lse.data_ptr(), shard_dot.data_ptr(), workspace.data_ptr(),
+                nbytes(workspace))
     elif shard_lse is not None:
         raise ValueError("shard_lse given with with_lse=False")
-    _same_device(*(t for t in (logits, teacher, shard_dot, shard_lse, workspace) if t is not None))
-    enqueue("vpe_distill_shard", logits.device, logits.data_ptr(), logits.shape[1], int(col_offset),
-            m, rows, dt, int(vocab_start), int(vocab), float(temperature), teacher_ids.data_ptr(),
-            itype, teacher.data_ptr(), tdt, k, None if teacher_lse is None else
-            teacher_lse.data_ptr(), None if shard_lse is None else shard_lse.data_ptr(),
-            shard_dot.data_ptr(), None if workspace is None else workspace.data_ptr(), 0 if
-            workspace is None else _nbytes(workspace))
+    else:
+        index = placed("logits teacher_ids teacher shard_dot", logits, teacher_ids, teacher,
+                       shard_dot)
+        tail = (None, shard_dot.data_ptr(), None, 0)
+    enqueue("vpe_distill_shard", index, logits.data_ptr(), ld, col_offset, m, rows,
+            dtype_code(logits), vocab_start, vocab, temperature, *entries, *tail)
     return shard_lse, shard_dot
 
 
 def vpe_distill_loss(shard_lse: Sequence, shard_dot: Sequence, teacher_ids, teacher, vocab: int,
                      temperature: float = 1.0, teacher_lse=None, loss=None, lse=None):
     """(loss, lse) per row, float32 [m], from the shards' parts in shard order."""
-    lses, dots = list(shard_lse), list(shard_dot)
-    if not lses or len(lses) != len(dots):
+    n = len(shard_lse)
+    if n == 0 or n != len(shard_dot):
         raise ValueError("need one shard_lse and one shard_dot per shard")
-    m, k, itype, tdt = _teacher(teacher_ids, teacher, teacher_lse, None)
-    for i, (a, b) in enumerate(zip(lses, dots)):
-        _float_rows(f"shard_lse[{i}]", a, m)
-        _float_rows(f"shard_dot[{i}]", b, m)
+    entries, m = _teacher(teacher_ids, teacher, teacher_lse, None)
     if loss is None:
         loss = torch.empty(m, dtype=torch.float32, device=teacher.device)
     if lse is None:
         lse = torch.empty(m, dtype=torch.float32, device=teacher.device)
-    _float_rows("loss", loss, m)
-    _float_rows("lse", lse, m)
-    _same_device(teacher, loss, lse, *lses, *dots)
-    n = len(lses)
-    lp = (ctypes.c_void_p * n)(*[t.data_ptr() for t in lses])
-    dp = (ctypes.c_void_p * n)(*[t.data_ptr() for t in dots])
-    enqueue("vpe_distill_loss", teacher.device, lp, dp, n, m, int(vocab), float(temperature),
-            teacher_ids.data_ptr(), itype, teacher.data_ptr(), tdt, k, None if teacher_lse is None
-            else teacher_lse.data_ptr(), loss.data_ptr(), lse.data_ptr())
+    for t in (*shard_lse, *shard_dot, loss, lse):
+        float_rows("shard_lse, shard_dot, loss and lse each", t, m)
+    index = placed("teacher_ids teacher loss lse" + " shard_lse" * n + " shard_dot" * n,
+                   teacher_ids, teacher, loss, lse, *shard_lse, *shard_dot)
+    array = ctypes.c_void_p * n
+    enqueue("vpe_distill_loss", index, array(*[t.data_ptr() for t in shard_lse]),
+            array(*[t.data_ptr() for t in shard_dot]), n, m, vocab, temperature, *entries,
+            loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
 
@@ -228,26 +238,23 @@ def vpe_distill_grad(logits, lse, grad_loss, teacher_ids, teacher, vocab_start: 
     None) of grad_logits [m, ld], which may be the logits themselves, or to a
     new [m, shard_rows] tensor.
     """
-    m, rows = logits_shard("logits", logits, shard_rows, col_offset)
-    _, k, itype, tdt = _teacher(teacher_ids, teacher, teacher_lse, m)
-    dt = _dtype_code(logits)
-    _float_rows("lse", lse, m)
-    _float_rows("grad_loss", grad_loss, m)
+    m, ld, rows = logits_shard("logits", logits, shard_rows, col_offset)
+    entries, _ = _teacher(teacher_ids, teacher, teacher_lse, m)
+    float_rows("lse", lse, m)
+    float_rows("grad_loss", grad_loss, m)
     if grad_logits is None:
         if grad_col_offset:
             raise ValueError("grad_col_offset needs a grad_logits buffer")
         grad_logits = torch.empty((m, rows), dtype=logits.dtype, device=logits.device)
         grad_col_offset = 0
     else:
-        _need_device("grad_logits", grad_logits)
         if (grad_logits.dim() != 2 or grad_logits.shape[0] != m
                 or grad_logits.dtype != logits.dtype):
             raise ValueError("grad_logits must be [m, ld] of the logits' dtype")
         grad_col_offset = col_offset if grad_col_offset is None else grad_col_offset
-    _same_device(logits, lse, grad_loss, teacher, grad_logits)
-    enqueue("vpe_distill_grad", logits.device, logits.data_ptr(), logits.shape[1], int(col_offset),
-            m, rows, dt, int(vocab_start), int(vocab), float(temperature), teacher_ids.data_ptr(),
-            itype, teacher.data_ptr(), tdt, k, None if teacher_lse is None else
-            teacher_lse.data_ptr(), lse.data_ptr(), grad_loss.data_ptr(), grad_logits.data_ptr(),
-            grad_logits.shape[1], int(grad_col_offset))
+    index = placed("logits teacher_ids teacher lse grad_loss grad_logits", logits, teacher_ids,
+                   teacher, lse, grad_loss, grad_logits)
+    enqueue("vpe_distill_grad", index, logits.data_ptr(), ld, col_offset, m, rows,
+            dtype_code(logits), vocab_start, vocab, temperature, *entries, lse.data_ptr(),
+            grad_loss.data_ptr(), grad_logits.data_ptr(), grad_logits.shape[1], grad_col_offset)
     return grad_logits
