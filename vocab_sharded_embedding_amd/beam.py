@@ -6,6 +6,7 @@ package itself.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Sequence
 
@@ -16,6 +17,7 @@ from .training import (dtype_code, enqueue, float_rows, logits_shard, nbytes, ne
                        placed)
 
 
+@functools.lru_cache(maxsize=256)
 def vpe_beam_select_workspace(n_seqs: int, beams: int, shard_rows: int, picks: int) -> int:
     """Bytes of workspace vpe_beam_select needs."""
     b = ctypes.c_int64()
@@ -48,9 +50,9 @@ def vpe_beam_select(logits, lse, scores, beams: int, picks: int, vocab_start: in
     elif keys.dtype != torch.int64 or keys.numel() != n * picks:
         raise ValueError("keys must be an int64 tensor [n_seqs, picks] (uint64 keys)")
     index = placed("logits lse scores keys workspace", logits, lse, scores, keys, workspace)
-    enqueue("vpe_beam_select", index, logits.data_ptr(), ld, col_offset, dtype_code(logits), n,
-            beams, rows, vocab_start, vocab, lse.data_ptr(), scores.data_ptr(), picks,
-            keys.data_ptr(), workspace.data_ptr(), nbytes(workspace))
+    enqueue("vpe_beam_select", index, logits.data_ptr(), ld, int(col_offset),
+            dtype_code(logits), n, beams, rows, int(vocab_start), int(vocab), lse.data_ptr(),
+            scores.data_ptr(), picks, keys.data_ptr(), workspace.data_ptr(), nbytes(workspace))
     return keys
 
 
@@ -68,7 +70,7 @@ def vpe_beam_merge(keys: Sequence, vocab: int):
     score = torch.empty((n, picks), dtype=torch.float32, device=first.device)
     parent, token = torch.empty_like(first), torch.empty_like(first)
     array = (ctypes.c_void_p * len(keys))(*[t.data_ptr() for t in keys])
-    enqueue("vpe_beam_merge", index, array, len(keys), n, picks, vocab, score.data_ptr(),
+    enqueue("vpe_beam_merge", index, array, len(keys), n, picks, int(vocab), score.data_ptr(),
             parent.data_ptr(), token.data_ptr())
     return score, parent, token
 

@@ -13,10 +13,12 @@
 //    is beaten by k candidates, one in each, so only about k groups are read
 //    again, and of those only the scores at the k-th group's best and above are
 //    looked at: usually little more than k.
-//  - The k-th largest of many keys is found by their digits of 11 bits from the
-//    top, counted in LDS: two rounds for scores that differ.  A selection by
-//    single bits (ballots in one wave) took 150 to 400 cycles a bit, 14000 a
-//    selection, and a selection per row slice 32 us for [256, 75968] logits.
+//  - The k-th largest of many keys is found by digits of 11 bits, counted in
+//    LDS, of their distance from a score that 64 of them reach: one round for
+//    scores that differ.  (Digits from the top of the key put most scores into
+//    a few counters, whose atomics then follow each other: 18000 cycles for
+//    6304 keys.  A selection by single bits, ballots in one wave, took 150 to
+//    400 cycles a bit, and one per row slice 32 us for [256, 75968] logits.)
 //  - Few candidates (kDirect) are ordered by the second kernel alone.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -41,6 +43,7 @@ constexpr int kDigitBits = 11;
 constexpr int kBins = 1 << kDigitBits;
 constexpr int kCap = 2048;               // keys collected
 constexpr int kFew = 256;                // keys ordered by counting
+constexpr int kHeld = 8192;              // groups whose best scores are held in LDS
 
 // Unsigned integers ordered like the scores, NaN below all.
 __device__ __forceinline__ uint32_t order_of(float c) {
@@ -129,35 +132,66 @@ __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t row0,
 // ---------------------------------------------------------------------------
 struct SelectLds {
   uint32_t bins[kBins];
-  uint32_t sums[kThreads / 64];
+  uint32_t sums[kThreads / 64], least[kThreads / 64];
   uint64_t cand[kCap];
   uint64_t few[kFew];
   float lse[kMaxPicks], score[kMaxPicks];  // of the sequence's beams
   uint32_t group[kFew];                    // groups read again
+  uint32_t held[kHeld];                    // order of the groups' best scores
   int n;                                   // keys collected
+  uint32_t rank[kFew];
   uint32_t digit, above, reach;
 };
 
-// A bound that at least k of the keys (key 0 stands for none) reach, and at
-// most k + slack unless they are copies of one key; 1 where there are fewer.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+      static_cast<int>(v), static_cast<int>(v), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, dpp_u32<0x111>(v)), v = max(v, dpp_u32<0x112>(v));
+  v = max(v, dpp_u32<0x114>(v)), v = max(v, dpp_u32<0x118>(v));
+  v = max(v, dpp_u32<0x142>(v)), v = max(v, dpp_u32<0x143>(v));
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+}
+
+// A bound that at least k <= 64 of the keys (key 0 stands for none) reach, and
+// at most k + slack unless they are copies of one key; 1 where there are fewer.
 template <class Keys>
 __device__ __forceinline__ uint64_t bound_of(const Keys &keys, int n, int k, int slack,
                                              SelectLds &s) {
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
+  // the largest order; and the best, over the waves, of the least of the lanes'
+  // largest, which 64 keys reach
+  uint32_t most = 0;
+#pragma unroll 2
+  for (int i = tid; i < n; i += kThreads) most = max(most, static_cast<uint32_t>(keys(i) >> 32));
+  const uint32_t wave_most = wave_max_u32(most), wave_least = ~wave_max_u32(~most);
+  for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
+  if (lane == 0) s.sums[wave] = wave_most, s.least[wave] = wave_least;
+  __syncthreads();
+  uint32_t top = 0, low = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) top = max(top, s.sums[w]), low = max(low, s.least[w]);
+  const uint64_t base = static_cast<uint64_t>(low) << 32;
+  const int span = 64 - __builtin_clz((top - low) | 1u);  // bits of a distance from base, >= 33
+
   uint64_t prefix = 0;
   int need = k;  // keys still to be found among those of the prefix
 #pragma nounroll
-  for (int open = 64; open > 0;) {  // low bits not decided yet
+  for (int open = span; open > 0;) {  // low bits not decided yet
     const int bits = open < kDigitBits ? open : kDigitBits;
     const int shift = open - bits;
-    for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
+    if (open != span) {
+      for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
+    }
     if (tid == 0) s.reach = 0;
     __syncthreads();
-#pragma nounroll
+#pragma unroll 2
     for (int i = tid; i < n; i += kThreads) {
-      const uint64_t key = keys(i);
-      if (key != 0 && (open == 64 || key >> open == prefix))
-        atomicAdd(&s.bins[(key >> shift) & ((1 << bits) - 1)], 1u);
+      const uint64_t key = keys(i), far = key - base;
+      if (key != 0 && key >= base && (open >= 64 || far >> open == prefix))
+        atomicAdd(&s.bins[(far >> shift) & ((1 << bits) - 1)], 1u);
     }
     __syncthreads();
     // thread t: digits kBins - 1 - 2t and the one below; `above`: keys of larger ones
@@ -172,8 +206,8 @@ __device__ __forceinline__ uint64_t bound_of(const Keys &keys, int n, int k, int
     if (lane == 63) s.sums[wave] = above;
     __syncthreads();
     above -= hi + lo;
-#pragma nounroll
-    for (int w = 0; w < wave; ++w) above += s.sums[w];
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) above += w < wave ? s.sums[w] : 0;
     const uint32_t want = static_cast<uint32_t>(need);
     if (above < want && above + hi + lo >= want) {
       const bool upper = above + hi >= want;
@@ -189,7 +223,7 @@ __device__ __forceinline__ uint64_t bound_of(const Keys &keys, int n, int k, int
     need -= static_cast<int>(s.above);
     open = shift;
     __syncthreads();  // read before the next round (or call) clears it
-    if (total <= k + slack || open == 0) return prefix << open;
+    if (total <= k + slack || open == 0) return base + (prefix << open);
   }
   return 1;  // not reached
 }
@@ -217,15 +251,21 @@ __device__ __forceinline__ uint64_t best_of_few(int n, int k, SelectLds &s) {
   const int tid = threadIdx.x;
   if (n > kFew) n = kFew;  // copies of one key
   if (tid < k) s.cand[tid] = 0;
+  if (tid < kFew) s.rank[tid] = 0;
   __syncthreads();
-  if (tid < n) {
-    const uint64_t mine = s.few[tid];
-    int rank = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j)
-      rank += s.few[j] > mine || (s.few[j] == mine && j < tid);
-    if (rank < k) s.cand[rank] = mine;
+  // thread (i, part): how many of a quarter of the keys come before key i
+  constexpr int kParts = kThreads / kFew;
+  const int i = tid % kFew, share = (n + kParts - 1) / kParts;
+  const int j0 = tid / kFew * share, j1 = j0 + share < n ? j0 + share : n;
+  const uint64_t mine = i < n ? s.few[i] : 0;
+  if (i < n) {
+    uint32_t rank = 0;
+#pragma unroll 8
+    for (int j = j0; j < j1; ++j) rank += s.few[j] > mine || (s.few[j] == mine && j < i);
+    atomicAdd(&s.rank[i], rank);
   }
+  __syncthreads();
+  if (tid < n && s.rank[tid] < static_cast<uint32_t>(k)) s.cand[s.rank[tid]] = mine;
   __syncthreads();
   return tid < k ? s.cand[tid] : 0;
 }
@@ -281,6 +321,14 @@ struct GroupKeys {
                  c.best[i]);
   }
 };
+// the same with the order of the score held in LDS, and group numbers for
+// places (they are ordered alike)
+struct HeldKeys {
+  const uint32_t *held;
+  __device__ __forceinline__ uint64_t operator()(int i) const {
+    return (static_cast<uint64_t>(held[i]) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(i));
+  }
+};
 // those of the groups listed in s.group
 template <bool BF16>
 struct ListedKeys {
@@ -316,8 +364,19 @@ __global__ __launch_bounds__(kThreads) void beam_pick(BeamArgs a, const float *_
     // the k best groups (up to as many again where that saves a round)
     const GroupKeys<BF16> groups{c};
     const int n = static_cast<int>(a.beams * a.groups);
-    const uint64_t bound = bound_of(groups, n, k, k, s);
-    collect(groups, TheIndex{}, n, bound, s.group, kFew, s);
+    uint64_t bound;
+    if (n <= kHeld) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kThreads)
+        s.held[i] = static_cast<uint32_t>(groups(i) >> 32);
+      __syncthreads();
+      const HeldKeys held{s.held};
+      bound = bound_of(held, n, k, k, s);
+      collect(held, TheIndex{}, n, bound, s.group, kFew, s);
+    } else {
+      bound = bound_of(groups, n, k, k, s);
+      collect(groups, TheIndex{}, n, bound, s.group, kFew, s);
+    }
     const int listed = s.n;
     __syncthreads();
     // their scores at the bound and above
@@ -326,26 +385,41 @@ __global__ __launch_bounds__(kThreads) void beam_pick(BeamArgs a, const float *_
     if (tid == 0) s.n = 0;
     __syncthreads();
     const uint32_t least = static_cast<uint32_t>(bound >> 32);
-    for (int i = wave_in_block(); i < listed; i += kThreads / 64) {
-      const uint32_t group = s.group[i], ng = static_cast<uint32_t>(a.groups);
-      const uint32_t beam = group / ng;
-      const int64_t j = (static_cast<int64_t>(group - beam * ng) * 64 + (tid & 63)) * kEpv;
-      const char *p = c.base + beam * a.ld_bytes;
-      float v[kEpv];
-      if (j + kEpv <= a.cols) {
-        Vec<BF16, kEpv>::widen(
-            *reinterpret_cast<const typename R::loose *>(p + j * (BF16 ? 2 : 4)), v);
-      } else {
+    constexpr int kWaves = kThreads / 64, kDeep = 8;  // groups in flight per wave
+    const uint32_t ng = static_cast<uint32_t>(a.groups);
+    for (int i0 = wave_in_block(); i0 < listed; i0 += kDeep * kWaves) {
+      u32x4 raw[kDeep];
 #pragma unroll
-        for (int e = 0; e < kEpv; ++e) v[e] = j + e < a.cols ? load_one<BF16>(p, j + e) : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < kEpv; ++e) {
-        const uint64_t key = c.key(static_cast<int>(beam), static_cast<uint32_t>(j) + e, v[e]);
-        if (j + e < a.cols && static_cast<uint32_t>(key >> 32) >= least) {
-          const int at = atomicAdd(&s.n, 1);
-          if (at < kCap) s.cand[at] = key;
+      for (int u = 0; u < kDeep; ++u) {
+        const int i = i0 + u * kWaves;
+        raw[u] = u32x4(0);
+        if (i < listed) {
+          const uint32_t group = s.group[i], beam = group / ng;
+          const int64_t col = (static_cast<int64_t>(group - beam * ng) * 64 + (tid & 63)) * kEpv;
+          if (col + kEpv <= a.cols)
+            raw[u] = *reinterpret_cast<const typename R::loose *>(c.base + beam * a.ld_bytes +
+                                                                  col * R::kSize);
         }
+      }
+      // rolled, the vectors moving down: cold instructions cost more than moves
+#pragma nounroll
+      for (int u = 0; u < kDeep && i0 + u * kWaves < listed; ++u) {
+        const uint32_t group = s.group[i0 + u * kWaves], beam = group / ng;
+        const uint32_t col = ((group - beam * ng) * 64 + (tid & 63)) * kEpv;
+        float v[kEpv];
+        Vec<BF16, kEpv>::widen(raw[0], v);
+        if (col < a.cols && col + kEpv > a.cols)
+          load_vec<BF16, kEpv>(c.base + beam * a.ld_bytes, col, a.cols, v);
+#pragma unroll
+        for (int e = 0; e < kEpv; ++e) {
+          const uint64_t key = c.key(static_cast<int>(beam), col + e, v[e]);
+          if (col + e < a.cols && static_cast<uint32_t>(key >> 32) >= least) {
+            const int at = atomicAdd(&s.n, 1);
+            if (at < kCap) s.cand[at] = key;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q + 1 < kDeep; ++q) raw[q] = raw[q + 1];
       }
     }
     __syncthreads();
@@ -464,8 +538,8 @@ int launch_reorder(const void *src, int64_t outer, int64_t n_seqs, int beams_in,
   for (int64_t r = 0; r < rows; r += step) {
     const int64_t nr = std::min(step, rows - r);
     const int64_t threads = (nr * units) << log2g;
-    hipLaunchKernelGGL((reorder_rows<V>), dim3(static_cast<unsigned>((threads + kBlock - 1) / kBlock)),
-                       dim3(kBlock), 0, st, static_cast<const V *>(src), r,
+    const dim3 grid(static_cast<unsigned>((threads + kBlock - 1) / kBlock));
+    hipLaunchKernelGGL((reorder_rows<V>), grid, dim3(kBlock), 0, st, static_cast<const V *>(src), r,
                        static_cast<uint32_t>(nr), n_seqs * beams_out, beams_in, beams_out, n_seqs,
                        vr, static_cast<uint32_t>(units), span, log2g, parent, ld_parent,
                        static_cast<V *>(dst));
@@ -517,8 +591,8 @@ int launch_beam_merge(const uint64_t *const *keys, int n_parts, int64_t n_seqs, 
   (void)hipGetLastError();
   PartKeys parts{};
   for (int r = 0; r < n_parts; ++r) parts.part[r] = keys[r];
-  hipLaunchKernelGGL(beam_merge_rows, dim3(static_cast<unsigned>(n_seqs)), dim3(kThreads), 0, st, parts,
-                     n_parts, picks, vocab, score, parent, token);
+  hipLaunchKernelGGL(beam_merge_rows, dim3(static_cast<unsigned>(n_seqs)), dim3(kThreads), 0, st,
+                     parts, n_parts, picks, vocab, score, parent, token);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -529,8 +603,9 @@ int launch_beam_reorder(const void *src, int64_t outer, int64_t n_seqs, int beam
   (void)hipGetLastError();
   const uint64_t low = reinterpret_cast<uint64_t>(src) | reinterpret_cast<uint64_t>(dst) |
                        static_cast<uint64_t>(row_bytes);
-#define VPE_REORDER(V, B) \
-  launch_reorder<V>(src, outer, n_seqs, beams_in, row_bytes / B, parent, ld_parent, beams_out, dst, st)
+#define VPE_REORDER(V, B)                                                                  \
+  launch_reorder<V>(src, outer, n_seqs, beams_in, row_bytes / B, parent, ld_parent, beams_out, \
+                    dst, st)
   if ((low & 15) == 0) return VPE_REORDER(u32x4, 16);
   if ((low & 7) == 0) return VPE_REORDER(u32x2, 8);
   if ((low & 3) == 0) return VPE_REORDER(uint32_t, 4);

@@ -59,7 +59,9 @@ inline EmbedGradLayout embed_grad_layout(int64_t n, int64_t shard_rows, int64_t 
   }
   l.partial_ld = (dim + 7) / 8 * 8;
   l.chunk = kGradChunk;
-  while (l.chunk > 4 && (n + l.chunk - 1) / l.chunk < kGradFillChunks) l.chunk /= 2;
+  // (a single chunk needs no join)
+  while (n > kGradChunk && l.chunk > 4 && (n + l.chunk - 1) / l.chunk < kGradFillChunks)
+    l.chunk /= 2;
   // at most one run that enters a chunk and one that leaves it having begun in
   // it; the most chunks of any number of ids up to n, so that a workspace for
   // more ids serves fewer

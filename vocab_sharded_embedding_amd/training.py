@@ -10,6 +10,7 @@ current HIP stream of the tensors' device to the library.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence
 
 import torch
@@ -85,10 +86,12 @@ def vpe_embed_scaled(ids, weight, vocab_start: int, scale: float, out=None):
         raise ValueError("out must have the weight's dtype and ids.numel() * dim elements")
     index = placed("ids weight out", ids, weight, out)
     enqueue("vpe_embed_scaled", index, ids.data_ptr(), itype_code(ids), ids.numel(),
-            weight.data_ptr(), dtype_code(weight), rows, dim, vocab_start, scale, out.data_ptr())
+            weight.data_ptr(), dtype_code(weight), rows, dim, int(vocab_start), scale,
+            out.data_ptr())
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def vpe_embed_grad_workspace(n: int, shard_rows: int, dim: int) -> int:
     """Bytes of workspace vpe_embed_grad needs for n ids; as much serves fewer."""
     b = ctypes.c_int64()
@@ -123,8 +126,9 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
         workspace = new_workspace(vpe_embed_grad_workspace(n, shard_rows, dim), grad_out.device)
     index = placed("ids grad_out grad_weight workspace", ids, grad_out, grad_weight, workspace)
     enqueue("vpe_embed_grad", index, ids.data_ptr(), itype_code(ids), n, grad_out.data_ptr(),
-            dtype_code(grad_out), dim, vocab_start, shard_rows, scale, grad_weight.data_ptr(),
-            dtype_code(grad_weight), bool(accumulate), workspace.data_ptr(), nbytes(workspace))
+            dtype_code(grad_out), dim, int(vocab_start), shard_rows, scale,
+            grad_weight.data_ptr(), dtype_code(grad_weight), bool(accumulate),
+            workspace.data_ptr(), nbytes(workspace))
     return grad_weight
 
 
@@ -156,6 +160,7 @@ def logits_shard(name: str, logits, shard_rows: Optional[int], col_offset: int):
     return m, ld, ld - col_offset if shard_rows is None else shard_rows
 
 
+@functools.lru_cache(maxsize=256)
 def vpe_distill_workspace(m: int, shard_rows: int) -> int:
     """Bytes of workspace vpe_distill_shard needs (unless with_lse is False)."""
     b = ctypes.c_int64()
@@ -200,8 +205,8 @@ def vpe_distill_shard(logits, teacher_ids, teacher, vocab_start: int, vocab: int
         index = placed("logits teacher_ids teacher shard_dot", logits, teacher_ids, teacher,
                        shard_dot)
         tail = (None, shard_dot.data_ptr(), None, 0)
-    enqueue("vpe_distill_shard", index, logits.data_ptr(), ld, col_offset, m, rows,
-            dtype_code(logits), vocab_start, vocab, temperature, *entries, *tail)
+    enqueue("vpe_distill_shard", index, logits.data_ptr(), ld, int(col_offset), m, rows,
+            dtype_code(logits), int(vocab_start), int(vocab), temperature, *entries, *tail)
     return shard_lse, shard_dot
 
 
@@ -222,8 +227,8 @@ def vpe_distill_loss(shard_lse: Sequence, shard_dot: Sequence, teacher_ids, teac
                    teacher_ids, teacher, loss, lse, *shard_lse, *shard_dot)
     array = ctypes.c_void_p * n
     enqueue("vpe_distill_loss", index, array(*[t.data_ptr() for t in shard_lse]),
-            array(*[t.data_ptr() for t in shard_dot]), n, m, vocab, temperature, *entries,
-            loss.data_ptr(), lse.data_ptr())
+            array(*[t.data_ptr() for t in shard_dot]), n, m, int(vocab), temperature,
+            *entries, loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
 
@@ -254,7 +259,8 @@ def vpe_distill_grad(logits, lse, grad_loss, teacher_ids, teacher, vocab_start: 
         grad_col_offset = col_offset if grad_col_offset is None else grad_col_offset
     index = placed("logits teacher_ids teacher lse grad_loss grad_logits", logits, teacher_ids,
                    teacher, lse, grad_loss, grad_logits)
-    enqueue("vpe_distill_grad", index, logits.data_ptr(), ld, col_offset, m, rows,
-            dtype_code(logits), vocab_start, vocab, temperature, *entries, lse.data_ptr(),
-            grad_loss.data_ptr(), grad_logits.data_ptr(), grad_logits.shape[1], grad_col_offset)
+    enqueue("vpe_distill_grad", index, logits.data_ptr(), ld, int(col_offset), m, rows,
+            dtype_code(logits), int(vocab_start), int(vocab), temperature, *entries, lse.data_ptr(),
+            grad_loss.data_ptr(), grad_logits.data_ptr(), grad_logits.shape[1],
+            int(grad_col_offset))
     return grad_logits
