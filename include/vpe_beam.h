@@ -60,7 +60,8 @@ vpe_status vpe_beam_select_workspace(int64_t n_seqs, int32_t beams, int64_t shar
  * n_seqs == 0 is a no-op.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (n_seqs <
  * 0, n_seqs * beams > 2^21, beams outside [1, VPE_MAX_BEAMS], picks outside
- * [1, VPE_MAX_BEAM_PICKS], shard_rows < 1, vocab < 1, a tensor too large),
+ * [1, VPE_MAX_BEAM_PICKS], shard_rows < 1 or >= 2^31, vocab < 1, a tensor too
+ * large),
  * VPE_ERR_RANGE (the shard does not lie in [0, vocab), beams * vocab >= 2^32,
  * the columns do not fit ld), VPE_ERR_WORKSPACE.
  */

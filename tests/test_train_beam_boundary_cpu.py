@@ -205,7 +205,7 @@ def test_beam_select_validation():
         scores=FAKE, picks=8, keys=FAKE, ws=FAKE, bytes=1 << 20, stream=None))
     assert call(dt=4) == vpe.VPE_ERR_DTYPE
     for bad in (dict(n=-1), dict(n=2 ** 20), dict(beams=0), dict(beams=65), dict(picks=0),
-                dict(picks=65), dict(rows=0), dict(vocab=0), dict(bytes=-1), dict(ld=2 ** 38)):
+                dict(picks=65), dict(rows=0), dict(rows=2 ** 31), dict(vocab=0), dict(bytes=-1), dict(ld=2 ** 38)):
         assert call(**bad) == vpe.VPE_ERR_SHAPE, bad
     for bad in (dict(start=-1), dict(start=1), dict(vocab=999), dict(vocab=2 ** 30),
                 dict(vocab=2 ** 63 - 1), dict(ld=999), dict(col=1), dict(col=-1)):
@@ -222,7 +222,7 @@ def test_beam_select_validation():
     f = vpe.load_library().vpe_beam_select_workspace
     assert f(1, 1, 1, 1, None) == vpe.VPE_ERR_NULL
     for bad in ((-1, 1, 1, 1), (1, 0, 1, 1), (1, 65, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0),
-                (1, 1, 1, 65), (2 ** 20, 4, 1, 1)):
+                (1, 1, 1, 65), (2 ** 20, 4, 1, 1), (1, 1, 2 ** 31, 1)):
         assert f(*bad, ctypes.byref(b)) == vpe.VPE_ERR_SHAPE, bad
 
 

@@ -6,8 +6,9 @@
 // a 64-bit key (order of the score, then the lower place), and all keys of a
 // sequence are distinct, so "the k best" is one definite set.
 //  - A first kernel leaves the largest logit of every group of 64 vectors of a
-//    row: a widening and half a maximum per logit, no branches, bound by HBM.
-//    The score rises with the logit, so the group's best score follows from it.
+//    row (of 8 where a sequence has few): a widening and half a maximum per
+//    logit, no branches, bound by HBM.  The score rises with the logit, so the
+//    group's best score follows from it.
 //  - A second kernel, one workgroup per sequence, orders the groups of all
 //    beams by (best score, lower place).  A candidate outside the k best groups
 //    is beaten by k candidates, one in each, so only about k groups are read
@@ -35,12 +36,13 @@ using namespace dev;
 
 constexpr int kBlock = 256;
 constexpr int kMaxPicks = 64;
-constexpr int kGroupsPerWave = 4;        // vectors in flight per lane
+constexpr int kVecsAhead = 4;            // vectors in flight per lane
 constexpr int64_t kRowsPerGrid = 32768;
 constexpr int64_t kDirect = 16384;       // candidates a workgroup orders by itself
 constexpr int kThreads = 1024;           // of that workgroup
 constexpr int kDigitBits = 11;
 constexpr int kBins = 1 << kDigitBits;
+constexpr int kLoose = 48;               // 16 of them bits of the score's order
 constexpr int kCap = 2048;               // keys collected
 constexpr int kFew = 256;                // keys ordered by counting
 constexpr int kHeld = 8192;              // groups whose best scores are held in LDS
@@ -68,10 +70,11 @@ struct BeamArgs {
   const float *lse, *scores;
   int beams, picks;
   int64_t groups;  // per row
+  int group_log2;  // vectors per group: 2^6, or 2^3
 };
 
-// best[row * groups + g] = the largest logit of columns [g, g + 1) * 64 vectors
-// of the row, NaN if there is none (grid: groups / 16, rows).
+// best[row * groups + g] = the largest logit of group g of the row, NaN if
+// there is none (grid: vectors of the row / 1024, rows).
 template <bool BF16>
 __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t row0,
                                                      float *__restrict__ best) {
@@ -79,14 +82,15 @@ __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t row0,
   constexpr int kEpv = R::kEpv, kSize = BF16 ? 2 : 4;
   const int lane = threadIdx.x & 63;
   const int64_t row = row0 + blockIdx.y;
+  // waves take kVecsAhead times 64 vectors, from vector 64 * g0 on
   const int64_t g0 =
-      (static_cast<int64_t>(blockIdx.x) * (kBlock / 64) + wave_in_block()) * kGroupsPerWave;
-  if (g0 >= a.groups) return;
+      (static_cast<int64_t>(blockIdx.x) * (kBlock / 64) + wave_in_block()) * kVecsAhead;
+  if (g0 * 64 * kEpv >= a.cols) return;
   const char *p = a.base + row * a.ld_bytes;
   const uint32_t none = BF16 ? 0x7fc07fc0u : 0x7fc00000u;
-  u32x4 raw[kGroupsPerWave];
+  u32x4 raw[kVecsAhead];
 #pragma unroll
-  for (int u = 0; u < kGroupsPerWave; ++u) {
+  for (int u = 0; u < kVecsAhead; ++u) {
     const int64_t j = ((g0 + u) * 64 + lane) * kEpv;
     raw[u] = u32x4(none);
     if (j + kEpv <= a.cols) raw[u] = *reinterpret_cast<const typename R::loose *>(p + j * kSize);
@@ -96,9 +100,9 @@ __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t row0,
   const float inf = __builtin_huge_valf();
   const float top = (inf - a.lse[row]) + a.scores[row];
   const bool no_inf = top != top;
-  float mx[kGroupsPerWave];
+  float mx[kVecsAhead];
 #pragma unroll
-  for (int u = 0; u < kGroupsPerWave; ++u) {
+  for (int u = 0; u < kVecsAhead; ++u) {
     float v[kEpv];
     Vec<BF16, kEpv>::widen(raw[u], v);
     if (no_inf) {
@@ -118,13 +122,27 @@ __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t row0,
       }
     }
   }
-  float mine = 0.f;
+  float *out = best + row * a.groups;
+  if (a.group_log2 == 6) {
+    float mine = 0.f;
 #pragma unroll
-  for (int u = 0; u < kGroupsPerWave; ++u) {
-    const float m = wave_max(mx[u]);
-    if (lane == u) mine = m;
+    for (int u = 0; u < kVecsAhead; ++u) {
+      const float m = wave_max(mx[u]);
+      if (lane == u) mine = m;
+    }
+    if (lane < kVecsAhead && g0 + lane < a.groups) out[g0 + lane] = mine;
+  } else {
+    // lanes 7, 15, ... end with the maximum of their eight
+#pragma unroll
+    for (int u = 0; u < kVecsAhead; ++u) {
+      float m = mx[u];
+      m = fmaxf(m, dpp<0x111, 0xf>(m, m));
+      m = fmaxf(m, dpp<0x112, 0xf>(m, m));
+      m = fmaxf(m, dpp<0x114, 0xf>(m, m));
+      const int64_t g = (g0 + u) * 8 + lane / 8;
+      if ((lane & 7) == 7 && g < a.groups) out[g] = m;
+    }
   }
-  if (lane < kGroupsPerWave && g0 + lane < a.groups) best[row * a.groups + g0 + lane] = mine;
 }
 
 // ---------------------------------------------------------------------------
@@ -157,6 +175,8 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 
 // A bound that at least k <= 64 of the keys (key 0 stands for none) reach, and
 // at most k + slack unless they are copies of one key; 1 where there are fewer.
+// At most kLoose low bits are left open below it: the score of the bound is
+// within 2^-7 of the k-th largest, also where fewer keys than k + slack exist.
 template <class Keys>
 __device__ __forceinline__ uint64_t bound_of(const Keys &keys, int n, int k, int slack,
                                              SelectLds &s) {
@@ -223,7 +243,7 @@ __device__ __forceinline__ uint64_t bound_of(const Keys &keys, int n, int k, int
     need -= static_cast<int>(s.above);
     open = shift;
     __syncthreads();  // read before the next round (or call) clears it
-    if (total <= k + slack || open == 0) return base + (prefix << open);
+    if ((total <= k + slack && open <= kLoose) || open == 0) return base + (prefix << open);
   }
   return 1;  // not reached
 }
@@ -290,8 +310,9 @@ struct Candidates {
   const SelectLds &s;
   const char *base;  // the sequence's first row
   const float *best; // its groups' largest logits
-  static constexpr int kGroupCols = 64 * Row<BF16>::kEpv;
+  static constexpr int kEpv = Row<BF16>::kEpv;
 
+  __device__ __forceinline__ uint32_t group_cols() const { return kEpv << a.group_log2; }
   __device__ __forceinline__ uint64_t key(int beam, uint32_t col, float z) const {
     const float c = ((z - s.lse[beam]) + s.score[beam]) + 0.f;  // -0 becomes +0
     const uint32_t place = static_cast<uint32_t>(beam * a.vocab + a.vocab_start) + col;
@@ -317,7 +338,7 @@ struct GroupKeys {
   __device__ __forceinline__ uint64_t operator()(int i) const {
     const uint32_t groups = static_cast<uint32_t>(c.a.groups);
     const uint32_t beam = static_cast<uint32_t>(i) / groups;
-    return c.key(static_cast<int>(beam), (static_cast<uint32_t>(i) - beam * groups) * c.kGroupCols,
+    return c.key(static_cast<int>(beam), (static_cast<uint32_t>(i) - beam * groups) * c.group_cols(),
                  c.best[i]);
   }
 };
@@ -334,9 +355,10 @@ template <bool BF16>
 struct ListedKeys {
   const Candidates<BF16> &c;
   __device__ __forceinline__ uint64_t operator()(int i) const {
-    const uint32_t group = c.s.group[i / c.kGroupCols];
+    const uint32_t cols = c.group_cols();
+    const uint32_t group = c.s.group[static_cast<uint32_t>(i) / cols];
     const uint32_t groups = static_cast<uint32_t>(c.a.groups), beam = group / groups;
-    const uint32_t col = (group - beam * groups) * c.kGroupCols + i % c.kGroupCols;
+    const uint32_t col = (group - beam * groups) * cols + static_cast<uint32_t>(i) % cols;
     return col < c.a.cols ? c.at(static_cast<int>(beam), col) : 0;
   }
 };
@@ -385,41 +407,44 @@ __global__ __launch_bounds__(kThreads) void beam_pick(BeamArgs a, const float *_
     if (tid == 0) s.n = 0;
     __syncthreads();
     const uint32_t least = static_cast<uint32_t>(bound >> 32);
-    constexpr int kWaves = kThreads / 64, kDeep = 8;  // groups in flight per wave
+    constexpr int kDeep = 4;  // vectors in flight per thread
     const uint32_t ng = static_cast<uint32_t>(a.groups);
-    for (int i0 = wave_in_block(); i0 < listed; i0 += kDeep * kWaves) {
+    const int vecs = listed << a.group_log2;
+    for (int i0 = tid; i0 < vecs; i0 += kDeep * kThreads) {
       u32x4 raw[kDeep];
+      uint32_t beam[kDeep], col[kDeep];
 #pragma unroll
       for (int u = 0; u < kDeep; ++u) {
-        const int i = i0 + u * kWaves;
-        raw[u] = u32x4(0);
-        if (i < listed) {
-          const uint32_t group = s.group[i], beam = group / ng;
-          const int64_t col = (static_cast<int64_t>(group - beam * ng) * 64 + (tid & 63)) * kEpv;
-          if (col + kEpv <= a.cols)
-            raw[u] = *reinterpret_cast<const typename R::loose *>(c.base + beam * a.ld_bytes +
-                                                                  col * R::kSize);
+        const int i = i0 + u * kThreads;
+        raw[u] = u32x4(0), beam[u] = 0, col[u] = 0xFFFFFFFFu - kEpv;  // past every row
+        if (i < vecs) {
+          const uint32_t group = s.group[i >> a.group_log2];
+          beam[u] = group / ng;
+          col[u] = (((group - beam[u] * ng) << a.group_log2) + (i & ((1 << a.group_log2) - 1))) * kEpv;
+          if (col[u] + kEpv <= a.cols)
+            raw[u] = *reinterpret_cast<const typename R::loose *>(
+                c.base + beam[u] * a.ld_bytes + static_cast<int64_t>(col[u]) * R::kSize);
         }
       }
       // rolled, the vectors moving down: cold instructions cost more than moves
 #pragma nounroll
-      for (int u = 0; u < kDeep && i0 + u * kWaves < listed; ++u) {
-        const uint32_t group = s.group[i0 + u * kWaves], beam = group / ng;
-        const uint32_t col = ((group - beam * ng) * 64 + (tid & 63)) * kEpv;
+      for (int u = 0; u < kDeep; ++u) {
+        if (__ballot(col[0] < a.cols) == 0) break;
         float v[kEpv];
         Vec<BF16, kEpv>::widen(raw[0], v);
-        if (col < a.cols && col + kEpv > a.cols)
-          load_vec<BF16, kEpv>(c.base + beam * a.ld_bytes, col, a.cols, v);
+        if (col[0] < a.cols && col[0] + kEpv > a.cols)
+          load_vec<BF16, kEpv>(c.base + beam[0] * a.ld_bytes, col[0], a.cols, v);
 #pragma unroll
         for (int e = 0; e < kEpv; ++e) {
-          const uint64_t key = c.key(static_cast<int>(beam), col + e, v[e]);
-          if (col + e < a.cols && static_cast<uint32_t>(key >> 32) >= least) {
+          const uint64_t key = c.key(static_cast<int>(beam[0]), col[0] + e, v[e]);
+          if (col[0] + e < a.cols && static_cast<uint32_t>(key >> 32) >= least) {
             const int at = atomicAdd(&s.n, 1);
             if (at < kCap) s.cand[at] = key;
           }
         }
 #pragma unroll
-        for (int q = 0; q + 1 < kDeep; ++q) raw[q] = raw[q + 1];
+        for (int q = 0; q + 1 < kDeep; ++q)
+          raw[q] = raw[q + 1], beam[q] = beam[q + 1], col[q] = col[q + 1];
       }
     }
     __syncthreads();
@@ -431,7 +456,7 @@ __global__ __launch_bounds__(kThreads) void beam_pick(BeamArgs a, const float *_
               s.few, kFew, s);
     } else {  // many equal scores
       const ListedKeys<BF16> some{c};
-      const int n_some = listed * c.kGroupCols;
+      const int n_some = listed * static_cast<int>(c.group_cols());
       collect(some, TheKey{}, n_some, bound_of(some, n_some, k, kFew - k, s), s.few, kFew, s);
     }
   }
@@ -547,10 +572,19 @@ int launch_reorder(const void *src, int64_t outer, int64_t n_seqs, int beams_in,
   return static_cast<int>(hipGetLastError());
 }
 
+// Vectors per group, as a power of two: 8 where all of a sequence's groups
+// still fit LDS.  Groups of 64 are too few there: 30 picks of 15 x 1619 logits
+// need half of the 60 groups, in which 2000 scores reach the bound (28 us).
+int group_log2(int beams, int64_t cols, int dtype) {
+  const int64_t small = 8 * (dtype == 1 ? Row<true>::kEpv : Row<false>::kEpv);
+  return beams * ((cols + small - 1) / small) <= kHeld ? 3 : 6;
+}
+
 }  // namespace
 
-int64_t beam_groups_per_row(int64_t cols, int dtype) {
-  const int64_t group = 64 * (dtype == 1 ? Row<true>::kEpv : Row<false>::kEpv);
+int64_t beam_groups_per_row(int beams, int64_t cols, int dtype) {
+  const int64_t group = int64_t(dtype == 1 ? Row<true>::kEpv : Row<false>::kEpv)
+                        << group_log2(beams, cols, dtype);
   return (cols + group - 1) / group;
 }
 
@@ -560,13 +594,13 @@ int launch_beam_select(const void *base, int64_t ld, int dtype, int64_t n_seqs, 
                        void *stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();  // clear a stale error so the status returned is this launch's
-  const int64_t groups = beam_groups_per_row(cols, dtype);
+  const int64_t groups = beam_groups_per_row(beams, cols, dtype);
   const BeamArgs a{static_cast<const char *>(base), ld * (dtype == 1 ? 2 : 4), cols, vocab_start,
-                   vocab, lse, scores, beams, picks, groups};
+                   vocab, lse, scores, beams, picks, groups, group_log2(beams, cols, dtype)};
   const bool direct = beams * cols <= kDirect;
   if (!direct) {
-    constexpr int64_t kPerBlock = kGroupsPerWave * (kBlock / 64);
-    const unsigned gx = static_cast<unsigned>((groups + kPerBlock - 1) / kPerBlock);
+    const int64_t per_block = kVecsAhead * kBlock * (dtype == 1 ? Row<true>::kEpv : Row<false>::kEpv);
+    const unsigned gx = static_cast<unsigned>((cols + per_block - 1) / per_block);
     const int64_t rows = n_seqs * beams;
     for (int64_t r = 0; r < rows; r += kRowsPerGrid) {
       const dim3 grid(gx, static_cast<unsigned>(std::min(kRowsPerGrid, rows - r)));

@@ -584,11 +584,11 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
   write_row<OUT16, 4>(a, token, col, v);
 }
 
-// Workgroups of `threads` threads for `rows` rows of zeros: about 64 KB each.
+// Workgroups of `threads` threads for `rows` rows of zeros: about 256 KB each.
 unsigned zero_blocks(int64_t rows, int64_t row_bytes) {
   if (rows <= 0) return 0;
   const double bytes = static_cast<double>(rows) * static_cast<double>(row_bytes);
-  return static_cast<unsigned>(std::max(1.0, std::min(bytes / 65536.0, 65536.0)));
+  return static_cast<unsigned>(std::max(1.0, std::min(bytes / 262144.0, 65536.0)));
 }
 
 template <bool IN16, bool OUT16>

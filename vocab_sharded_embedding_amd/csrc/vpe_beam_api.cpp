@@ -17,11 +17,12 @@ vpe_status launched(int rc) { return rc == 0 ? VPE_OK : VPE_ERR_LAUNCH; }
 
 constexpr int64_t kMaxElems = int64_t(1) << 39;
 constexpr int64_t kMaxRows = int64_t(1) << 21;
+constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
 constexpr int64_t kMax32 = (int64_t(1) << 32) - 1;
 
 bool beam_shape_ok(int64_t n_seqs, int32_t beams, int64_t shard_rows, int32_t picks) {
   return beams >= 1 && beams <= VPE_MAX_BEAMS && picks >= 1 && picks <= VPE_MAX_BEAM_PICKS &&
-         n_seqs >= 0 && n_seqs <= kMaxRows / beams && shard_rows >= 1 && shard_rows <= kMax32;
+         n_seqs >= 0 && n_seqs <= kMaxRows / beams && shard_rows >= 1 && shard_rows <= kMax31;
 }
 
 }  // namespace
@@ -32,7 +33,10 @@ vpe_status vpe_beam_select_workspace(int64_t n_seqs, int32_t beams, int64_t shar
                                      int32_t picks, int64_t *bytes) {
   if (!bytes) return VPE_ERR_NULL;
   if (!beam_shape_ok(n_seqs, beams, shard_rows, picks)) return VPE_ERR_SHAPE;
-  *bytes = n_seqs * beams * vpe::beam_groups_per_row(shard_rows, 0) * 4;
+  // of either type of logits
+  const int64_t f32 = vpe::beam_groups_per_row(beams, shard_rows, 0);
+  const int64_t bf16 = vpe::beam_groups_per_row(beams, shard_rows, 1);
+  *bytes = n_seqs * beams * (f32 > bf16 ? f32 : bf16) * 4;
   return VPE_OK;
 }
 

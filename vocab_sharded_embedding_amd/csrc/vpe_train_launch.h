@@ -118,8 +118,8 @@ int launch_distill_grad(const LogitsShard &z, const Teacher &t, const float *lse
 // beam search
 // ---------------------------------------------------------------------------
 // Groups of columns of a row, whose largest logits (one float each) the
-// workspace holds; the most for f32.
-int64_t beam_groups_per_row(int64_t cols, int dtype);
+// workspace holds.
+int64_t beam_groups_per_row(int beams, int64_t cols, int dtype);
 
 int launch_beam_select(const void *base, int64_t ld, int dtype, int64_t n_seqs, int beams,
                        int64_t cols, int64_t vocab_start, int64_t vocab, const float *lse,
