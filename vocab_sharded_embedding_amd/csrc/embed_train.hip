@@ -37,26 +37,19 @@ constexpr int kWaves = kBlock / 64;
 // ---------------------------------------------------------------------------
 // scaled lookup
 // ---------------------------------------------------------------------------
-// 2^log2g lanes (at most 64) serve one row; each covers VPL vectors per sweep,
-// loaded before any is stored.
-template <bool BF16, int VPL, typename IdT>
-__global__ __launch_bounds__(kBlock) void scaled_rows(const IdT *__restrict__ ids, int64_t n,
-                                                     const char *__restrict__ weight,
-                                                     uint64_t start, uint64_t rows, int64_t dim,
-                                                     float scale, int log2g,
-                                                     char *__restrict__ out) {
+// Local row of an id, or -1: one unsigned compare covers both ends of the shard
+// (a wrapped difference is >= rows).
+template <typename IdT>
+__device__ __forceinline__ int64_t local_row(IdT id, uint64_t start, uint64_t rows) {
+  const uint64_t local = static_cast<uint64_t>(static_cast<int64_t>(id)) - start;
+  return local < rows ? static_cast<int64_t>(local) : -1;
+}
+
+// One row by `group` lanes, VPL vectors per lane loaded before any is stored.
+template <bool BF16, int VPL>
+__device__ __forceinline__ void scale_row(const char *src, char *dst, int64_t dim, float scale,
+                                          int lane, int group) {
   constexpr int kEpv = BF16 ? 8 : 4;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
-  const int64_t row = t >> log2g;
-  if (row >= n) return;
-  const int group = 1 << log2g;
-  const int lane = static_cast<int>(t) & (group - 1);
-  // one unsigned compare covers both ends (a wrapped difference is >= rows)
-  const uint64_t local = static_cast<uint64_t>(static_cast<int64_t>(ids[row])) - start;
-  const bool owned = local < rows;
-  const int64_t row_bytes = dim * (BF16 ? 2 : 4);
-  const char *src = weight + static_cast<int64_t>(owned ? local : 0) * row_bytes;
-  char *dst = out + row * row_bytes;
   typedef Vec<BF16, kEpv> V;
   const typename V::loose *src_v = reinterpret_cast<const typename V::loose *>(src);
   typename V::loose *dst_v = reinterpret_cast<typename V::loose *>(dst);
@@ -66,7 +59,7 @@ __global__ __launch_bounds__(kBlock) void scaled_rows(const IdT *__restrict__ id
 #pragma unroll
     for (int c = 0; c < VPL; ++c) {
       r[c] = typename V::raw(0);
-      if (owned && c0 + c * group < whole) r[c] = src_v[c0 + c * group];
+      if (src != nullptr && c0 + c * group < whole) r[c] = src_v[c0 + c * group];
     }
 #pragma unroll
     for (int c = 0; c < VPL; ++c) {
@@ -75,12 +68,31 @@ __global__ __launch_bounds__(kBlock) void scaled_rows(const IdT *__restrict__ id
 #pragma unroll
       for (int e = 0; e < kEpv; ++e) v[e] *= scale;
       typename V::raw o = V::narrow(v);
-      if (!owned) o = typename V::raw(0);  // +0, also for a negative factor
+      if (src == nullptr) o = typename V::raw(0);  // +0, also for a negative factor
       if (c0 + c * group < whole) __builtin_nontemporal_store(o, dst_v + c0 + c * group);
     }
   }
   for (int64_t i = whole * kEpv + lane; i < dim; i += group)
-    store_one<BF16>(dst, i, owned ? load_one<BF16>(src, i) * scale : 0.f);
+    store_one<BF16>(dst, i, src != nullptr ? load_one<BF16>(src, i) * scale : 0.f);
+}
+
+// 2^log2g lanes (at most 64) serve one row.  131072 rows of 8 KB, a quarter of
+// them owned: 220 us, 5.7 TB/s; 8 rows in turn per wave, for longer spans of
+// stores, took 246 us (less in flight).
+template <bool BF16, int VPL, typename IdT>
+__global__ __launch_bounds__(kBlock) void scaled_rows(const IdT *__restrict__ ids, int64_t n,
+                                                     const char *__restrict__ weight,
+                                                     uint64_t start, uint64_t rows, int64_t dim,
+                                                     float scale, int log2g,
+                                                     char *__restrict__ out) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+  const int64_t row = t >> log2g;
+  if (row >= n) return;
+  const int group = 1 << log2g;
+  const int64_t row_bytes = dim * (BF16 ? 2 : 4);
+  const int64_t local = local_row(ids[row], start, rows);
+  scale_row<BF16, VPL>(local >= 0 ? weight + local * row_bytes : nullptr, out + row * row_bytes,
+                       dim, scale, static_cast<int>(t) & (group - 1), group);
 }
 
 int ceil_log2(int64_t v) {
@@ -168,22 +180,30 @@ struct ZeroRows {
   unsigned blocks;
 };
 
-// `block` of z.blocks workgroups of `threads` threads.
+// `block` of z.blocks workgroups of `threads` threads.  Plain stores where the
+// whole shard is cleared beside one sorting workgroup (8192 ids, 156 MB: 35 us
+// against 39 with non-temporal ones), non-temporal ones (NT) where many sorted
+// rows are read meanwhile and after, which plain ones push out of the caches
+// (65536 ids, 622 MB: 170 us against 184).
+template <bool NT>
 __device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int threads) {
   const int64_t share = (z.row1 - z.row0 + z.blocks - 1) / z.blocks;
   const int64_t r0 = z.row0 + block * share, r1 = r0 + share < z.row1 ? r0 + share : z.row1;
   if (r0 >= r1) return;
   if (z.flags == nullptr) {
-    zero_bytes(z.dw + r0 * z.row_bytes, (r1 - r0) * z.row_bytes, threadIdx.x, threads);
+    zero_bytes<NT>(z.dw + r0 * z.row_bytes, (r1 - r0) * z.row_bytes, threadIdx.x, threads);
     return;
   }
-  const int lane = threadIdx.x & 63;
-  for (int64_t r = r0 + wave_in_block() * 64; r < r1; r += threads) {
-    uint64_t empty = __ballot(r + lane < r1 && z.flags[r + lane < r1 ? r + lane : r0] == 0);
+  // a contiguous part per wave
+  const int lane = threadIdx.x & 63, waves = threads / 64;
+  const int64_t part = (r1 - r0 + waves - 1) / waves, w0 = r0 + wave_in_block() * part;
+  const int64_t w1 = w0 + part < r1 ? w0 + part : r1;
+  for (int64_t r = w0; r < w1; r += 64) {
+    uint64_t empty = __ballot(r + lane < w1 && z.flags[r + lane < w1 ? r + lane : w0] == 0);
     while (empty) {
       const int64_t row = r + __builtin_ctzll(empty);
       empty &= empty - 1;
-      zero_bytes(z.dw + row * z.row_bytes, z.row_bytes, lane, 64);
+      zero_bytes<NT>(z.dw + row * z.row_bytes, z.row_bytes, lane, 64);
     }
   }
 }
@@ -202,7 +222,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_block(
   __shared__ uint16_t spos[2][kGradOneBlockIds];
   __shared__ uint32_t at_[kSortWaves][kDigits];
   __shared__ uint32_t sums[kDigits / 64];
-  if (blockIdx.x > 0) return zero_rows(zero, blockIdx.x - 1, kSortThreads);
+  if (blockIdx.x > 0) return zero_rows<false>(zero, blockIdx.x - 1, kSortThreads);
   // a wave reads and updates its own counters in program order
   volatile uint32_t(*at)[kDigits] = at_;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
@@ -306,7 +326,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_counts(SortItems<FIRST, IdT
                                                            uint32_t *hist, uint8_t *flags,
                                                            ZeroRows zero) {
   __shared__ uint32_t h[kDigits];
-  if (blockIdx.x >= pass.blocks) return zero_rows(zero, blockIdx.x - pass.blocks, kSortThreads);
+  if (blockIdx.x >= pass.blocks) return zero_rows<true>(zero, blockIdx.x - pass.blocks, kSortThreads);
   const int tid = threadIdx.x;
   if (FIRST && flags != nullptr) {
     u32x4 *f = reinterpret_cast<u32x4 *>(flags);
@@ -344,7 +364,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter(
   __shared__ u32x2 part_before[kParts][kDigits / 2], part_total[kParts][kDigits / 2];
   __shared__ uint32_t base[kDigits];
   __shared__ uint32_t sums[kDigits / 128];
-  if (blockIdx.x >= pass.blocks) return zero_rows(zero, blockIdx.x - pass.blocks, kSortThreads);
+  if (blockIdx.x >= pass.blocks) return zero_rows<true>(zero, blockIdx.x - pass.blocks, kSortThreads);
   // a wave reads and updates its own counters in program order
   volatile uint32_t(*at)[kDigits] = at_;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
@@ -460,7 +480,7 @@ __device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64
 template <bool IN16, bool OUT16, int EPV>
 __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0, int64_t n_chunks,
                                                      unsigned chunk_blocks, ZeroRows zero) {
-  if (blockIdx.x >= chunk_blocks) return zero_rows(zero, blockIdx.x - chunk_blocks, kBlock);
+  if (blockIdx.x >= chunk_blocks) return zero_rows<true>(zero, blockIdx.x - chunk_blocks, kBlock);
   typedef Vec<IN16, EPV> V;
   constexpr int kDeep = 8;
   const int lane = threadIdx.x & 63;
@@ -584,11 +604,11 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
   write_row<OUT16, 4>(a, token, col, v);
 }
 
-// Workgroups of `threads` threads for `rows` rows of zeros: about 256 KB each.
-unsigned zero_blocks(int64_t rows, int64_t row_bytes) {
+// Workgroups for `rows` rows of zeros: about `span` bytes each.
+unsigned zero_blocks(int64_t rows, int64_t row_bytes, double span = 262144.0) {
   if (rows <= 0) return 0;
   const double bytes = static_cast<double>(rows) * static_cast<double>(row_bytes);
-  return static_cast<unsigned>(std::max(1.0, std::min(bytes / 262144.0, 65536.0)));
+  return static_cast<unsigned>(std::max(1.0, std::min(bytes / span, 65536.0)));
 }
 
 template <bool IN16, bool OUT16>
@@ -681,7 +701,7 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
       }
     }
     zero.row0 = zero.row1, zero.row1 = zero_to;
-    zero.blocks = zero_blocks(zero.row1 - zero.row0, zero.row_bytes);
+    zero.blocks = zero_blocks(zero.row1 - zero.row0, zero.row_bytes, 65536.0);
   }
   a.key = key[last], a.pos = pos[last], a.count = count;
   a.partial = reinterpret_cast<float *>(ws + l.partial);

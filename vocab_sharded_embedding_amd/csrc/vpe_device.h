@@ -111,12 +111,16 @@ __device__ __forceinline__ void store_vec_nt(void *row, int64_t i, int64_t n,
 
 // `bytes` (even) zero bytes at p (even), by `lanes` lanes: whole 16-byte words
 // where they are aligned.
+template <bool NT>
 __device__ __forceinline__ void zero_bytes(char *p, int64_t bytes, int64_t lane, int64_t lanes) {
   int64_t head = static_cast<int64_t>(-reinterpret_cast<uintptr_t>(p) & 15);
   if (head > bytes) head = bytes;
   const int64_t words = (bytes - head) / 16;
   u32x4 *w = reinterpret_cast<u32x4 *>(p + head);
-  for (int64_t i = lane; i < words; i += lanes) __builtin_nontemporal_store(u32x4(0), w + i);
+  for (int64_t i = lane; i < words; i += lanes) {
+    if constexpr (NT) __builtin_nontemporal_store(u32x4(0), w + i);
+    else w[i] = u32x4(0);
+  }
   if (head != 0 || (bytes & 15) != 0) {
     for (int64_t i = lane * 2; i < head; i += lanes * 2) *reinterpret_cast<uint16_t *>(p + i) = 0;
     for (int64_t i = head + words * 16 + lane * 2; i < bytes; i += lanes * 2)
