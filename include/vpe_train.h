@@ -63,7 +63,7 @@ vpe_status vpe_embed_grad_workspace(int64_t n, int64_t shard_rows, int64_t dim, 
  *              be shared by calls that may run at the same time.
  * n == 0 writes zeros (accumulate == 0) or does nothing.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (n < 0 or
- * >= 2^31, dim < 1, shard_rows < 1 or >= 2^31, a tensor too large),
+ * >= 2^31, dim < 1 or > 2^20, shard_rows < 1 or >= 2^31, a tensor too large),
  * VPE_ERR_RANGE (vocab_start < 0 or vocab_start + shard_rows past INT64_MAX,
  * scale not finite), VPE_ERR_WORKSPACE.
  */
@@ -170,12 +170,12 @@ vpe_status vpe_distill_loss(const float *const *shard_lse, const float *const *s
  * grad_logits  device, row-major with row stride ld_grad elements, of `dt`:
  *              only columns [grad_col_offset, grad_col_offset + shard_rows) of
  *              rows [0, m) are written.  May be the logits themselves (the
- *              same pointer, stride and offset); any other overlap is not
- *              allowed.
+ *              same columns of the same rows), or other columns of their
+ *              buffer; any other overlap is refused.
  * The rest as vpe_distill_shard.  m == 0 is a no-op.
  * Errors: as vpe_distill_shard where they apply; VPE_ERR_RANGE also for the
- * columns of grad_logits, and for the logits' own pointer with another stride
- * or offset.
+ * columns of grad_logits, and where these overlap the logits' without being
+ * the same.
  */
 vpe_status vpe_distill_grad(const void *logits, int64_t ld, int64_t col_offset, int64_t m,
                             int64_t shard_rows, vpe_dtype dt, int64_t vocab_start, int64_t vocab,

@@ -85,7 +85,7 @@ def test_embed_grad_validation():
     for bad in (dict(dt=2), dict(gdt=-1), dict(itype=2)):
         assert call(**bad) == vpe.VPE_ERR_DTYPE, bad
     for bad in (dict(n=-1), dict(n=2 ** 31), dict(dim=0), dict(rows=0), dict(rows=2 ** 31),
-                dict(dim=2 ** 38), dict(bytes=-1)):
+                dict(dim=2 ** 20 + 1), dict(rows=2 ** 30, dim=2 ** 10), dict(bytes=-1)):
         assert call(**bad) == vpe.VPE_ERR_SHAPE, bad
     for bad in (dict(start=-1), dict(start=2 ** 63 - 100), dict(scale=-INF), dict(scale=NAN)):
         assert call(**bad) == vpe.VPE_ERR_RANGE, bad
@@ -105,7 +105,7 @@ def test_embed_grad_workspace():
     f = lib.vpe_embed_grad_workspace
     assert f(10, 10, 10, None) == vpe.VPE_ERR_NULL
     for bad in ((-1, 10, 10), (2 ** 31, 10, 10), (10, 0, 10), (10, 2 ** 31, 10), (10, 10, 0),
-                (10, 10, 2 ** 39)):
+                (10, 10, 2 ** 20 + 1), (2 ** 30, 10, 2 ** 10)):
         assert f(*bad, ctypes.byref(b)) == vpe.VPE_ERR_SHAPE, bad
     last = 0
     for n in [*range(0, 70), *range(4000, 140000, 997), 10 ** 6, 2 * 10 ** 8]:
@@ -194,7 +194,11 @@ def test_distill_grad_validation():
     for bad in (dict(lse=FAKE + 2), dict(go=FAKE + 1), dict(dz=FAR + 1)):
         assert call(**bad) == vpe.VPE_ERR_ALIGN, bad
     for bad in (dict(ld_grad=999), dict(gcol=1), dict(gcol=-1),
-                dict(dz=FAKE, ld_grad=1001), dict(dz=FAKE, ld_grad=1001, gcol=1)):
+                dict(dz=FAKE, ld_grad=1001), dict(dz=FAKE, ld_grad=1001, gcol=1),
+                dict(dz=FAKE + 2), dict(dz=FAKE - 2), dict(dz=FAKE + 2000),
+                dict(dz=FAKE + 2 * 3999), dict(dz=FAKE, ld=3000, ld_grad=3000, gcol=999),
+                dict(dz=FAKE, ld=3000, ld_grad=3000, col=2000, gcol=1001),
+                dict(dz=FAKE - 6000, ld=3000, ld_grad=3000, gcol=500)):
         assert call(**bad) == vpe.VPE_ERR_RANGE, bad
     assert call(m=0, z=None, dz=None) == vpe.VPE_OK
 

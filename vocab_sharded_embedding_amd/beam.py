@@ -37,6 +37,7 @@ def vpe_beam_select(logits, lse, scores, beams: int, picks: int, vocab_start: in
     row, the log-sum-exp over the whole vocabulary and the beam's accumulated
     log-probability.
     """
+    beams, picks = int(beams), int(picks)
     m, ld, rows = logits_shard("logits", logits, shard_rows, col_offset)
     if beams < 1 or m % beams != 0:
         raise ValueError("logits must have `beams` rows per sequence")
@@ -106,6 +107,6 @@ def vpe_beam_reorder(state, parents, beams: int, dim: int = 0, out=None):
         raise ValueError(f"parents must be on the state's device, got {parents.device}")
     row_bytes = math.prod(shape[dim + 1:]) * state.element_size()
     if row_bytes != 0:
-        enqueue("vpe_beam_reorder", index, state.data_ptr(), math.prod(shape[:dim]), n, beams,
-                row_bytes, parents.data_ptr(), ld, beams_out, out.data_ptr())
+        enqueue("vpe_beam_reorder", index, state.data_ptr(), math.prod(shape[:dim]), n,
+                int(beams), row_bytes, parents.data_ptr(), ld, beams_out, out.data_ptr())
     return out

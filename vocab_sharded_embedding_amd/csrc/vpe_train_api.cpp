@@ -28,8 +28,8 @@ constexpr int64_t kMaxElems = int64_t(1) << 39;
 constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
 
 bool embed_grad_shape_ok(int64_t n, int64_t shard_rows, int64_t dim) {
-  return n >= 0 && n <= kMax31 && dim >= 1 && shard_rows >= 1 && shard_rows <= kMax31 &&
-         n <= kMaxElems / dim && shard_rows <= kMaxElems / dim;
+  return n >= 0 && n <= kMax31 && dim >= 1 && dim <= (int64_t(1) << 20) && shard_rows >= 1 &&
+         shard_rows <= kMax31 && n <= kMaxElems / dim && shard_rows <= kMaxElems / dim;
 }
 
 // What vpe_distill_shard, _loss and _grad check alike.
@@ -53,6 +53,22 @@ vpe_status check_shard(int64_t ld, int64_t col_offset, int64_t m, int64_t shard_
   if (col_offset < 0 || ld < 1 || shard_rows > ld - col_offset) return VPE_ERR_RANGE;
   if (m > kMaxElems / ld) return VPE_ERR_SHAPE;
   return VPE_OK;
+}
+
+// Whether rows of `cols` elements at a (stride ld_a) and at b (stride ld_b) share
+// bytes, unless they are the same rows.
+bool partly_overlap(const char *a, int64_t ld_a, const char *b, int64_t ld_b, int64_t m,
+                    int64_t cols, int64_t size) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + static_cast<uintptr_t>(((m - 1) * ld_a + cols) * size);
+  const uintptr_t b1 = b0 + static_cast<uintptr_t>(((m - 1) * ld_b + cols) * size);
+  if (b1 <= a0 || a1 <= b0) return false;
+  if (ld_a != ld_b) return true;
+  // one stride: other columns of the same rows are apart
+  const uintptr_t row = static_cast<uintptr_t>(ld_a * size), width = static_cast<uintptr_t>(cols * size);
+  const uintptr_t off = b0 >= a0 ? (b0 - a0) % row : (row - (a0 - b0) % row) % row;
+  if (a0 == b0) return false;
+  return off < width || off > row - width;
 }
 
 vpe_status check_teacher_pointers(const void *ids, vpe_itype itype, const void *teacher,
@@ -208,9 +224,11 @@ vpe_status vpe_distill_grad(const void *logits, int64_t ld, int64_t col_offset, 
   if (!aligned(logits, dtype_bytes(dt)) || !aligned(grad_logits, dtype_bytes(dt)) ||
       !aligned(lse, 4) || !aligned(grad_loss, 4))
     return VPE_ERR_ALIGN;
-  if (logits == grad_logits && (ld != ld_grad || col_offset != grad_col_offset))
+  const int64_t size = dtype_bytes(dt);
+  char *base = static_cast<char *>(grad_logits) + grad_col_offset * size;
+  if (partly_overlap(static_cast<const char *>(logits) + col_offset * size, ld, base, ld_grad, m,
+                     shard_rows, size))
     return VPE_ERR_RANGE;
-  char *base = static_cast<char *>(grad_logits) + grad_col_offset * dtype_bytes(dt);
   return launched(vpe::launch_distill_grad(
       shard_of(logits, ld, col_offset, m, shard_rows, dt, vocab_start),
       teacher_of(teacher_ids, itype, teacher, tdt, k, teacher_lse, vocab, temperature), lse,

@@ -123,10 +123,10 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
         if grad_weight.shape != (shard_rows, dim):
             raise ValueError("grad_weight must be [shard_rows, dim]")
     if workspace is None:
-        workspace = new_workspace(vpe_embed_grad_workspace(n, shard_rows, dim), grad_out.device)
+        workspace = new_workspace(vpe_embed_grad_workspace(n, int(shard_rows), dim), grad_out.device)
     index = placed("ids grad_out grad_weight workspace", ids, grad_out, grad_weight, workspace)
     enqueue("vpe_embed_grad", index, ids.data_ptr(), itype_code(ids), n, grad_out.data_ptr(),
-            dtype_code(grad_out), dim, int(vocab_start), shard_rows, scale,
+            dtype_code(grad_out), dim, int(vocab_start), int(shard_rows), scale,
             grad_weight.data_ptr(), dtype_code(grad_weight), bool(accumulate),
             workspace.data_ptr(), nbytes(workspace))
     return grad_weight
@@ -157,7 +157,7 @@ def logits_shard(name: str, logits, shard_rows: Optional[int], col_offset: int):
     if logits.dim() != 2:
         raise ValueError(f"{name} must be [m, ld]")
     m, ld = logits.shape
-    return m, ld, ld - col_offset if shard_rows is None else shard_rows
+    return m, ld, int(ld - col_offset if shard_rows is None else shard_rows)
 
 
 @functools.lru_cache(maxsize=256)
