@@ -589,7 +589,7 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
   const int64_t i0 = wave * share, i1 = i0 + share <= more ? i0 + share : more + 1;
   f32x4 sum = f32x4(0.f);
   if (col < a.dim) {
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t i = i0; i < i1; ++i) {
       const int64_t slot = i == 0 ? 2 * c + (whole_chunk ? 0 : 1) : 2 * (c + i);
       sum += *reinterpret_cast<const f32x4 *>(a.partial + slot * a.partial_ld + col);
@@ -671,36 +671,41 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
     SortPass ps{n, kSortTile * ((n + unit - 1) / unit), 0, 0, bits};
     ps.blocks = static_cast<unsigned>((n + ps.tile - 1) / ps.tile);
     uint8_t *flags = a.accumulate ? nullptr : reinterpret_cast<uint8_t *>(ws + l.flags);
-    zero.flags = flags;
-    // the flags are complete after the first pass: each later launch of the
-    // sort clears an equal part of half the rows without an id
-    const int riders = 2 * passes - 2;
-    auto ride = [&]() {
+    // The flags are complete after the first pass: each later launch of the
+    // sort clears an equal part of half the rows without an id.  The first two
+    // clear what fits their time, about 24 MB, with or without one.
+    auto ride = [&](int64_t ride_rows, const uint8_t *ride_flags) {
+      zero.flags = ride_flags;
       zero.row0 = zero.row1;
-      zero.row1 = std::min(zero_to, zero.row0 + (zero_to / 2 + riders - 1) / riders);
+      zero.row1 = std::min(zero_to, zero.row0 + ride_rows);
       zero.blocks = zero_blocks(zero.row1 - zero.row0, zero.row_bytes);
     };
+    const int64_t early = std::min(zero_to / 16, (int64_t(24) << 20) / zero.row_bytes);
+    const int64_t later = passes > 1 ? (zero_to / 2 + 2 * passes - 3) / (2 * passes - 2) : 0;
     for (int pass = 0; pass < passes; ++pass) {
       last = pass & 1;
       ps.shift = pass * bits;
       if (pass == 0) {
         SortItems<true, IdT> it{ids, nullptr, nullptr, start, urows};
-        hipLaunchKernelGGL((sort_counts<true, IdT>), dim3(ps.blocks), dim3(kSortThreads), 0, st,
-                           it, ps, count, hist, flags, zero);
-        hipLaunchKernelGGL((sort_scatter<true, IdT>), dim3(ps.blocks), dim3(kSortThreads), 0, st,
-                           it, ps, count, hist, key[0], pos[0], flags, zero);
+        ride(early, nullptr);
+        hipLaunchKernelGGL((sort_counts<true, IdT>), dim3(ps.blocks + zero.blocks),
+                           dim3(kSortThreads), 0, st, it, ps, count, hist, flags, zero);
+        ride(early, nullptr);
+        hipLaunchKernelGGL((sort_scatter<true, IdT>), dim3(ps.blocks + zero.blocks),
+                           dim3(kSortThreads), 0, st, it, ps, count, hist, key[0], pos[0], flags,
+                           zero);
       } else {
         SortItems<false, IdT> it{nullptr, key[1 - last], pos[1 - last], start, urows};
-        ride();
+        ride(later, flags);
         hipLaunchKernelGGL((sort_counts<false, IdT>), dim3(ps.blocks + zero.blocks),
                            dim3(kSortThreads), 0, st, it, ps, count, hist, flags, zero);
-        ride();
+        ride(later, flags);
         hipLaunchKernelGGL((sort_scatter<false, IdT>), dim3(ps.blocks + zero.blocks),
                            dim3(kSortThreads), 0, st, it, ps, count, hist, key[last], pos[last],
                            flags, zero);
       }
     }
-    zero.row0 = zero.row1, zero.row1 = zero_to;
+    zero.flags = flags, zero.row0 = zero.row1, zero.row1 = zero_to;
     zero.blocks = zero_blocks(zero.row1 - zero.row0, zero.row_bytes, 65536.0);
   }
   a.key = key[last], a.pos = pos[last], a.count = count;
