@@ -8,8 +8,8 @@
  * caller's, nothing is allocated, kept or synchronised, arguments are checked
  * on the host before anything is enqueued on `stream`, and values in device
  * memory (ids, teacher entries) are not checked but have defined results.
- * Every sum is taken in fp32 in an order fixed by the arguments: no atomics on
- * values, so the same inputs give the same bits.
+ * Every sum is taken in fp32 or more, in an order fixed by the arguments: no
+ * atomics on values, so the same inputs give the same bits.
  */
 #ifndef VPE_TRAIN_H
 #define VPE_TRAIN_H
@@ -88,12 +88,15 @@ vpe_status vpe_embed_grad(const void *ids, vpe_itype itype, int64_t n, const voi
  * An id that occurs twice in a row counts twice.  An entry with p_e = 0 (t_e
  * = -inf) counts for nothing.  A row without entries that count has loss 0
  * and gradient 0, whatever its logits hold: that is how padded rows are
- * marked.  Elsewhere infinities and NaN follow the formulas.
+ * marked.  Elsewhere infinities and NaN follow the formulas (the log-sum-exp
+ * of a row that holds +inf is +inf).  The gradient has the resolution of lse in
+ * fp32: a row whose logits are all a mask's lowest value is best marked as
+ * padding.
  *
  * Over vocabulary shards: vpe_distill_shard per rank (one pass over its
  * logits), the ranks exchange two floats per row, vpe_distill_loss, and
- * vpe_distill_grad per rank.  Exponentials, sums and logarithms are taken in
- * fp32.
+ * vpe_distill_grad per rank.  Exponentials are taken in fp32, sums and
+ * logarithms in fp32 or more.
  */
 
 /* Most entries per row, and most rows, of one distillation call. */
@@ -129,7 +132,7 @@ vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes);
  * > VPE_MAX_DISTILL_ROWS, shard_rows < 1 or >= 2^31, k outside [1,
  * VPE_MAX_TEACHER_ENTRIES], vocab < 1, a tensor too large), VPE_ERR_RANGE (the
  * shard does not lie in [0, vocab), the columns do not fit ld, temperature not
- * a finite positive number), VPE_ERR_WORKSPACE.
+ * positive or past 2^100, or its reciprocal infinite), VPE_ERR_WORKSPACE.
  */
 vpe_status vpe_distill_shard(const void *logits, int64_t ld, int64_t col_offset, int64_t m,
                              int64_t shard_rows, vpe_dtype dt, int64_t vocab_start, int64_t vocab,

@@ -251,6 +251,54 @@ def test_infinite_and_nan_values_follow_the_formulas():
     assert bool(torch.isnan(grad[1]).all()) and bool(torch.isfinite(grad[3]).all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("temp", [1.0, 2.0])
+def test_shards_that_hold_the_lowest_value_only(temp, dtype):
+    # row 0: all of one shard of two; row 1: everything, where 64 bits give a
+    # log-sum-exp whose nearest fp32 value is lowest / T, and exp(z / T - that) = 1
+    m, v, k = 3, 6000, 4
+    low = torch.finfo(dtype).min
+    z = torch.randn(m, v, generator=_gen(9), device="cuda").to(dtype)
+    z[0, v // 2:] = low
+    z[1] = low
+    ids = torch.tensor([[5, 17, 100, 1000]] * m, device="cuda")
+    t = torch.zeros(m, k, device="cuda")
+    parts = _shards(z, ids, t, None, temp, 2)
+    loss, full = vpe.vpe_distill_loss([a for a, _ in parts], [b for _, b in parts], ids, t, v,
+                                      temperature=temp)
+    assert float(parts[1][0][0]) == low / temp and float(parts[0][0][1]) == low / temp
+    _, rlse, rgrad, _ = _definition(z, ids, t, temp, lse=full)
+    assert float(full[1]) == low / temp and bool(torch.isfinite(loss).all())
+    grad = vpe.vpe_distill_grad(z, full, torch.ones(m, device="cuda"), ids, t, 0, v,
+                                temperature=temp)
+    # q and p are at most 1 here; |z / T| and |lse| at most 16 where they enter the bound
+    bound = (6 * 32 + 16 + 32 + 8) * U + torch.finfo(dtype).eps / 2 * rgrad.abs()
+    assert bool(((grad.double() - rgrad).abs() <= bound).all())
+    assert bool((grad[0, v // 2:] == 0).all())
+
+
+def test_rows_that_hold_plus_infinity():
+    m, v, k = 3, 9000, 2
+    z = torch.randn(m, v, generator=_gen(10), device="cuda")
+    z[0, 8998] = INF    # not the teacher's: excluded by the student for good
+    z[1, [7, 6000]] = INF
+    ids = torch.tensor([[1, 7]] * m, device="cuda")
+    t = torch.zeros(m, k, device="cuda")
+    for tp in (1, 2):
+        parts = _shards(z, ids, t, None, 1.5, tp)
+        loss, full = vpe.vpe_distill_loss([a for a, _ in parts], [b for _, b in parts], ids, t, v,
+                                          temperature=1.5)
+        assert full.tolist()[:2] == [INF, INF] and bool(torch.isfinite(full[2]))
+        assert float(loss[0]) == INF and bool(torch.isnan(loss[1]))  # inf - inf
+        grad = vpe.vpe_distill_grad(z, full, torch.ones(m, device="cuda"), ids, t, 0, v,
+                                    temperature=1.5)
+        nan = torch.zeros_like(z, dtype=torch.bool)
+        nan[0, 8998] = nan[1, 7] = nan[1, 6000] = True
+        assert torch.equal(torch.isnan(grad), nan)
+        p = (grad[0] * 1.5)[[1, 7]] + 0.5
+        assert bool((p.abs() <= 8 * U).all())
+
+
 def test_shard_lse_of_the_lm_head_can_be_used():
     g = _gen(21)
     m, v, d, k, tp = 17, 512, 64, 9, 2

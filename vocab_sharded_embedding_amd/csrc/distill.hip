@@ -4,10 +4,10 @@
 // All of it is bound by HBM: the statistics read a rank's logits once, the
 // gradient reads them once and writes once; a row's teacher entries (at most
 // 1024) are small beside its columns.
-//  - Statistics: one wave per 256 vectors of a row, in base 2 (x = z log2(e) /
-//    T): their maximum first, then one fma and one v_exp_f32 per logit, so no
-//    sum is ever rescaled; a second kernel joins a row's (maximum, sum) pairs
-//    and takes the products with the teacher's entries, one wave per row.
+//  - Statistics: one wave per 256 vectors of a row: their maximum first, then
+//    2^((z - maximum) log2(e) / T), one v_exp_f32 per logit, so no sum is ever
+//    rescaled; a second kernel joins a row's (maximum, sum) pairs and takes the
+//    products with the teacher's entries, one wave per row.
 //  - Gradient: P exp(z/T - lse) for every column, and for the entries' columns
 //    the entries' probabilities taken off.  Those columns are read before the
 //    dense pass (the gradient may overwrite the logits) and written again
@@ -30,8 +30,7 @@ constexpr int kBlock = 256;
 constexpr int kWaves = kBlock / 64;
 constexpr int kMaxEntries = 1024;
 constexpr int kEntriesPerThread = kMaxEntries / kBlock;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLn2 = 0.6931471805599453;
+constexpr float kMostFloat = 3.4028234663852886e38f;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_huge_valf(); }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -69,9 +68,7 @@ struct TeacherArgs {
   int64_t vocab;
   float temperature;
   float inv_t;   // 1 / T
-  float to_log2; // log2(e) / T, rounded; ...
-  double unit;   // ... and what a power 2^x of it stands for: ln(2) times the
-                 // exact log2(e) / T over the rounded one
+  float to_log2; // log2(e) / T
 };
 
 // Entry e of the row: its scaled logit t_e / T, or -inf (p_e = 0) for padding.
@@ -141,29 +138,29 @@ struct Row : Vec<BF16, BF16 ? 8 : 4> {
   static constexpr int kEpv = BF16 ? 8 : 4;
 };
 
-// log2 of a sum of powers of two kept as (largest exponent, sum of
-// 2^(x - largest)).
+// The sum of exp(z / T) over some columns as (their largest logit, the sum of
+// exp((z - largest) / T)).  The difference comes before the factor: multiples
+// of a mask's lowest value would be infinite.
 struct Pair {
   float mx, sum;
 };
-__device__ __forceinline__ Pair join(Pair a, Pair b) {
+__device__ __forceinline__ Pair join(Pair a, Pair b, float to_log2) {
   const float m = fmaxf(a.mx, b.mx);
-  // (-inf) - (-inf) would be NaN: an empty side adds nothing
-  const float sa = a.mx == neg_inf() ? a.sum : a.sum * exp2_fast(a.mx - m);
-  const float sb = b.mx == neg_inf() ? b.sum : b.sum * exp2_fast(b.mx - m);
+  // (of equal infinities the difference would be NaN)
+  const float sa = a.mx == m ? a.sum : a.sum * exp2_fast((a.mx - m) * to_log2);
+  const float sb = b.mx == m ? b.sum : b.sum * exp2_fast((b.mx - m) * to_log2);
   return Pair{m, sa + sb};
 }
-// In 64 bits (one value per row).  The largest exponent carries the rounding of
-// to_log2, which `unit` takes back: what remains is that rounding times the
-// others' distance from the largest.
-__device__ __forceinline__ float natural_log(Pair p, double unit) {
-  return static_cast<float>(static_cast<double>(p.mx) * unit +
-                            log2(static_cast<double>(p.sum)) * kLn2);
+// In 64 bits (one value per row).
+__device__ __forceinline__ float natural_log(Pair p, float temperature) {
+  return static_cast<float>(static_cast<double>(p.mx) / static_cast<double>(temperature) +
+                            log(static_cast<double>(p.sum)));
 }
 
-__device__ __forceinline__ Pair wave_join(Pair p) {
+__device__ __forceinline__ Pair wave_join(Pair p, float to_log2) {
 #pragma unroll
-  for (int d = 32; d > 0; d /= 2) p = join(p, Pair{__shfl_xor(p.mx, d), __shfl_xor(p.sum, d)});
+  for (int d = 32; d > 0; d /= 2)
+    p = join(p, Pair{__shfl_xor(p.mx, d), __shfl_xor(p.sum, d)}, to_log2);
   return p;
 }
 
@@ -214,20 +211,20 @@ __global__ __launch_bounds__(kBlock) void distill_pairs(ShardArgs z, float to_lo
 #pragma nounroll
     for (int64_t i = tail; i < z.cols; ++i) mx = fmaxf(mx, load_one<BF16>(p, i));
   }
-  mx = wave_max(mx) * to_log2;
-  const float off = mx == neg_inf() ? 0.f : mx;
+  mx = wave_max(mx);
+  const float off = __builtin_isinf(mx) ? 0.f : mx;  // +inf: an infinite sum
   float sum = 0.f;
 #pragma unroll
   for (int u = 0; u < kPairVecs; ++u) {
     float v[kEpv];
     Vec<BF16, kEpv>::widen(raw[u], v);
 #pragma unroll
-    for (int e = 0; e < kEpv; ++e) sum += exp2_fast(fmaf(v[e], to_log2, -off));
+    for (int e = 0; e < kEpv; ++e) sum += exp2_fast((v[e] - off) * to_log2);
   }
   if (ragged) {
 #pragma nounroll
     for (int64_t i = tail; i < z.cols; ++i)
-      sum += exp2_fast(fmaf(load_one<BF16>(p, i), to_log2, -off));
+      sum += exp2_fast((load_one<BF16>(p, i) - off) * to_log2);
   }
   sum = wave_sum(sum);
   if (lane == 0) pairs[row * z.slices + s] = Pair{mx, sum};
@@ -270,9 +267,10 @@ __global__ __launch_bounds__(kBlock) void distill_rows(ShardArgs z, TeacherArgs 
   }
   if (shard_lse != nullptr) {
     Pair a{neg_inf(), 0.f};
-    for (int s = lane; s < z.slices; s += 64) a = join(a, pairs[row * z.slices + s]);
-    a = wave_join(a);
-    if (lane == 0) shard_lse[row] = natural_log(a, t.unit);
+    for (int s = lane; s < z.slices; s += 64)
+      a = join(a, pairs[row * z.slices + s], t.to_log2);
+    a = wave_join(a, t.to_log2);
+    if (lane == 0) shard_lse[row] = natural_log(a, t.temperature);
   }
   dot = wave_sum(dot);
   total = t.lse != nullptr ? 1.0 : wave_sum(total);
@@ -301,7 +299,7 @@ __global__ __launch_bounds__(kBlock) void distill_loss_rows(Parts parts, int n_p
     dot += static_cast<double>(parts.dot[r][row]);
     top = fmaxf(top, parts.lse[r][row]);
   }
-  const float shift = top == neg_inf() ? 0.f : top;
+  const float shift = __builtin_isinf(top) ? 0.f : top;
   double total = 0.0;
   for (int r = 0; r < n_parts; ++r)
     total += exp(static_cast<double>(parts.lse[r][row]) - static_cast<double>(shift));
@@ -406,8 +404,11 @@ __global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, Teacher
     }
   }
 
+  // exp(z / T - lse) = 2^((z - off) c): as in the statistics, the difference
+  // comes first (a finite lse times T stays finite)
   const float c = t.to_log2;
-  const float off = -lse[row] * kLog2e;
+  float off = lse[row] * t.temperature;
+  if (__builtin_isinf(off) && !__builtin_isinf(lse[row])) off = copysignf(kMostFloat, off);
   const float a = g * mass;
   for (int64_t i = tid; i < nv; i += kBlock * kUnroll) {
     u32x4 r[kUnroll];
@@ -424,26 +425,25 @@ __global__ __launch_bounds__(kBlock) void distill_grad_rows(ShardArgs z, Teacher
       float v[kEpv];
       Vec<BF16, kEpv>::widen(r[u], v);
 #pragma unroll
-      for (int e = 0; e < kEpv; ++e) v[e] = a * exp2_fast(fmaf(v[e], c, off));
+      for (int e = 0; e < kEpv; ++e) v[e] = a * exp2_fast((v[e] - off) * c);
       if (j < nv)
         __builtin_nontemporal_store(Vec<BF16, kEpv>::narrow(v),
                                     reinterpret_cast<typename R::loose *>(dst) + j);
     }
   }
   for (int64_t i = nv * kEpv + tid; i < n; i += kBlock)
-    store_one<BF16>(dst, i, a * exp2_fast(fmaf(load_one<BF16>(src, i), c, off)));
+    store_one<BF16>(dst, i, a * exp2_fast((load_one<BF16>(src, i) - off) * c));
   __syncthreads();  // the dense pass's stores come before the entries'
 #pragma unroll
   for (int i = 0; i < kEntriesPerThread; ++i)
     if (col[i] >= 0)
-      store_one<BF16>(dst, col[i], g * (mass * exp2_fast(fmaf(zk[i], c, off)) - p[i]));
+      store_one<BF16>(dst, col[i], g * (mass * exp2_fast((zk[i] - off) * c) - p[i]));
 }
 
 TeacherArgs args_of(const Teacher &t) {
-  const double c = 1.4426950408889634 / static_cast<double>(t.temperature);
-  const float to_log2 = static_cast<float>(c);
-  return TeacherArgs{t.ids, t.logits, t.lse, t.itype, t.dtype, t.k, t.vocab, t.temperature,
-                     1.f / t.temperature, to_log2, kLn2 * (c / static_cast<double>(to_log2))};
+  return TeacherArgs{
+      t.ids, t.logits, t.lse, t.itype, t.dtype, t.k, t.vocab, t.temperature, 1.f / t.temperature,
+      static_cast<float>(1.4426950408889634 / static_cast<double>(t.temperature))};
 }
 
 ShardArgs args_of(const LogitsShard &z, int64_t slice) {

@@ -38,8 +38,8 @@ vpe_status check_teacher(int64_t m, int64_t vocab, float temperature, vpe_itype 
   if (!known_dtype(tdt) || !known_itype(itype)) return VPE_ERR_DTYPE;
   if (m < 0 || m > VPE_MAX_DISTILL_ROWS || k < 1 || k > VPE_MAX_TEACHER_ENTRIES || vocab < 1)
     return VPE_ERR_SHAPE;
-  // 1 / temperature has to be finite and non-zero as well
-  if (!(temperature > 0.f) || !isfinite(temperature) || !isnormal(1.f / temperature))
+  // 1 / temperature has to be finite as well, and any log-sum-exp times it
+  if (!(temperature > 0.f) || temperature > 0x1p100f || !isnormal(1.f / temperature))
     return VPE_ERR_RANGE;
   return VPE_OK;
 }
