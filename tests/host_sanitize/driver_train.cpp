@@ -106,6 +106,11 @@ int main() {
                           f, f, static_cast<char *>(p) + 160, 20, 0, nullptr) == VPE_ERR_RANGE);
   EXPECT(vpe_distill_grad(p, 20, 0, 3, 10, VPE_F32, 0, 10, 1.f, p, VPE_I64, p, VPE_F32, 2, nullptr,
                           f, f, static_cast<char *>(p) + 240, 20, 0, nullptr) == VPE_OK);
+  // a single row in place, whatever the strides; past the largest temperature
+  EXPECT(vpe_distill_grad(p, 20, 0, 1, 10, VPE_F32, 0, 10, 1.f, p, VPE_I64, p, VPE_F32, 2, nullptr,
+                          f, f, p, 10, 0, nullptr) == VPE_OK);
+  EXPECT(vpe_distill_grad(p, 20, 0, 1, 10, VPE_F32, 0, 10, 0x1.8p100f, p, VPE_I64, p, VPE_F32, 2,
+                          nullptr, f, f, p, 10, 0, nullptr) == VPE_ERR_RANGE);
   const float *two[2] = {f, f};
   EXPECT(vpe_distill_loss(two, two, 2, 4, 10, 1.f, p, VPE_I32, p, VPE_BF16, 3, nullptr, f, f,
                           nullptr) == VPE_OK);

@@ -63,6 +63,7 @@ bool partly_overlap(const char *a, int64_t ld_a, const char *b, int64_t ld_b, in
   const uintptr_t a1 = a0 + static_cast<uintptr_t>(((m - 1) * ld_a + cols) * size);
   const uintptr_t b1 = b0 + static_cast<uintptr_t>(((m - 1) * ld_b + cols) * size);
   if (b1 <= a0 || a1 <= b0) return false;
+  if (a0 == b0 && m == 1) return false;
   if (ld_a != ld_b) return true;
   // one stride: other columns of the same rows are apart
   const uintptr_t row = static_cast<uintptr_t>(ld_a * size), width = static_cast<uintptr_t>(cols * size);
