@@ -181,10 +181,10 @@ struct ZeroRows {
 };
 
 // `block` of z.blocks workgroups of `threads` threads.  Plain stores where the
-// whole shard is cleared beside one sorting workgroup (8192 ids, 156 MB: 35 us
+// whole shard is cleared beside one sorting workgroup (8192 ids, 156 MB: 30 us
 // against 39 with non-temporal ones), non-temporal ones (NT) where many sorted
 // rows are read meanwhile and after, which plain ones push out of the caches
-// (65536 ids, 622 MB: 170 us against 184).
+// (65536 ids, 622 MB: 166 us against 186).
 template <bool NT>
 __device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int threads) {
   const int64_t share = (z.row1 - z.row0 + z.blocks - 1) / z.blocks;
@@ -558,10 +558,12 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
 
 // One workgroup per chunk and block of 256 columns: the run that leaves the
 // chunk having begun in it is joined from its partial sums, a quarter of them
-// per wave, in order.
+// per wave, in order.  Workgroups after them write zero rows.
 template <bool OUT16>
-__global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int col_blocks) {
+__global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int col_blocks,
+                                                   unsigned join_blocks, ZeroRows zero) {
   __shared__ f32x4 part[kWaves][64];
+  if (blockIdx.x >= join_blocks) return zero_rows<true>(zero, blockIdx.x - join_blocks, kBlock);
   const int lane = threadIdx.x & 63, wave = wave_in_block();
   const unsigned rel = blockIdx.x / static_cast<unsigned>(col_blocks);
   const int64_t c = chunk0 + rel;
@@ -612,7 +614,7 @@ unsigned zero_blocks(int64_t rows, int64_t row_bytes, double span = 262144.0) {
 }
 
 template <bool IN16, bool OUT16>
-int launch_sums(GradArgs a, int64_t n, ZeroRows zero, hipStream_t st) {
+int launch_sums(GradArgs a, int64_t n, ZeroRows zero, ZeroRows join_zero, hipStream_t st) {
   // 16-byte vectors on the wider side
   constexpr int kEpv = IN16 && OUT16 ? 8 : 4;
   const int64_t chunks = (n + a.chunk - 1) / a.chunk;
@@ -630,11 +632,12 @@ int launch_sums(GradArgs a, int64_t n, ZeroRows zero, hipStream_t st) {
   if (chunks > 1) {
     const int64_t join_blocks = (a.dim + 255) / 256;
     const int64_t join_step = std::max<int64_t>(1, (int64_t(1) << 22) / join_blocks);
-    for (int64_t c = 0; c < chunks - 1; c += join_step)
-      hipLaunchKernelGGL(
-          (grad_join<OUT16>),
-          dim3(static_cast<unsigned>(std::min(join_step, chunks - 1 - c) * join_blocks)),
-          dim3(kBlock), 0, st, a, c, static_cast<int>(join_blocks));
+    for (int64_t c = 0; c < chunks - 1; c += join_step) {
+      const unsigned jb = static_cast<unsigned>(std::min(join_step, chunks - 1 - c) * join_blocks);
+      hipLaunchKernelGGL((grad_join<OUT16>), dim3(jb + join_zero.blocks), dim3(kBlock), 0, st, a, c,
+                         static_cast<int>(join_blocks), jb, join_zero);
+      join_zero.blocks = 0;
+    }
   }
   return static_cast<int>(hipGetLastError());
 }
@@ -655,6 +658,7 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
   const uint64_t urows = static_cast<uint64_t>(rows);
   const int64_t zero_to = a.accumulate ? 0 : rows;
   ZeroRows zero{a.dw, a.dim * (gdtype == 1 ? 2 : 4), 0, 0, nullptr, 0};
+  ZeroRows join_zero = zero;
   int last = 0;
   if (n <= kGradOneBlockIds) {
     // few rows have an id: all are cleared while they are sorted, and those
@@ -705,18 +709,27 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
                            flags, zero);
       }
     }
-    zero.flags = flags, zero.row0 = zero.row1, zero.row1 = zero_to;
-    zero.blocks = zero_blocks(zero.row1 - zero.row0, zero.row_bytes, 65536.0);
+    // The rest beside the sums; the last 64 MB beside their join, which waits
+    // for the pieces of the longest runs one after the other (65536 Zipf ids:
+    // 162 us, 165 with none there).
+    const int64_t rest = zero_to - zero.row1;
+    const int64_t sums_to = zero_to - std::min(rest / 2, (int64_t(64) << 20) / zero.row_bytes);
+    auto beside = [&](int64_t row0, int64_t row1) {
+      return ZeroRows{zero.dw, zero.row_bytes, row0, row1, flags,
+                      zero_blocks(row1 - row0, zero.row_bytes, 65536.0)};
+    };
+    join_zero = beside(sums_to, zero_to);
+    zero = beside(zero.row1, sums_to);
   }
   a.key = key[last], a.pos = pos[last], a.count = count;
   a.partial = reinterpret_cast<float *>(ws + l.partial);
   a.partial_ld = l.partial_ld;
   a.chunk = static_cast<int>(l.chunk);
   if (dtype == 1)
-    return gdtype == 1 ? launch_sums<true, true>(a, n, zero, st)
-                       : launch_sums<true, false>(a, n, zero, st);
-  return gdtype == 1 ? launch_sums<false, true>(a, n, zero, st)
-                     : launch_sums<false, false>(a, n, zero, st);
+    return gdtype == 1 ? launch_sums<true, true>(a, n, zero, join_zero, st)
+                       : launch_sums<true, false>(a, n, zero, join_zero, st);
+  return gdtype == 1 ? launch_sums<false, true>(a, n, zero, join_zero, st)
+                     : launch_sums<false, false>(a, n, zero, join_zero, st);
 }
 
 }  // namespace
