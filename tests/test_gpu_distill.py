@@ -146,6 +146,16 @@ def test_loss_and_gradient(m, v, k, tp, temp, tail, dtype):
     _check(z, ids, t, tl, temp, tp, g, k)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,v,k,tp", [(256, 50001, 33, 1), (257, 9001, 7, 1), (3, 70003, 9, 1),
+                                      (3, 140006, 9, 2), (40, 120001, 65, 1), (1, 41000, 2, 1),
+                                      (1, 82000, 2, 1)])
+def test_few_and_many_rows_of_many_slices(m, v, k, tp, dtype):
+    # the statistics take a workgroup per row, or cut few long rows over the chip
+    z, ids, t, tl, g = _case(m + v, m, v, k, dtype, F32, torch.int32, tail=bool(k % 2))
+    _check(z, ids, t, tl, 1.5, tp, g, k)
+
+
 @pytest.mark.parametrize("col,extra", [(0, 5), (1, 0), (3, 2), (8, 8), (13, 1)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_strided_rows_and_untouched_columns(col, extra, dtype):

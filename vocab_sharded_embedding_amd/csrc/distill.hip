@@ -4,10 +4,12 @@
 // All of it is bound by HBM: the statistics read a rank's logits once, the
 // gradient reads them once and writes once; a row's teacher entries (at most
 // 1024) are small beside its columns.
-//  - Statistics: one wave per 256 vectors of a row: their maximum first, then
-//    2^((z - maximum) log2(e) / T), one v_exp_f32 per logit, so no sum is ever
-//    rescaled; a second kernel joins a row's (maximum, sum) pairs and takes the
-//    products with the teacher's entries, one wave per row.
+//  - Statistics: waves take slices of 256 vectors of a row: their maximum first,
+//    then 2^((z - maximum) log2(e) / T), one v_exp_f32 per logit, so no sum is
+//    rescaled inside; the slices' (maximum, sum) pairs are joined, and one wave
+//    per row takes the products with the teacher's entries.  One workgroup per
+//    row does all of it; a few long rows are cut into slices over the chip, and a
+//    second kernel joins their pairs from memory.
 //  - Gradient: P exp(z/T - lse) for every column, and for the entries' columns
 //    the entries' probabilities taken off.  Those columns are read before the
 //    dense pass (the gradient may overwrite the logits) and written again
@@ -175,59 +177,71 @@ struct ShardArgs {
 constexpr int kPairVecs = 4;  // vectors per lane and pair
 constexpr int64_t kRowsPerGrid = 32768;
 
-// One wave per pair of a row (grid: pairs / kWaves, rows): the maximum and the
-// sum of its columns.
+// Slice `s` of the row at p, by one wave: its vectors, -inf where they end.
+template <bool BF16>
+struct Slice {
+  typedef Row<BF16> R;
+  static constexpr int kEpv = R::kEpv, kSize = BF16 ? 2 : 4;
+  u32x4 raw[kPairVecs];
+  __device__ __forceinline__ void load(const ShardArgs &z, const char *p, int64_t s) {
+    const int64_t j0 = s * z.slice + (threadIdx.x & 63) * kEpv;
+#pragma unroll
+    for (int u = 0; u < kPairVecs; ++u) {
+      const int64_t j = j0 + u * (64 * kEpv);
+      raw[u] = BF16 ? u32x4(0xff80ff80u) : u32x4(0xff800000u);  // -inf: adds nothing
+      if (j + kEpv <= z.cols) raw[u] = *reinterpret_cast<const typename R::loose *>(p + j * kSize);
+    }
+  }
+  // The maximum, and the sum with it taken off.
+  __device__ __forceinline__ Pair pair(const ShardArgs &z, const char *p, int64_t s,
+                                       float to_log2) const {
+    // the row's last columns where they do not fill a vector: one lane's
+    const int64_t j0 = s * z.slice + (threadIdx.x & 63) * kEpv, tail = z.cols - z.cols % kEpv;
+    const bool ragged = tail < z.cols && j0 <= tail && (tail - j0) % (64 * kEpv) == 0 &&
+                        tail - j0 < kPairVecs * 64 * kEpv;
+    float mx = neg_inf();
+#pragma unroll
+    for (int u = 0; u < kPairVecs; ++u) {
+      float v[kEpv];
+      Vec<BF16, kEpv>::widen(raw[u], v);
+#pragma unroll
+      for (int e = 0; e < kEpv; ++e) mx = fmaxf(mx, v[e]);
+    }
+    if (ragged) {
+#pragma nounroll
+      for (int64_t i = tail; i < z.cols; ++i) mx = fmaxf(mx, load_one<BF16>(p, i));
+    }
+    mx = wave_max(mx);
+    const float off = __builtin_isinf(mx) ? 0.f : mx;  // +inf: an infinite sum
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < kPairVecs; ++u) {
+      float v[kEpv];
+      Vec<BF16, kEpv>::widen(raw[u], v);
+#pragma unroll
+      for (int e = 0; e < kEpv; ++e) sum += exp2_fast((v[e] - off) * to_log2);
+    }
+    if (ragged) {
+#pragma nounroll
+      for (int64_t i = tail; i < z.cols; ++i)
+        sum += exp2_fast((load_one<BF16>(p, i) - off) * to_log2);
+    }
+    return Pair{mx, wave_sum(sum)};
+  }
+};
+
+// One wave per pair of a row (grid: pairs / kWaves, rows).
 template <bool BF16>
 __global__ __launch_bounds__(kBlock) void distill_pairs(ShardArgs z, float to_log2, int64_t row0,
                                                        Pair *__restrict__ pairs) {
-  typedef Row<BF16> R;
-  constexpr int kEpv = R::kEpv, kSize = BF16 ? 2 : 4;
-  const int lane = threadIdx.x & 63;
   const int64_t row = row0 + blockIdx.y;
   const int64_t s = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
   if (s >= z.slices) return;
   const char *p = z.base + row * z.ld_bytes;
-  const int64_t j0 = s * z.slice + lane * kEpv;
-  u32x4 raw[kPairVecs];
-#pragma unroll
-  for (int u = 0; u < kPairVecs; ++u) {
-    const int64_t j = j0 + u * (64 * kEpv);
-    raw[u] = BF16 ? u32x4(0xff80ff80u) : u32x4(0xff800000u);  // -inf: adds nothing
-    if (j + kEpv <= z.cols) raw[u] = *reinterpret_cast<const typename R::loose *>(p + j * kSize);
-  }
-  // the row's last columns where they do not fill a vector: one lane's
-  const int64_t tail = z.cols - z.cols % kEpv;
-  const bool ragged = tail < z.cols && j0 <= tail && (tail - j0) % (64 * kEpv) == 0 &&
-                      tail - j0 < kPairVecs * 64 * kEpv;
-  float mx = neg_inf();
-#pragma unroll
-  for (int u = 0; u < kPairVecs; ++u) {
-    float v[kEpv];
-    Vec<BF16, kEpv>::widen(raw[u], v);
-#pragma unroll
-    for (int e = 0; e < kEpv; ++e) mx = fmaxf(mx, v[e]);
-  }
-  if (ragged) {
-#pragma nounroll
-    for (int64_t i = tail; i < z.cols; ++i) mx = fmaxf(mx, load_one<BF16>(p, i));
-  }
-  mx = wave_max(mx);
-  const float off = __builtin_isinf(mx) ? 0.f : mx;  // +inf: an infinite sum
-  float sum = 0.f;
-#pragma unroll
-  for (int u = 0; u < kPairVecs; ++u) {
-    float v[kEpv];
-    Vec<BF16, kEpv>::widen(raw[u], v);
-#pragma unroll
-    for (int e = 0; e < kEpv; ++e) sum += exp2_fast((v[e] - off) * to_log2);
-  }
-  if (ragged) {
-#pragma nounroll
-    for (int64_t i = tail; i < z.cols; ++i)
-      sum += exp2_fast((load_one<BF16>(p, i) - off) * to_log2);
-  }
-  sum = wave_sum(sum);
-  if (lane == 0) pairs[row * z.slices + s] = Pair{mx, sum};
+  Slice<BF16> slice;
+  slice.load(z, p, s);
+  const Pair a = slice.pair(z, p, s, to_log2);
+  if ((threadIdx.x & 63) == 0) pairs[row * z.slices + s] = a;
 }
 
 // A row's entries by one wave: the largest t_e / T (or the given
@@ -241,21 +255,14 @@ __device__ __forceinline__ float entries_shift(const TeacherArgs &t, int64_t row
   return mx == neg_inf() ? 0.f : mx;  // no entry counts (NaN ones stay NaN)
 }
 
-// One wave per row: the pairs joined (shard_lse != nullptr), and the entries'
-// product with the shard's logits.
+// The entries' product with the shard's logits (the row at p), by one wave.
 template <bool BF16>
-__global__ __launch_bounds__(kBlock) void distill_rows(ShardArgs z, TeacherArgs t, int64_t m,
-                                                      const Pair *__restrict__ pairs,
-                                                      float *__restrict__ shard_lse,
-                                                      float *__restrict__ shard_dot) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
-  if (row >= m) return;
-  const char *p = z.base + row * z.ld_bytes;
+__device__ __forceinline__ float entries_dot(const ShardArgs &z, const TeacherArgs &t, int64_t row,
+                                             const char *p) {
   const float shift = entries_shift(t, row);
   // in 64 bits: the loss is a small difference of this and the log-sum-exp
   double dot = 0.0, total = 0.0;
-  for (int e = lane; e < t.k; e += 64) {
+  for (int e = threadIdx.x & 63; e < t.k; e += 64) {
     int64_t id;
     const float v = entry(t, row, e, id);
     const float w = v == neg_inf() ? 0.f : expf(v - shift);
@@ -265,19 +272,61 @@ __global__ __launch_bounds__(kBlock) void distill_rows(ShardArgs z, TeacherArgs 
       dot += static_cast<double>(w) *
              static_cast<double>(load_one<BF16>(p, static_cast<int64_t>(local)));
   }
-  if (shard_lse != nullptr) {
-    Pair a{neg_inf(), 0.f};
-    for (int s = lane; s < z.slices; s += 64)
-      a = join(a, pairs[row * z.slices + s], t.to_log2);
-    a = wave_join(a, t.to_log2);
-    if (lane == 0) shard_lse[row] = natural_log(a, t.temperature);
-  }
   dot = wave_sum(dot);
   total = t.lse != nullptr ? 1.0 : wave_sum(total);
-  if (lane == 0)
-    shard_dot[row] =
-        total == 0.0 ? 0.f
-                     : static_cast<float>(dot / total / static_cast<double>(t.temperature));
+  return total == 0.0 ? 0.f : static_cast<float>(dot / total / static_cast<double>(t.temperature));
+}
+
+// One wave per row: the pairs joined (shard_lse != nullptr), and the entries'
+// product.
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void distill_rows(ShardArgs z, TeacherArgs t, int64_t m,
+                                                      const Pair *__restrict__ pairs,
+                                                      float *__restrict__ shard_lse,
+                                                      float *__restrict__ shard_dot) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
+  if (row >= m) return;
+  const float dot = entries_dot<BF16>(z, t, row, z.base + row * z.ld_bytes);
+  if (lane == 0) shard_dot[row] = dot;
+  if (shard_lse == nullptr) return;
+  Pair a{neg_inf(), 0.f};
+  for (int s = lane; s < z.slices; s += 64) a = join(a, pairs[row * z.slices + s], t.to_log2);
+  a = wave_join(a, t.to_log2);
+  if (lane == 0) shard_lse[row] = natural_log(a, t.temperature);
+}
+
+// One workgroup per row: both at once, without pairs in memory.  The last wave
+// takes the entries, the others the row's slices in turn, the next one's vectors
+// on their way.
+constexpr int kRowWaves = 8;  // at most
+template <bool BF16>
+__global__ __launch_bounds__(64 * (kRowWaves + 1)) void distill_whole_rows(
+    ShardArgs z, TeacherArgs t, int waves, float *__restrict__ shard_lse,
+    float *__restrict__ shard_dot) {
+  __shared__ Pair part[kRowWaves];
+  const int lane = threadIdx.x & 63, wave = wave_in_block();
+  const int64_t row = blockIdx.x;
+  const char *p = z.base + row * z.ld_bytes;
+  if (wave == waves) {
+    const float dot = entries_dot<BF16>(z, t, row, p);
+    if (lane == 0) shard_dot[row] = dot;
+  } else {
+    Slice<BF16> next;
+    next.load(z, p, wave);
+    Pair a{neg_inf(), 0.f};
+#pragma nounroll
+    for (int s = wave; s < z.slices; s += waves) {
+      const Slice<BF16> now = next;
+      if (s + waves < z.slices) next.load(z, p, s + waves);
+      a = join(a, now.pair(z, p, s, t.to_log2), t.to_log2);
+    }
+    if (lane == 0) part[wave] = a;
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  const Pair a = wave_join(lane < waves ? part[lane] : Pair{neg_inf(), 0.f}, t.to_log2);
+  if (lane == 0) shard_lse[row] = natural_log(a, t.temperature);
 }
 
 struct Parts {
@@ -466,6 +515,23 @@ int launch_distill_shard(const LogitsShard &z, const Teacher &t, float *shard_ls
   const ShardArgs a = args_of(z, pair_cols(z.dtype));
   const TeacherArgs ta = args_of(t);
   Pair *pr = reinterpret_cast<Pair *>(pairs);
+  // A workgroup per row, unless a few long rows would leave the chip idle.  us
+  // with a workgroup per row / with pairs in memory, in a graph, fp32: 8 rows of
+  // 38 slices 6.3 / 6.7, of 149 slices 16.6 / 8.5; 64 rows of 75 slices 9.9 /
+  // 10.8, of 149 slices 18.8 / 14.9; 256 rows of 149 slices 29.7 / 33.5; 4096
+  // rows of 4 slices 16.7 / 20.6.  Waves have two slices each where they can:
+  // 4096 bf16 rows of 8 slices 30.8 with 4 waves, 34.6 with 8.
+  if (shard_lse && (z.m >= 256 || a.slices <= 40 + z.m / 2)) {
+    const int waves = std::min((a.slices + 1) / 2, kRowWaves);
+    const dim3 grid(static_cast<unsigned>(z.m)), block(64 * (waves + 1));
+    if (z.dtype == 1)
+      hipLaunchKernelGGL((distill_whole_rows<true>), grid, block, 0, st, a, ta, waves, shard_lse,
+                         shard_dot);
+    else
+      hipLaunchKernelGGL((distill_whole_rows<false>), grid, block, 0, st, a, ta, waves, shard_lse,
+                         shard_dot);
+    return static_cast<int>(hipGetLastError());
+  }
   if (shard_lse) {
     const unsigned gx = static_cast<unsigned>((a.slices + kWaves - 1) / kWaves);
     for (int64_t r = 0; r < z.m; r += kRowsPerGrid) {
