@@ -340,3 +340,34 @@ def test_layer_beam_calls():
     state = torch.randn(2, n * beams, 5, device="cuda")
     got = heads[0].reorder_beams(state, p[:, :beams], beams, dim=1)
     assert torch.equal(got, vpe.vpe_beam_reorder(state, p[:, :beams], beams, dim=1))
+
+
+def test_the_most_sequences():
+    n, v = 2 ** 21, 3
+    logits, lse, scores, _ = _case(81, n, 1, v, F32)
+    got = vpe.vpe_beam_merge([vpe.vpe_beam_select(logits, lse, scores, 1, 2, 0, v)], v)
+    c = (logits - lse[:, None]) + scores[:, None]
+    ref, at = torch.sort(c, dim=1, descending=True, stable=True)
+    assert torch.equal(got[0], ref[:, :2]) and torch.equal(got[2], at[:, :2])
+    assert not bool(got[1].any())
+
+
+def test_two_streams_at_once():
+    work = [(_case(90 + i, n, beams, v, BF16), beams, v)
+            for i, (n, beams, v) in enumerate(((2, 4, 30000), (9, 1, 7000), (1, 16, 50001)))]
+
+    def step(case, beams, v):
+        logits, lse, scores, _ = case
+        out = vpe.vpe_beam_merge([vpe.vpe_beam_select(logits, lse, scores, beams, 16, 0, v)], v)
+        return (*out, vpe.vpe_beam_reorder(logits, out[1], beams))
+
+    ref = [step(*w) for w in work]
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    got = []
+    for st, w in zip(streams, work):
+        with torch.cuda.stream(st):
+            got.append(step(*w))
+    torch.cuda.synchronize()
+    for a, b in zip(got, ref):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -477,3 +477,31 @@ def test_layer_distillation():
         assert torch.equal(a, vpe.vpe_distill_grad(z, lse, go, ids, t, s, V, temperature=2.0))
         with pytest.raises(ValueError):
             h.distill_grad(z[:, :-1].contiguous(), lse, go, ids, t)
+
+
+def test_the_most_rows():
+    m, v, k = 2 ** 21, 3, 2
+    z, ids, t, tl, g = _case(61, m, v, k, F32, F32, torch.int32)
+    _check(z, ids, t, tl, 1.0, 1, g, k)
+
+
+def test_two_streams_at_once():
+    v, k = 5000, 12
+    work = [_case(70 + i, m, v, k, BF16, F32, torch.int64)[:3]
+            for i, m in enumerate((3, 300, 40, 257))]
+
+    def step(z, ids, t):
+        lse, dot = vpe.vpe_distill_shard(z, ids, t, 0, v)
+        loss, lse = vpe.vpe_distill_loss([lse], [dot], ids, t, v)
+        return loss, vpe.vpe_distill_grad(z, lse, torch.ones_like(loss), ids, t, 0, v)
+
+    ref = [step(*w) for w in work]
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    got = []
+    for st, w in zip(streams, work):
+        with torch.cuda.stream(st):
+            got.append(step(*w))
+    torch.cuda.synchronize()
+    for a, b in zip(got, ref):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])

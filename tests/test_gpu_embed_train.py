@@ -306,3 +306,21 @@ def test_layer_weight_grad():
     assert torch.equal(got, vpe.vpe_embed_grad(ids, dy, 48, 48, 2.0))
     twice = emb.weight_grad(ids, dy, scale=2.0, grad_weight=got.clone(), accumulate=True)
     _check_grad(twice, ids, dy, 48, 48, 2.0, before=got)
+
+
+def test_more_rows_than_one_launch_takes():
+    n = 2 ** 24 + 5  # of the lookup; and 2^22 chunks times blocks of columns of the join
+    weight = torch.arange(7, device="cuda", dtype=F32)[:, None].contiguous()
+    ids = torch.arange(n, device="cuda") % 9
+    got = vpe.vpe_embed_scaled(ids, weight, 0, 3.0)
+    assert torch.equal(got[:, 0], torch.where(ids < 7, ids * 3.0, 0.0))
+    n, dim, rows = 2 ** 21, 16640, 4
+    if torch.cuda.mem_get_info()[0] < 110e9:
+        pytest.skip("needs 110 GB of device memory")
+    ids = torch.arange(n, device="cuda") * (rows + 1) // n  # 5 long runs, the last one's unowned
+    dy = torch.ones(n, dim, dtype=BF16, device="cuda")
+    dy[0], dy[-1] = 3.0, float("nan")
+    got = vpe.vpe_embed_grad(ids, dy, 0, rows, 0.5, dtype=F32)
+    count = torch.bincount(ids, minlength=rows + 1)[:rows].float()  # exact sums below 2^24
+    count[0] += 2
+    assert torch.equal(got, (0.5 * count)[:, None].expand(rows, dim))
