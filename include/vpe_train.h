@@ -103,7 +103,8 @@ vpe_status vpe_embed_grad(const void *ids, vpe_itype itype, int64_t n, const voi
 #define VPE_MAX_TEACHER_ENTRIES 1024
 #define VPE_MAX_DISTILL_ROWS (1 << 21)
 
-/* Bytes of workspace vpe_distill_shard needs.  Host-only.
+/* Bytes of workspace vpe_distill_shard needs for m rows; as much serves fewer.
+ * Host-only.
  * Errors: VPE_ERR_NULL, VPE_ERR_SHAPE (m < 0 or > VPE_MAX_DISTILL_ROWS,
  * shard_rows < 1 or >= 2^31). */
 vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes);

@@ -164,6 +164,8 @@ def test_distill_workspace():
         assert f(*bad, ctypes.byref(b)) == vpe.VPE_ERR_SHAPE, bad
     assert vpe.vpe_distill_workspace(0, 10 ** 6) == 0
     assert vpe.vpe_distill_workspace(2 ** 21, 2 ** 31 - 1) >= 0
+    sizes = [vpe.vpe_distill_workspace(m, 151936) for m in range(0, 600)]
+    assert sizes == sorted(sizes) and sizes[1] > 0
 
 
 def test_distill_loss_validation():

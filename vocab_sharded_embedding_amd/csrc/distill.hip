@@ -175,7 +175,6 @@ struct ShardArgs {
 };
 
 constexpr int kPairVecs = 4;  // vectors per lane and pair
-constexpr int64_t kRowsPerGrid = 32768;
 
 // Slice `s` of the row at p, by one wave: its vectors, -inf where they end.
 template <bool BF16>
@@ -235,9 +234,9 @@ struct Slice {
 // (8 vectors per lane instead of 4: 3.2 us; 31.4 instead of 30.6 us for 1024 bf16
 // rows of 75968.)
 template <bool BF16>
-__global__ __launch_bounds__(kBlock) void distill_pairs(ShardArgs z, float to_log2, int64_t row0,
+__global__ __launch_bounds__(kBlock) void distill_pairs(ShardArgs z, float to_log2,
                                                        Pair *__restrict__ pairs) {
-  const int64_t row = row0 + blockIdx.y;
+  const int64_t row = blockIdx.y;
   const int64_t s = static_cast<int64_t>(blockIdx.x) * kWaves + wave_in_block();
   if (s >= z.slices) return;
   const char *p = z.base + row * z.ld_bytes;
@@ -532,7 +531,7 @@ int launch_distill_shard(const LogitsShard &z, const Teacher &t, float *shard_ls
   // 10.8, of 149 slices 18.8 / 14.9; 256 rows of 149 slices 29.7 / 33.5; 4096
   // rows of 4 slices 16.7 / 20.6.  Waves have two slices each where they can:
   // 4096 bf16 rows of 8 slices 30.8 with 4 waves, 34.6 with 8.
-  if (shard_lse && (z.m >= 256 || a.slices <= 40 + z.m / 2)) {
+  if (shard_lse && (z.m >= kDistillWholeRows || a.slices <= 40 + z.m / 2)) {
     const int waves = std::min((a.slices + 1) / 2, kRowWaves);
     const dim3 grid(static_cast<unsigned>(z.m)), block(64 * (waves + 1));
     if (z.dtype == 1)
@@ -545,13 +544,11 @@ int launch_distill_shard(const LogitsShard &z, const Teacher &t, float *shard_ls
   }
   if (shard_lse) {
     const unsigned gx = static_cast<unsigned>((a.slices + kWaves - 1) / kWaves);
-    for (int64_t r = 0; r < z.m; r += kRowsPerGrid) {
-      const dim3 grid(gx, static_cast<unsigned>(std::min(kRowsPerGrid, z.m - r)));
-      if (z.dtype == 1)
-        hipLaunchKernelGGL((distill_pairs<true>), grid, dim3(kBlock), 0, st, a, ta.to_log2, r, pr);
-      else
-        hipLaunchKernelGGL((distill_pairs<false>), grid, dim3(kBlock), 0, st, a, ta.to_log2, r, pr);
-    }
+    const dim3 grid(gx, static_cast<unsigned>(z.m));
+    if (z.dtype == 1)
+      hipLaunchKernelGGL((distill_pairs<true>), grid, dim3(kBlock), 0, st, a, ta.to_log2, pr);
+    else
+      hipLaunchKernelGGL((distill_pairs<false>), grid, dim3(kBlock), 0, st, a, ta.to_log2, pr);
   }
   const dim3 rows(static_cast<unsigned>((z.m + kWaves - 1) / kWaves));
   if (z.dtype == 1)

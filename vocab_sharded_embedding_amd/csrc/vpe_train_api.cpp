@@ -147,7 +147,8 @@ vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes) 
   if (!bytes) return VPE_ERR_NULL;
   if (m < 0 || m > VPE_MAX_DISTILL_ROWS || shard_rows < 1 || shard_rows > kMax31)
     return VPE_ERR_SHAPE;
-  *bytes = m * vpe::distill_pairs_per_row(shard_rows, 0) * 8;
+  const int64_t rows = m < vpe::kDistillWholeRows ? m : vpe::kDistillWholeRows - 1;
+  *bytes = rows * vpe::distill_pairs_per_row(shard_rows, 0) * 8;
   return VPE_OK;
 }
 

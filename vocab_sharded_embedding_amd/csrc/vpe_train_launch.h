@@ -103,6 +103,9 @@ struct LogitsShard {
   int dtype;
 };
 
+// From this many rows on each has a workgroup of its own, and no pairs in memory.
+constexpr int64_t kDistillWholeRows = 256;
+
 // (maximum, sum) pairs of 8 bytes per row that the workspace holds; the most
 // for f32.
 int64_t distill_pairs_per_row(int64_t cols, int dtype);

@@ -162,7 +162,8 @@ def logits_shard(name: str, logits, shard_rows: Optional[int], col_offset: int):
 
 @functools.lru_cache(maxsize=256)
 def vpe_distill_workspace(m: int, shard_rows: int) -> int:
-    """Bytes of workspace vpe_distill_shard needs (unless with_lse is False)."""
+    """Bytes of workspace vpe_distill_shard needs for m rows (none if with_lse is
+    False); as much serves fewer."""
     b = ctypes.c_int64()
     _check("vpe_distill_workspace", load_library().vpe_distill_workspace(
         m, shard_rows, ctypes.byref(b)))
