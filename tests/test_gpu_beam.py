@@ -371,3 +371,13 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in zip(got, ref):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_more_rows_than_one_launch_takes():
+    n, v = 32768 + 40, 17001
+    logits = torch.randn(n, v, generator=_gen(99), device="cuda", dtype=F32).to(BF16)
+    lse, scores = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    got = vpe.vpe_beam_merge([vpe.vpe_beam_select(logits, lse, scores, 1, 5, 0, v)], v)
+    for rows in (slice(0, 40), slice(32760, n)):
+        ref, at = torch.sort(logits[rows].float(), dim=1, descending=True, stable=True)
+        assert torch.equal(got[0][rows], ref[:, :5]) and torch.equal(got[2][rows], at[:, :5])
