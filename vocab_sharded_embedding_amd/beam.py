@@ -97,16 +97,19 @@ def vpe_beam_reorder(state, parents, beams: int, dim: int = 0, out=None):
     shape = state.shape
     if not 0 <= dim < len(shape) or shape[dim] != n * beams:
         raise ValueError("dimension `dim` of state must have n_seqs * beams rows")
-    to = (*shape[:dim], n * beams_out, *shape[dim + 1:])
+    to = shape if beams_out == beams else (*shape[:dim], n * beams_out, *shape[dim + 1:])
     if out is None:
-        out = torch.empty(to, dtype=state.dtype, device=state.device)
+        out = (torch.empty_like(state) if to is shape
+               else torch.empty(to, dtype=state.dtype, device=state.device))
     elif out.shape != to or out.dtype != state.dtype:
-        raise ValueError(f"out must be {to} of the state's dtype")
+        raise ValueError(f"out must be {tuple(to)} of the state's dtype")
     index = placed("state out", state, out)
     if parents.get_device() != index:
         raise ValueError(f"parents must be on the state's device, got {parents.device}")
-    row_bytes = math.prod(shape[dim + 1:]) * state.element_size()
-    if row_bytes != 0:
-        enqueue("vpe_beam_reorder", index, state.data_ptr(), math.prod(shape[:dim]), n,
-                int(beams), row_bytes, parents.data_ptr(), ld, beams_out, out.data_ptr())
+    size = nbytes(state)
+    if size != 0:
+        outer = math.prod(shape[:dim]) if dim else 1
+        enqueue("vpe_beam_reorder", index, state.data_ptr(), outer, n, int(beams),
+                size // (outer * n * int(beams)), parents.data_ptr(), ld, beams_out,
+                out.data_ptr())
     return out

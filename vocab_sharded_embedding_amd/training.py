@@ -27,11 +27,16 @@ if _raw_stream is None:  # pragma: no cover
         return torch.cuda.current_stream(index).cuda_stream
 
 
+# The current device's index, without the look at whether one is initialised: the
+# tensors of a call are on one.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def enqueue(name: str, index: int, *args) -> None:
     """Call `name` of the library with `args` and device `index`'s current stream,
     that device being the current one meanwhile (kernels are enqueued there)."""
     fn = getattr(load_library(), name)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
