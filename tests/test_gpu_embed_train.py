@@ -324,3 +324,17 @@ def test_more_rows_than_one_launch_takes():
     count = torch.bincount(ids, minlength=rows + 1)[:rows].float()  # exact sums below 2^24
     count[0] += 2
     assert torch.equal(got, (0.5 * count)[:, None].expand(rows, dim))
+
+
+@pytest.mark.parametrize("n,rows,dim", [(300, 2 ** 28 + 3, 1), (9001, 2 ** 28 + 3, 1),
+                                        (70, 6, 2 ** 20), (9000, 700, 2 ** 15 + 1)])
+def test_gradient_of_many_rows_and_of_wide_ones(n, rows, dim):
+    g = _gen(n)
+    ids = torch.randint(0, rows, (n,), generator=g, device="cuda")
+    ids[:3] = rows - 1
+    dy = torch.randint(-8, 9, (n, dim), generator=g, device="cuda").to(BF16)
+    got = vpe.vpe_embed_grad(ids, dy, 0, rows, 0.5, dtype=F32)
+    ref = torch.zeros(rows, dim, device="cuda").index_add_(0, ids, dy.float() * 0.5)  # exact
+    assert torch.equal(got, ref)
+    vpe.vpe_embed_grad(ids, dy, 0, rows, 0.5, grad_weight=got, accumulate=True)
+    assert torch.equal(got, 2 * ref)
