@@ -178,6 +178,7 @@ struct ZeroRows {
   int64_t row0, row1;
   const uint8_t *flags;
   unsigned blocks;
+  int log2g;  // lanes that clear a row with flags
 };
 
 // `block` of z.blocks workgroups of `threads` threads.  Plain stores where the
@@ -198,6 +199,21 @@ __device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int
   const int lane = threadIdx.x & 63, waves = threads / 64;
   const int64_t part = (r1 - r0 + waves - 1) / waves, w0 = r0 + wave_in_block() * part;
   const int64_t w1 = w0 + part < r1 ? w0 + part : r1;
+  if (z.log2g < 6) {
+    // several rows at a time, 2^log2g lanes each
+    constexpr int kDeep = 4;
+    const int in = lane & ((1 << z.log2g) - 1), step = 64 >> z.log2g;
+    for (int64_t r = w0 + (lane >> z.log2g); r < w1; r += kDeep * step) {
+      uint8_t has_id[kDeep];
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) has_id[u] = r + u * step < w1 ? z.flags[r + u * step] : 1;
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u)
+        if (has_id[u] == 0)
+          zero_bytes<NT>(z.dw + (r + u * step) * z.row_bytes, z.row_bytes, in, 1 << z.log2g);
+    }
+    return;
+  }
   for (int64_t r = w0; r < w1; r += 64) {
     uint64_t empty = __ballot(r + lane < w1 && z.flags[r + lane < w1 ? r + lane : w0] == 0);
     while (empty) {
@@ -615,10 +631,11 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
   write_row<OUT16, 4>(a, token, col, v);
 }
 
-// Workgroups for `rows` rows of zeros: about `span` bytes each.
+// Workgroups for `rows` rows of zeros: about `span` bytes each (a row's flag
+// costs as much as 64).
 unsigned zero_blocks(int64_t rows, int64_t row_bytes, double span = 262144.0) {
   if (rows <= 0) return 0;
-  const double bytes = static_cast<double>(rows) * static_cast<double>(row_bytes);
+  const double bytes = static_cast<double>(rows) * std::max(64.0, static_cast<double>(row_bytes));
   return static_cast<unsigned>(std::max(1.0, std::min(bytes / span, 65536.0)));
 }
 
@@ -666,7 +683,8 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
   const int bits = (key_bits + passes - 1) / passes;
   const uint64_t urows = static_cast<uint64_t>(rows);
   const int64_t zero_to = a.accumulate ? 0 : rows;
-  ZeroRows zero{a.dw, a.dim * (gdtype == 1 ? 2 : 4), 0, 0, nullptr, 0};
+  const int64_t row_bytes = a.dim * (gdtype == 1 ? 2 : 4);
+  ZeroRows zero{a.dw, row_bytes, 0, 0, nullptr, 0, std::min(6, ceil_log2((row_bytes + 15) / 16))};
   ZeroRows join_zero = zero;
   int last = 0;
   if (n <= kGradOneBlockIds) {
@@ -725,7 +743,7 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
     const int64_t sums_to = zero_to - std::min(rest / 2, (int64_t(64) << 20) / zero.row_bytes);
     auto beside = [&](int64_t row0, int64_t row1) {
       return ZeroRows{zero.dw, zero.row_bytes, row0, row1, flags,
-                      zero_blocks(row1 - row0, zero.row_bytes, 65536.0)};
+                      zero_blocks(row1 - row0, zero.row_bytes, 65536.0), zero.log2g};
     };
     join_zero = beside(sums_to, zero_to);
     zero = beside(zero.row1, sums_to);
