@@ -391,6 +391,27 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter(
   const int64_t m = FIRST ? pass.n : static_cast<int64_t>(*count);
   const uint32_t low = (1u << pass.bits) - 1;
 
+  // A wave's items, kAhead rounds of 64 at a time: the first are on their way
+  // while the workgroups' counts are summed, and stay in registers where they
+  // are all there is (a tile of kSortTile).
+  constexpr int kAhead = static_cast<int>(kSortTile) / kSortThreads;
+  const int64_t per_wave = pass.tile / kSortWaves;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * pass.tile + wave * per_wave;
+  const int64_t i1 = i0 + per_wave < pass.n ? i0 + per_wave : pass.n;
+  uint32_t key[kAhead], from[kAhead];
+  bool have[kAhead];
+  auto take = [&](int64_t r) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t i = r + u * 64 + lane;
+      key[u] = 0, from[u] = static_cast<uint32_t>(i);
+      have[u] = i < i1 && items.get(i, key[u]);
+      if (!FIRST && i < i1) from[u] = items.pos_in[i];
+      have[u] = have[u] && i < m;
+    }
+  };
+  take(i0);
+
   // the workgroups' counts: pair of digits `pair`, every kParts-th workgroup
   const int pair = tid % (kDigits / 2), part = tid / (kDigits / 2);
   u32x2 before = u32x2(0), total = u32x2(0);
@@ -405,13 +426,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter(
   for (int d = tid; d < kSortWaves * kDigits; d += kSortThreads)
     reinterpret_cast<uint32_t *>(at_)[d] = 0;
   __syncthreads();
-  const int64_t per_wave = pass.tile / kSortWaves;
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * pass.tile + wave * per_wave;
-  const int64_t i1 = i0 + per_wave < pass.n ? i0 + per_wave : pass.n;
-#pragma unroll 2
-  for (int64_t i = i0 + lane; i < i1; i += 64) {
-    uint32_t key;
-    if (items.get(i, key) && i < m) atomicAdd(&at_[wave][(key >> pass.shift) & low], 1u);
+  const bool again = per_wave > kAhead * 64;  // items do not stay in registers
+  for (int64_t r = i0; r < i1; r += kAhead * 64) {
+    if (r != i0) take(r);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (have[u]) atomicAdd(&at_[wave][(key[u] >> pass.shift) & low], 1u);
   }
   part_before[part][pair] = before;
   part_total[part][pair] = total;
@@ -441,21 +461,20 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter(
     for (int w = 0; w < kSortWaves; ++w) at_[w][tid] = to, to += c[w];
   }
   __syncthreads();
-  for (int64_t r = i0; r < i1; r += 64) {
-    const int64_t i = r + lane;
-    uint32_t key = 0, from = static_cast<uint32_t>(i);
-    bool have = i < i1 && items.get(i, key);
-    if (!FIRST && i < i1) from = items.pos_in[i];
-    have = have && i < m;
-    const uint32_t d = (key >> pass.shift) & low;
-    const uint64_t same = same_digit(d, have);
-    if (have) {
-      const uint32_t seen = at[wave][d];
-      const uint32_t to = seen + below(same);
-      if (below(same) == 0) at[wave][d] = seen + __popcll(same);
-      key_out[to] = key;
-      pos_out[to] = from;
-      if (FIRST && flags != nullptr) flags[key] = 1;
+  for (int64_t r = i0; r < i1; r += kAhead * 64) {
+    if (again) take(r);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t d = (key[u] >> pass.shift) & low;
+      const uint64_t same = same_digit(d, have[u]);
+      if (have[u]) {
+        const uint32_t seen = at[wave][d];
+        const uint32_t to = seen + below(same);
+        if (below(same) == 0) at[wave][d] = seen + __popcll(same);
+        key_out[to] = key[u];
+        pos_out[to] = from[u];
+        if (FIRST && flags != nullptr) flags[key[u]] = 1;
+      }
     }
   }
 }
