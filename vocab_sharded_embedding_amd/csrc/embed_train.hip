@@ -618,16 +618,23 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
   if (a.key[next - 1] != token) return;
   const bool whole_chunk = a.key[next - a.chunk] == token;
   if (whole_chunk && c > 0 && a.key[next - a.chunk - 1] == token) return;  // began before
-  // chunks after c that begin with the token
+  // chunks after c that begin with the token: 64 at a time, and where those all
+  // do, by the last ones of the next 64 times 64
+  auto begin_with_it = [&](int64_t chunk) {  // how many of the lanes' chunks, all before the others
+    const int64_t q = chunk * a.chunk;
+    const uint64_t on = __ballot(q < n && a.key[q < n ? q : 0] == token);
+    return on == ~0ull ? 64 : __builtin_ctzll(~on);
+  };
   int64_t more = 1;
   for (;;) {
-    const int64_t q = (c + 1 + more + lane) * a.chunk;
-    const uint64_t on = __ballot(q < n && a.key[q < n ? q : 0] == token);
-    if (on != ~0ull) {
-      more += __builtin_ctzll(~on);
-      break;
-    }
-    more += 64;
+    const int some = begin_with_it(c + 1 + more + lane);
+    more += some;
+    if (some < 64) break;
+    int whole;
+    do {
+      whole = begin_with_it(c + 1 + more + 64 * lane + 63);
+      more += 64 * whole;
+    } while (whole == 64);
   }
   const int64_t col = (static_cast<int64_t>(blockIdx.x - rel * col_blocks) * 64 + lane) * 4;
   // pieces 0 (in chunk c) .. more; partial rows are padded past dim
