@@ -597,64 +597,103 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
   }
 }
 
-// One workgroup per chunk and block of 256 columns: the run that leaves the
-// chunk having begun in it is joined from its partial sums, a quarter of them
-// per wave, in order.  Workgroups after them write zero rows.  Bound by the
-// latency of the longest run: 12.6 us for 165 pieces (5300 positions of the
-// commonest of 65536 Zipf ids), 21 us with 64 MB of zero rows beside it; 3.9 us
-// where no run is long.
+// One wave per chunk and block of 256 columns: the run that leaves the chunk
+// having begun in it is joined from its partial sums, in order.  Long runs are
+// joined by the workgroup's waves together, a quarter each.  Workgroups after
+// them write zero rows.
 template <bool OUT16>
-__global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int col_blocks,
-                                                   unsigned join_blocks, ZeroRows zero) {
+__global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int64_t n_chunks,
+                                                   int col_blocks, unsigned join_blocks,
+                                                   ZeroRows zero) {
+  constexpr int kDeep = 16;  // partial sums in flight
   __shared__ f32x4 part[kWaves][64];
+  __shared__ int64_t long_more[kWaves], long_slot0[kWaves];
+  __shared__ uint32_t long_token[kWaves];
   if (blockIdx.x >= join_blocks) return zero_rows<true>(zero, blockIdx.x - join_blocks, kBlock);
   const int lane = threadIdx.x & 63, wave = wave_in_block();
-  const unsigned rel = blockIdx.x / static_cast<unsigned>(col_blocks);
-  const int64_t c = chunk0 + rel;
-  const int64_t n = *a.count;
-  const int64_t next = (c + 1) * a.chunk;
-  if (next >= n) return;
-  const uint32_t token = a.key[next];
-  if (a.key[next - 1] != token) return;
-  const bool whole_chunk = a.key[next - a.chunk] == token;
-  if (whole_chunk && c > 0 && a.key[next - a.chunk - 1] == token) return;  // began before
-  // chunks after c that begin with the token: 64 at a time, and where those all
-  // do, by the last ones of the next 64 times 64
-  auto begin_with_it = [&](int64_t chunk) {  // how many of the lanes' chunks, all before the others
-    const int64_t q = chunk * a.chunk;
-    const uint64_t on = __ballot(q < n && a.key[q < n ? q : 0] == token);
-    return on == ~0ull ? 64 : __builtin_ctzll(~on);
-  };
-  int64_t more = 1;
-  for (;;) {
-    const int some = begin_with_it(c + 1 + more + lane);
-    more += some;
-    if (some < 64) break;
-    int whole;
-    do {
-      whole = begin_with_it(c + 1 + more + 64 * lane + 63);
-      more += 64 * whole;
-    } while (whole == 64);
-  }
-  const int64_t col = (static_cast<int64_t>(blockIdx.x - rel * col_blocks) * 64 + lane) * 4;
-  // pieces 0 (in chunk c) .. more; partial rows are padded past dim
-  const int64_t share = (more + kWaves) / kWaves;
-  const int64_t i0 = wave * share, i1 = i0 + share <= more ? i0 + share : more + 1;
-  f32x4 sum = f32x4(0.f);
-  if (col < a.dim) {
-#pragma unroll 16
-    for (int64_t i = i0; i < i1; ++i) {
-      const int64_t slot = i == 0 ? 2 * c + (whole_chunk ? 0 : 1) : 2 * (c + i);
-      sum += *reinterpret_cast<const f32x4 *>(a.partial + slot * a.partial_ld + col);
+  const unsigned group = blockIdx.x / static_cast<unsigned>(col_blocks);
+  const int64_t col = (static_cast<int64_t>(blockIdx.x - group * col_blocks) * 64 + lane) * 4;
+  const int64_t c0 = chunk0 + static_cast<int64_t>(group) * kWaves;  // the workgroup's chunks
+
+  // the chunk of this wave: how many chunks after it begin with its last token
+  const int64_t c = c0 + wave, next = (c + 1) * a.chunk;
+  int64_t more = 0, slot0 = 0;  // slot0: of the run's first piece, slot 2c if it is all of the chunk
+  uint32_t token = 0;
+  if (c < chunk0 + n_chunks) {
+    const int64_t n = *a.count;
+    token = a.key[next];  // (a place of the buffer, whatever n is)
+    const uint32_t last = a.key[next - 1], first = a.key[next - a.chunk];
+    const uint32_t before = a.key[c > 0 ? next - a.chunk - 1 : 0];
+    slot0 = 2 * c + (first != token);
+    const bool begun = c > 0 && first == token && before == token;
+    if (next < n && last == token && !begun) {
+      // 64 at a time, and where those all do, by the last ones of the next 64
+      // times 64
+      auto begin_with_it = [&](int64_t chunk) {  // how many of the lanes' chunks do
+        const int64_t q = chunk * a.chunk;
+        const uint64_t on = __ballot(q < n && a.key[q < n ? q : 0] == token);
+        return on == ~0ull ? 64 : __builtin_ctzll(~on);
+      };
+      more = 1;
+      for (;;) {
+        const int some = begin_with_it(c + 1 + more + lane);
+        more += some;
+        if (some < 64) break;
+        int whole;
+        do {
+          whole = begin_with_it(c + 1 + more + 64 * lane + 63);
+          more += 64 * whole;
+        } while (whole == 64);
+      }
     }
   }
-  part[wave][lane] = sum;
-  __syncthreads();
-  if (wave != 0 || col >= a.dim) return;
+
+  // pieces i0 .. i1 - 1 of the run of chunk `of`: 0 in that chunk, i in chunk of +
+  // i, at its first position; partial rows are padded past dim
+  auto pieces = [&](int64_t of, int64_t slot0, int64_t i0, int64_t i1) {
+    f32x4 sum = f32x4(0.f);
+    if (col < a.dim) {
+      for (int64_t i = i0; i < i1; i += kDeep) {
+        f32x4 r[kDeep];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) sum += part[w][lane];
-  const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-  write_row<OUT16, 4>(a, token, col, v);
+        for (int u = 0; u < kDeep; ++u) {
+          const int64_t slot = i + u == 0 ? slot0 : 2 * (of + i + u);
+          r[u] = f32x4(0.f);
+          if (i + u < i1)
+            r[u] = *reinterpret_cast<const f32x4 *>(a.partial + slot * a.partial_ld + col);
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u)
+          if (i + u < i1) sum += r[u];
+      }
+    }
+    return sum;
+  };
+  auto write = [&](uint32_t run, f32x4 sum) {
+    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    if (col < a.dim) write_row<OUT16, 4>(a, run, col, v);
+  };
+
+  const bool alone = more < kDeep;
+  if (more > 0 && alone) write(token, pieces(c, slot0, 0, more + 1));
+  if (lane == 0)
+    long_more[wave] = alone ? 0 : more, long_slot0[wave] = slot0, long_token[wave] = token;
+  __syncthreads();
+#pragma nounroll
+  for (int w = 0; w < kWaves; ++w) {
+    const int64_t m = long_more[w];
+    if (m == 0) continue;  // the same in all waves
+    const int64_t share = (m + kWaves) / kWaves, i0 = wave * share;
+    part[wave][lane] = pieces(c0 + w, long_slot0[w], i0, i0 + share <= m ? i0 + share : m + 1);
+    __syncthreads();
+    if (wave == 0) {
+      f32x4 sum = part[0][lane];
+#pragma unroll
+      for (int q = 1; q < kWaves; ++q) sum += part[q][lane];
+      write(long_token[w], sum);
+    }
+    __syncthreads();
+  }
 }
 
 // Workgroups for `rows` rows of zeros: about `span` bytes each (a row's flag
@@ -682,12 +721,13 @@ int launch_sums(GradArgs a, int64_t n, ZeroRows zero, ZeroRows join_zero, hipStr
     zero.blocks = 0;
   }
   if (chunks > 1) {
-    const int64_t join_blocks = (a.dim + 255) / 256;
-    const int64_t join_step = std::max<int64_t>(1, (int64_t(1) << 22) / join_blocks);
+    const int64_t join_cols = (a.dim + 255) / 256;
+    const int64_t join_step = std::max<int64_t>(1, (int64_t(1) << 22) / join_cols) * kWaves;
     for (int64_t c = 0; c < chunks - 1; c += join_step) {
-      const unsigned jb = static_cast<unsigned>(std::min(join_step, chunks - 1 - c) * join_blocks);
+      const int64_t nc = std::min(join_step, chunks - 1 - c);
+      const unsigned jb = static_cast<unsigned>((nc + kWaves - 1) / kWaves * join_cols);
       hipLaunchKernelGGL((grad_join<OUT16>), dim3(jb + join_zero.blocks), dim3(kBlock), 0, st, a, c,
-                         static_cast<int>(join_blocks), jb, join_zero);
+                         nc, static_cast<int>(join_cols), jb, join_zero);
       join_zero.blocks = 0;
     }
   }
