@@ -600,7 +600,10 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
 // One wave per chunk and block of 256 columns: the run that leaves the chunk
 // having begun in it is joined from its partial sums, in order.  Long runs are
 // joined by the workgroup's waves together, a quarter each.  Workgroups after
-// them write zero rows.
+// them write zero rows.  Bound by latency: 4 us where no run is long; 65536 Zipf
+// ids, 165 pieces in the longest run, 19.4 us with 64 MB of zero rows beside it.
+// (The whole gradient of those took 162.4, 167 and 177 us with a workgroup of 4, 8
+// and 16 waves per chunk, 159.7 us this way: most chunks have nothing to join.)
 template <bool OUT16>
 __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int64_t n_chunks,
                                                    int col_blocks, unsigned join_blocks,
@@ -617,7 +620,7 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
 
   // the chunk of this wave: how many chunks after it begin with its last token
   const int64_t c = c0 + wave, next = (c + 1) * a.chunk;
-  int64_t more = 0, slot0 = 0;  // slot0: of the run's first piece, slot 2c if it is all of the chunk
+  int64_t more = 0, slot0 = 0;  // slot0: where the run's piece in this chunk is
   uint32_t token = 0;
   if (c < chunk0 + n_chunks) {
     const int64_t n = *a.count;
@@ -804,7 +807,7 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
     }
     // The rest beside the sums; the last 64 MB beside their join, which waits
     // for the pieces of the longest runs one after the other (65536 Zipf ids:
-    // 162 us, 165 with none there).
+    // 3 us less of 160 than with none there).
     const int64_t rest = zero_to - zero.row1;
     const int64_t sums_to = zero_to - std::min(rest / 2, (int64_t(64) << 20) / zero.row_bytes);
     auto beside = [&](int64_t row0, int64_t row1) {
