@@ -133,7 +133,8 @@ vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes);
  * > VPE_MAX_DISTILL_ROWS, shard_rows < 1 or >= 2^31, k outside [1,
  * VPE_MAX_TEACHER_ENTRIES], vocab < 1, a tensor too large), VPE_ERR_RANGE (the
  * shard does not lie in [0, vocab), the columns do not fit ld, temperature not
- * positive or past 2^100, or its reciprocal infinite), VPE_ERR_WORKSPACE.
+ * positive or past 2^100, or log2(e) / temperature infinite in fp32: below
+ * 4.24e-39), VPE_ERR_WORKSPACE.
  */
 vpe_status vpe_distill_shard(const void *logits, int64_t ld, int64_t col_offset, int64_t m,
                              int64_t shard_rows, vpe_dtype dt, int64_t vocab_start, int64_t vocab,

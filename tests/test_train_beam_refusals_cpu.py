@@ -1,0 +1,25 @@
+"""Calls of the training and beam-search boundary that documentation refuses,
+each by itself, without a GPU (the calls never reach a kernel launch)."""
+import vocab_sharded_embedding_amd as vpe
+
+F32, I64 = vpe.VPE_F32, vpe.VPE_I64
+
+
+def test_temperatures_whose_power_of_two_factor_is_infinite():
+    # exponentials are powers of two of z log2(e) / T: the factor has to be finite
+    # in fp32, so T past log2(e) / 2^128 = 4.24e-39, and not only 1 / T (2.94e-39).
+    # No rows: what is not refused is a no-op.
+    lib = vpe.load_library()
+    calls = (
+        lambda t: lib.vpe_distill_shard(None, 8, 0, 0, 8, F32, 0, 8, t, None, I64, None, F32, 1,
+                                        None, None, None, None, 0, None),
+        lambda t: lib.vpe_distill_loss(None, None, 1, 0, 8, t, None, I64, None, F32, 1, None, None,
+                                       None, None),
+        lambda t: lib.vpe_distill_grad(None, 8, 0, 0, 8, F32, 0, 8, t, None, I64, None, F32, 1,
+                                       None, None, None, None, 8, 0, None),
+    )
+    for call in calls:
+        for temp in (3e-39, 4e-39, 4.23e-39):
+            assert call(temp) == vpe.VPE_ERR_RANGE, temp
+        for temp in (4.3e-39, 1e-38, 1.0, 2.0 ** 100):
+            assert call(temp) == vpe.VPE_OK, temp

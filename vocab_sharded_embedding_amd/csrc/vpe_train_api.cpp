@@ -3,6 +3,7 @@
 // C++ with no HIP headers: a rejected call enqueues nothing.
 #include "../../include/vpe_train.h"
 
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -38,8 +39,10 @@ vpe_status check_teacher(int64_t m, int64_t vocab, float temperature, vpe_itype 
   if (!known_dtype(tdt) || !known_itype(itype)) return VPE_ERR_DTYPE;
   if (m < 0 || m > VPE_MAX_DISTILL_ROWS || k < 1 || k > VPE_MAX_TEACHER_ENTRIES || vocab < 1)
     return VPE_ERR_SHAPE;
-  // 1 / temperature has to be finite as well, and any log-sum-exp times it
-  if (!(temperature > 0.f) || temperature > 0x1p100f || !isnormal(1.f / temperature))
+  // log2(e) / temperature, the factor of the powers of two, has to be finite in
+  // fp32 as well (so 1 / temperature is), and any log-sum-exp times temperature
+  if (!(temperature > 0.f) || temperature > 0x1p100f ||
+      1.4426950408889634 / static_cast<double>(temperature) > static_cast<double>(FLT_MAX))
     return VPE_ERR_RANGE;
   return VPE_OK;
 }
