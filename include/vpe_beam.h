@@ -107,7 +107,7 @@ vpe_status vpe_beam_merge(const uint64_t *const *keys, int32_t n_parts, int64_t 
  * outer == 0 or n_seqs == 0 is a no-op.
  * Errors: VPE_ERR_NULL, VPE_ERR_ALIGN (parent), VPE_ERR_SHAPE (a size
  * negative, beams_in or beams_out < 1, row_bytes < 1, too large),
- * VPE_ERR_RANGE (ld_parent < beams_out, src and dst overlap).
+ * VPE_ERR_RANGE (ld_parent < beams_out, dst overlaps src or parent).
  */
 vpe_status vpe_beam_reorder(const void *src, int64_t outer, int64_t n_seqs, int32_t beams_in,
                             int64_t row_bytes, const int64_t *parent, int64_t ld_parent,

@@ -23,3 +23,11 @@ def test_temperatures_whose_power_of_two_factor_is_infinite():
             assert call(temp) == vpe.VPE_ERR_RANGE, temp
         for temp in (4.3e-39, 1e-38, 1.0, 2.0 ** 100):
             assert call(temp) == vpe.VPE_OK, temp
+
+
+def test_reordered_states_over_their_parents():
+    # dst [2, 3 * 4, 100] bytes = 2400; parents: 3 rows of 4 int64, 8 apart
+    src, dst, n_parents = 0x10000, 0x7000000000, 2 * 8 + 4
+    call = vpe.load_library().vpe_beam_reorder
+    for parent in (dst, dst + 2392, dst - 8 * n_parents + 8, dst + 96):
+        assert call(src, 2, 3, 4, 100, parent, 8, 4, dst, None) == vpe.VPE_ERR_RANGE, parent

@@ -105,6 +105,10 @@ vpe_status vpe_beam_reorder(const void *src, int64_t outer, int64_t n_seqs, int3
   const uintptr_t sb = static_cast<uintptr_t>(outer * n_seqs * beams_in * row_bytes);
   const uintptr_t db = static_cast<uintptr_t>(outer * n_seqs * beams_out * row_bytes);
   if (d0 < s0 + sb && s0 < d0 + db) return VPE_ERR_RANGE;
+  // parents are read while other rows are written
+  const uintptr_t p0 = reinterpret_cast<uintptr_t>(parent);
+  const uintptr_t pb = static_cast<uintptr_t>(((n_seqs - 1) * ld_parent + beams_out) * 8);
+  if (d0 < p0 + pb && p0 < d0 + db) return VPE_ERR_RANGE;
   return launched(vpe::launch_beam_reorder(src, outer, n_seqs, beams_in, row_bytes, parent,
                                            ld_parent, beams_out, dst, stream));
 }
