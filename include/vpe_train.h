@@ -57,10 +57,12 @@ vpe_status vpe_embed_grad_workspace(int64_t n, int64_t shard_rows, int64_t dim, 
  * ids          device, [n] of `itype`, any values.
  * grad_out     device, [n, dim] of `dt`.
  * grad_weight  device, [shard_rows, dim] of `gdt` (either type, whatever `dt`
- *              is: fp32 gradients of a bf16 model); must not overlap the others.
+ *              is: fp32 gradients of a bf16 model).
  * workspace    device, at least vpe_embed_grad_workspace(n, shard_rows, dim)
  *              bytes, 16-byte aligned; needs no initialisation, and must not
  *              be shared by calls that may run at the same time.
+ * grad_weight and workspace must overlap neither each other nor the inputs:
+ * that is the caller's to see to here (the Python binding refuses it).
  * n == 0 writes zeros (accumulate == 0) or does nothing.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (n < 0 or
  * >= 2^31, dim < 1 or > 2^20, shard_rows < 1 or >= 2^31, a tensor too large),

@@ -1,6 +1,10 @@
 """Calls of the training and beam-search boundary that documentation refuses,
 each by itself, without a GPU (the calls never reach a kernel launch)."""
-import vocab_sharded_embedding_amd as vpe
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import vocab_sharded_embedding_amd as vpe  # noqa: E402
 
 F32, I64 = vpe.VPE_F32, vpe.VPE_I64
 
@@ -31,3 +35,33 @@ def test_reordered_states_over_their_parents():
     call = vpe.load_library().vpe_beam_reorder
     for parent in (dst, dst + 2392, dst - 8 * n_parents + 8, dst + 96):
         assert call(src, 2, 3, 4, 100, parent, 8, 4, dst, None) == vpe.VPE_ERR_RANGE, parent
+
+
+def test_lookup_gradient_over_its_own_inputs():
+    # refused before the tensors' device is looked at, so host tensors show it
+    n, rows, dim = 12, 6, 8
+    need = vpe.vpe_embed_grad_workspace(n, rows, dim)
+    pool = torch.zeros(need + 4096, dtype=torch.uint8)
+
+    def at(byte, shape, dtype):
+        size = torch.empty(shape, dtype=dtype).nbytes
+        return pool[byte:byte + size].view(dtype).view(shape)
+
+    def call(ids=torch.zeros(n, dtype=torch.int64), dy=torch.zeros(n, dim), dw=None, ws=None):
+        vpe.vpe_embed_grad(ids, dy, 0, rows, grad_weight=dw, workspace=ws)
+
+    dw = at(16, (rows, dim), torch.float32)  # bytes 16 to 208
+    for over in (dict(dy=at(200, (n, dim), torch.float32)), dict(ids=at(192, (n,), torch.int64)),
+                 dict(ws=at(0, (need,), torch.uint8)), dict(ws=at(192, (need,), torch.uint8)),
+                 dict(dw=at(16, (rows, dim), torch.bfloat16), dy=at(16, (n, dim), torch.float32)),
+                 dict(dw=None, ws=at(0, (need,), torch.uint8), dy=at(64, (n, dim), torch.float32)),
+                 dict(dw=None, ws=at(0, (need,), torch.uint8),
+                      ids=at(need // 8 * 8 - 8, (n,), torch.int64))):
+        with pytest.raises(ValueError, match="overlap"):
+            call(**{"dw": dw, **over})
+    # neighbours, and an empty view inside, are no overlap: the device is what is wrong
+    for beside in (dict(dy=at(208, (n, dim), torch.float32)), dict(ws=at(208, (need,), torch.uint8)),
+                   dict(ids=pool[32:32].view(torch.int64), dy=pool[64:64].view(torch.float32)
+                        .view(0, dim))):
+        with pytest.raises(ValueError, match="device|HIP|cuda"):
+            call(**{"dw": dw, **beside})

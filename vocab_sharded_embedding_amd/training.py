@@ -80,6 +80,15 @@ def nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
+def apart(name: str, t, *others) -> None:
+    """Refuse a `t` (written) that shares bytes with one of the `others`."""
+    begin, end = t.data_ptr(), t.data_ptr() + nbytes(t)
+    for o in others:
+        at, size = o.data_ptr(), nbytes(o)
+        if at < end and begin < at + size and size and begin < end:
+            raise ValueError(f"{name} must not overlap the call's other tensors")
+
+
 def vpe_embed_scaled(ids, weight, vocab_start: int, scale: float, out=None):
     """vpe_embed with every owned row times `scale` (fp32 product, one rounding)."""
     if weight.dim() != 2:
@@ -112,7 +121,8 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
     ids [*] and grad_out [*, dim] are the lookup's ids and the gradient of its
     output.  The result goes to `grad_weight` (added to it when `accumulate`),
     or to a new tensor of `dtype` (grad_out's when None).  Rows of positions
-    whose id lies outside the shard add nothing.
+    whose id lies outside the shard add nothing.  A `grad_weight` or `workspace`
+    that overlaps another tensor of the call is refused.
     """
     if grad_out.dim() < 1 or grad_out.shape[:-1] != ids.shape:
         raise ValueError("grad_out must be [*ids.shape, dim]")
@@ -127,7 +137,10 @@ def vpe_embed_grad(ids, grad_out, vocab_start: int, shard_rows: int, scale: floa
             raise ValueError("dtype differs from grad_weight's")
         if grad_weight.shape != (shard_rows, dim):
             raise ValueError("grad_weight must be [shard_rows, dim]")
-    if workspace is None:
+        apart("grad_weight", grad_weight, ids, grad_out)
+    if workspace is not None:
+        apart("workspace", workspace, ids, grad_out, grad_weight)
+    else:
         workspace = new_workspace(vpe_embed_grad_workspace(n, int(shard_rows), dim), grad_out.device)
     index = placed("ids grad_out grad_weight workspace", ids, grad_out, grad_weight, workspace)
     enqueue("vpe_embed_grad", index, ids.data_ptr(), itype_code(ids), n, grad_out.data_ptr(),
