@@ -48,8 +48,9 @@ vpe_status vpe_embed_grad_workspace(int64_t n, int64_t shard_rows, int64_t dim, 
  *                     = rnd(grad_weight[j, :] + s[j, :])   accumulate != 0
  *
  * The positions are sorted by token (stable) and each token's rows summed in
- * fp32, in ascending i inside fixed pieces of the sorted order; one rounding
- * to `gdt`.  Ids outside the shard add nothing, whatever their grad_out rows
+ * ascending i inside fixed pieces of the sorted order, one rounding to `gdt`: at
+ * most 32 rows, and 16 such sums, in fp32, and what is longer in 64 bits, so that
+ * a sum's error does not grow with the number of its rows.  Ids outside the shard add nothing, whatever their grad_out rows
  * hold (a padding id such as -1 takes no gradient).  With accumulate == 0
  * every row of grad_weight is written, +0.0 where the shard row has no id;
  * with accumulate != 0 rows without an id are left as they are.

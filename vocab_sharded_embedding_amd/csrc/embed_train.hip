@@ -598,7 +598,11 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
 }
 
 // One wave per chunk and block of 256 columns: the run that leaves the chunk
-// having begun in it is joined from its partial sums, in order.  Long runs are
+// having begun in it is joined from its partial sums, in order: 16 in fp32, and
+// those sums in 64 bits, as a run has up to 2^26 pieces (added one by one in fp32,
+// pieces of one sign lost 1.6e-4 of the sum of 2^21 positions; each of them in 64
+// bits took 160 instead of 109 us for 131072 Zipf ids over 8192 rows x 1024, this
+// takes 110).  Long runs are
 // joined by the workgroup's waves together, a quarter each.  Workgroups after
 // them write zero rows.  Bound by latency: 4 us where no run is long; 65536 Zipf
 // ids, 165 pieces in the longest run, 19.4 us with 64 MB of zero rows beside it.
@@ -609,7 +613,7 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
                                                    int col_blocks, unsigned join_blocks,
                                                    ZeroRows zero) {
   constexpr int kDeep = 16;  // partial sums in flight
-  __shared__ f32x4 part[kWaves][64];
+  __shared__ f64x4 part[kWaves][64];
   __shared__ int64_t long_more[kWaves], long_slot0[kWaves];
   __shared__ uint32_t long_token[kWaves];
   if (blockIdx.x >= join_blocks) return zero_rows<true>(zero, blockIdx.x - join_blocks, kBlock);
@@ -654,7 +658,7 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
   // pieces i0 .. i1 - 1 of the run of chunk `of`: 0 in that chunk, i in chunk of +
   // i, at its first position; partial rows are padded past dim
   auto pieces = [&](int64_t of, int64_t slot0, int64_t i0, int64_t i1) {
-    f32x4 sum = f32x4(0.f);
+    f64x4 sum = f64x4(0.0);
     if (col < a.dim) {
       for (int64_t i = i0; i < i1; i += kDeep) {
         f32x4 r[kDeep];
@@ -665,15 +669,18 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
           if (i + u < i1)
             r[u] = *reinterpret_cast<const f32x4 *>(a.partial + slot * a.partial_ld + col);
         }
+        f32x4 some = f32x4(0.f);
 #pragma unroll
         for (int u = 0; u < kDeep; ++u)
-          if (i + u < i1) sum += r[u];
+          if (i + u < i1) some += r[u];
+        sum += __builtin_convertvector(some, f64x4);
       }
     }
     return sum;
   };
-  auto write = [&](uint32_t run, f32x4 sum) {
-    const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+  auto write = [&](uint32_t run, f64x4 sum) {
+    const f32x4 r = __builtin_convertvector(sum, f32x4);
+    const float v[4] = {r[0], r[1], r[2], r[3]};
     if (col < a.dim) write_row<OUT16, 4>(a, run, col, v);
   };
 
@@ -690,7 +697,7 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
     part[wave][lane] = pieces(c0 + w, long_slot0[w], i0, i0 + share <= m ? i0 + share : m + 1);
     __syncthreads();
     if (wave == 0) {
-      f32x4 sum = part[0][lane];
+      f64x4 sum = part[0][lane];
 #pragma unroll
       for (int q = 1; q < kWaves; ++q) sum += part[q][lane];
       write(long_token[w], sum);
