@@ -106,8 +106,12 @@ vpe_status vpe_embed_grad(const void *ids, vpe_itype itype, int64_t n, const voi
 #define VPE_MAX_TEACHER_ENTRIES 1024
 #define VPE_MAX_DISTILL_ROWS (1 << 21)
 
-/* Bytes of workspace vpe_distill_shard needs for m rows; as much serves fewer.
- * Host-only.
+/* From this many rows on vpe_distill_shard gives each a workgroup of its own,
+ * and needs no workspace. */
+#define VPE_DISTILL_WHOLE_ROWS 256
+
+/* Bytes of workspace that serve vpe_distill_shard for m rows and for fewer (so
+ * not 0 from VPE_DISTILL_WHOLE_ROWS rows on).  Host-only.
  * Errors: VPE_ERR_NULL, VPE_ERR_SHAPE (m < 0 or > VPE_MAX_DISTILL_ROWS,
  * shard_rows < 1 or >= 2^31). */
 vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes);
@@ -130,7 +134,8 @@ vpe_status vpe_distill_workspace(int64_t m, int64_t shard_rows, int64_t *bytes);
  * shard_dot    device float [m].
  * workspace    device, at least vpe_distill_workspace(m, shard_rows) bytes,
  *              8-byte aligned; needs no initialisation, not shared by calls
- *              that may run at the same time; may be NULL where shard_lse is.
+ *              that may run at the same time; may be NULL where shard_lse is,
+ *              and from VPE_DISTILL_WHOLE_ROWS rows on.
  * m == 0 is a no-op.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (m < 0 or
  * > VPE_MAX_DISTILL_ROWS, shard_rows < 1 or >= 2^31, k outside [1,

@@ -44,6 +44,7 @@ BEAM_SYMBOLS = ("vpe_beam_select_workspace", "vpe_beam_select", "vpe_beam_merge"
                 "vpe_beam_reorder")
 VPE_MAX_TEACHER_ENTRIES = 1024
 VPE_MAX_DISTILL_ROWS = 1 << 21
+VPE_DISTILL_WHOLE_ROWS = 256
 VPE_MAX_BEAMS = VPE_MAX_BEAM_PICKS = 64
 
 

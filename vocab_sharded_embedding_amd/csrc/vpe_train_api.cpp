@@ -173,7 +173,8 @@ vpe_status vpe_distill_shard(const void *logits, int64_t ld, int64_t col_offset,
   if (!aligned(logits, dtype_bytes(dt)) || !aligned(shard_lse, 4) || !aligned(shard_dot, 4) ||
       !aligned(workspace, 8))
     return VPE_ERR_ALIGN;
-  if (shard_lse) {
+  static_assert(vpe::kDistillWholeRows == VPE_DISTILL_WHOLE_ROWS, "rows without pairs in memory");
+  if (shard_lse && m < VPE_DISTILL_WHOLE_ROWS) {
     int64_t need = 0;
     rs = vpe_distill_workspace(m, shard_rows, &need);
     if (rs != VPE_OK) return rs;

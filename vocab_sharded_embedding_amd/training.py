@@ -15,7 +15,8 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import _check, _dtype_code, _itype_code, _need_device, _same_device, load_library
+from . import (VPE_DISTILL_WHOLE_ROWS, _check, _dtype_code, _itype_code, _need_device,
+               _same_device, load_library)
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 _ITYPES = {torch.int32: 0, torch.int64: 1}
@@ -180,8 +181,8 @@ def logits_shard(name: str, logits, shard_rows: Optional[int], col_offset: int):
 
 @functools.lru_cache(maxsize=256)
 def vpe_distill_workspace(m: int, shard_rows: int) -> int:
-    """Bytes of workspace vpe_distill_shard needs for m rows (none if with_lse is
-    False); as much serves fewer."""
+    """Bytes of workspace that serve vpe_distill_shard for m rows and for fewer (it
+    needs none if with_lse is False, or from VPE_DISTILL_WHOLE_ROWS rows on)."""
     b = ctypes.c_int64()
     _check("vpe_distill_workspace", load_library().vpe_distill_workspace(
         m, shard_rows, ctypes.byref(b)))
@@ -212,12 +213,13 @@ def vpe_distill_shard(logits, teacher_ids, teacher, vocab_start: int, vocab: int
             shard_lse = torch.empty_like(shard_dot)
         else:
             float_rows("shard_lse", shard_lse, m)
-        if workspace is None:
+        if workspace is None and m < VPE_DISTILL_WHOLE_ROWS:
             workspace = new_workspace(vpe_distill_workspace(m, rows), logits.device)
+        given = () if workspace is None else (workspace,)
         index = placed("logits teacher_ids teacher shard_dot shard_lse workspace", logits,
-                       teacher_ids, teacher, shard_dot, shard_lse, workspace)
-        tail = (shard_lse.data_ptr(), shard_dot.data_ptr(), workspace.data_ptr(),
-                nbytes(workspace))
+                       teacher_ids, teacher, shard_dot, shard_lse, *given)
+        tail = (shard_lse.data_ptr(), shard_dot.data_ptr(),
+                *((workspace.data_ptr(), nbytes(workspace)) if given else (None, 0)))
     elif shard_lse is not None:
         raise ValueError("shard_lse given with with_lse=False")
     else:
