@@ -181,20 +181,25 @@ struct ZeroRows {
   int log2g;  // lanes that clear a row with flags
 };
 
-// `block` of z.blocks workgroups of `threads` threads.  Plain stores where the
-// whole shard is cleared beside one sorting workgroup (8192 ids, 156 MB: 30 us
-// against 39 with non-temporal ones), non-temporal ones (NT) where many sorted
-// rows are read meanwhile and after, which plain ones push out of the caches
-// (65536 ids, 622 MB: 166 us against 186).
+// `block` of z.blocks workgroups of `threads` threads, all of their rows.  Plain
+// stores where the whole shard is cleared beside one sorting workgroup (8192 ids,
+// 156 MB: 30 us against 39 with non-temporal ones), non-temporal ones (NT) where
+// many sorted rows are read meanwhile and after, which plain ones push out of the
+// caches (65536 ids, 622 MB: 166 us against 186).
 template <bool NT>
+__device__ __forceinline__ void zero_all_rows(const ZeroRows &z, unsigned block, int threads) {
+  const int64_t share = (z.row1 - z.row0 + z.blocks - 1) / z.blocks;
+  const int64_t r0 = z.row0 + block * share, r1 = r0 + share < z.row1 ? r0 + share : z.row1;
+  if (r0 < r1)
+    zero_bytes<NT>(z.dw + r0 * z.row_bytes, (r1 - r0) * z.row_bytes, threadIdx.x, threads);
+}
+
+// The same beside the passes, and of rows with flags those without an id.
 __device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int threads) {
+  if (z.flags == nullptr) return zero_all_rows<true>(z, block, threads);
   const int64_t share = (z.row1 - z.row0 + z.blocks - 1) / z.blocks;
   const int64_t r0 = z.row0 + block * share, r1 = r0 + share < z.row1 ? r0 + share : z.row1;
   if (r0 >= r1) return;
-  if (z.flags == nullptr) {
-    zero_bytes<NT>(z.dw + r0 * z.row_bytes, (r1 - r0) * z.row_bytes, threadIdx.x, threads);
-    return;
-  }
   // a contiguous part per wave
   const int lane = threadIdx.x & 63, waves = threads / 64;
   const int64_t part = (r1 - r0 + waves - 1) / waves, w0 = r0 + wave_in_block() * part;
@@ -210,7 +215,7 @@ __device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int
 #pragma unroll
       for (int u = 0; u < kDeep; ++u)
         if (has_id[u] == 0)
-          zero_bytes<NT>(z.dw + (r + u * step) * z.row_bytes, z.row_bytes, in, 1 << z.log2g);
+          zero_bytes<true>(z.dw + (r + u * step) * z.row_bytes, z.row_bytes, in, 1 << z.log2g);
     }
     return;
   }
@@ -219,7 +224,7 @@ __device__ __forceinline__ void zero_rows(const ZeroRows &z, unsigned block, int
     while (empty) {
       const int64_t row = r + __builtin_ctzll(empty);
       empty &= empty - 1;
-      zero_bytes<NT>(z.dw + row * z.row_bytes, z.row_bytes, lane, 64);
+      zero_bytes<true>(z.dw + row * z.row_bytes, z.row_bytes, lane, 64);
     }
   }
 }
@@ -240,7 +245,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_block(
   __shared__ uint16_t spos[2][kGradOneBlockIds];
   __shared__ uint32_t at_[kSortWaves][kDigits];
   __shared__ uint32_t sums[kDigits / 64];
-  if (blockIdx.x > 0) return zero_rows<false>(zero, blockIdx.x - 1, kSortThreads);
+  if (blockIdx.x > 0) return zero_all_rows<false>(zero, blockIdx.x - 1, kSortThreads);
   // a wave reads and updates its own counters in program order
   volatile uint32_t(*at)[kDigits] = at_;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
@@ -318,6 +323,7 @@ struct SortItems {
   const IdT *ids;
   const uint32_t *key_in, *pos_in;
   uint64_t start, rows;
+  uint8_t *flags;  // FIRST: of the rows, or nullptr
   __device__ __forceinline__ bool get(int64_t i, uint32_t &key) const {
     if constexpr (FIRST) {
       const uint64_t local = static_cast<uint64_t>(static_cast<int64_t>(ids[i])) - start;
@@ -343,13 +349,12 @@ struct SortPass {
 template <bool FIRST, typename IdT>
 __global__ __launch_bounds__(kSortThreads) void sort_counts(SortItems<FIRST, IdT> items,
                                                            SortPass pass, const uint32_t *count,
-                                                           uint32_t *hist, uint8_t *flags,
-                                                           ZeroRows zero) {
+                                                           uint32_t *hist, ZeroRows zero) {
   __shared__ uint32_t h[kDigits];
-  if (blockIdx.x >= pass.blocks) return zero_rows<true>(zero, blockIdx.x - pass.blocks, kSortThreads);
+  if (blockIdx.x >= pass.blocks) return zero_rows(zero, blockIdx.x - pass.blocks, kSortThreads);
   const int tid = threadIdx.x;
-  if (FIRST && flags != nullptr) {
-    u32x4 *f = reinterpret_cast<u32x4 *>(flags);
+  if (FIRST && items.flags != nullptr) {
+    u32x4 *f = reinterpret_cast<u32x4 *>(items.flags);
     const int64_t nf = static_cast<int64_t>((items.rows + 15) / 16);
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; i < nf;
          i += static_cast<int64_t>(pass.blocks) * kSortThreads)
@@ -377,14 +382,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_counts(SortItems<FIRST, IdT
 template <bool FIRST, typename IdT>
 __global__ __launch_bounds__(kSortThreads) void sort_scatter(
     SortItems<FIRST, IdT> items, SortPass pass, uint32_t *count, const uint32_t *__restrict__ hist,
-    uint32_t *__restrict__ key_out, uint32_t *__restrict__ pos_out, uint8_t *flags,
-    ZeroRows zero) {
+    uint32_t *__restrict__ key_out, uint32_t *__restrict__ pos_out, ZeroRows zero) {
   constexpr int kParts = kSortThreads / (kDigits / 2);  // threads that share a pair of digits
   __shared__ uint32_t at_[kSortWaves][kDigits];
   __shared__ u32x2 part_before[kParts][kDigits / 2], part_total[kParts][kDigits / 2];
   __shared__ uint32_t base[kDigits];
   __shared__ uint32_t sums[kDigits / 128];
-  if (blockIdx.x >= pass.blocks) return zero_rows<true>(zero, blockIdx.x - pass.blocks, kSortThreads);
+  if (blockIdx.x >= pass.blocks) return zero_rows(zero, blockIdx.x - pass.blocks, kSortThreads);
   // a wave reads and updates its own counters in program order
   volatile uint32_t(*at)[kDigits] = at_;
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_in_block();
@@ -473,7 +477,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter(
         if (below(same) == 0) at[wave][d] = seen + __popcll(same);
         key_out[to] = key[u];
         pos_out[to] = from[u];
-        if (FIRST && flags != nullptr) flags[key[u]] = 1;
+        if (FIRST && items.flags != nullptr) items.flags[key[u]] = 1;
       }
     }
   }
@@ -521,7 +525,7 @@ __device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64
 template <bool IN16, bool OUT16, int EPV>
 __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0, int64_t n_chunks,
                                                      unsigned chunk_blocks, ZeroRows zero) {
-  if (blockIdx.x >= chunk_blocks) return zero_rows<true>(zero, blockIdx.x - chunk_blocks, kBlock);
+  if (blockIdx.x >= chunk_blocks) return zero_rows(zero, blockIdx.x - chunk_blocks, kBlock);
   typedef Vec<IN16, EPV> V;
   constexpr int kDeep = 8;
   const int lane = threadIdx.x & 63;
@@ -616,7 +620,7 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
   __shared__ f64x4 part[kWaves][64];
   __shared__ int64_t long_more[kWaves], long_slot0[kWaves];
   __shared__ uint32_t long_token[kWaves];
-  if (blockIdx.x >= join_blocks) return zero_rows<true>(zero, blockIdx.x - join_blocks, kBlock);
+  if (blockIdx.x >= join_blocks) return zero_rows(zero, blockIdx.x - join_blocks, kBlock);
   const int lane = threadIdx.x & 63, wave = wave_in_block();
   const unsigned group = blockIdx.x / static_cast<unsigned>(col_blocks);
   const int64_t col = (static_cast<int64_t>(blockIdx.x - group * col_blocks) * 64 + lane) * 4;
@@ -723,8 +727,8 @@ int launch_sums(GradArgs a, int64_t n, ZeroRows zero, ZeroRows join_zero, hipStr
   a.col_blocks = static_cast<int>(blocks);
   // chunks per launch: grids stay inside the 32-bit range
   const int64_t step = std::max<int64_t>(1, (int64_t(1) << 24) / blocks);
-  for (int64_t c = 0; c < chunks || zero.blocks > 0; c += step) {
-    const int64_t nc = std::max<int64_t>(0, std::min(step, chunks - c));
+  for (int64_t c = 0; c < chunks; c += step) {
+    const int64_t nc = std::min(step, chunks - c);
     const unsigned cb = static_cast<unsigned>((nc * blocks + kWaves - 1) / kWaves);
     hipLaunchKernelGGL((grad_chunks<IN16, OUT16, kEpv>), dim3(cb + zero.blocks), dim3(kBlock), 0,
                        st, a, c, nc, cb, zero);
@@ -793,23 +797,22 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
       last = pass & 1;
       ps.shift = pass * bits;
       if (pass == 0) {
-        SortItems<true, IdT> it{ids, nullptr, nullptr, start, urows};
+        SortItems<true, IdT> it{ids, nullptr, nullptr, start, urows, flags};
         ride(early, nullptr);
         hipLaunchKernelGGL((sort_counts<true, IdT>), dim3(ps.blocks + zero.blocks),
-                           dim3(kSortThreads), 0, st, it, ps, count, hist, flags, zero);
+                           dim3(kSortThreads), 0, st, it, ps, count, hist, zero);
         ride(early, nullptr);
         hipLaunchKernelGGL((sort_scatter<true, IdT>), dim3(ps.blocks + zero.blocks),
-                           dim3(kSortThreads), 0, st, it, ps, count, hist, key[0], pos[0], flags,
-                           zero);
+                           dim3(kSortThreads), 0, st, it, ps, count, hist, key[0], pos[0], zero);
       } else {
-        SortItems<false, IdT> it{nullptr, key[1 - last], pos[1 - last], start, urows};
+        SortItems<false, IdT> it{nullptr, key[1 - last], pos[1 - last], start, urows, nullptr};
         ride(later, flags);
         hipLaunchKernelGGL((sort_counts<false, IdT>), dim3(ps.blocks + zero.blocks),
-                           dim3(kSortThreads), 0, st, it, ps, count, hist, flags, zero);
+                           dim3(kSortThreads), 0, st, it, ps, count, hist, zero);
         ride(later, flags);
         hipLaunchKernelGGL((sort_scatter<false, IdT>), dim3(ps.blocks + zero.blocks),
                            dim3(kSortThreads), 0, st, it, ps, count, hist, key[last], pos[last],
-                           flags, zero);
+                           zero);
       }
     }
     // The rest beside the sums; the last 64 MB beside their join, which waits
