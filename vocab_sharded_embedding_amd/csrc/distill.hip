@@ -525,13 +525,18 @@ int launch_distill_shard(const LogitsShard &z, const Teacher &t, float *shard_ls
   const ShardArgs a = args_of(z, pair_cols(z.dtype));
   const TeacherArgs ta = args_of(t);
   Pair *pr = reinterpret_cast<Pair *>(pairs);
-  // A workgroup per row, unless a few long rows would leave the chip idle.  us
-  // with a workgroup per row / with pairs in memory, in a graph, fp32: 8 rows of
-  // 38 slices 6.3 / 6.7, of 149 slices 16.6 / 8.5; 64 rows of 75 slices 9.9 /
-  // 10.8, of 149 slices 18.8 / 14.9; 256 rows of 149 slices 29.7 / 33.5; 4096
-  // rows of 4 slices 16.7 / 20.6.  Waves have two slices each where they can:
+  // A workgroup per row, unless a few long rows would leave the chip idle; a bf16
+  // slice has twice the columns of an fp32 one.  us with a workgroup per row / with
+  // pairs in memory, in a graph, fp32: 8 rows of 38 slices 6.4 / 7.1, of 149 slices
+  // 16.4 / 8.7; 64 rows of 75 slices 10.8 / 11.2, of 149 slices 18.4 / 14.7; 255
+  // rows of 149 slices 28.9 / 33.1; 4096 rows of 4 slices 16.7 / 20.6.  bf16: 8 rows
+  // of 24 slices 6.8 / 7.3, of 75 slices 13.4 / 8.5; 128 rows of 44 slices 12.0 /
+  // 12.7, of 75 slices 18.3 / 15.8; 255 rows of 75 slices 21.3 / 22.1.  (Of 240
+  // points of 1 to 255 rows and 24 to 149 slices the rule takes the slower side by
+  // more than a tenth at one, 11%.)  Waves have two slices each where they can:
   // 4096 bf16 rows of 8 slices 30.8 with 4 waves, 34.6 with 8.
-  if (shard_lse && (z.m >= kDistillWholeRows || a.slices <= 40 + z.m / 2)) {
+  const int64_t few = z.dtype == 1 ? 26 + z.m / 4 : 44 + z.m / 2;
+  if (shard_lse && (z.m >= kDistillWholeRows || a.slices <= few)) {
     const int waves = std::min((a.slices + 1) / 2, kRowWaves);
     const dim3 grid(static_cast<unsigned>(z.m)), block(64 * (waves + 1));
     if (z.dtype == 1)
