@@ -65,3 +65,16 @@ def test_lookup_gradient_over_its_own_inputs():
                         .view(0, dim))):
         with pytest.raises(ValueError, match="device|HIP|cuda"):
             call(**{"dw": dw, **beside})
+
+
+def test_scaled_lookup_over_its_own_inputs():
+    rows, dim, n = 10, 8, 4
+    pool = torch.zeros(4096)
+    weight, out = pool[:rows * dim].view(rows, dim), pool[72:72 + n * dim].view(n, dim)
+    ids = pool[100:100 + n].view(torch.int32)  # inside out
+    for bad in ((torch.zeros(n, dtype=torch.int32), weight), (ids, torch.zeros(rows, dim))):
+        with pytest.raises(ValueError, match="overlap"):
+            vpe.vpe_embed_scaled(*bad, 0, 2.0, out=out)
+    with pytest.raises(ValueError, match="HIP"):  # neighbours: the device is what is wrong
+        vpe.vpe_embed_scaled(pool[112:116].view(torch.int32), weight, 0, 2.0,
+                             out=pool[80:80 + n * dim].view(n, dim))

@@ -97,8 +97,10 @@ def vpe_embed_scaled(ids, weight, vocab_start: int, scale: float, out=None):
     rows, dim = weight.shape
     if out is None:
         out = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=weight.device)
-    elif out.dtype != weight.dtype or out.numel() != ids.numel() * dim:
-        raise ValueError("out must have the weight's dtype and ids.numel() * dim elements")
+    else:
+        if out.dtype != weight.dtype or out.numel() != ids.numel() * dim:
+            raise ValueError("out must have the weight's dtype and ids.numel() * dim elements")
+        apart("out", out, ids, weight)
     index = placed("ids weight out", ids, weight, out)
     enqueue("vpe_embed_scaled", index, ids.data_ptr(), itype_code(ids), ids.numel(),
             weight.data_ptr(), dtype_code(weight), rows, dim, int(vocab_start), scale,
