@@ -9,7 +9,8 @@
  * on the host before anything is enqueued on `stream`, and values in device
  * memory (ids, teacher entries) are not checked but have defined results.
  * Every sum is taken in fp32 or more, in an order fixed by the arguments: no
- * atomics on values, so the same inputs give the same bits.
+ * atomics on values, so the same inputs give the same bits.  Gradients are calls
+ * of their own; the Python binding builds no autograd graph either.
  */
 #ifndef VPE_TRAIN_H
 #define VPE_TRAIN_H

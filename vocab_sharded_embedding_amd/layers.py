@@ -9,7 +9,9 @@ parameter.  Their ``forward`` calls the library; there is no collective here:
 ranks emulated in one process combine their outputs with
 ``VocabParallelEmbedding.sum_partials`` (the embedding's all-reduce) and by
 writing their logits at ``vocab_start`` into one [M, V] buffer (the LM head's
-gather and concatenation).
+gather and concatenation).  No call builds an autograd graph: ``backward()`` does
+not reach through these layers, and ``weight_grad`` and ``distill_grad`` are
+called explicitly.
 """
 from __future__ import annotations
 

@@ -5,7 +5,9 @@ teacher's top logits over the ranks' shards of the logits.
 As in the package itself, functions only marshal arguments: they check
 placement, dtype and layout, allocate outputs and workspaces with
 ``torch.empty`` when none is given, and pass raw device pointers plus the
-current HIP stream of the tensors' device to the library.
+current HIP stream of the tensors' device to the library.  No autograd graph is
+built: outputs do not require gradients, whatever the inputs do, and the
+gradient calls are made explicitly.
 """
 from __future__ import annotations
 
