@@ -343,8 +343,8 @@ struct SortPass {
 };
 
 // hist[b][d] = items of digit d in workgroup b's tile.  The first pass also
-// clears the rows' flags.  Latency again: 65536 ids of 18 bits, counts 6.2 and
-// scatter 8.5 us in the first pass; the second pass's 28 us each are the time of
+// clears the rows' flags.  Latency again: 65536 ids of 18 bits, counts 6.4 and
+// scatter 8.7 us in the first pass; the second pass's 28 us each are the time of
 // the 142 MB that the workgroups beside them clear (5.1 TB/s).
 template <bool FIRST, typename IdT>
 __global__ __launch_bounds__(kSortThreads) void sort_counts(SortItems<FIRST, IdT> items,
@@ -609,9 +609,10 @@ __global__ __launch_bounds__(kBlock) void grad_chunks(GradArgs a, int64_t chunk0
 // takes 110).  Long runs are
 // joined by the workgroup's waves together, a quarter each.  Workgroups after
 // them write zero rows.  Bound by latency: 4 us where no run is long; 65536 Zipf
-// ids, 165 pieces in the longest run, 19.4 us with 64 MB of zero rows beside it.
-// (The whole gradient of those took 162.4, 167 and 177 us with a workgroup of 4, 8
-// and 16 waves per chunk, 159.7 us this way: most chunks have nothing to join.)
+// ids (exponent 1.1), 272 pieces in the longest run, 19.2 us with 64 MB of zero
+// rows beside it.  (The whole gradient of those took 162.4, 167 and 177 us with a
+// workgroup of 4, 8 and 16 waves per chunk, 159.7 us this way: most chunks have
+// nothing to join.  Rows of 64 columns, 131072 Zipf ids: 60 us then, 63 now.)
 template <bool OUT16>
 __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, int64_t n_chunks,
                                                    int col_blocks, unsigned join_blocks,
@@ -711,7 +712,12 @@ __global__ __launch_bounds__(kBlock) void grad_join(GradArgs a, int64_t chunk0, 
 }
 
 // Workgroups for `rows` rows of zeros: about `span` bytes each (a row's flag
-// costs as much as 64).
+// costs as much as 64).  Of 1024 threads beside the sort, us of the whole gradient
+// with 64 KB / 256 KB / 1 MB each: 8192 ids over 75968 rows of bf16 30.5 / 30.2 /
+// 38.3; 65536 Zipf ids over 151936 fp32 rows 161.2 / 159.4 / 166.5, uniform ones
+// 166.0 / 165.0 / 171.6; 131072 Zipf ids over as many bf16 rows 149.9 / 153.8 /
+// 161.4.  Of 256 threads beside the sums, with 64 / 256 KB: 65536 Zipf ids 159.6 /
+// 161.4, uniform ones 165.1 / 167.6.
 unsigned zero_blocks(int64_t rows, int64_t row_bytes, double span = 262144.0) {
   if (rows <= 0) return 0;
   const double bytes = static_cast<double>(rows) * std::max(64.0, static_cast<double>(row_bytes));
@@ -784,7 +790,9 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
     uint8_t *flags = a.accumulate ? nullptr : reinterpret_cast<uint8_t *>(ws + l.flags);
     // The flags are complete after the first pass: each later launch of the
     // sort clears an equal part of half the rows without an id.  The first two
-    // clear what fits their time, about 24 MB, with or without one.
+    // clear what fits their time, about 24 MB, with or without one (65536 Zipf ids:
+    // 159.6 us, 164.5 with none, 161.8 with 12 MB, 159.7 with 48; uniform ids 165.0,
+    // 168.1, 167.2 and 166.8).
     auto ride = [&](int64_t ride_rows, const uint8_t *ride_flags) {
       zero.flags = ride_flags;
       zero.row0 = zero.row1;
@@ -816,8 +824,9 @@ int grad_any(const IdT *ids, int64_t n, GradArgs a, int64_t rows, int dtype, int
       }
     }
     // The rest beside the sums; the last 64 MB beside their join, which waits
-    // for the pieces of the longest runs one after the other (65536 Zipf ids:
-    // 3 us less of 160 than with none there).
+    // for the pieces of the longest runs one after the other (65536 Zipf ids: 159.4
+    // us, 163.6 with none there, 161.1 with 32 MB, 159.9 with 128; uniform ids 165.2,
+    // 166.2, 164.8 and 167.7).
     const int64_t rest = zero_to - zero.row1;
     const int64_t sums_to = zero_to - std::min(rest / 2, (int64_t(64) << 20) / zero.row_bytes);
     auto beside = [&](int64_t row0, int64_t row1) {
