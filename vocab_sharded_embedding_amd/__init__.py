@@ -9,7 +9,8 @@ loading fails loudly when the library is missing or cannot be loaded.
 
 Names follow the C ABI: ``vpe_shard_range``, ``vpe_embed``,
 ``vpe_sum_partials``, ``vpe_last_token_select``, ``vpe_lmhead``.  The training
-calls live in ``training.py`` and the beam-search calls in ``beam.py``, and are
+calls live in ``training.py``, the beam-search calls in ``beam.py`` and the loss
+calls (cross entropy, the head's backward, clipping) in ``loss.py``, and are
 re-exported here.
 """
 from __future__ import annotations
@@ -42,10 +43,18 @@ TRAIN_SYMBOLS = ("vpe_embed_scaled", "vpe_embed_grad_workspace", "vpe_embed_grad
                  "vpe_distill_grad")
 BEAM_SYMBOLS = ("vpe_beam_select_workspace", "vpe_beam_select", "vpe_beam_merge",
                 "vpe_beam_reorder")
+# include/vpe_loss.h
+LOSS_SYMBOLS = ("vpe_lmhead_xent_workspace", "vpe_lmhead_xent", "vpe_xent_loss",
+                "vpe_lmhead_xent_grad_workspace", "vpe_lmhead_xent_grad",
+                "vpe_lmhead_grad_workspace", "vpe_lmhead_grad", "vpe_grad_sumsq_workspace",
+                "vpe_grad_sumsq", "vpe_grad_clip")
 VPE_MAX_TEACHER_ENTRIES = 1024
 VPE_MAX_DISTILL_ROWS = 1 << 21
 VPE_DISTILL_WHOLE_ROWS = 256
 VPE_MAX_BEAMS = VPE_MAX_BEAM_PICKS = 64
+VPE_MAX_LOSS_ROWS = 1 << 21
+VPE_MAX_LOSS_DIM = 1 << 16
+VPE_MAX_GRAD_TENSORS = 1 << 16
 
 
 class VpeError(RuntimeError):
@@ -131,7 +140,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                     vp, i64, vp]
     lib.vpe_beam_merge.argtypes = [pvp, i32, i64, i32, i64, vp, vp, vp, vp]
     lib.vpe_beam_reorder.argtypes = [vp, i64, i64, i32, i64, vp, i64, i32, vp, vp]
-    for name in EXPORTED_SYMBOLS[:-1] + TRAIN_SYMBOLS + BEAM_SYMBOLS:
+    pi32 = ctypes.POINTER(i32)
+    lib.vpe_lmhead_xent_workspace.argtypes = [i64, i64, i64, ci, pi64]
+    lib.vpe_lmhead_xent.argtypes = [vp, i64, i64, vp, i64, ci, i64, i64, vp, ci, vp, vp, vp, i64,
+                                    vp]
+    lib.vpe_xent_loss.argtypes = [pvp, pvp, i32, i64, i64, vp, ci, vp, vp, vp]
+    lib.vpe_lmhead_xent_grad_workspace.argtypes = [i64, i64, i64, ci, pi64]
+    lib.vpe_lmhead_xent_grad.argtypes = [vp, i64, i64, vp, i64, ci, i64, i64, vp, ci, vp, vp, vp,
+                                         ci, vp, ci, i32, vp, i64, vp]
+    lib.vpe_lmhead_grad_workspace.argtypes = [i64, i64, i64, ci, pi64]
+    lib.vpe_lmhead_grad.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, ci, vp, ci, vp, ci, i32,
+                                    vp, i64, vp]
+    lib.vpe_grad_sumsq_workspace.argtypes = [pi64, i32, pi64]
+    lib.vpe_grad_sumsq.argtypes = [pvp, pi64, pi32, i32, vp, vp, i64, vp]
+    lib.vpe_grad_clip.argtypes = [pvp, pi64, pi32, i32, pvp, pvp, i32, ctypes.c_double, vp, vp]
+    for name in EXPORTED_SYMBOLS[:-1] + TRAIN_SYMBOLS + BEAM_SYMBOLS + LOSS_SYMBOLS:
         getattr(lib, name).restype = ci
     lib.vpe_status_string.argtypes = [ci]
     lib.vpe_status_string.restype = ctypes.c_char_p
@@ -585,6 +608,10 @@ from .training import (vpe_distill_grad, vpe_distill_loss, vpe_distill_shard,  #
                        vpe_embed_scaled)
 from .beam import (vpe_beam_merge, vpe_beam_reorder, vpe_beam_select,  # noqa: E402
                    vpe_beam_select_workspace)
+from .loss import (vpe_grad_clip, vpe_grad_sumsq, vpe_grad_sumsq_workspace,  # noqa: E402
+                   vpe_lmhead_grad, vpe_lmhead_grad_workspace, vpe_lmhead_xent,
+                   vpe_lmhead_xent_grad, vpe_lmhead_xent_grad_workspace,
+                   vpe_lmhead_xent_workspace, vpe_xent_loss)
 from .layers import ParallelLMHead, VocabParallelEmbedding  # noqa: E402
 
 __all__ = [
@@ -598,4 +625,7 @@ __all__ = [
     "vpe_embed_scaled", "vpe_embed_grad_workspace", "vpe_embed_grad", "vpe_distill_workspace",
     "vpe_distill_shard", "vpe_distill_loss", "vpe_distill_grad", "vpe_beam_select_workspace",
     "vpe_beam_select", "vpe_beam_merge", "vpe_beam_reorder",
+    "vpe_lmhead_xent_workspace", "vpe_lmhead_xent", "vpe_xent_loss",
+    "vpe_lmhead_xent_grad_workspace", "vpe_lmhead_xent_grad", "vpe_lmhead_grad_workspace",
+    "vpe_lmhead_grad", "vpe_grad_sumsq_workspace", "vpe_grad_sumsq", "vpe_grad_clip",
 ]

@@ -20,8 +20,9 @@ OBJDIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-HIP_SOURCES = ["gather.hip", "lmhead.hip", "embed_train.hip", "distill.hip", "beam.hip"]
-CXX_SOURCES = ["vpe_api.cpp", "vpe_train_api.cpp", "vpe_beam_api.cpp"]
+HIP_SOURCES = ["gather.hip", "lmhead.hip", "embed_train.hip", "distill.hip", "beam.hip",
+               "head_loss.hip", "grad_clip.hip"]
+CXX_SOURCES = ["vpe_api.cpp", "vpe_train_api.cpp", "vpe_beam_api.cpp", "vpe_loss_api.cpp"]
 
 HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17", "-Wall",
@@ -37,7 +38,8 @@ def source_files() -> List[str]:
     internal headers, the public headers and build.py itself."""
     names = sorted(f for f in os.listdir(CSRC)
                    if f.endswith((".hip", ".cpp", ".h")))
-    headers = [os.path.join(INCLUDE, h) for h in ("vpe.h", "vpe_train.h", "vpe_beam.h")]
+    headers = [os.path.join(INCLUDE, h) for h in ("vpe.h", "vpe_train.h", "vpe_beam.h",
+                                                     "vpe_loss.h")]
     return [os.path.join(CSRC, f) for f in names] + headers + [os.path.abspath(__file__)]
 
 

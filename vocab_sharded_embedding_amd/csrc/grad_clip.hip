@@ -1,0 +1,199 @@
+// Global gradient norm over many tensors, and clipping, for gfx950.
+//
+// Both read every element once and are bound by HBM (the clip also writes every
+// one).  A launch takes a table of up to kClipTable tensors in its arguments, so
+// that nothing is copied to the device and a captured launch keeps it; its
+// workgroups are pieces of `chunk` elements of one tensor each.  A piece's sum of
+// squares is one double, and one workgroup adds all pieces in order: the same
+// bits every time, whatever the order the pieces ran in.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "vpe_device.h"
+#include "vpe_loss_launch.h"
+
+namespace vpe {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Table {
+  const void *g[kClipTable];
+  int64_t count[kClipTable];
+  int32_t first[kClipTable + 1];  // first workgroup of a tensor
+  uint32_t bf16[(kClipTable + 31) / 32];
+  int64_t chunk;
+  int n;
+};
+
+struct Outputs {
+  void *out[kClipTable];
+};
+
+// The tensor that workgroup b works on.
+__device__ __forceinline__ int tensor_of(const Table &t, int b) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.first[mid] <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Squares and their sums in fp64: neither the square of a large fp32 gradient
+// nor that of a small one leaves its range, and no bits are lost over 10^10 of
+// them.  Four sums per thread keep the additions apart.
+template <bool BF16>
+__device__ __forceinline__ double squares(const void *g, int64_t begin, int64_t end) {
+  constexpr int kEpv = BF16 ? 8 : 4;
+  double s[4] = {0., 0., 0., 0.};
+  for (int64_t i = begin + threadIdx.x * kEpv; i < end; i += kThreads * kEpv) {
+    float v[kEpv];
+    dev::load_vec<BF16, kEpv>(g, i, end, v);
+#pragma unroll
+    for (int e = 0; e < kEpv; ++e) s[e & 3] = fma(double(v[e]), double(v[e]), s[e & 3]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Sum over the workgroup, on thread 0.
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double part[16];
+  v = dev::wave_sum(v);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0.;
+  if (threadIdx.x == 0)
+    for (unsigned w = 0; w < blockDim.x / 64; ++w) s += part[w];
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void sumsq_pieces(Table t, double *__restrict__ partial) {
+  const int at = tensor_of(t, blockIdx.x);
+  const int64_t begin = (blockIdx.x - t.first[at]) * t.chunk;
+  const int64_t end = begin + t.chunk < t.count[at] ? begin + t.chunk : t.count[at];
+  const bool bf16 = (t.bf16[at / 32] >> (at % 32)) & 1;
+  const double s = block_sum(bf16 ? squares<true>(t.g[at], begin, end)
+                                  : squares<false>(t.g[at], begin, end));
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(1024) void sumsq_join(const double *__restrict__ partial, int64_t n,
+                                                   double *__restrict__ sumsq) {
+  double s = 0.;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += partial[i];
+  s = block_sum(s);
+  if (threadIdx.x == 0) *sumsq = s;
+}
+
+struct Norms {
+  const double *sumsq[64];
+  int n;
+  double max_norm;
+};
+
+__device__ __forceinline__ double global_norm(const Norms &p) {
+  double s = 0.;
+  for (int r = 0; r < p.n; ++r) s += *p.sumsq[r];
+  return sqrt(s);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void scale_piece(const void *g, void *out, int64_t begin, int64_t end,
+                                            float f) {
+  constexpr int kEpv = BF16 ? 8 : 4;
+  for (int64_t i = begin + threadIdx.x * kEpv; i < end; i += kThreads * kEpv) {
+    float v[kEpv];
+    dev::load_vec<BF16, kEpv>(g, i, end, v);
+#pragma unroll
+    for (int e = 0; e < kEpv; ++e) v[e] *= f;
+    dev::store_vec_nt<BF16, kEpv>(out, i, end, v);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void clip_pieces(Table t, Outputs o, Norms p,
+                                                        float *__restrict__ norm) {
+  const double whole = global_norm(p);
+  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(whole);
+  if (t.n == 0) return;
+  const double ratio = p.max_norm / (whole + 1e-6);
+  const float f = ratio < 1. ? static_cast<float>(ratio) : (ratio != ratio ? __builtin_nanf("") : 1.f);
+  const int at = tensor_of(t, blockIdx.x);
+  const void *g = t.g[at];
+  // (times 1 in place: nothing to write)
+  if (f == 1.f && g == o.out[at]) return;
+  const int64_t begin = (blockIdx.x - t.first[at]) * t.chunk;
+  const int64_t end = begin + t.chunk < t.count[at] ? begin + t.chunk : t.count[at];
+  if ((t.bf16[at / 32] >> (at % 32)) & 1) scale_piece<true>(g, o.out[at], begin, end, f);
+  else scale_piece<false>(g, o.out[at], begin, end, f);
+}
+
+// Calls launch(table, outputs, workgroups) for the tensors that have elements,
+// kClipTable at a time.
+template <class F>
+void each_table(const void *const *tensors, const int64_t *counts, const int32_t *dtypes, int n,
+                int64_t total, void *const *out, F launch) {
+  Table t{};
+  Outputs o{};
+  t.chunk = clip_chunk(total);
+  int64_t groups = 0;
+  auto flush = [&]() {
+    if (t.n == 0) return;
+    t.first[t.n] = static_cast<int32_t>(groups);
+    launch(t, o, groups);
+    t = Table{};
+    t.chunk = clip_chunk(total);
+    groups = 0;
+  };
+  for (int i = 0; i < n; ++i) {
+    if (counts[i] == 0) continue;
+    t.g[t.n] = tensors[i];
+    if (out != nullptr) o.out[t.n] = out[i];
+    t.count[t.n] = counts[i];
+    t.first[t.n] = static_cast<int32_t>(groups);
+    if (dtypes[i] == 1) t.bf16[t.n / 32] |= uint32_t(1) << (t.n % 32);
+    groups += (counts[i] + t.chunk - 1) / t.chunk;
+    if (++t.n == kClipTable) flush();
+  }
+  flush();
+}
+
+}  // namespace
+
+int launch_grad_sumsq(const void *const *tensors, const int64_t *counts, const int32_t *dtypes,
+                      int n, int64_t total, double *sumsq, double *partial, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();  // clear a stale error so the status below is this launch's
+  int64_t pieces = 0;
+  each_table(tensors, counts, dtypes, n, total, nullptr,
+             [&](const Table &t, const Outputs &, int64_t groups) {
+               hipLaunchKernelGGL(sumsq_pieces, dim3(static_cast<unsigned>(groups)),
+                                  dim3(kThreads), 0, st, t, partial + pieces);
+               pieces += groups;
+             });
+  hipLaunchKernelGGL(sumsq_join, dim3(1), dim3(1024), 0, st, partial, pieces, sumsq);
+  return static_cast<int>(hipGetLastError());
+}
+
+int launch_grad_clip(const void *const *tensors, const int64_t *counts, const int32_t *dtypes,
+                     int n, int64_t total, void *const *out, const double *const *sumsq,
+                     int n_parts, double max_norm, float *norm, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  Norms p{};
+  for (int r = 0; r < n_parts; ++r) p.sumsq[r] = sumsq[r];
+  p.n = n_parts, p.max_norm = max_norm;
+  bool first = true;
+  each_table(tensors, counts, dtypes, n, total, out,
+             [&](const Table &t, const Outputs &o, int64_t groups) {
+               hipLaunchKernelGGL(clip_pieces, dim3(static_cast<unsigned>(groups)),
+                                  dim3(kThreads), 0, st, t, o, p, first ? norm : nullptr);
+               first = false;
+             });
+  if (first)
+    hipLaunchKernelGGL(clip_pieces, dim3(1), dim3(kThreads), 0, st, Table{}, Outputs{}, p, norm);
+  return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace vpe

@@ -1,0 +1,948 @@
+// Cross entropy straight from the LM head's shard, its gradients, and the head's
+// backward, for gfx950.
+//
+// The logits z = x W^T are products for the matrix cores and, at training sizes,
+// far larger than their operands; they are never kept.  Rows without a target
+// are left out first: `collect_rows` copies the live rows of x, so that what a
+// padded row holds is never read and no tile is spent on it.
+//  - Loss: every tile of z becomes one pair (maximum, sum of exponentials) per
+//    row in the workgroup that computed it, and the one logit that is a row's
+//    target; `join_pairs` merges a row's pairs.
+//  - Gradients, a piece of the vocabulary at a time: the piece's
+//    d = softmax - onehot goes to a buffer that the caches hold (128 MB), and
+//    feeds two products, grad_x += d W and grad_weight = d^T x, that read d and W
+//    (x) in place, in rows or in columns.  The sum over the vocabulary in grad_x
+//    is kept in fp32 between pieces, split over several sums where there are few
+//    rows; `finish_grad_x` joins and rounds them.
+//  - The head's backward is the same two products on a given d.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "vpe_device.h"
+#include "vpe_loss_launch.h"
+#include "vpe_tile.h"
+
+namespace vpe {
+namespace {
+
+using tile::f32x16;
+using tile::f32x4;
+
+[[maybe_unused]] constexpr float kLog2e = 1.4426950408889634f;
+
+int last_error() { return static_cast<int>(hipGetLastError()); }
+
+// ---------------------------------------------------------------------------
+// live rows
+// ---------------------------------------------------------------------------
+struct Collect {
+  const void *x;
+  int64_t m, dim, dim_pad;
+  const void *targets;
+  int64_t vocab_start, vocab, rows;
+  const float *lse, *grad_loss;  // gradients; nullptr for the loss
+  int rows_per_block;
+  int32_t *count;
+  float *scale;
+  int32_t *row_of, *target, *place;
+  float *lse_of, *ratio;
+  void *xl;
+  float *shard_lse, *target_logit;  // loss: written 0
+};
+
+template <class I>
+__device__ __forceinline__ bool row_lives(const Collect &c, int64_t i) {
+  const int64_t t = static_cast<const I *>(c.targets)[i];
+  return t >= 0 && t < c.vocab && (c.grad_loss == nullptr || c.grad_loss[i] != 0.f);
+}
+
+// Live rows in order, without a second pass: every workgroup counts the live
+// rows before its own (targets are small against x).  The gradients' factors are
+// taken over the largest finite |grad_loss|, so that a loss averaged over its
+// rows has factors of exactly 1 and d is rounded as softmax - onehot.
+template <bool BF16, class I>
+__global__ __launch_bounds__(256) void collect_rows(Collect c) {
+  __shared__ int wave_n[4];
+  __shared__ float wave_top[4];
+  __shared__ int kept[1024], kept_at[1024];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * c.rows_per_block;
+  const int64_t end = row0 + c.rows_per_block < c.m ? row0 + c.rows_per_block : c.m;
+  int before = 0;
+  float top = 0.f;
+  if (c.grad_loss != nullptr) {
+    for (int64_t i = threadIdx.x; i < c.m; i += 256) {
+      const bool live = row_lives<I>(c, i);
+      before += live && i < row0;
+      const float a = fabsf(c.grad_loss[i]);
+      if (live && a > top && a < __builtin_huge_valf()) top = a;
+    }
+  } else {
+    for (int64_t i = threadIdx.x; i < row0; i += 256) before += row_lives<I>(c, i);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) {
+    before += __shfl_xor(before, d);
+    top = fmaxf(top, __shfl_xor(top, d));
+  }
+  if (lane == 0) wave_n[wave] = before, wave_top[wave] = top;
+  __syncthreads();
+  before = wave_n[0] + wave_n[1] + wave_n[2] + wave_n[3];
+  top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+  if (top == 0.f) top = 1.f;
+  int mine = 0;
+  for (int64_t base = row0; base < end; base += 256) {
+    const int64_t i = base + threadIdx.x;
+    const bool live = i < end && row_lives<I>(c, i);
+    const uint64_t votes = __ballot(live);
+    __syncthreads();
+    if (lane == 0) wave_n[wave] = __popcll(votes);
+    __syncthreads();
+    int at = mine + __popcll(votes & ((uint64_t(1) << lane) - 1));
+    for (int w = 0; w < wave; ++w) at += wave_n[w];
+    mine += wave_n[0] + wave_n[1] + wave_n[2] + wave_n[3];
+    if (live) {
+      const int64_t local = static_cast<const I *>(c.targets)[i] - c.vocab_start;
+      const int to = before + at;
+      c.row_of[to] = static_cast<int32_t>(i);
+      c.target[to] = local >= 0 && local < c.rows ? static_cast<int32_t>(local) : -1;
+      if (c.grad_loss != nullptr) {
+        c.lse_of[to] = c.lse[i];
+        c.ratio[to] = c.grad_loss[i] / top;
+      }
+      kept[at] = static_cast<int>(i - row0);
+      kept_at[at] = to;
+    }
+    if (i < end) {
+      if (c.place != nullptr) c.place[i] = live ? before + at : -1;
+      if (c.shard_lse != nullptr) c.shard_lse[i] = 0.f, c.target_logit[i] = 0.f;
+    }
+  }
+  __syncthreads();
+  if (end == c.m && threadIdx.x == 0) {
+    *c.count = before + mine;
+    *c.scale = top;
+  }
+  // rows of x, with zeros up to dim_pad
+  constexpr int kSize = BF16 ? 2 : 4, kEpv = 16 / kSize;
+  const char *x = static_cast<const char *>(c.x);
+  char *xl = static_cast<char *>(c.xl);
+  const int vecs = static_cast<int>(c.dim_pad / kEpv);
+  for (int k = wave; k < mine; k += 4) {
+    const char *src = x + (row0 + kept[k]) * c.dim * kSize;
+    char *dst = xl + static_cast<int64_t>(kept_at[k]) * c.dim_pad * kSize;
+    for (int v = lane; v < vecs; v += 64) {
+      float e[kEpv];
+      dev::load_vec<BF16, kEpv>(src, static_cast<int64_t>(v) * kEpv, c.dim, e);
+      *reinterpret_cast<dev::u32x4 *>(dst + v * 16) = dev::Vec<BF16, kEpv>::narrow(e);
+    }
+  }
+}
+
+// `rows` rows of `cols` bf16 at stride ld, any alignment, copied to stride ld_to
+// with zeros up to it.
+__global__ __launch_bounds__(256) void copy_rows(const uint16_t *__restrict__ from, int64_t ld,
+                                                 int64_t rows, int64_t cols,
+                                                 uint16_t *__restrict__ to, int64_t ld_to) {
+  const int lane = threadIdx.x & 63;
+  const int64_t vecs = ld_to / 8;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); r < rows;
+       r += static_cast<int64_t>(gridDim.x) * 4)
+    for (int64_t v = lane; v < vecs; v += 64) {
+      float e[8];
+      dev::load_vec<true, 8>(from + r * ld, v * 8, cols, e);
+      *reinterpret_cast<dev::u32x4 *>(to + r * ld_to + v * 8) = dev::Vec<true, 8>::narrow(e);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------
+// Workgroup b's tile (n, m) of tiles_n x tiles_m.  Workgroups go to the 8 XCDs
+// in turn; each XCD gets one contiguous run of tiles, ordered in groups of
+// group_n tiles of n, so that the tiles it runs at once share both operands in
+// its own L2.
+[[maybe_unused]] __device__ __forceinline__ void tile_of(int b, int tiles_n, int tiles_m, int group_n, int &tn,
+                                        int &tm) {
+  const int total = tiles_n * tiles_m;
+  const int xcd = b & 7, idx = b >> 3, per = total >> 3, rem = total & 7;
+  const int t = xcd < rem ? xcd * (per + 1) + idx : rem * (per + 1) + (xcd - rem) * per + idx;
+  const int group = group_n * tiles_m;
+  const int g = t / group, in = t - g * group;
+  const int gn = min(group_n, tiles_n - g * group_n);
+  tm = in / gn;
+  tn = g * group_n + (in - tm * gn);
+}
+
+// The bf16 and the fp32 product under one name: `run` sets acc to the tile whose
+// operands begin at a and b.
+template <class S, bool BF16, bool NCOLS, bool MCOLS>
+struct Core;
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <class S, bool NCOLS, bool MCOLS>
+struct Core<S, true, NCOLS, MCOLS> {
+  typedef tile::Product<S, NCOLS, MCOLS> P;
+  static constexpr int kLdsBytes = P::kLdsElems * 2;
+  static __device__ __forceinline__ void run(const void *a, int64_t lda, int64_t n_left,
+                                             int64_t ka, const void *b, int64_t ldb,
+                                             int64_t m_left, int64_t kb, int64_t k, char *lds,
+                                             f32x16 (&acc)[S::FN][S::FM]) {
+    const int wave = tile::wave_id();
+    typename P::StageN sa;
+    typename P::StageM sb;
+    sa.init(static_cast<const uint16_t *>(a), lda, n_left, ka, wave % S::WN * S::TN);
+    sb.init(static_cast<const uint16_t *>(b), ldb, m_left, kb, wave / S::WN * S::TM);
+    P::run(sa, sb, static_cast<int>((k + S::BK - 1) / S::BK), reinterpret_cast<uint16_t *>(lds),
+           acc);
+  }
+};
+template <class S, bool NCOLS, bool MCOLS>
+struct Core<S, false, NCOLS, MCOLS> {
+  typedef tile::ProductF<S, NCOLS, MCOLS> P;
+  static constexpr int kLdsBytes = P::kLdsElems * 4;
+  static __device__ __forceinline__ void run(const void *a, int64_t lda, int64_t n_left,
+                                             int64_t ka, const void *b, int64_t ldb,
+                                             int64_t m_left, int64_t kb, int64_t k, char *lds,
+                                             f32x16 (&acc)[S::FN][S::FM]) {
+    const int wave = tile::wave_id();
+    typename P::StageN sa;
+    typename P::StageM sb;
+    sa.init(static_cast<const float *>(a), lda, n_left, ka);
+    sb.init(static_cast<const float *>(b), ldb, m_left, kb);
+    P::run(sa, sb, static_cast<int>((k + S::BK - 1) / S::BK), reinterpret_cast<float *>(lds),
+           wave % S::WN * S::TN, wave / S::WN * S::TM, acc);
+  }
+};
+
+// A wave's accumulators as rows of m: fragments pass through the wave's part of
+// the LDS (the stages: every wave is done with them), 64 columns of 32 rows at a
+// time, and `put(m, n, v)` gets 4 consecutive columns n.. of row m, neighbouring
+// lanes neighbouring columns.  m and n count from the workgroup's tile.
+template <class S>
+struct RowWriter {
+  static constexpr int kCols = S::TN < 64 ? S::TN : 64, kLd = kCols + 4;
+  static constexpr int kLdsBytes = S::NW * 32 * kLd * 4;
+  template <class Put>
+  static __device__ __forceinline__ void run(const f32x16 (&acc)[S::FN][S::FM], char *lds,
+                                             Put put) {
+    const int lane = threadIdx.x & 63, wave = tile::wave_id();
+    const int wn = wave % S::WN, wm = wave / S::WN, row = lane & 31, hi = lane >> 5;
+    float *mine = reinterpret_cast<float *>(lds) + wave * 32 * kLd;
+    constexpr int kPer = kCols / 4, kRows = 64 / kPer;
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j)
+#pragma unroll
+      for (int h = 0; h < S::TN / kCols; ++h) {
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16 &f = acc[h * (kCols / 32) + i][j];
+            *reinterpret_cast<f32x4 *>(mine + row * kLd + i * 32 + 8 * q + 4 * hi) =
+                f32x4{f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]};
+          }
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+        for (int t = 0; t < 32 / kRows; ++t) {
+          const int r = t * kRows + lane / kPer, n = lane % kPer * 4;
+          const f32x4 v = *reinterpret_cast<const f32x4 *>(mine + r * kLd + n);
+          put(wm * S::TM + j * 32 + r, wn * S::TN + h * kCols + n, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+      }
+  }
+};
+#endif
+
+[[maybe_unused]] constexpr int max_of(int a, int b) { return a > b ? a : b; }
+
+// ---------------------------------------------------------------------------
+// logits
+// ---------------------------------------------------------------------------
+struct Logits {
+  const void *x;  // live rows, stride ldx
+  int64_t ldx;
+  const void *w;  // a piece of the shard's rows, stride ldw
+  int64_t ldw, w_rows, w_dim;  // w_dim: values of a row that may be read
+  int64_t k;
+  const int32_t *count;
+  int tiles_n, tiles_m, group_n;
+  const int32_t *target;
+  int64_t row0;  // the piece's first row in the shard
+  // loss
+  float *pairs;  // [tile][pair_ld] (maximum, sum)
+  int64_t pair_ld, tile0;
+  float *target_logit;
+  const int32_t *row_of;
+  // gradients
+  const float *lse, *ratio;
+  void *d;
+  int64_t ldd;  // the piece's columns, zeros after the last
+};
+
+// (m, s) of two disjoint sets of logits; an empty one is (-inf, 0).
+__device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
+  const float top = (m != m || m > m2) ? m : m2;
+  const float a = m == -__builtin_huge_valf() ? 0.f : s * __expf(m - top);
+  const float b = m2 == -__builtin_huge_valf() ? 0.f : s2 * __expf(m2 - top);
+  m = top;
+  s = a + b;
+}
+
+template <class S, bool BF16, bool GRAD>
+__global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef Core<S, BF16, false, false> C;
+  constexpr int kLds = max_of(C::kLdsBytes, GRAD ? RowWriter<S>::kLdsBytes : S::BM * S::WN * 8);
+  __shared__ __attribute__((aligned(16))) char lds[kLds];
+  constexpr int kSize = BF16 ? 2 : 4;
+  int tn, tm;
+  tile_of(blockIdx.x, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
+  const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
+  const int64_t live = *a.count;
+  if (m0 >= live) return;
+  f32x16 acc[S::FN][S::FM];
+#pragma unroll
+  for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
+  C::run(static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
+         static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.k, a.k, lds, acc);
+  const int lane = threadIdx.x & 63, wave = tile::wave_id();
+  const int wn = wave % S::WN, wm = wave / S::WN, hi = lane >> 5;
+  const int64_t nb = n0 + wn * S::TN;  // this wave's first column
+  // this lane's columns nb + c, c = 32 i + 8 (r / 4) + 4 hi + r % 4, exist for
+  // c < lim
+  const int64_t left = a.w_rows - nb;
+  const int lim = left < 0 ? 0 : (left < S::TN ? static_cast<int>(left) : S::TN);
+  __syncthreads();  // every wave is done with the stages
+  if constexpr (!GRAD) {
+    float *out = reinterpret_cast<float *>(lds);  // [BM][WN] pairs
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j) {
+      const int64_t m = m0 + wm * S::TM + j * 32 + (lane & 31);
+      float top = -__builtin_huge_valf();
+#pragma unroll
+      for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (lim == S::TN || i * 32 + 8 * (r / 4) + 4 * hi + r % 4 < lim)
+            top = fmaxf(top, acc[i][j][r]);
+      const float shift = top == -__builtin_huge_valf() ? 0.f : -top * kLog2e;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, shift));
+          if (lim == S::TN || i * 32 + 8 * (r / 4) + 4 * hi + r % 4 < lim) s += e;
+        }
+      if (s != s) top = s;  // a NaN logit, or +inf
+      merge(top, s, __shfl_xor(top, 32), __shfl_xor(s, 32));
+      if (hi == 0) {
+        float *e = out + ((wm * S::TM + j * 32 + lane) * S::WN + wn) * 2;
+        e[0] = top, e[1] = s;
+      }
+      // the row's target, where this wave has its column
+      int64_t rel = -1;
+      if (m < live) {
+        const int32_t t = a.target[m];
+        rel = t < 0 ? -1 : t - a.row0 - nb;
+      }
+      if (__any(rel >= 0 && rel < S::TN)) {
+        float z = 0.f;
+        const int at = rel >= 0 && rel < lim ? static_cast<int>(rel) : -1;
+#pragma unroll
+        for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (at == i * 32 + 8 * (r / 4) + 4 * hi + r % 4) z = acc[i][j][r];
+        if (at >= 0 && ((at >> 2) & 1) == hi) a.target_logit[a.row_of[m]] = z;
+      }
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < S::BM; r += S::NT) {
+      if (m0 + r >= live) continue;
+      float top = out[r * S::WN * 2], s = out[r * S::WN * 2 + 1];
+#pragma unroll
+      for (int w = 1; w < S::WN; ++w)
+        merge(top, s, out[(r * S::WN + w) * 2], out[(r * S::WN + w) * 2 + 1]);
+      float *e = a.pairs + ((a.tile0 + tn) * a.pair_ld + m0 + r) * 2;
+      e[0] = top, e[1] = s;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j) {
+      const int64_t m = m0 + wm * S::TM + j * 32 + (lane & 31);
+      float lse = 0.f, ratio = 0.f;
+      int at = -1;
+      if (m < live) {
+        lse = a.lse[m], ratio = a.ratio[m];
+        const int32_t t = a.target[m];
+        const int64_t rel = t < 0 ? -1 : t - a.row0 - nb;
+        at = rel >= 0 && rel < lim ? static_cast<int>(rel) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int c = i * 32 + 8 * (r / 4) + 4 * hi + r % 4;
+          // (fp32: the difference first, whose rounding the exponential does
+          // not magnify)
+          float e = BF16 ? __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -lse * kLog2e))
+                         : __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e);
+          if (at == c) e -= 1.f;
+          acc[i][j][r] = c < lim ? e * ratio : 0.f;
+        }
+    }
+    RowWriter<S>::run(acc, lds, [&](int m, int n, f32x4 v) {
+      // (ldd is a multiple of 64, so 4 columns are inside or past it together)
+      if (m0 + m >= live || n0 + n >= a.ldd) return;
+      char *to = static_cast<char *>(a.d) + ((m0 + m) * a.ldd + n0 + n) * kSize;
+      if constexpr (BF16)
+        *reinterpret_cast<dev::u32x2 *>(to) =
+            dev::u32x2{dev::pack_bf16(v[0], v[1]), dev::pack_bf16(v[2], v[3])};
+      else
+        *reinterpret_cast<f32x4 *>(to) = v;
+    });
+  }
+#endif
+}
+
+// A row's pairs joined: shard_lse[row] = log sum exp.  64 rows per workgroup of
+// 16 waves, each every 16th tile; few rows: a workgroup each.
+template <bool FEW>
+__global__ __launch_bounds__(1024) void join_pairs(const float *__restrict__ pairs, int64_t ld,
+                                                   int tiles, const int32_t *__restrict__ count,
+                                                   const int32_t *__restrict__ row_of,
+                                                   float *__restrict__ shard_lse) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float part[16][64][2];
+  const int64_t live = *count;
+  const int64_t row = FEW ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  if ((FEW ? row : static_cast<int64_t>(blockIdx.x) * 64) >= live) return;
+  float m = -__builtin_huge_valf(), s = 0.f;
+  if (row < live)
+    for (int t = FEW ? threadIdx.x : wave; t < tiles; t += FEW ? 1024 : 16) {
+      const float *e = pairs + (t * ld + row) * 2;
+      merge(m, s, e[0], e[1]);
+    }
+  if (FEW) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) merge(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+  }
+  part[wave][lane][0] = m, part[wave][lane][1] = s;
+  __syncthreads();
+  if (wave == 0 && row < live) {
+    for (int w = 1; w < 16; ++w) merge(m, s, part[w][lane][0], part[w][lane][1]);
+    if (!FEW || lane == 0)
+      shard_lse[row_of[row]] = m == -__builtin_huge_valf() ? m : m + logf(s);
+  }
+}
+
+struct Parts {
+  const float *lse[64];
+  const float *target[64];
+};
+
+template <class I>
+__global__ __launch_bounds__(256) void xent_loss(Parts p, int n, int64_t m, int64_t vocab,
+                                                 const I *targets, float *loss, float *lse) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= m) return;
+  const int64_t t = targets[i];
+  float whole = 0.f, value = 0.f;
+  if (t >= 0 && t < vocab) {
+    float top = p.lse[0][i], s = 1.f, z = p.target[0][i];
+    if (top == -__builtin_huge_valf()) s = 0.f;
+    for (int r = 1; r < n; ++r) {
+      merge(top, s, p.lse[r][i], 1.f);
+      z += p.target[r][i];
+    }
+    whole = n == 1 || top == -__builtin_huge_valf() ? top : top + logf(s);
+    value = whole - z;
+  }
+  loss[i] = value;
+  lse[i] = whole;
+}
+
+// ---------------------------------------------------------------------------
+// products with the logits' gradient
+// ---------------------------------------------------------------------------
+struct Products {
+  const void *d;  // [rows][cols] at stride ldd
+  int64_t ldd, cols;
+  const void *w;  // the same piece of the table, stride ldw
+  int64_t ldw;
+  const void *x;  // rows of x, stride ldx
+  int64_t ldx;
+  int64_t rows;          // rows of d and x,
+  const int32_t *count;  // or (not nullptr) how many of them
+  int64_t dim;
+  // gradient of x
+  float *sums;  // [splits][rows][ld_sums]
+  int64_t ld_sums, per_split;  // columns of d per split, a multiple of the k step
+  bool first;
+  int x_tiles_n, x_tiles_m, splits;
+  // gradient of the table
+  void *gw;  // the piece's first row
+  bool gw_bf16, accumulate;
+  const float *scale;
+  int w_tiles_n, w_tiles_m;
+};
+
+template <bool USED, class C>
+struct LdsOf {
+  static constexpr int bytes = 0;
+};
+template <class C>
+struct LdsOf<true, C> {
+  static constexpr int bytes = C::kLdsBytes;
+};
+
+// Parts of the launch: 1 the gradient of x, 2 that of the table, 3 both, the
+// first's workgroups before the second's.
+template <class S, bool BF16, int PARTS>
+__global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef Core<S, BF16, true, false> CX;
+  typedef Core<S, BF16, true, true> CW;
+  constexpr int kSize = BF16 ? 2 : 4;
+  constexpr int kTiles =
+      max_of(LdsOf<(PARTS & 1) != 0, CX>::bytes, LdsOf<(PARTS & 2) != 0, CW>::bytes);
+  __shared__ __attribute__((aligned(16))) char lds[max_of(kTiles, RowWriter<S>::kLdsBytes)];
+  const int64_t live = a.count != nullptr ? *a.count : a.rows;
+  f32x16 acc[S::FN][S::FM];
+#pragma unroll
+  for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
+  const int x_blocks = (PARTS & 1) ? a.x_tiles_n * a.x_tiles_m * a.splits : 0;
+  const int b = blockIdx.x;
+  if constexpr ((PARTS & 1) != 0) {
+    if (b < x_blocks) {
+      int tn, t2;  // (tiles of m and splits together)
+      tile_of(b, a.x_tiles_n, a.x_tiles_m * a.splits, a.x_tiles_n, tn, t2);
+      const int split = t2 / a.x_tiles_m, tm = t2 - split * a.x_tiles_m;
+      const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
+      if (m0 >= live) return;
+      const int64_t k0 = split * a.per_split;
+      int64_t k = a.cols - k0 < a.per_split ? a.cols - k0 : a.per_split;
+      if (k < 0) k = 0;
+      if (k == 0 && !a.first) return;
+      CX::run(static_cast<const char *>(a.w) + (k0 * a.ldw + n0) * kSize, a.ldw, a.dim - n0, k,
+              static_cast<const char *>(a.d) + (m0 * a.ldd + k0) * kSize, a.ldd, live - m0,
+              // (bf16: columns up to a multiple of 8, the table's rows end before)
+              BF16 ? (k + 7) / 8 * 8 : k, k, lds, acc);
+      __syncthreads();
+      float *sums = a.sums + split * a.rows * a.ld_sums;
+      RowWriter<S>::run(acc, lds, [&](int m, int n, f32x4 v) {
+        if (m0 + m >= live || n0 + n >= a.ld_sums) return;
+        f32x4 *to = reinterpret_cast<f32x4 *>(sums + (m0 + m) * a.ld_sums + n0 + n);
+        *to = a.first ? v : *to + v;
+      });
+      return;
+    }
+  }
+  if constexpr ((PARTS & 2) != 0) {
+    int tn, tm;
+    tile_of(b - x_blocks, a.w_tiles_n, a.w_tiles_m, a.w_tiles_n, tn, tm);
+    const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
+    CW::run(static_cast<const char *>(a.x) + n0 * kSize, a.ldx, a.dim - n0, live,
+            static_cast<const char *>(a.d) + m0 * kSize, a.ldd, a.cols - m0, live, live, lds, acc);
+    __syncthreads();
+    const float scale = a.scale != nullptr ? *a.scale : 1.f;
+    const bool wide = (a.dim & 3) == 0 && (reinterpret_cast<uintptr_t>(a.gw) & 15) == 0;
+    RowWriter<S>::run(acc, lds, [&](int m, int n, f32x4 v) {
+      const int64_t left = a.dim - (n0 + n);
+      if (m0 + m >= a.cols || left <= 0) return;
+      const int64_t at = (m0 + m) * a.dim + n0 + n;
+      v *= scale;
+      if (a.gw_bf16) {
+        uint16_t *to = static_cast<uint16_t *>(a.gw) + at;
+        if (wide) {  // (rows of a multiple of 4 values: 8-byte words)
+          dev::u32x2 *w = reinterpret_cast<dev::u32x2 *>(to);
+          if (a.accumulate) {
+            const dev::u32x2 o = *w;
+            v += f32x4{dev::bf16_lo(o[0]), dev::bf16_hi(o[0]), dev::bf16_lo(o[1]),
+                       dev::bf16_hi(o[1])};
+          }
+          *w = dev::u32x2{dev::pack_bf16(v[0], v[1]), dev::pack_bf16(v[2], v[3])};
+        } else {
+          for (int e = 0; e < 4 && e < left; ++e)
+            to[e] = dev::one_bf16(a.accumulate ? dev::load_one<true>(to, e) + v[e] : v[e]);
+        }
+      } else {
+        float *to = static_cast<float *>(a.gw) + at;
+        if (wide) {
+          f32x4 *w = reinterpret_cast<f32x4 *>(to);
+          *w = a.accumulate ? *w + v : v;
+        } else {
+          for (int e = 0; e < 4 && e < left; ++e) to[e] = a.accumulate ? to[e] + v[e] : v[e];
+        }
+      }
+    });
+  }
+#endif
+}
+
+// grad_x from its sums: row i's is at place[i] (nullptr: i), 0 where that is -1.
+template <bool BF16>
+__global__ __launch_bounds__(256) void finish_grad_x(const float *__restrict__ sums,
+                                                     int64_t ld_sums, int64_t split_stride,
+                                                     int splits, const int32_t *place,
+                                                     const float *scale, int64_t m, int64_t dim,
+                                                     void *gx) {
+  const int64_t vecs = (dim + 3) / 4;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t i = at / vecs, n = (at - i * vecs) * 4;
+  if (i >= m) return;
+  const int64_t from = place != nullptr ? place[i] : i;
+  f32x4 v = f32x4(0.f);
+  if (from >= 0) {
+    const float *p = sums + from * ld_sums + n;
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * split_stride);
+    if (scale != nullptr) v *= *scale;
+  }
+  float e[4] = {v[0], v[1], v[2], v[3]};
+  char *row = static_cast<char *>(gx) + i * dim * (BF16 ? 2 : 4);
+  dev::store_vec_nt<BF16, 4>(row, n, dim, e);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+// bf16 tiles: 8 waves of 128 x 64 each on 256 x 256, one workgroup per CU; 4
+// waves on 128 x 128, two per CU; narrow ones for few hidden rows.
+typedef tile::Shape<256, 256, 2, 4, 64, 2> Large;
+typedef tile::Shape<128, 128, 2, 2, 64, 2> Medium;
+typedef tile::Shape<128, 64, 2, 2, 64, 3> Low64;
+typedef tile::Shape<128, 32, 4, 1, 64, 3> Low32;
+// fp32 tiles
+typedef tile::Shape<128, 128, 2, 2, 16, 2> MediumF;
+typedef tile::Shape<128, 32, 4, 1, 32, 2> LowF;
+
+int blocks(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
+
+char *at(void *workspace, int64_t offset) { return static_cast<char *>(workspace) + offset; }
+
+int run_collect(const LossRows &r, const LossLayout &l, const float *lse, const float *grad_loss,
+                float *shard_lse, float *target_logit, void *ws, hipStream_t st) {
+  Collect c{};
+  c.x = r.x, c.m = r.m, c.dim = r.dim, c.dim_pad = l.dim_pad;
+  c.targets = r.targets, c.vocab_start = r.vocab_start, c.vocab = r.vocab, c.rows = r.rows;
+  c.lse = lse, c.grad_loss = grad_loss;
+  // 16 rows per workgroup fill the chip from 4096 rows on; past that the
+  // counting of earlier rows is kept in proportion to the copying
+  int64_t per = loss_max(16, loss_min(1024, loss_up(r.m / 256, 16)));
+  c.rows_per_block = static_cast<int>(per);
+  c.count = reinterpret_cast<int32_t *>(at(ws, l.count));
+  c.scale = reinterpret_cast<float *>(at(ws, l.count)) + 1;
+  c.row_of = reinterpret_cast<int32_t *>(at(ws, l.row_of));
+  c.target = reinterpret_cast<int32_t *>(at(ws, l.target));
+  if (grad_loss != nullptr) {
+    c.place = reinterpret_cast<int32_t *>(at(ws, l.place));
+    c.lse_of = reinterpret_cast<float *>(at(ws, l.lse));
+    c.ratio = reinterpret_cast<float *>(at(ws, l.ratio));
+  }
+  c.xl = at(ws, l.x);
+  c.shard_lse = shard_lse, c.target_logit = target_logit;
+  const dim3 grid(blocks(r.m, per));
+  if (r.dtype == 1) {
+    if (r.itype == 0) hipLaunchKernelGGL((collect_rows<true, int32_t>), grid, dim3(256), 0, st, c);
+    else hipLaunchKernelGGL((collect_rows<true, int64_t>), grid, dim3(256), 0, st, c);
+  } else {
+    if (r.itype == 0) hipLaunchKernelGGL((collect_rows<false, int32_t>), grid, dim3(256), 0, st, c);
+    else hipLaunchKernelGGL((collect_rows<false, int64_t>), grid, dim3(256), 0, st, c);
+  }
+  return last_error();
+}
+
+// Rows of a bf16 table that 16-byte loads can take in place.
+bool loads_in_place(const void *p, int64_t ld) {
+  return ld % 8 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
+void run_copy(const void *from, int64_t ld, int64_t rows, int64_t cols, void *to, int64_t ld_to,
+              hipStream_t st) {
+  hipLaunchKernelGGL(copy_rows, dim3(static_cast<unsigned>(loss_min(blocks(rows, 4), 4096))),
+                     dim3(256), 0, st, static_cast<const uint16_t *>(from), ld, rows, cols,
+                     static_cast<uint16_t *>(to), ld_to);
+}
+
+template <class S, bool BF16, bool GRAD>
+void run_logits(Logits a, int64_t m, hipStream_t st) {
+  a.tiles_n = blocks(GRAD ? a.ldd : a.w_rows, S::BN);
+  a.tiles_m = blocks(m, S::BM);
+  a.group_n = 8;
+  hipLaunchKernelGGL((logits_tiles<S, BF16, GRAD>), dim3(a.tiles_n * a.tiles_m), dim3(S::NT), 0, st,
+                     a);
+}
+
+// Width of the tiles that `pick_logits` takes, as the loss counts its pairs.
+int64_t logits_tile_rows(int64_t m, int dtype) {
+  return dtype == 1 && m > 128 ? Large::BN : kLossTileRows;
+}
+
+template <bool GRAD>
+void pick_logits(const Logits &a, int64_t m, int dtype, hipStream_t st) {
+  if (dtype == 0) {
+    if (m <= 32) run_logits<LowF, false, GRAD>(a, m, st);
+    else run_logits<MediumF, false, GRAD>(a, m, st);
+  } else if (m <= 32) {
+    run_logits<Low32, true, GRAD>(a, m, st);
+  } else if (m <= 64) {
+    run_logits<Low64, true, GRAD>(a, m, st);
+  } else if (m <= 128) {
+    run_logits<Medium, true, GRAD>(a, m, st);
+  } else {
+    run_logits<Large, true, GRAD>(a, m, st);
+  }
+}
+
+template <class S, bool BF16, int PARTS>
+void run_products(Products a, bool first, hipStream_t st) {
+  a.first = first;
+  a.x_tiles_n = blocks(a.dim, S::BN);
+  a.x_tiles_m = blocks(a.rows, S::BM);
+  a.w_tiles_n = blocks(a.dim, S::BN);
+  a.w_tiles_m = blocks(a.cols, S::BM);
+  const int n = ((PARTS & 1) ? a.x_tiles_n * a.x_tiles_m * a.splits : 0) +
+                ((PARTS & 2) ? a.w_tiles_n * a.w_tiles_m : 0);
+  if (n > 0)
+    hipLaunchKernelGGL((grad_tiles<S, BF16, PARTS>), dim3(n), dim3(S::NT), 0, st, a);
+}
+
+// Splits of the sum over the vocabulary so that about `want` workgroups of
+// tiles of n x m share it.
+int64_t splits_for(int64_t rows, int64_t dim, int64_t cols, int64_t bn, int64_t bm, int64_t want,
+                   int64_t most) {
+  const int64_t tiles = blocks(dim, bn) * static_cast<int64_t>(blocks(rows, bm));
+  int64_t s = want / tiles;
+  s = loss_min(s, (cols + kLossSplitRows - 1) / kLossSplitRows);
+  return loss_max(1, loss_min(s, most));
+}
+
+// The two products of a piece.  `splits` is fixed for all pieces of a call.
+void pick_products(Products a, int dtype, bool gx, bool gw, bool first, hipStream_t st) {
+  if (dtype == 0) {
+    if (gx && a.rows <= 32) run_products<LowF, false, 1>(a, first, st);
+    else if (gx) run_products<MediumF, false, 1>(a, first, st);
+    if (gw) run_products<MediumF, false, 2>(a, first, st);
+    return;
+  }
+  if (a.rows > 1024 && gx && gw) {
+    run_products<Large, true, 3>(a, first, st);
+    return;
+  }
+  if (gx && a.rows <= 32) run_products<Low32, true, 1>(a, first, st);
+  else if (gx && a.rows <= 64) run_products<Low64, true, 1>(a, first, st);
+  else if (gx && a.rows <= 1024) run_products<Medium, true, 1>(a, first, st);
+  else if (gx) run_products<Large, true, 1>(a, first, st);
+  if (gw && a.rows <= 1024) run_products<Medium, true, 2>(a, first, st);
+  else if (gw) run_products<Large, true, 2>(a, first, st);
+}
+
+int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, int64_t most) {
+  if (dtype == 0)
+    return splits_for(rows, dim, cols, 128, rows <= 32 ? 32 : 128, 512, most);
+  if (rows > 1024) return splits_for(rows, dim, cols, 256, 256, 256, most);
+  return splits_for(rows, dim, cols, 128, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 512, most);
+}
+
+void run_finish(const Products &a, const LossRows &r, const LossGrads &g, const int32_t *place,
+                hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>((r.m * ((r.dim + 3) / 4) + 255) / 256));
+  const int64_t stride = a.rows * a.ld_sums;
+  if (g.gxt == 1)
+    hipLaunchKernelGGL(finish_grad_x<true>, grid, dim3(256), 0, st, a.sums, a.ld_sums, stride,
+                       a.splits, place, a.scale, r.m, r.dim, g.gx);
+  else
+    hipLaunchKernelGGL(finish_grad_x<false>, grid, dim3(256), 0, st, a.sums, a.ld_sums, stride,
+                       a.splits, place, a.scale, r.m, r.dim, g.gx);
+}
+
+// The gradients of an empty batch: zeros.
+int zero_table(const LossRows &r, const LossGrads &g, hipStream_t st) {
+  if (g.gw == nullptr || g.accumulate) return 0;
+  Products a{};
+  a.dim = r.dim, a.cols = r.rows, a.gw = g.gw, a.gw_bf16 = g.gwt == 1;
+  // (no rows: no operand is read)
+  if (r.dtype == 1) run_products<Medium, true, 2>(a, true, st);
+  else run_products<MediumF, false, 2>(a, true, st);
+  return last_error();
+}
+
+}  // namespace
+
+int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit, void *workspace,
+                       void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();  // clear a stale error so the status below is this launch's
+  const LossLayout l = loss_layout(kLossForward, r.m, r.dim, r.rows, r.dtype);
+  const int64_t e = r.dtype == 1 ? 2 : 4;
+  int rc = run_collect(r, l, nullptr, nullptr, shard_lse, target_logit, workspace, st);
+  if (rc != 0) return rc;
+  Logits a{};
+  a.x = at(workspace, l.x), a.ldx = l.dim_pad;
+  a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
+  a.row_of = reinterpret_cast<const int32_t *>(at(workspace, l.row_of));
+  a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
+  a.pairs = reinterpret_cast<float *>(at(workspace, l.pairs)), a.pair_ld = r.m;
+  a.target_logit = target_logit;
+  const bool in_place = r.dtype == 0 || loads_in_place(r.w, r.dim);
+  const int64_t tile_rows = logits_tile_rows(r.m, r.dtype);
+  const int64_t piece = in_place ? r.rows : l.table_rows / tile_rows * tile_rows;
+  const int64_t step = piece > 0 ? piece : l.table_rows;
+  for (int64_t row = 0; row < r.rows; row += step) {
+    const char *w = static_cast<const char *>(r.w) + row * r.dim * e;
+    a.w_rows = loss_min(step, r.rows - row), a.row0 = row, a.tile0 = row / tile_rows;
+    if (in_place) {
+      a.w = w, a.ldw = r.dim, a.w_dim = r.dim;
+    } else {
+      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, st);
+      a.w = at(workspace, l.table), a.ldw = l.dim_pad, a.w_dim = l.dim_pad;
+    }
+    a.k = r.dtype == 1 ? l.dim_pad : r.dim;
+    pick_logits<false>(a, r.m, r.dtype, st);
+    rc = last_error();
+    if (rc != 0) return rc;
+  }
+  const int tiles = blocks(r.rows, tile_rows);
+  if (r.m <= 256)
+    hipLaunchKernelGGL(join_pairs<true>, dim3(static_cast<unsigned>(r.m)), dim3(1024), 0, st,
+                       a.pairs, a.pair_ld, tiles, a.count, a.row_of, shard_lse);
+  else
+    hipLaunchKernelGGL(join_pairs<false>, dim3(blocks(r.m, 64)), dim3(1024), 0, st, a.pairs,
+                       a.pair_ld, tiles, a.count, a.row_of, shard_lse);
+  return last_error();
+}
+
+int launch_xent_loss(const float *const *shard_lse, const float *const *target_logit, int n_parts,
+                     int64_t m, int64_t vocab, const void *targets, int itype, float *loss,
+                     float *lse, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  Parts p{};
+  for (int i = 0; i < n_parts; ++i) p.lse[i] = shard_lse[i], p.target[i] = target_logit[i];
+  const dim3 grid(blocks(m, 256));
+  if (itype == 0)
+    hipLaunchKernelGGL(xent_loss<int32_t>, grid, dim3(256), 0, st, p, n_parts, m, vocab,
+                       static_cast<const int32_t *>(targets), loss, lse);
+  else
+    hipLaunchKernelGGL(xent_loss<int64_t>, grid, dim3(256), 0, st, p, n_parts, m, vocab,
+                       static_cast<const int64_t *>(targets), loss, lse);
+  return last_error();
+}
+
+int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *grad_loss,
+                            const LossGrads &g, void *workspace, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (r.m == 0) return zero_table(r, g, st);
+  const LossLayout l = loss_layout(kLossGrad, r.m, r.dim, r.rows, r.dtype);
+  const int64_t e = r.dtype == 1 ? 2 : 4;
+  int rc = run_collect(r, l, lse, grad_loss, nullptr, nullptr, workspace, st);
+  if (rc != 0) return rc;
+  const bool in_place = r.dtype == 0 || loads_in_place(r.w, r.dim);
+  // columns of a piece: what the buffer holds, in pieces of one size
+  int64_t most = l.piece_cap / (r.m * e) / 256 * 256;
+  if (!in_place) most = loss_min(most, l.table_rows);
+  const int64_t pieces = (r.rows + most - 1) / most;
+  const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
+  Logits a{};
+  a.x = at(workspace, l.x), a.ldx = l.dim_pad, a.k = r.dtype == 1 ? l.dim_pad : r.dim;
+  a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
+  a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
+  a.lse = reinterpret_cast<const float *>(at(workspace, l.lse));
+  a.ratio = reinterpret_cast<const float *>(at(workspace, l.ratio));
+  a.d = at(workspace, l.piece);
+  Products p{};
+  p.d = a.d, p.x = a.x, p.ldx = a.ldx, p.rows = r.m, p.count = a.count, p.dim = r.dim;
+  p.sums = reinterpret_cast<float *>(at(workspace, l.sums)), p.ld_sums = l.dim_pad;
+  p.scale = reinterpret_cast<const float *>(at(workspace, l.count)) + 1;
+  p.gw_bf16 = g.gwt == 1, p.accumulate = g.accumulate;
+  p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype,
+                                          loss_most_splits(r.m, l.dim_pad, r.rows)));
+  p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
+  for (int64_t row = 0; row < r.rows; row += step) {
+    const char *w = static_cast<const char *>(r.w) + row * r.dim * e;
+    a.w_rows = loss_min(step, r.rows - row), a.row0 = row, a.ldd = loss_up(a.w_rows, 64);
+    if (in_place) {
+      a.w = w, a.ldw = r.dim, a.w_dim = r.dim;
+    } else {
+      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, st);
+      a.w = at(workspace, l.table), a.ldw = l.dim_pad, a.w_dim = l.dim_pad;
+    }
+    pick_logits<true>(a, r.m, r.dtype, st);
+    rc = last_error();
+    if (rc != 0) return rc;
+    p.ldd = a.ldd, p.cols = a.w_rows, p.w = a.w, p.ldw = a.ldw;
+    p.gw = g.gw == nullptr ? nullptr
+                           : static_cast<char *>(g.gw) + row * r.dim * (g.gwt == 1 ? 2 : 4);
+    pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, row == 0, st);
+    rc = last_error();
+    if (rc != 0) return rc;
+  }
+  if (g.gx != nullptr)
+    run_finish(p, r, g, reinterpret_cast<const int32_t *>(at(workspace, l.place)), st);
+  return last_error();
+}
+
+int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossGrads &g,
+                       void *workspace, void *stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (r.m == 0) return zero_table(r, g, st);
+  const LossLayout l = loss_layout(kHeadGrad, r.m, r.dim, r.rows, r.dtype);
+  const int64_t e = r.dtype == 1 ? 2 : 4;
+  const bool f32 = r.dtype == 0;
+  // d is read in place when its rows take 16-byte loads and end at a multiple
+  // of 8 columns (what lies behind may be anything, a NaN too)
+  const bool d_in_place = f32 || (loads_in_place(d, ld) && r.rows % 8 == 0);
+  const bool w_in_place = f32 || loads_in_place(r.w, r.dim);
+  const bool x_in_place = f32 || loads_in_place(r.x, r.dim);
+  int64_t most = r.rows;
+  if (!d_in_place) most = loss_min(most, l.piece_cap / (r.m * e) / 256 * 256);
+  if (!w_in_place) most = loss_min(most, l.table_rows);
+  const int64_t pieces = (r.rows + most - 1) / most;
+  const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
+  Products p{};
+  p.rows = r.m, p.dim = r.dim;
+  p.sums = reinterpret_cast<float *>(at(workspace, l.sums)), p.ld_sums = l.dim_pad;
+  p.gw_bf16 = g.gwt == 1, p.accumulate = g.accumulate;
+  p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype,
+                                          loss_most_splits(r.m, l.dim_pad, r.rows)));
+  p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
+  p.x = r.x, p.ldx = r.dim;
+  if (!x_in_place) {
+    run_copy(r.x, r.dim, r.m, r.dim, at(workspace, l.x), l.dim_pad, st);
+    p.x = at(workspace, l.x), p.ldx = l.dim_pad;
+  }
+  for (int64_t row = 0; row < r.rows; row += step) {
+    const int64_t cols = loss_min(step, r.rows - row);
+    p.cols = cols;
+    p.d = static_cast<const char *>(d) + row * e, p.ldd = ld;
+    if (!d_in_place) {
+      run_copy(p.d, ld, r.m, cols, at(workspace, l.piece), loss_up(cols, 64), st);
+      p.d = at(workspace, l.piece), p.ldd = loss_up(cols, 64);
+    }
+    p.w = static_cast<const char *>(r.w) + row * r.dim * e, p.ldw = r.dim;
+    if (!w_in_place) {
+      run_copy(p.w, r.dim, cols, r.dim, at(workspace, l.table), l.dim_pad, st);
+      p.w = at(workspace, l.table), p.ldw = l.dim_pad;
+    }
+    p.gw = g.gw == nullptr ? nullptr
+                           : static_cast<char *>(g.gw) + row * r.dim * (g.gwt == 1 ? 2 : 4);
+    pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, row == 0, st);
+    const int rc = last_error();
+    if (rc != 0) return rc;
+  }
+  if (g.gx != nullptr) run_finish(p, r, g, nullptr, st);
+  return last_error();
+}
+
+}  // namespace vpe

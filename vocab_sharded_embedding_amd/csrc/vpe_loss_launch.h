@@ -1,0 +1,150 @@
+// Internal interface between the validating C-ABI layer of the loss calls
+// (vpe_loss_api.cpp: plain C++ with no HIP headers) and their kernel launchers
+// (*.hip).  As in vpe_launch.h, launchers receive validated arguments, enqueue
+// on `stream` and return 0 or the hipError_t value the runtime reported.
+// dtype: 0 = f32, 1 = bf16; itype: 0 = int32, 1 = int64.
+#ifndef VPE_LOSS_LAUNCH_H
+#define VPE_LOSS_LAUNCH_H
+
+#include <stdint.h>
+
+namespace vpe {
+
+// ---------------------------------------------------------------------------
+// cross entropy and the head's backward
+// ---------------------------------------------------------------------------
+// Narrowest tile of table rows: a row of hidden states has at most one
+// (maximum, sum) pair per this many table rows.
+constexpr int64_t kLossTileRows = 128;
+// Table rows copied to an aligned buffer at a time, where they are not aligned.
+constexpr int64_t kLossCopyRows = 16384;
+// Bytes of one piece of the logits' gradient, where the whole is more; at least
+// kLossMinPiece columns of it.
+constexpr int64_t kLossPieceBytes = int64_t(1) << 27;
+constexpr int64_t kLossMinPiece = 512;
+// Most fp32 sums for the gradient of the hidden rows where its sum over the
+// vocabulary is split: at least kLossSplitRows table rows each.
+constexpr int64_t kLossSums = int64_t(1) << 23;
+constexpr int64_t kLossSplitRows = 512;
+
+constexpr int64_t loss_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+constexpr int64_t loss_min(int64_t a, int64_t b) { return a < b ? a : b; }
+constexpr int64_t loss_max(int64_t a, int64_t b) { return a > b ? a : b; }
+
+// Byte offsets of the workspaces, 256-byte aligned.  Every size grows with m, so
+// that a workspace for m rows serves fewer.
+struct LossLayout {
+  int64_t count;   // int32: live rows; float: scale of the gradients
+  int64_t row_of;  // int32 [m]: row of the i-th live one
+  int64_t target;  // int32 [m]: its target in the shard, or -1
+  int64_t lse;     // float [m]: (gradients) its log-sum-exp
+  int64_t ratio;   // float [m]: (gradients) its grad_loss over the largest one
+  int64_t place;   // int32 [m]: (gradients) a row's place among the live ones, or -1
+  int64_t x;       // [m][dim_pad] of the type: the live rows
+  int64_t pairs;   // (loss) float2 [tiles][m]
+  int64_t sums;    // (gradients) float [splits][m][dim_pad]
+  int64_t piece;   // (gradients) [m][piece_cols] of the type
+  int64_t piece_cap;
+  int64_t table;   // bf16 [kLossCopyRows or a piece][dim_pad]
+  int64_t table_rows;
+  int64_t dim_pad;
+  int64_t bytes;
+};
+
+enum LossCall { kLossForward, kLossGrad, kHeadGrad };
+
+// Times that sum may be split.
+constexpr int64_t loss_most_splits(int64_t m, int64_t dim_pad, int64_t shard_rows) {
+  return loss_max(1, loss_min(kLossSums / dim_pad / loss_max(m, 1),
+                              (shard_rows + kLossSplitRows - 1) / kLossSplitRows));
+}
+
+inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t shard_rows,
+                              int dtype) {
+  LossLayout l{};
+  const int64_t e = dtype == 1 ? 2 : 4;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += loss_up(bytes, 256);
+    return here;
+  };
+  l.dim_pad = loss_up(dim, 64);
+  l.count = take(256);
+  if (call != kHeadGrad) l.row_of = take(m * 4), l.target = take(m * 4);
+  if (call == kLossGrad) l.lse = take(m * 4), l.ratio = take(m * 4), l.place = take(m * 4);
+  if (call != kHeadGrad || dtype == 1) l.x = take(m * l.dim_pad * e);
+  l.table_rows = loss_min(loss_up(shard_rows, 64), kLossCopyRows);
+  if (call == kLossForward) {
+    l.pairs = take(m * ((shard_rows + kLossTileRows - 1) / kLossTileRows) * 8);
+  } else {
+    // (no less than loss_most_splits() times m rows, and growing with m)
+    const int64_t most = (shard_rows + kLossSplitRows - 1) / kLossSplitRows;
+    l.sums = take(loss_max(m, loss_min(kLossSums / l.dim_pad, m * most)) * l.dim_pad * 4);
+    const int64_t rows = loss_up(shard_rows, 256);
+    l.piece_cap = loss_max(loss_min(m * rows * e, kLossPieceBytes),
+                           m * loss_min(rows, kLossMinPiece) * e);
+    l.piece = take(l.piece_cap);
+  }
+  if (dtype == 1) l.table = take(l.table_rows * l.dim_pad * 2);
+  l.bytes = at;
+  return l;
+}
+
+struct LossRows {  // hidden rows and their targets
+  const void *x;
+  int64_t m, dim;
+  const void *w;
+  int64_t rows;
+  int dtype;
+  int64_t vocab_start, vocab;
+  const void *targets;
+  int itype;
+};
+
+// What the gradients are written to: `gxt`, `gwt` their types.
+struct LossGrads {
+  void *gx;
+  int gxt;
+  void *gw;
+  int gwt;
+  bool accumulate;
+};
+
+int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit, void *workspace,
+                       void *stream);
+int launch_xent_loss(const float *const *shard_lse, const float *const *target_logit, int n_parts,
+                     int64_t m, int64_t vocab, const void *targets, int itype, float *loss,
+                     float *lse, void *stream);
+int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *grad_loss,
+                            const LossGrads &g, void *workspace, void *stream);
+// `d`: the shard's columns of the logits' gradient, row stride ld.
+int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossGrads &g,
+                       void *workspace, void *stream);
+
+// ---------------------------------------------------------------------------
+// clipping
+// ---------------------------------------------------------------------------
+// Tensors per launch: their table travels in the kernel's arguments.
+constexpr int kClipTable = 96;
+
+// Elements per workgroup: a multiple of 2048, so that about 4096 workgroups
+// share the elements, and at least 16384.
+inline int64_t clip_chunk(int64_t total) {
+  return loss_max(loss_up((total + 4095) / 4096, 2048), 16384);
+}
+inline int64_t clip_chunks(const int64_t *counts, int n, int64_t chunk) {
+  int64_t chunks = 0;
+  for (int i = 0; i < n; ++i) chunks += (counts[i] + chunk - 1) / chunk;
+  return chunks;
+}
+
+int launch_grad_sumsq(const void *const *tensors, const int64_t *counts, const int32_t *dtypes,
+                      int n, int64_t total, double *sumsq, double *partial, void *stream);
+int launch_grad_clip(const void *const *tensors, const int64_t *counts, const int32_t *dtypes,
+                     int n, int64_t total, void *const *out, const double *const *sumsq,
+                     int n_parts, double max_norm, float *norm, void *stream);
+
+}  // namespace vpe
+
+#endif

@@ -10,8 +10,8 @@ ranks emulated in one process combine their outputs with
 ``VocabParallelEmbedding.sum_partials`` (the embedding's all-reduce) and by
 writing their logits at ``vocab_start`` into one [M, V] buffer (the LM head's
 gather and concatenation).  No call builds an autograd graph: ``backward()`` does
-not reach through these layers, and ``weight_grad`` and ``distill_grad`` are
-called explicitly.
+not reach through these layers, and ``weight_grad``, ``distill_grad``,
+``xent_grad`` and ``grad`` are called explicitly.
 """
 from __future__ import annotations
 
@@ -23,6 +23,7 @@ from . import (vpe_embed, vpe_lmhead, vpe_lmhead_argmax, vpe_lmhead_logsumexp, v
                vpe_lmhead_prefill_argmax, vpe_lmhead_prefill_logsumexp, vpe_load_shard,
                vpe_logsumexp_combine, vpe_shard_range, vpe_sum_partials)
 from .beam import vpe_beam_merge, vpe_beam_reorder, vpe_beam_select
+from .loss import vpe_lmhead_grad, vpe_lmhead_xent, vpe_lmhead_xent_grad, vpe_xent_loss
 from .training import (vpe_distill_grad, vpe_distill_loss, vpe_distill_shard, vpe_embed_grad,
                        vpe_embed_scaled)
 
@@ -206,6 +207,38 @@ class ParallelLMHead(VocabParallelEmbedding):
                                 self.vocab_start_idx, self.num_embeddings,
                                 temperature=temperature, teacher_lse=teacher_lse,
                                 **self._columns(logits), **to)
+
+    def grad(self, grad_logits: torch.Tensor, hidden: torch.Tensor,
+             grad_weight: Optional[torch.Tensor] = None, accumulate: bool = False, **kw):
+        """(grad_hidden, grad_weight) of ``forward`` from the gradient of its logits
+        ([M, V/tp] or [M, V], such as ``distill_grad``'s).  grad_hidden is this
+        rank's part: the ranks' parts sum to the whole (``sum_partials``).
+        ``grad_weight`` is written, or added to with ``accumulate``; ``kw``:
+        ``x_dtype``, ``weight_dtype``, ``with_x``, ``with_weight``, ``grad_x``."""
+        return vpe_lmhead_grad(grad_logits, hidden, self.weight,
+                               col_offset=self._columns(grad_logits)["col_offset"],
+                               grad_weight=grad_weight, accumulate=accumulate, **kw)
+
+    def xent_shard(self, hidden: torch.Tensor, targets: torch.Tensor):
+        """This rank's (shard_lse, target_logit) of the cross entropy of ``hidden``
+        against the vocabulary ids ``targets``, the logits not kept; rows whose
+        target lies outside the vocabulary (such as -100) take no part.  The
+        ranks' values go to ``xent_loss``."""
+        return vpe_lmhead_xent(hidden, self.weight, targets, self.vocab_start_idx,
+                               self.num_embeddings)
+
+    def xent_loss(self, shard_lse: Sequence[torch.Tensor], target_logit: Sequence[torch.Tensor],
+                  targets: torch.Tensor):
+        """(loss, lse) per row from the ranks' parts (the exchange step, on one device)."""
+        return vpe_xent_loss(shard_lse, target_logit, targets, self.num_embeddings)
+
+    def xent_grad(self, hidden: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                  grad_loss: torch.Tensor, grad_weight: Optional[torch.Tensor] = None,
+                  accumulate: bool = False, **kw):
+        """(grad_hidden, grad_weight) of sum(grad_loss * loss), as ``grad`` gives them."""
+        return vpe_lmhead_xent_grad(hidden, self.weight, targets, lse, grad_loss,
+                                    self.vocab_start_idx, self.num_embeddings,
+                                    grad_weight=grad_weight, accumulate=accumulate, **kw)
 
     def beam_select(self, logits: torch.Tensor, lse: torch.Tensor, scores: torch.Tensor,
                     beams: int, picks: int) -> torch.Tensor:
