@@ -95,3 +95,32 @@ def test_head_backward(m, vocab, dim, tp, dtype):
             rx, ex, rw, ew = products(dd, torch.zeros_like(dd), x.double(), w[s].double(), xd, wd)
             assert_within(gx, rx, ex, f"grad_x {xd} of {s}")
             assert_within(gw, rw, ew, f"grad_weight {wd} of {s}")
+
+
+@pytest.mark.parametrize("m,vocab,dim,dtype", [
+    # several pieces of the vocabulary: 128 MB of bf16 (of fp32) each
+    (2047, 75001, 64, BF16), (1200, 130000, 72, BF16), (4100, 40000, 40, BF16),
+    (700, 100007, 33, F32),
+])
+def test_pieces(m, vocab, dim, dtype):
+    x, w, t, gl = _inputs(m, vocab, dim, dtype, m)
+    ref = Reference(x, w, t, vocab, gl)
+    (loss, lse), _ = _loss(x, w, t, vocab, 1)
+    assert_within(loss, ref.loss, ref.loss_err, "loss")
+    rx, ex, rw, ew = ref.grads(slice(0, vocab), dtype, dtype)
+    gx, gw = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab)
+    assert_within(gx, rx, ex, "grad_x")
+    assert_within(gw, rw, ew, "grad_weight")
+    # one gradient alone: the same bits where the same tiles take it
+    only_x, none = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab, with_weight=False)
+    assert none is None
+    assert_within(only_x, rx, ex, "grad_x alone")
+    none, only_w = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab, with_x=False)
+    assert none is None
+    assert_within(only_w, rw, ew, "grad_weight alone")
+    del rx, ex, rw, ew
+    base = (0.1 * torch.randn(vocab, dim, device="cuda")).to(dtype)
+    acc = base.clone()
+    vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab, grad_weight=acc, accumulate=True)
+    rx, ex, rw, ew = ref.grads(slice(0, vocab), dtype, dtype, base)
+    assert_within(acc, rw, ew, "grad_weight added")

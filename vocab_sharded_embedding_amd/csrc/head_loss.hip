@@ -183,81 +183,122 @@ struct Core;
 template <class S, bool NCOLS, bool MCOLS>
 struct Core<S, true, NCOLS, MCOLS> {
   typedef tile::Product<S, NCOLS, MCOLS> P;
-  static constexpr int kLdsBytes = P::kLdsElems * 2;
   static __device__ __forceinline__ void run(const void *a, int64_t lda, int64_t n_left,
                                              int64_t ka, const void *b, int64_t ldb,
-                                             int64_t m_left, int64_t kb, int64_t k, char *lds,
+                                             int64_t m_left, int64_t kb, int64_t k,
+                                             char *const (&st)[tile::kStages],
                                              f32x16 (&acc)[S::FN][S::FM]) {
     const int wave = tile::wave_id();
-    typename P::StageN sa;
-    typename P::StageM sb;
-    sa.init(static_cast<const uint16_t *>(a), lda, n_left, ka, wave % S::WN * S::TN);
-    sb.init(static_cast<const uint16_t *>(b), ldb, m_left, kb, wave / S::WN * S::TM);
-    P::run(sa, sb, static_cast<int>((k + S::BK - 1) / S::BK), reinterpret_cast<uint16_t *>(lds),
-           acc);
+    P p;
+    p.a.init(static_cast<const uint16_t *>(a), lda, n_left, ka, wave % S::WN * S::TN);
+    p.b.init(static_cast<const uint16_t *>(b), ldb, m_left, kb, wave / S::WN * S::TM);
+    p.run(static_cast<int>((k + S::BK - 1) / S::BK), st, acc);
   }
 };
 template <class S, bool NCOLS, bool MCOLS>
 struct Core<S, false, NCOLS, MCOLS> {
   typedef tile::ProductF<S, NCOLS, MCOLS> P;
-  static constexpr int kLdsBytes = P::kLdsElems * 4;
   static __device__ __forceinline__ void run(const void *a, int64_t lda, int64_t n_left,
                                              int64_t ka, const void *b, int64_t ldb,
-                                             int64_t m_left, int64_t kb, int64_t k, char *lds,
+                                             int64_t m_left, int64_t kb, int64_t k,
+                                             char *const (&st)[tile::kStages],
                                              f32x16 (&acc)[S::FN][S::FM]) {
     const int wave = tile::wave_id();
-    typename P::StageN sa;
-    typename P::StageM sb;
-    sa.init(static_cast<const float *>(a), lda, n_left, ka);
-    sb.init(static_cast<const float *>(b), ldb, m_left, kb);
-    P::run(sa, sb, static_cast<int>((k + S::BK - 1) / S::BK), reinterpret_cast<float *>(lds),
-           wave % S::WN * S::TN, wave / S::WN * S::TM, acc);
+    P p;
+    p.a.init(static_cast<const float *>(a), lda, n_left, ka);
+    p.b.init(static_cast<const float *>(b), ldb, m_left, kb);
+    p.run(static_cast<int>((k + S::BK - 1) / S::BK), st, wave % S::WN * S::TN,
+          wave / S::WN * S::TM, acc);
   }
 };
 
-// A wave's accumulators as rows of m: fragments pass through the wave's part of
-// the LDS (the stages: every wave is done with them), 64 columns of 32 rows at a
-// time, and `put(m, n, v)` gets 4 consecutive columns n.. of row m, neighbouring
-// lanes neighbouring columns.  m and n count from the workgroup's tile.
+// A wave's accumulators as rows of m: 32 rows at a time pass through the wave's
+// part of the LDS (the stages: every wave is done with them), and `put(m, n, v)`
+// gets 16 bytes of consecutive columns n.. of row m, neighbouring lanes
+// neighbouring columns: 4 of fp32 (BF16 false; 64 columns at a time) or 8 rounded
+// to bf16.  m and n count from the workgroup's tile.
 template <class S>
 struct RowWriter {
-  static constexpr int kCols = S::TN < 64 ? S::TN : 64, kLd = kCols + 4;
-  static constexpr int kLdsBytes = S::NW * 32 * kLd * 4;
-  template <class Put>
-  static __device__ __forceinline__ void run(const f32x16 (&acc)[S::FN][S::FM], char *lds,
-                                             Put put) {
+  static constexpr int kCols = S::TN < 64 ? S::TN : 64;
+  static constexpr int kLd = kCols + 4, kLd16 = S::TN + 8;
+  static constexpr int kWaveBytes = 32 * kLd * 4 > 32 * kLd16 * 2 ? 32 * kLd * 4 : 32 * kLd16 * 2;
+
+  static __device__ __forceinline__ char *region(char *const (&st)[tile::kStages]) {
+    // (half of the waves in each of two stages)
+    const int wave = tile::wave_id();
+    return ((wave & 1) ? st[1] : st[0]) + wave / 2 * kWaveBytes;
+  }
+  static __device__ __forceinline__ void turn() {
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+  }
+  template <bool BF16, class Put>
+  static __device__ __forceinline__ void run(const f32x16 (&acc)[S::FN][S::FM],
+                                             char *const (&st)[tile::kStages], Put put) {
     const int lane = threadIdx.x & 63, wave = tile::wave_id();
-    const int wn = wave % S::WN, wm = wave / S::WN, row = lane & 31, hi = lane >> 5;
-    float *mine = reinterpret_cast<float *>(lds) + wave * 32 * kLd;
-    constexpr int kPer = kCols / 4, kRows = 64 / kPer;
+    const int m0 = wave / S::WN * S::TM, n0 = wave % S::WN * S::TN;
+    const int row = lane & 31, hi = lane >> 5;
 #pragma unroll
-    for (int j = 0; j < S::FM; ++j)
+    for (int j = 0; j < S::FM; ++j) {
+      if constexpr (BF16) {
+        uint16_t *mine = reinterpret_cast<uint16_t *>(region(st));
+        constexpr int kPer = S::TN / 8, kRows = 64 / kPer;
 #pragma unroll
-      for (int h = 0; h < S::TN / kCols; ++h) {
-#pragma unroll
-        for (int i = 0; i < kCols / 32; ++i)
+        for (int i = 0; i < S::FN; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const f32x16 &f = acc[h * (kCols / 32) + i][j];
-            *reinterpret_cast<f32x4 *>(mine + row * kLd + i * 32 + 8 * q + 4 * hi) =
-                f32x4{f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]};
+            const f32x16 &f = acc[i][j];
+            *reinterpret_cast<dev::u32x2 *>(mine + row * kLd16 + i * 32 + 8 * q + 4 * hi) =
+                dev::u32x2{dev::pack_bf16(f[4 * q], f[4 * q + 1]),
+                           dev::pack_bf16(f[4 * q + 2], f[4 * q + 3])};
           }
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        turn();
 #pragma unroll
         for (int t = 0; t < 32 / kRows; ++t) {
-          const int r = t * kRows + lane / kPer, n = lane % kPer * 4;
-          const f32x4 v = *reinterpret_cast<const f32x4 *>(mine + r * kLd + n);
-          put(wm * S::TM + j * 32 + r, wn * S::TN + h * kCols + n, v);
+          const int r = t * kRows + lane / kPer, n = lane % kPer * 8;
+          const dev::u32x4 v = *reinterpret_cast<const dev::u32x4 *>(mine + r * kLd16 + n);
+          put(m0 + j * 32 + r, n0 + n, v);
         }
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        turn();
+      } else {
+        float *mine = reinterpret_cast<float *>(region(st));
+        constexpr int kPer = kCols / 4, kRows = 64 / kPer;
+#pragma unroll
+        for (int h = 0; h < S::TN / kCols; ++h) {
+#pragma unroll
+          for (int i = 0; i < kCols / 32; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x16 &f = acc[h * (kCols / 32) + i][j];
+              *reinterpret_cast<f32x4 *>(mine + row * kLd + i * 32 + 8 * q + 4 * hi) =
+                  f32x4{f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]};
+            }
+          turn();
+#pragma unroll
+          for (int t = 0; t < 32 / kRows; ++t) {
+            const int r = t * kRows + lane / kPer, n = lane % kPer * 4;
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(mine + r * kLd + n);
+            put(m0 + j * 32 + r, n0 + h * kCols + n, v);
+          }
+          turn();
+        }
       }
+    }
   }
 };
 #endif
 
-[[maybe_unused]] constexpr int max_of(int a, int b) { return a > b ? a : b; }
+// The stages of a kernel's tile, `st`: LDS arrays of their own (see Product).  Each
+// holds a stage of the product C, and half of the waves' rows.
+#define VPE_STAGES(C)                                                                \
+  constexpr int kRowBytes = (S::NW + 1) / 2 * RowWriter<S>::kWaveBytes;              \
+  constexpr int kStageBytes =                                                        \
+      C::P::kStageBytes > kRowBytes ? C::P::kStageBytes : kRowBytes;                 \
+  __shared__ __attribute__((aligned(16))) char stage0[kStageBytes];                  \
+  __shared__ __attribute__((aligned(16))) char stage1[kStageBytes];                  \
+  __shared__ __attribute__((aligned(16))) char stage2[S::NS > 2 ? kStageBytes : 16]; \
+  char *st[tile::kStages];                                                           \
+  st[0] = stage0, st[1] = stage1, st[2] = stage2;
 
 // ---------------------------------------------------------------------------
 // logits
@@ -292,15 +333,14 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
   s = a + b;
 }
 
-template <class S, bool BF16, bool GRAD>
-__global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
+template <class S, bool BF16, bool GRAD>
+__device__ __forceinline__ void logits_tile(const Logits &a, int block,
+                                            char *const (&st)[tile::kStages]) {
   typedef Core<S, BF16, false, false> C;
-  constexpr int kLds = max_of(C::kLdsBytes, GRAD ? RowWriter<S>::kLdsBytes : S::BM * S::WN * 8);
-  __shared__ __attribute__((aligned(16))) char lds[kLds];
   constexpr int kSize = BF16 ? 2 : 4;
   int tn, tm;
-  tile_of(blockIdx.x, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
+  tile_of(block, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
   const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
   const int64_t live = *a.count;
   if (m0 >= live) return;
@@ -310,7 +350,8 @@ __global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
   C::run(static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
-         static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.k, a.k, lds, acc);
+         static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.k, a.k, st,
+         acc);
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
   const int wn = wave % S::WN, wm = wave / S::WN, hi = lane >> 5;
   const int64_t nb = n0 + wn * S::TN;  // this wave's first column
@@ -320,26 +361,30 @@ __global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
   const int lim = left < 0 ? 0 : (left < S::TN ? static_cast<int>(left) : S::TN);
   __syncthreads();  // every wave is done with the stages
   if constexpr (!GRAD) {
-    float *out = reinterpret_cast<float *>(lds);  // [BM][WN] pairs
+    float *out = reinterpret_cast<float *>(st[0]);  // [BM][WN] pairs
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) {
       const int64_t m = m0 + wm * S::TM + j * 32 + (lane & 31);
+      if (lim < S::TN) {  // columns past the last: exponentials of 0
+#pragma unroll
+        for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (i * 32 + 8 * (r / 4) + 4 * hi + r % 4 >= lim)
+              acc[i][j][r] = -__builtin_huge_valf();
+      }
       float top = -__builtin_huge_valf();
 #pragma unroll
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (lim == S::TN || i * 32 + 8 * (r / 4) + 4 * hi + r % 4 < lim)
-            top = fmaxf(top, acc[i][j][r]);
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
       const float shift = top == -__builtin_huge_valf() ? 0.f : -top * kLog2e;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, shift));
-          if (lim == S::TN || i * 32 + 8 * (r / 4) + 4 * hi + r % 4 < lim) s += e;
-        }
+        for (int r = 0; r < 16; ++r)
+          s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, shift));
       if (s != s) top = s;  // a NaN logit, or +inf
       merge(top, s, __shfl_xor(top, 32), __shfl_xor(s, 32));
       if (hi == 0) {
@@ -374,6 +419,8 @@ __global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
       e[0] = top, e[1] = s;
     }
   } else {
+    // (elementwise work is as long as several steps of the product: what few
+    // elements need is kept out of the common path)
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) {
       const int64_t m = m0 + wm * S::TM + j * 32 + (lane & 31);
@@ -385,30 +432,50 @@ __global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
         const int64_t rel = t < 0 ? -1 : t - a.row0 - nb;
         at = rel >= 0 && rel < lim ? static_cast<int>(rel) : -1;
       }
+      const float shift = -lse * kLog2e;
 #pragma unroll
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int c = i * 32 + 8 * (r / 4) + 4 * hi + r % 4;
+        for (int r = 0; r < 16; ++r)
           // (fp32: the difference first, whose rounding the exponential does
           // not magnify)
-          float e = BF16 ? __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, -lse * kLog2e))
-                         : __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e);
-          if (at == c) e -= 1.f;
-          acc[i][j][r] = c < lim ? e * ratio : 0.f;
-        }
+          acc[i][j][r] = __builtin_amdgcn_exp2f(BF16 ? fmaf(acc[i][j][r], kLog2e, shift)
+                                                     : (acc[i][j][r] - lse) * kLog2e);
+      if (__any(at >= 0)) {
+#pragma unroll
+        for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (at == i * 32 + 8 * (r / 4) + 4 * hi + r % 4) acc[i][j][r] -= 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < S::FN; ++i) acc[i][j] *= ratio;
+      if (lim < S::TN) {
+#pragma unroll
+        for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (i * 32 + 8 * (r / 4) + 4 * hi + r % 4 >= lim) acc[i][j][r] = 0.f;
+      }
     }
-    RowWriter<S>::run(acc, lds, [&](int m, int n, f32x4 v) {
-      // (ldd is a multiple of 64, so 4 columns are inside or past it together)
+    auto put = [&](int m, int n, auto v) {
+      // (ldd is a multiple of 64: the columns of v are inside or past it together)
       if (m0 + m >= live || n0 + n >= a.ldd) return;
       char *to = static_cast<char *>(a.d) + ((m0 + m) * a.ldd + n0 + n) * kSize;
-      if constexpr (BF16)
-        *reinterpret_cast<dev::u32x2 *>(to) =
-            dev::u32x2{dev::pack_bf16(v[0], v[1]), dev::pack_bf16(v[2], v[3])};
-      else
-        *reinterpret_cast<f32x4 *>(to) = v;
-    });
+      *reinterpret_cast<decltype(v) *>(to) = v;
+    };
+    RowWriter<S>::template run<BF16>(acc, st, put);
   }
+}
+#endif
+
+template <class S, bool BF16, bool GRAD>
+__global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef Core<S, BF16, false, false> C;
+  VPE_STAGES(C)
+  static_assert(kStageBytes >= S::BM * S::WN * 8, "the pairs fit a stage");
+  logits_tile<S, BF16, GRAD>(a, blockIdx.x, st);
 #endif
 }
 
@@ -494,26 +561,15 @@ struct Products {
   int w_tiles_n, w_tiles_m;
 };
 
-template <bool USED, class C>
-struct LdsOf {
-  static constexpr int bytes = 0;
-};
-template <class C>
-struct LdsOf<true, C> {
-  static constexpr int bytes = C::kLdsBytes;
-};
-
+#if defined(__HIP_DEVICE_COMPILE__)
 // Parts of the launch: 1 the gradient of x, 2 that of the table, 3 both, the
 // first's workgroups before the second's.
 template <class S, bool BF16, int PARTS>
-__global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
-#if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ void products_tile(const Products &a, int b,
+                                              char *const (&st)[tile::kStages]) {
   typedef Core<S, BF16, true, false> CX;
   typedef Core<S, BF16, true, true> CW;
   constexpr int kSize = BF16 ? 2 : 4;
-  constexpr int kTiles =
-      max_of(LdsOf<(PARTS & 1) != 0, CX>::bytes, LdsOf<(PARTS & 2) != 0, CW>::bytes);
-  __shared__ __attribute__((aligned(16))) char lds[max_of(kTiles, RowWriter<S>::kLdsBytes)];
   const int64_t live = a.count != nullptr ? *a.count : a.rows;
   f32x16 acc[S::FN][S::FM];
 #pragma unroll
@@ -521,7 +577,6 @@ __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
   const int x_blocks = (PARTS & 1) ? a.x_tiles_n * a.x_tiles_m * a.splits : 0;
-  const int b = blockIdx.x;
   if constexpr ((PARTS & 1) != 0) {
     if (b < x_blocks) {
       int tn, t2;  // (tiles of m and splits together)
@@ -536,10 +591,10 @@ __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
       CX::run(static_cast<const char *>(a.w) + (k0 * a.ldw + n0) * kSize, a.ldw, a.dim - n0, k,
               static_cast<const char *>(a.d) + (m0 * a.ldd + k0) * kSize, a.ldd, live - m0,
               // (bf16: columns up to a multiple of 8, the table's rows end before)
-              BF16 ? (k + 7) / 8 * 8 : k, k, lds, acc);
+              BF16 ? (k + 7) / 8 * 8 : k, k, st, acc);
       __syncthreads();
       float *sums = a.sums + split * a.rows * a.ld_sums;
-      RowWriter<S>::run(acc, lds, [&](int m, int n, f32x4 v) {
+      RowWriter<S>::template run<false>(acc, st, [&](int m, int n, f32x4 v) {
         if (m0 + m >= live || n0 + n >= a.ld_sums) return;
         f32x4 *to = reinterpret_cast<f32x4 *>(sums + (m0 + m) * a.ld_sums + n0 + n);
         *to = a.first ? v : *to + v;
@@ -552,40 +607,69 @@ __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
     tile_of(b - x_blocks, a.w_tiles_n, a.w_tiles_m, a.w_tiles_n, tn, tm);
     const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
     CW::run(static_cast<const char *>(a.x) + n0 * kSize, a.ldx, a.dim - n0, live,
-            static_cast<const char *>(a.d) + m0 * kSize, a.ldd, a.cols - m0, live, live, lds, acc);
+            static_cast<const char *>(a.d) + m0 * kSize, a.ldd, a.cols - m0, live, live, st, acc);
     __syncthreads();
     const float scale = a.scale != nullptr ? *a.scale : 1.f;
-    const bool wide = (a.dim & 3) == 0 && (reinterpret_cast<uintptr_t>(a.gw) & 15) == 0;
-    RowWriter<S>::run(acc, lds, [&](int m, int n, f32x4 v) {
-      const int64_t left = a.dim - (n0 + n);
-      if (m0 + m >= a.cols || left <= 0) return;
-      const int64_t at = (m0 + m) * a.dim + n0 + n;
-      v *= scale;
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FM; ++j) acc[i][j] *= scale;
+    // (rows may begin at any element: the vector types ask for no more)
+    if (a.gw_bf16 && !a.accumulate) {
+      RowWriter<S>::template run<true>(acc, st, [&](int m, int n, dev::u32x4 v) {
+        const int64_t left = a.dim - (n0 + n);
+        if (m0 + m >= a.cols || left <= 0) return;
+        uint16_t *to = static_cast<uint16_t *>(a.gw) + (m0 + m) * a.dim + n0 + n;
+        if (left >= 8)
+          __builtin_nontemporal_store(v, reinterpret_cast<dev::Vec<true, 8>::loose *>(to));
+        else
+          for (int e = 0; e < left; ++e)
+            to[e] = static_cast<uint16_t>(v[e / 2] >> (e % 2 * 16));
+      });
+      return;
+    }
+    RowWriter<S>::template run<false>(acc, st, [&](int m, int n, f32x4 v) {
+      if (m0 + m >= a.cols || n0 + n >= a.dim) return;
+      const int64_t row = (m0 + m) * a.dim;
+      float e[4] = {v[0], v[1], v[2], v[3]}, old[4];
       if (a.gw_bf16) {
-        uint16_t *to = static_cast<uint16_t *>(a.gw) + at;
-        if (wide) {  // (rows of a multiple of 4 values: 8-byte words)
-          dev::u32x2 *w = reinterpret_cast<dev::u32x2 *>(to);
-          if (a.accumulate) {
-            const dev::u32x2 o = *w;
-            v += f32x4{dev::bf16_lo(o[0]), dev::bf16_hi(o[0]), dev::bf16_lo(o[1]),
-                       dev::bf16_hi(o[1])};
-          }
-          *w = dev::u32x2{dev::pack_bf16(v[0], v[1]), dev::pack_bf16(v[2], v[3])};
-        } else {
-          for (int e = 0; e < 4 && e < left; ++e)
-            to[e] = dev::one_bf16(a.accumulate ? dev::load_one<true>(to, e) + v[e] : v[e]);
-        }
+        uint16_t *to = static_cast<uint16_t *>(a.gw) + row;
+        dev::load_vec<true, 4>(to, n0 + n, a.dim, old);  // (only to accumulate)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] += old[k];
+        dev::store_vec_nt<true, 4>(to, n0 + n, a.dim, e);
       } else {
-        float *to = static_cast<float *>(a.gw) + at;
-        if (wide) {
-          f32x4 *w = reinterpret_cast<f32x4 *>(to);
-          *w = a.accumulate ? *w + v : v;
-        } else {
-          for (int e = 0; e < 4 && e < left; ++e) to[e] = a.accumulate ? to[e] + v[e] : v[e];
+        float *to = static_cast<float *>(a.gw) + row;
+        if (a.accumulate) {
+          dev::load_vec<false, 4>(to, n0 + n, a.dim, old);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k] += old[k];
         }
+        dev::store_vec_nt<false, 4>(to, n0 + n, a.dim, e);
       }
     });
   }
+}
+#endif
+
+template <class S, bool BF16, int PARTS>
+__global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef Core<S, BF16, true, (PARTS & 2) != 0> CS;
+  VPE_STAGES(CS)
+  products_tile<S, BF16, PARTS>(a, blockIdx.x, st);
+#endif
+}
+
+// Both products of one piece, and the logits' gradient of the next: the second
+// fills the CUs that the first, with few and long tiles, leaves idle.
+template <class S>
+__global__ __launch_bounds__(S::NT) void grad_and_logits_tiles(Products p, int n, Logits a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef Core<S, true, true, true> CS;
+  VPE_STAGES(CS)
+  if (static_cast<int>(blockIdx.x) < n) products_tile<S, true, 3>(p, blockIdx.x, st);
+  else logits_tile<S, true, true>(a, blockIdx.x - n, st);
 #endif
 }
 
@@ -623,6 +707,7 @@ typedef tile::Shape<128, 64, 2, 2, 64, 3> Low64;
 typedef tile::Shape<128, 32, 4, 1, 64, 3> Low32;
 // fp32 tiles
 typedef tile::Shape<128, 128, 2, 2, 16, 2> MediumF;
+typedef tile::Shape<64, 64, 2, 2, 16, 2> SmallF;
 typedef tile::Shape<128, 32, 4, 1, 32, 2> LowF;
 
 int blocks(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
@@ -673,24 +758,41 @@ void run_copy(const void *from, int64_t ld, int64_t rows, int64_t cols, void *to
                      static_cast<uint16_t *>(to), ld_to);
 }
 
-template <class S, bool BF16, bool GRAD>
-void run_logits(Logits a, int64_t m, hipStream_t st) {
+// Sets a's tiles of shape S; returns how many.
+template <class S, bool GRAD>
+int set_tiles(Logits &a, int64_t m) {
   a.tiles_n = blocks(GRAD ? a.ldd : a.w_rows, S::BN);
   a.tiles_m = blocks(m, S::BM);
   a.group_n = 8;
+  return a.tiles_n * a.tiles_m;
+}
+
+template <class S, bool BF16, bool GRAD>
+void run_logits(Logits a, int64_t m, hipStream_t st) {
+  set_tiles<S, GRAD>(a, m);
   hipLaunchKernelGGL((logits_tiles<S, BF16, GRAD>), dim3(a.tiles_n * a.tiles_m), dim3(S::NT), 0, st,
                      a);
 }
 
+// fp32 products with too few tiles of 128 x 128 to fill the chip take 64 x 64.
+bool few_tiles(int64_t n, int64_t m) {
+  return blocks(n, 128) * static_cast<int64_t>(blocks(m, 128)) < 384;
+}
+
+static_assert(SmallF::BN == loss_tile_rows(0) && Medium::BN == loss_tile_rows(1),
+              "the workspace holds a pair per tile");
+
 // Width of the tiles that `pick_logits` takes, as the loss counts its pairs.
-int64_t logits_tile_rows(int64_t m, int dtype) {
-  return dtype == 1 && m > 128 ? Large::BN : kLossTileRows;
+int64_t logits_tile_rows(int64_t m, int64_t rows, int dtype) {
+  if (dtype == 1) return m > 128 ? Large::BN : Medium::BN;
+  return m > 32 && few_tiles(rows, m) ? SmallF::BN : MediumF::BN;
 }
 
 template <bool GRAD>
 void pick_logits(const Logits &a, int64_t m, int dtype, hipStream_t st) {
   if (dtype == 0) {
     if (m <= 32) run_logits<LowF, false, GRAD>(a, m, st);
+    else if (few_tiles(a.w_rows, m)) run_logits<SmallF, false, GRAD>(a, m, st);
     else run_logits<MediumF, false, GRAD>(a, m, st);
   } else if (m <= 32) {
     run_logits<Low32, true, GRAD>(a, m, st);
@@ -703,15 +805,20 @@ void pick_logits(const Logits &a, int64_t m, int dtype, hipStream_t st) {
   }
 }
 
-template <class S, bool BF16, int PARTS>
-void run_products(Products a, bool first, hipStream_t st) {
-  a.first = first;
+// Sets a's tiles of shape S; returns how many.
+template <class S, int PARTS>
+int set_tiles(Products &a) {
   a.x_tiles_n = blocks(a.dim, S::BN);
   a.x_tiles_m = blocks(a.rows, S::BM);
   a.w_tiles_n = blocks(a.dim, S::BN);
   a.w_tiles_m = blocks(a.cols, S::BM);
-  const int n = ((PARTS & 1) ? a.x_tiles_n * a.x_tiles_m * a.splits : 0) +
-                ((PARTS & 2) ? a.w_tiles_n * a.w_tiles_m : 0);
+  return ((PARTS & 1) ? a.x_tiles_n * a.x_tiles_m * a.splits : 0) +
+         ((PARTS & 2) ? a.w_tiles_n * a.w_tiles_m : 0);
+}
+
+template <class S, bool BF16, int PARTS>
+void run_products(Products a, hipStream_t st) {
+  const int n = set_tiles<S, PARTS>(a);
   if (n > 0)
     hipLaunchKernelGGL((grad_tiles<S, BF16, PARTS>), dim3(n), dim3(S::NT), 0, st, a);
 }
@@ -726,31 +833,47 @@ int64_t splits_for(int64_t rows, int64_t dim, int64_t cols, int64_t bn, int64_t 
   return loss_max(1, loss_min(s, most));
 }
 
+// Rows from which the bf16 products take 256 x 256 tiles.
+constexpr int64_t kLargeRows = 1025;
+
 // The two products of a piece.  `splits` is fixed for all pieces of a call.
-void pick_products(Products a, int dtype, bool gx, bool gw, bool first, hipStream_t st) {
+void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t st) {
   if (dtype == 0) {
-    if (gx && a.rows <= 32) run_products<LowF, false, 1>(a, first, st);
-    else if (gx) run_products<MediumF, false, 1>(a, first, st);
-    if (gw) run_products<MediumF, false, 2>(a, first, st);
+    if (gx) {
+      if (a.rows <= 32) run_products<LowF, false, 1>(a, st);
+      else if (few_tiles(a.dim, a.rows)) run_products<SmallF, false, 1>(a, st);
+      else run_products<MediumF, false, 1>(a, st);
+    }
+    if (gw) {
+      if (few_tiles(a.dim, a.cols)) run_products<SmallF, false, 2>(a, st);
+      else run_products<MediumF, false, 2>(a, st);
+    }
     return;
   }
-  if (a.rows > 1024 && gx && gw) {
-    run_products<Large, true, 3>(a, first, st);
+  if (a.rows >= kLargeRows) {
+    if (gx && gw) run_products<Large, true, 3>(a, st);
+    else if (gx) run_products<Large, true, 1>(a, st);
+    else run_products<Large, true, 2>(a, st);
     return;
   }
-  if (gx && a.rows <= 32) run_products<Low32, true, 1>(a, first, st);
-  else if (gx && a.rows <= 64) run_products<Low64, true, 1>(a, first, st);
-  else if (gx && a.rows <= 1024) run_products<Medium, true, 1>(a, first, st);
-  else if (gx) run_products<Large, true, 1>(a, first, st);
-  if (gw && a.rows <= 1024) run_products<Medium, true, 2>(a, first, st);
-  else if (gw) run_products<Large, true, 2>(a, first, st);
+  if (gx && gw && a.rows > 64) {
+    run_products<Medium, true, 3>(a, st);
+    return;
+  }
+  if (gx && a.rows <= 32) run_products<Low32, true, 1>(a, st);
+  else if (gx && a.rows <= 64) run_products<Low64, true, 1>(a, st);
+  else if (gx) run_products<Medium, true, 1>(a, st);
+  if (gw) run_products<Medium, true, 2>(a, st);
 }
 
 int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, int64_t most) {
-  if (dtype == 0)
-    return splits_for(rows, dim, cols, 128, rows <= 32 ? 32 : 128, 512, most);
-  if (rows > 1024) return splits_for(rows, dim, cols, 256, 256, 256, most);
-  return splits_for(rows, dim, cols, 128, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 512, most);
+  const int64_t side = rows <= 32 ? 32 : (rows <= 64 && dtype == 1) ? 64 : 128;
+  if (dtype == 0) {
+    if (rows > 32 && few_tiles(dim, rows)) return splits_for(rows, dim, cols, 64, 64, 512, most);
+    return splits_for(rows, dim, cols, 128, side, 512, most);
+  }
+  if (rows >= kLargeRows) return splits_for(rows, dim, cols, 256, 256, 256, most);
+  return splits_for(rows, dim, cols, 128, side, 512, most);
 }
 
 void run_finish(const Products &a, const LossRows &r, const LossGrads &g, const int32_t *place,
@@ -771,8 +894,8 @@ int zero_table(const LossRows &r, const LossGrads &g, hipStream_t st) {
   Products a{};
   a.dim = r.dim, a.cols = r.rows, a.gw = g.gw, a.gw_bf16 = g.gwt == 1;
   // (no rows: no operand is read)
-  if (r.dtype == 1) run_products<Medium, true, 2>(a, true, st);
-  else run_products<MediumF, false, 2>(a, true, st);
+  if (r.dtype == 1) run_products<Medium, true, 2>(a, st);
+  else run_products<MediumF, false, 2>(a, st);
   return last_error();
 }
 
@@ -794,7 +917,7 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
   a.pairs = reinterpret_cast<float *>(at(workspace, l.pairs)), a.pair_ld = r.m;
   a.target_logit = target_logit;
   const bool in_place = r.dtype == 0 || loads_in_place(r.w, r.dim);
-  const int64_t tile_rows = logits_tile_rows(r.m, r.dtype);
+  const int64_t tile_rows = logits_tile_rows(r.m, r.rows, r.dtype);
   const int64_t piece = in_place ? r.rows : l.table_rows / tile_rows * tile_rows;
   const int64_t step = piece > 0 ? piece : l.table_rows;
   for (int64_t row = 0; row < r.rows; row += step) {
@@ -859,31 +982,48 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
   a.lse = reinterpret_cast<const float *>(at(workspace, l.lse));
   a.ratio = reinterpret_cast<const float *>(at(workspace, l.ratio));
-  a.d = at(workspace, l.piece);
   Products p{};
-  p.d = a.d, p.x = a.x, p.ldx = a.ldx, p.rows = r.m, p.count = a.count, p.dim = r.dim;
+  p.x = a.x, p.ldx = a.ldx, p.rows = r.m, p.count = a.count, p.dim = r.dim;
   p.sums = reinterpret_cast<float *>(at(workspace, l.sums)), p.ld_sums = l.dim_pad;
   p.scale = reinterpret_cast<const float *>(at(workspace, l.count)) + 1;
   p.gw_bf16 = g.gwt == 1, p.accumulate = g.accumulate;
   p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype,
                                           loss_most_splits(r.m, l.dim_pad, r.rows)));
   p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
-  for (int64_t row = 0; row < r.rows; row += step) {
+  // the piece of d that begins at `row`
+  auto piece_logits = [&](int64_t row) {
     const char *w = static_cast<const char *>(r.w) + row * r.dim * e;
     a.w_rows = loss_min(step, r.rows - row), a.row0 = row, a.ldd = loss_up(a.w_rows, 64);
+    a.d = at(workspace, l.piece[row / step % 2]);
     if (in_place) {
       a.w = w, a.ldw = r.dim, a.w_dim = r.dim;
     } else {
       run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, st);
       a.w = at(workspace, l.table), a.ldw = l.dim_pad, a.w_dim = l.dim_pad;
     }
-    pick_logits<true>(a, r.m, r.dtype, st);
-    rc = last_error();
-    if (rc != 0) return rc;
-    p.ldd = a.ldd, p.cols = a.w_rows, p.w = a.w, p.ldw = a.ldw;
+  };
+  // its products, once `a` is it
+  auto piece_products = [&]() {
+    p.d = a.d, p.ldd = a.ldd, p.cols = a.w_rows, p.w = a.w, p.ldw = a.ldw, p.first = a.row0 == 0;
     p.gw = g.gw == nullptr ? nullptr
-                           : static_cast<char *>(g.gw) + row * r.dim * (g.gwt == 1 ? 2 : 4);
-    pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, row == 0, st);
+                           : static_cast<char *>(g.gw) + a.row0 * r.dim * (g.gwt == 1 ? 2 : 4);
+  };
+  // (a copied table leaves no second copy to read beside the products of the first)
+  const bool together = r.dtype == 1 && in_place && r.m >= kLargeRows && g.gx && g.gw;
+  for (int64_t row = 0; row < r.rows; row += step) {
+    if (!together || row == 0) {
+      piece_logits(row);
+      pick_logits<true>(a, r.m, r.dtype, st);
+    }
+    piece_products();
+    if (together && row + step < r.rows) {
+      piece_logits(row + step);
+      const int n = set_tiles<Large, 3>(p), more = set_tiles<Large, true>(a, r.m);
+      hipLaunchKernelGGL(grad_and_logits_tiles<Large>, dim3(n + more), dim3(Large::NT), 0, st, p,
+                         n, a);
+    } else {
+      pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
+    }
     rc = last_error();
     if (rc != 0) return rc;
   }
@@ -927,8 +1067,8 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
     p.cols = cols;
     p.d = static_cast<const char *>(d) + row * e, p.ldd = ld;
     if (!d_in_place) {
-      run_copy(p.d, ld, r.m, cols, at(workspace, l.piece), loss_up(cols, 64), st);
-      p.d = at(workspace, l.piece), p.ldd = loss_up(cols, 64);
+      run_copy(p.d, ld, r.m, cols, at(workspace, l.piece[0]), loss_up(cols, 64), st);
+      p.d = at(workspace, l.piece[0]), p.ldd = loss_up(cols, 64);
     }
     p.w = static_cast<const char *>(r.w) + row * r.dim * e, p.ldw = r.dim;
     if (!w_in_place) {
@@ -937,7 +1077,8 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
     }
     p.gw = g.gw == nullptr ? nullptr
                            : static_cast<char *>(g.gw) + row * r.dim * (g.gwt == 1 ? 2 : 4);
-    pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, row == 0, st);
+    p.first = row == 0;
+    pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
     const int rc = last_error();
     if (rc != 0) return rc;
   }

@@ -13,11 +13,12 @@ namespace vpe {
 // ---------------------------------------------------------------------------
 // cross entropy and the head's backward
 // ---------------------------------------------------------------------------
-// Narrowest tile of table rows: a row of hidden states has at most one
+// Narrowest tile of table rows, by type: a row of hidden states has at most one
 // (maximum, sum) pair per this many table rows.
-constexpr int64_t kLossTileRows = 128;
-// Table rows copied to an aligned buffer at a time, where they are not aligned.
-constexpr int64_t kLossCopyRows = 16384;
+constexpr int64_t loss_tile_rows(int dtype) { return dtype == 1 ? 128 : 64; }
+// Bytes of table rows copied to an aligned buffer at a time, where they are not
+// aligned.
+constexpr int64_t kLossCopyBytes = int64_t(1) << 27;
 // Bytes of one piece of the logits' gradient, where the whole is more; at least
 // kLossMinPiece columns of it.
 constexpr int64_t kLossPieceBytes = int64_t(1) << 27;
@@ -25,7 +26,7 @@ constexpr int64_t kLossMinPiece = 512;
 // Most fp32 sums for the gradient of the hidden rows where its sum over the
 // vocabulary is split: at least kLossSplitRows table rows each.
 constexpr int64_t kLossSums = int64_t(1) << 23;
-constexpr int64_t kLossSplitRows = 512;
+constexpr int64_t kLossSplitRows = 128;
 
 constexpr int64_t loss_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 constexpr int64_t loss_min(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -43,9 +44,10 @@ struct LossLayout {
   int64_t x;       // [m][dim_pad] of the type: the live rows
   int64_t pairs;   // (loss) float2 [tiles][m]
   int64_t sums;    // (gradients) float [splits][m][dim_pad]
-  int64_t piece;   // (gradients) [m][piece_cols] of the type
+  int64_t piece[2];  // (gradients) [m][columns of a piece] of the type; the second
+                     // where there is more than one piece of bf16
   int64_t piece_cap;
-  int64_t table;   // bf16 [kLossCopyRows or a piece][dim_pad]
+  int64_t table;   // bf16 [table_rows][dim_pad]
   int64_t table_rows;
   int64_t dim_pad;
   int64_t bytes;
@@ -74,9 +76,11 @@ inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t sha
   if (call != kHeadGrad) l.row_of = take(m * 4), l.target = take(m * 4);
   if (call == kLossGrad) l.lse = take(m * 4), l.ratio = take(m * 4), l.place = take(m * 4);
   if (call != kHeadGrad || dtype == 1) l.x = take(m * l.dim_pad * e);
-  l.table_rows = loss_min(loss_up(shard_rows, 64), kLossCopyRows);
+  l.table_rows = loss_min(loss_up(shard_rows, 256),
+                          loss_max(4096, kLossCopyBytes / (2 * l.dim_pad) / 256 * 256));
   if (call == kLossForward) {
-    l.pairs = take(m * ((shard_rows + kLossTileRows - 1) / kLossTileRows) * 8);
+    const int64_t tile = loss_tile_rows(dtype);
+    l.pairs = take(m * ((shard_rows + tile - 1) / tile) * 8);
   } else {
     // (no less than loss_most_splits() times m rows, and growing with m)
     const int64_t most = (shard_rows + kLossSplitRows - 1) / kLossSplitRows;
@@ -84,7 +88,8 @@ inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t sha
     const int64_t rows = loss_up(shard_rows, 256);
     l.piece_cap = loss_max(loss_min(m * rows * e, kLossPieceBytes),
                            m * loss_min(rows, kLossMinPiece) * e);
-    l.piece = take(l.piece_cap);
+    l.piece[0] = take(l.piece_cap);
+    l.piece[1] = call == kLossGrad && dtype == 1 ? take(l.piece_cap) : l.piece[0];
   }
   if (dtype == 1) l.table = take(l.table_rows * l.dim_pad * 2);
   l.bytes = at;

@@ -32,6 +32,9 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// Most stages of a tile.
+constexpr int kStages = 3;
+
 // Tile of BN x BM of C over WN x WM waves, k in steps of BK through NS stages.
 // Each wave owns FN x FM fragments of 32 x 32: fragment (i, j) of a lane holds,
 // in register r, n = 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 and m = 32 j + lane % 32.
@@ -42,6 +45,7 @@ struct Shape {
   static constexpr int TN = BN / WN, TM = BM / WM;
   static constexpr int FN = TN / 32, FM = TM / 32;
   static_assert(FN * 32 == TN && FM * 32 == TM, "a wave's tile is whole fragments");
+  static_assert(NS >= 2 && NS <= kStages, "two or three stages");
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -60,8 +64,11 @@ template <bool COLS, int SIDE, int BK, int NW>
 struct Stage;
 
 // In rows: LDS row n holds BK values as pieces of 16 bytes, piece p at slot
-// p ^ f(n), so that the 8 lanes of an LDS pass, which read one piece of 8
-// consecutive rows, meet 8 different groups of banks.
+// p ^ f(n).  The LDS serves a 16-byte read 16 lanes at a time over 64 banks (256
+// bytes), and those lanes read one piece of 16 consecutive rows: f changes with
+// every 256 bytes of rows, so that they meet 16 different groups of 4 banks
+// (counted bank conflicts: half of the LDS's cycles with f changing every 128
+// bytes).
 template <int SIDE, int BK, int NW>
 struct Stage<false, SIDE, BK, NW> {
   static constexpr int kElems = SIDE * BK;
@@ -69,14 +76,14 @@ struct Stage<false, SIDE, BK, NW> {
   static constexpr int kLoads = SIDE / kRowsPerLoad / NW;
   static_assert(kLoads * kRowsPerLoad * NW == SIDE, "whole loads per wave");
   const char *base;
-  int64_t left;  // bytes from base to the operand's end
-  int64_t k_left;
+  int left;  // bytes from base to the operand's end (of SIDE rows: below 2^31)
+  int k_left;
   int voff[kLoads];
-  int piece8;  // first k of this lane's piece
+  int piece8[2];  // first k of this lane's piece, by load
   int rd[BK / 16];
 
   static __device__ __forceinline__ int swizzle(int row) {
-    constexpr int kGroup = BK * 2 >= 128 ? 1 : 128 / (BK * 2);
+    constexpr int kGroup = BK * 2 >= 256 ? 1 : 256 / (BK * 2);
     return (row / kGroup) & (kPieces - 1);
   }
   // `rows` rows from p on exist, of k_limit values (a multiple of 8) each.
@@ -84,8 +91,8 @@ struct Stage<false, SIDE, BK, NW> {
                                        int64_t k_limit, int side_base) {
     const int lane = threadIdx.x & 63, wave = wave_id();
     base = reinterpret_cast<const char *>(p);
-    left = rows > 0 ? ((rows < SIDE ? rows : SIDE) - 1) * ld * 2 + k_limit * 2 : 0;
-    k_left = k_limit;
+    left = static_cast<int>(rows > 0 ? ((rows < SIDE ? rows : SIDE) - 1) * ld * 2 + k_limit * 2 : 0);
+    k_left = static_cast<int>(k_limit);
     const int lrow = lane / kPieces, slot = lane % kPieces;
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
@@ -93,25 +100,24 @@ struct Stage<false, SIDE, BK, NW> {
       const int piece = slot ^ swizzle(row);
       voff[q] = row < rows ? static_cast<int>(row * ld * 2) + piece * 16 : kLoadMask;
     }
-    // (kRowsPerLoad is a multiple of the swizzle's period: one piece for all loads)
-    piece8 = (slot ^ swizzle(lrow)) * 8;
-    static_assert(kRowsPerLoad % 8 == 0, "one piece per lane");
+    // (two loads cover whole periods of f)
+    piece8[0] = (slot ^ swizzle(wave * kRowsPerLoad + lrow)) * 8;
+    piece8[1] = (slot ^ swizzle((NW + wave) * kRowsPerLoad + lrow)) * 8;
+    static_assert(2 * NW * kRowsPerLoad % 16 == 0, "loads two apart take one piece");
     const int row = side_base + (lane & 31);
 #pragma unroll
     for (int ks = 0; ks < BK / 16; ++ks)
       rd[ks] = row * BK + (((ks * 2 + (lane >> 5)) ^ swizzle(row)) << 3);
   }
-  // The next BK values of k into the stage at `dst`.
-  __device__ __forceinline__ void load(uint16_t *dst) {
+  // This wave's q-th load of the next BK values of k into the stage at `dst`.
+  __device__ __forceinline__ void load(uint16_t *dst, int q) const {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char *>(base), 0, static_cast<int>(left > 0 ? left : 0), kRawBuffer);
-    const int wave = wave_id();
-    const bool in = piece8 < k_left;
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave) * 512), 16,
-          in ? voff[q] : kLoadMask, 0, 0, 0);
+        const_cast<char *>(base), 0, left > 0 ? left : 0, kRawBuffer);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave_id()) * 512), 16,
+        piece8[q & 1] < k_left ? voff[q] : kLoadMask, 0, 0, 0);
+  }
+  __device__ __forceinline__ void advance() {
     base += BK * 2;
     left -= BK * 2;
     k_left -= BK;
@@ -162,17 +168,15 @@ struct Stage<true, SIDE, BK, NW> {
     for (int i = 0; i < 4; ++i)
       rd[i] = (8 * hi + r) * SIDE + (((side_base / 16 + 2 * i + b) ^ f) << 4) + (lane & 3) * 4;
   }
-  __device__ __forceinline__ void load(uint16_t *dst) {
-    const int64_t most = kLoadMask;
+  __device__ __forceinline__ void load(uint16_t *dst, int q) const {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char *>(base), 0,
-        static_cast<int>(left > most ? most : (left > 0 ? left : 0)), kRawBuffer);
-    const int wave = wave_id();
-#pragma unroll
-    for (int q = 0; q < kLoads; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave) * 512), 16,
-          voff[q], 0, 0, 0);
+        static_cast<int>(left > kLoadMask ? kLoadMask : (left > 0 ? left : 0)), kRawBuffer);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave_id()) * 512), 16,
+        voff[q], 0, 0, 0);
+  }
+  __device__ __forceinline__ void advance() {
     base += step;
     left -= step;
   }
@@ -186,102 +190,148 @@ struct Stage<true, SIDE, BK, NW> {
   }
 };
 
+// The stages are LDS arrays of their own, and every access names one: the
+// compiler then sees that a read does not touch the stage that a load in flight
+// fills, and waits for no load on its account (it puts a wait for all of them
+// before every transposing read otherwise: 8192^3 in columns 1091 against 956 us).
 template <class S, bool NCOLS, bool MCOLS>
 struct Product {
   typedef Stage<NCOLS, S::BN, S::BK, S::NW> StageN;
   typedef Stage<MCOLS, S::BM, S::BK, S::NW> StageM;
-  static constexpr int kStageElems = StageN::kElems + StageM::kElems;
+  static constexpr int kStageBytes = (StageN::kElems + StageM::kElems) * 2;
   static constexpr int kLoads = StageN::kLoads + StageM::kLoads;
   static constexpr int KS = S::BK / 16;
   static constexpr int kReads = S::FN * (NCOLS ? 2 : 1) + S::FM * (MCOLS ? 2 : 1);
   static constexpr int kMfma = S::FN * S::FM;
-  static constexpr int kLdsElems = S::NS * kStageElems;
   static_assert(KS % 2 == 0, "fragments alternate between two sets of registers");
   static_assert((S::NS - 1) * kLoads <= 63, "outstanding loads fit the counter");
+  // The loads of a step go out over kSpread rounds, from the one in which its
+  // stage is free: the memory path takes one load of 64 x 16 bytes per 16 cycles
+  // and CU, and a wave that finds its queue full issues no MFMA either.
+  static constexpr int kSpread = KS < 3 ? KS : 3;
+  static constexpr int kPart = (kLoads + kSpread - 1) / kSpread;
 
-  // Reads, and in a step's last round the loads of a later step, go out between
-  // the MFMAs: 8192 x 8192 x 1024 in rows 125 -> 123 us, 128 x 128 tiles 143 -> 139.
-  static __device__ __forceinline__ void schedule(bool last) {
-    constexpr int kHalf = kMfma / 2 > 0 ? kMfma / 2 : 1;
-    if (!last) {
-      constexpr int kPer = (kReads + kMfma - 1) / kMfma;
-#pragma unroll
-      for (int g = 0; g < kReads / kPer; ++g) {
-        __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);  // LDS reads
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // MFMAs
-      }
-      __builtin_amdgcn_sched_group_barrier(0x008, kMfma, 0);
-    } else {
-      constexpr int kPer = (kReads + kHalf - 1) / kHalf, kLoad = (kLoads + kHalf - 1) / kHalf;
-#pragma unroll
-      for (int g = 0; g < kHalf; ++g) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);
-      }
-#pragma unroll
-      for (int g = 0; g < kHalf; ++g) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x020, kLoad, 0);  // global loads
-      }
-    }
+  StageN a;
+  StageM b;
+  bf16x8 fa[2][S::FN], fb[2][S::FM];
+
+  __device__ __forceinline__ void load(char *stage, int q) {
+    uint16_t *dst = reinterpret_cast<uint16_t *>(stage);
+    if (q < StageN::kLoads) a.load(dst, q);
+    else if (q < kLoads) b.load(dst + StageN::kElems, q - StageN::kLoads);
   }
-
-  // acc += the product over nk steps.  A wave reads each fragment one MFMA round
-  // ahead; the loads of a step go out NS - 1 steps before it.
-  static __device__ __forceinline__ void run(StageN &a, StageM &b, int nk, uint16_t *lds,
-                                             f32x16 (&acc)[S::FN][S::FM]) {
-    if (nk <= 0) return;
-    bf16x8 fa[2][S::FN], fb[2][S::FM];
-    auto load = [&](int buf) {
-      a.load(lds + buf * kStageElems);
-      b.load(lds + buf * kStageElems + StageN::kElems);
-    };
-    auto frags = [&](int set, int buf, int ks) {
-      const uint16_t *src = lds + buf * kStageElems;
+  __device__ __forceinline__ void load_parts(char *stage, int from, int to) {
 #pragma unroll
-      for (int i = 0; i < S::FN; ++i) fa[set][i] = a.frag(src, ks, i);
+    for (int q = from * kPart; q < to * kPart; ++q) load(stage, q);
+    if (to == kSpread) a.advance(), b.advance();
+  }
+  // The fragments of round ks of a stage, and (part >= 0) a part of the loads into
+  // stage `to` in turn with them.
+  __device__ __forceinline__ void frags(int set, const char *stage, int ks, int part, char *to) {
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(stage);
+    constexpr int kF = S::FN + S::FM;
 #pragma unroll
-      for (int j = 0; j < S::FM; ++j) fb[set][j] = b.frag(src + StageN::kElems, ks, j);
-    };
-    auto mfma = [&](int set) {
+    for (int f = 0; f < (kF > kPart ? kF : kPart); ++f) {
+      if (f < S::FM) fb[set][f] = b.frag(src + StageN::kElems, ks, f);
+      else if (f < kF) fa[set][f - S::FM] = a.frag(src, ks, f - S::FM);
+      if (part >= 0 && f < kPart) load(to, part * kPart + f);
+    }
+    if (part == kSpread - 1) a.advance(), b.advance();
+  }
+  __device__ __forceinline__ void mfma(int set, f32x16 (&acc)[S::FN][S::FM]) const {
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i)
 #pragma unroll
       for (int j = 0; j < S::FM; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0,
+                                                            0, 0);
+  }
+  // Order of a round: the next round's reads and `loads` loads between the MFMAs;
+  // nothing crosses a round's end.  (Left to the compiler, reads sink to just
+  // before their use.)
+  static __device__ __forceinline__ void schedule(int loads) {
+    constexpr int kPer = (kReads + kMfma - 1) / kMfma;
+    constexpr int kLoad = (kPart + kMfma - 1) / kMfma;
 #pragma unroll
-        for (int i = 0; i < S::FN; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j],
-                                                              0, 0, 0);
-    };
+    for (int g = 0; g < kMfma; ++g) {
+      if (g * kPer < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);   // LDS reads
+      if (g * kLoad < loads) __builtin_amdgcn_sched_group_barrier(0x020, kLoad, 0);  // loads
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                             // MFMAs
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // A step whose later steps have loads to send: `prev` takes the rest of step
+  // kt + NS - 1, `cur` the first of step kt + NS.
+  __device__ __forceinline__ void step(char *cur, const char *next, char *prev,
+                                       f32x16 (&acc)[S::FN][S::FM]) {
 #pragma unroll
-    for (int st = 0; st < S::NS; ++st)
-      if (st < nk) load(st);
-    if (nk >= S::NS) __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 1) * kLoads));
-    else __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    for (int ks = 0; ks + 1 < KS; ++ks) {
+      const bool loads = ks + 1 < kSpread;
+      frags((ks + 1) & 1, cur, ks + 1, loads ? ks + 1 : -1, prev);
+      mfma(ks & 1, acc);
+      schedule(loads ? kPart : 0);
+    }
+    // step kt + 1 has landed for this wave, and this wave has read step kt; after
+    // the barrier both hold for all waves
+    __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 2) * kLoads));
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    frags(0, next, 0, 0, cur);
+    mfma((KS - 1) & 1, acc);
+    schedule(kPart);
+  }
+  // acc += the product over nk steps, through the stages st (NS of them).  A wave
+  // reads each fragment one round of MFMAs ahead; the loads of a step begin NS - 1
+  // steps before it.  Ends with every load landed.
+  __device__ __forceinline__ void run(int nk, char *const (&st)[kStages],
+                                      f32x16 (&acc)[S::FN][S::FM]) {
+    if (nk <= 0) return;
+    // (few steps: every stage at once, nothing spread)
+    bool rest = nk >= 2 * S::NS;
+#pragma unroll
+    for (int s = 0; s < S::NS - 1; ++s)
+      if (s < nk) load_parts(st[s], 0, kSpread);
+    if (rest) {
+      load_parts(st[S::NS - 1], 0, 1);
+      __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 2) * kLoads + kPart));
+    } else if (S::NS - 1 < nk) {
+      load_parts(st[S::NS - 1], 0, kSpread);
+      __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 1) * kLoads));
+    } else {
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    }
     asm volatile("s_barrier" ::: "memory");
-    frags(0, 0, 0);
-    int cur = 0;
-    for (int kt = 0; kt < nk; ++kt) {
-      const int next = cur + 1 == S::NS ? 0 : cur + 1;
+    frags(0, st[0], 0, -1, nullptr);
+    int kt = 0;
+    for (; kt + 2 * S::NS - 1 < nk; kt += S::NS) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (ks + 1 < KS) {
-          frags((ks + 1) & 1, cur, ks + 1);
-        } else if (kt + 1 < nk) {
-          // step kt + 1 has landed for this wave, and this wave has read step kt;
-          // after the barrier both hold for all waves
-          if (kt + S::NS <= nk) __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 2) * kLoads));
-          else __builtin_amdgcn_s_waitcnt(wait_vm(0));
-          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          if (kt + S::NS < nk) load(cur);
-          frags(0, next, 0);
-        }
-        mfma(ks & 1);
-        schedule(ks + 1 == KS);
+      for (int u = 0; u < S::NS; ++u)
+        step(st[u], st[(u + 1) % S::NS], st[(u + S::NS - 1) % S::NS], acc);
+    }
+    // the last steps, at most 2 NS - 1 of them
+    char *cur = st[0], *next = st[1], *prev = st[S::NS - 1];
+    for (; kt < nk; ++kt) {
+      if (kSpread > 1 && rest) load_parts(prev, 1, kSpread);
+      rest = false;
+#pragma unroll
+      for (int ks = 0; ks + 1 < KS; ++ks) {
+        frags((ks + 1) & 1, cur, ks + 1, -1, nullptr);
+        mfma(ks & 1, acc);
+        schedule(0);
       }
+      if (kt + 1 < nk) {
+        __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        frags(0, next, 0, -1, nullptr);
+        if (kt + S::NS < nk) load_parts(cur, 0, kSpread);
+      }
+      mfma((KS - 1) & 1, acc);
+      char *const free = cur;
       cur = next;
+      next = S::NS == 2 ? free : prev;
+      prev = free;
     }
   }
 };
-
 
 // ---------------------------------------------------------------------------
 // fp32
@@ -351,20 +401,24 @@ template <class S, bool NCOLS, bool MCOLS>
 struct ProductF {
   typedef StageF<NCOLS, S::BN, S::BK, S::NT> StageN;
   typedef StageF<MCOLS, S::BM, S::BK, S::NT> StageM;
-  static constexpr int kStageElems = StageN::kElems + StageM::kElems;
-  static constexpr int kLdsElems = 2 * kStageElems;
+  static constexpr int kStageBytes = (StageN::kElems + StageM::kElems) * 4;
 
-  static __device__ __forceinline__ void run(StageN &a, StageM &b, int nk, float *lds, int side_n,
-                                             int side_m, f32x16 (&acc)[S::FN][S::FM]) {
+  StageN a;
+  StageM b;
+
+  __device__ __forceinline__ void run(int nk, char *const (&st)[kStages], int side_n, int side_m,
+                                      f32x16 (&acc)[S::FN][S::FM]) {
+    static_assert(S::NS == 2, "two stages");
     if (nk <= 0) return;
     const int lane = threadIdx.x & 63, row = lane & 31, hi = lane >> 5;
     a.load();
     b.load();
-    a.store(lds);
-    b.store(lds + StageN::kElems);
+    float *even = reinterpret_cast<float *>(st[0]), *odd = reinterpret_cast<float *>(st[1]);
+    a.store(even);
+    b.store(even + StageN::kElems);
     for (int kt = 0; kt < nk; ++kt) {
       __syncthreads();
-      float *cur = lds + (kt & 1) * kStageElems, *next = lds + ((kt + 1) & 1) * kStageElems;
+      float *cur = kt & 1 ? odd : even, *next = kt & 1 ? even : odd;
       if (kt + 1 < nk) {
         a.load();
         b.load();
