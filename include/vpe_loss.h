@@ -70,7 +70,7 @@ vpe_status vpe_lmhead_xent_workspace(int64_t m, int64_t dim, int64_t shard_rows,
  * m == 0 is a no-op.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (m < 0 or
  * > VPE_MAX_LOSS_ROWS, dim < 1 or > VPE_MAX_LOSS_DIM, shard_rows < 1 or >=
- * 2^31, vocab < 1, a tensor too large), VPE_ERR_RANGE (the shard does not lie in
+ * 2^31, vocab < 1, more than 2^42 logits, a tensor too large), VPE_ERR_RANGE (the shard does not lie in
  * [0, vocab)), VPE_ERR_WORKSPACE.
  */
 vpe_status vpe_lmhead_xent(const void *x, int64_t m, int64_t dim, const void *weight,

@@ -124,3 +124,24 @@ def test_pieces(m, vocab, dim, dtype):
     vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab, grad_weight=acc, accumulate=True)
     rx, ex, rw, ew = ref.grads(slice(0, vocab), dtype, dtype, base)
     assert_within(acc, rw, ew, "grad_weight added")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_rows_longer_than_a_tile_may_stride(dtype):
+    """Vocabularies past 2^22 ids: logits' gradients in pieces and copies."""
+    m, vocab, dim = 3, (1 << 22) + 77, 8
+    x, w, t, gl = _inputs(m, vocab, dim, dtype, 5, padded=False)
+    t[1] = vocab - 1
+    ref = Reference(x, w, t, vocab, gl)
+    (loss, lse), _ = _loss(x, w, t, vocab, 1)
+    assert_within(loss, ref.loss, ref.loss_err, "loss")
+    rx, ex, rw, ew = ref.grads(slice(0, vocab), dtype, dtype)
+    gx, gw = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab)
+    assert_within(gx, rx, ex, "grad_x")
+    assert_within(gw, rw, ew, "grad_weight")
+    d = ref.d.to(dtype)
+    gx, gw = vpe.vpe_lmhead_grad(d, x, w)
+    dd = d.double()
+    rx, ex, rw, ew = products(dd, torch.zeros_like(dd), x.double(), w.double(), dtype, dtype)
+    assert_within(gx, rx, ex, "grad_x")
+    assert_within(gw, rw, ew, "grad_weight")

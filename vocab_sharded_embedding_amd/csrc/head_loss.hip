@@ -139,19 +139,22 @@ __global__ __launch_bounds__(256) void collect_rows(Collect c) {
   }
 }
 
-// `rows` rows of `cols` bf16 at stride ld, any alignment, copied to stride ld_to
+// `rows` rows of `cols` values at stride ld, any alignment, copied to stride ld_to
 // with zeros up to it.
-__global__ __launch_bounds__(256) void copy_rows(const uint16_t *__restrict__ from, int64_t ld,
+template <bool BF16>
+__global__ __launch_bounds__(256) void copy_rows(const char *__restrict__ from, int64_t ld,
                                                  int64_t rows, int64_t cols,
-                                                 uint16_t *__restrict__ to, int64_t ld_to) {
+                                                 char *__restrict__ to, int64_t ld_to) {
+  constexpr int kSize = BF16 ? 2 : 4, kEpv = 16 / kSize;
   const int lane = threadIdx.x & 63;
-  const int64_t vecs = ld_to / 8;
+  const int64_t vecs = ld_to / kEpv;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); r < rows;
        r += static_cast<int64_t>(gridDim.x) * 4)
     for (int64_t v = lane; v < vecs; v += 64) {
-      float e[8];
-      dev::load_vec<true, 8>(from + r * ld, v * 8, cols, e);
-      *reinterpret_cast<dev::u32x4 *>(to + r * ld_to + v * 8) = dev::Vec<true, 8>::narrow(e);
+      float e[kEpv];
+      dev::load_vec<BF16, kEpv>(from + r * ld * kSize, v * kEpv, cols, e);
+      *reinterpret_cast<dev::u32x4 *>(to + (r * ld_to + v * kEpv) * kSize) =
+          dev::Vec<BF16, kEpv>::narrow(e);
     }
 }
 
@@ -174,43 +177,20 @@ __global__ __launch_bounds__(256) void copy_rows(const uint16_t *__restrict__ fr
   tn = g * group_n + (in - tm * gn);
 }
 
-// The bf16 and the fp32 product under one name: `run` sets acc to the tile whose
-// operands begin at a and b.
-template <class S, bool BF16, bool NCOLS, bool MCOLS>
-struct Core;
-
 #if defined(__HIP_DEVICE_COMPILE__)
-template <class S, bool NCOLS, bool MCOLS>
-struct Core<S, true, NCOLS, MCOLS> {
-  typedef tile::Product<S, NCOLS, MCOLS> P;
-  static __device__ __forceinline__ void run(const void *a, int64_t lda, int64_t n_left,
-                                             int64_t ka, const void *b, int64_t ldb,
-                                             int64_t m_left, int64_t kb, int64_t k,
-                                             char *const (&st)[tile::kStages],
-                                             f32x16 (&acc)[S::FN][S::FM]) {
-    const int wave = tile::wave_id();
-    P p;
-    p.a.init(static_cast<const uint16_t *>(a), lda, n_left, ka, wave % S::WN * S::TN);
-    p.b.init(static_cast<const uint16_t *>(b), ldb, m_left, kb, wave / S::WN * S::TM);
-    p.run(static_cast<int>((k + S::BK - 1) / S::BK), st, acc);
-  }
-};
-template <class S, bool NCOLS, bool MCOLS>
-struct Core<S, false, NCOLS, MCOLS> {
-  typedef tile::ProductF<S, NCOLS, MCOLS> P;
-  static __device__ __forceinline__ void run(const void *a, int64_t lda, int64_t n_left,
-                                             int64_t ka, const void *b, int64_t ldb,
-                                             int64_t m_left, int64_t kb, int64_t k,
-                                             char *const (&st)[tile::kStages],
-                                             f32x16 (&acc)[S::FN][S::FM]) {
-    const int wave = tile::wave_id();
-    P p;
-    p.a.init(static_cast<const float *>(a), lda, n_left, ka);
-    p.b.init(static_cast<const float *>(b), ldb, m_left, kb);
-    p.run(static_cast<int>((k + S::BK - 1) / S::BK), st, wave % S::WN * S::TN,
-          wave / S::WN * S::TM, acc);
-  }
-};
+// Adds to acc the tile whose operands begin at a and b: n_left and m_left rows (or
+// columns), ka and kb values of k that may be read, k to sum over.
+template <class S, int E, bool NCOLS, bool MCOLS>
+__device__ __forceinline__ void product(const void *a, int64_t lda, int64_t n_left, int64_t ka,
+                                        const void *b, int64_t ldb, int64_t m_left, int64_t kb,
+                                        int64_t k, char *const (&st)[tile::kStages],
+                                        f32x16 (&acc)[S::FN][S::FM]) {
+  const int wave = tile::wave_id();
+  tile::Product<S, E, NCOLS, MCOLS> p;
+  p.a.init(a, lda, n_left, ka, wave % S::WN * S::TN);
+  p.b.init(b, ldb, m_left, kb, wave / S::WN * S::TM);
+  p.run(static_cast<int>((k + S::BK - 1) / S::BK), st, acc);
+}
 
 // A wave's accumulators as rows of m: 32 rows at a time pass through the wave's
 // part of the LDS (the stages: every wave is done with them), and `put(m, n, v)`
@@ -289,11 +269,11 @@ struct RowWriter {
 #endif
 
 // The stages of a kernel's tile, `st`: LDS arrays of their own (see Product).  Each
-// holds a stage of the product C, and half of the waves' rows.
-#define VPE_STAGES(C)                                                                \
+// holds a stage of shape S of E-byte elements, and half of the waves' rows.
+#define VPE_STAGES(S, E)                                                             \
   constexpr int kRowBytes = (S::NW + 1) / 2 * RowWriter<S>::kWaveBytes;              \
-  constexpr int kStageBytes =                                                        \
-      C::P::kStageBytes > kRowBytes ? C::P::kStageBytes : kRowBytes;                 \
+  constexpr int kTileBytes = (S::BN + S::BM) * S::BK * E;                            \
+  constexpr int kStageBytes = kTileBytes > kRowBytes ? kTileBytes : kRowBytes;       \
   __shared__ __attribute__((aligned(16))) char stage0[kStageBytes];                  \
   __shared__ __attribute__((aligned(16))) char stage1[kStageBytes];                  \
   __shared__ __attribute__((aligned(16))) char stage2[S::NS > 2 ? kStageBytes : 16]; \
@@ -337,7 +317,6 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
 template <class S, bool BF16, bool GRAD>
 __device__ __forceinline__ void logits_tile(const Logits &a, int block,
                                             char *const (&st)[tile::kStages]) {
-  typedef Core<S, BF16, false, false> C;
   constexpr int kSize = BF16 ? 2 : 4;
   int tn, tm;
   tile_of(block, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
@@ -349,9 +328,9 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
   for (int i = 0; i < S::FN; ++i)
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
-  C::run(static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
-         static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.k, a.k, st,
-         acc);
+  product<S, kSize, false, false>(
+      static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
+      static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.k, a.k, st, acc);
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
   const int wn = wave % S::WN, wm = wave / S::WN, hi = lane >> 5;
   const int64_t nb = n0 + wn * S::TN;  // this wave's first column
@@ -472,8 +451,8 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
 template <class S, bool BF16, bool GRAD>
 __global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  typedef Core<S, BF16, false, false> C;
-  VPE_STAGES(C)
+  constexpr int kSize = BF16 ? 2 : 4;
+  VPE_STAGES(S, kSize)
   static_assert(kStageBytes >= S::BM * S::WN * 8, "the pairs fit a stage");
   logits_tile<S, BF16, GRAD>(a, blockIdx.x, st);
 #endif
@@ -567,8 +546,6 @@ struct Products {
 template <class S, bool BF16, int PARTS>
 __device__ __forceinline__ void products_tile(const Products &a, int b,
                                               char *const (&st)[tile::kStages]) {
-  typedef Core<S, BF16, true, false> CX;
-  typedef Core<S, BF16, true, true> CW;
   constexpr int kSize = BF16 ? 2 : 4;
   const int64_t live = a.count != nullptr ? *a.count : a.rows;
   f32x16 acc[S::FN][S::FM];
@@ -588,10 +565,12 @@ __device__ __forceinline__ void products_tile(const Products &a, int b,
       int64_t k = a.cols - k0 < a.per_split ? a.cols - k0 : a.per_split;
       if (k < 0) k = 0;
       if (k == 0 && !a.first) return;
-      CX::run(static_cast<const char *>(a.w) + (k0 * a.ldw + n0) * kSize, a.ldw, a.dim - n0, k,
-              static_cast<const char *>(a.d) + (m0 * a.ldd + k0) * kSize, a.ldd, live - m0,
-              // (bf16: columns up to a multiple of 8, the table's rows end before)
-              BF16 ? (k + 7) / 8 * 8 : k, k, st, acc);
+      // (columns of d up to whole 16 bytes: the table's rows end before)
+      constexpr int kEpp = 16 / kSize;
+      product<S, kSize, true, false>(
+          static_cast<const char *>(a.w) + (k0 * a.ldw + n0) * kSize, a.ldw, a.dim - n0, k,
+          static_cast<const char *>(a.d) + (m0 * a.ldd + k0) * kSize, a.ldd, live - m0,
+          (k + kEpp - 1) / kEpp * kEpp, k, st, acc);
       __syncthreads();
       float *sums = a.sums + split * a.rows * a.ld_sums;
       RowWriter<S>::template run<false>(acc, st, [&](int m, int n, f32x4 v) {
@@ -606,8 +585,9 @@ __device__ __forceinline__ void products_tile(const Products &a, int b,
     int tn, tm;
     tile_of(b - x_blocks, a.w_tiles_n, a.w_tiles_m, a.w_tiles_n, tn, tm);
     const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
-    CW::run(static_cast<const char *>(a.x) + n0 * kSize, a.ldx, a.dim - n0, live,
-            static_cast<const char *>(a.d) + m0 * kSize, a.ldd, a.cols - m0, live, live, st, acc);
+    product<S, kSize, true, true>(
+        static_cast<const char *>(a.x) + n0 * kSize, a.ldx, a.dim - n0, live,
+        static_cast<const char *>(a.d) + m0 * kSize, a.ldd, a.cols - m0, live, live, st, acc);
     __syncthreads();
     const float scale = a.scale != nullptr ? *a.scale : 1.f;
 #pragma unroll
@@ -655,8 +635,8 @@ __device__ __forceinline__ void products_tile(const Products &a, int b,
 template <class S, bool BF16, int PARTS>
 __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  typedef Core<S, BF16, true, (PARTS & 2) != 0> CS;
-  VPE_STAGES(CS)
+  constexpr int kSize = BF16 ? 2 : 4;
+  VPE_STAGES(S, kSize)
   products_tile<S, BF16, PARTS>(a, blockIdx.x, st);
 #endif
 }
@@ -666,8 +646,7 @@ __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
 template <class S>
 __global__ __launch_bounds__(S::NT) void grad_and_logits_tiles(Products p, int n, Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  typedef Core<S, true, true, true> CS;
-  VPE_STAGES(CS)
+  VPE_STAGES(S, 2)
   if (static_cast<int>(blockIdx.x) < n) products_tile<S, true, 3>(p, blockIdx.x, st);
   else logits_tile<S, true, true>(a, blockIdx.x - n, st);
 #endif
@@ -706,9 +685,9 @@ typedef tile::Shape<128, 128, 2, 2, 64, 2> Medium;
 typedef tile::Shape<128, 64, 2, 2, 64, 3> Low64;
 typedef tile::Shape<128, 32, 4, 1, 64, 3> Low32;
 // fp32 tiles
-typedef tile::Shape<128, 128, 2, 2, 16, 2> MediumF;
-typedef tile::Shape<64, 64, 2, 2, 16, 2> SmallF;
-typedef tile::Shape<128, 32, 4, 1, 32, 2> LowF;
+typedef tile::Shape<128, 128, 2, 2, 32, 2> MediumF;
+typedef tile::Shape<64, 64, 2, 2, 32, 2> SmallF;
+typedef tile::Shape<128, 32, 4, 1, 32, 3> LowF;
 
 int blocks(int64_t n, int64_t per) { return static_cast<int>((n + per - 1) / per); }
 
@@ -746,16 +725,21 @@ int run_collect(const LossRows &r, const LossLayout &l, const float *lse, const 
   return last_error();
 }
 
-// Rows of a bf16 table that 16-byte loads can take in place.
-bool loads_in_place(const void *p, int64_t ld) {
-  return ld % 8 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+// Rows that the tiles can read in place.
+bool loads_in_place(const void *p, int64_t ld, int dtype) {
+  return ld % (dtype == 1 ? 8 : 4) == 0 && ld <= kLossMaxStride &&
+         (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
 
 void run_copy(const void *from, int64_t ld, int64_t rows, int64_t cols, void *to, int64_t ld_to,
-              hipStream_t st) {
-  hipLaunchKernelGGL(copy_rows, dim3(static_cast<unsigned>(loss_min(blocks(rows, 4), 4096))),
-                     dim3(256), 0, st, static_cast<const uint16_t *>(from), ld, rows, cols,
-                     static_cast<uint16_t *>(to), ld_to);
+              int dtype, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(loss_min((rows + 3) / 4, 4096)));
+  if (dtype == 1)
+    hipLaunchKernelGGL(copy_rows<true>, grid, dim3(256), 0, st, static_cast<const char *>(from),
+                       ld, rows, cols, static_cast<char *>(to), ld_to);
+  else
+    hipLaunchKernelGGL(copy_rows<false>, grid, dim3(256), 0, st, static_cast<const char *>(from),
+                       ld, rows, cols, static_cast<char *>(to), ld_to);
 }
 
 // Sets a's tiles of shape S; returns how many.
@@ -774,9 +758,10 @@ void run_logits(Logits a, int64_t m, hipStream_t st) {
                      a);
 }
 
-// fp32 products with too few tiles of 128 x 128 to fill the chip take 64 x 64.
-bool few_tiles(int64_t n, int64_t m) {
-  return blocks(n, 128) * static_cast<int64_t>(blocks(m, 128)) < 384;
+// fp32 products with too few tiles of 128 x 128 to fill the chip (`splits` times)
+// take 64 x 64.
+bool few_tiles(int64_t n, int64_t m, int64_t splits = 1) {
+  return blocks(n, 128) * static_cast<int64_t>(blocks(m, 128)) * splits < 256;
 }
 
 static_assert(SmallF::BN == loss_tile_rows(0) && Medium::BN == loss_tile_rows(1),
@@ -841,7 +826,7 @@ void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t s
   if (dtype == 0) {
     if (gx) {
       if (a.rows <= 32) run_products<LowF, false, 1>(a, st);
-      else if (few_tiles(a.dim, a.rows)) run_products<SmallF, false, 1>(a, st);
+      else if (few_tiles(a.dim, a.rows, a.splits)) run_products<SmallF, false, 1>(a, st);
       else run_products<MediumF, false, 1>(a, st);
     }
     if (gw) {
@@ -868,12 +853,10 @@ void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t s
 
 int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, int64_t most) {
   const int64_t side = rows <= 32 ? 32 : (rows <= 64 && dtype == 1) ? 64 : 128;
-  if (dtype == 0) {
-    if (rows > 32 && few_tiles(dim, rows)) return splits_for(rows, dim, cols, 64, 64, 512, most);
-    return splits_for(rows, dim, cols, 128, side, 512, most);
-  }
-  if (rows >= kLargeRows) return splits_for(rows, dim, cols, 256, 256, 256, most);
-  return splits_for(rows, dim, cols, 128, side, 512, most);
+  if (dtype == 1 && rows >= kLargeRows) return splits_for(rows, dim, cols, 256, 256, 256, most);
+  const int64_t s = splits_for(rows, dim, cols, 128, side, 512, most);
+  if (dtype == 1 || rows <= 32 || !few_tiles(dim, rows, s)) return s;
+  return splits_for(rows, dim, cols, 64, 64, 512, most);
 }
 
 void run_finish(const Products &a, const LossRows &r, const LossGrads &g, const int32_t *place,
@@ -916,7 +899,7 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
   a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
   a.pairs = reinterpret_cast<float *>(at(workspace, l.pairs)), a.pair_ld = r.m;
   a.target_logit = target_logit;
-  const bool in_place = r.dtype == 0 || loads_in_place(r.w, r.dim);
+  const bool in_place = loads_in_place(r.w, r.dim, r.dtype);
   const int64_t tile_rows = logits_tile_rows(r.m, r.rows, r.dtype);
   const int64_t piece = in_place ? r.rows : l.table_rows / tile_rows * tile_rows;
   const int64_t step = piece > 0 ? piece : l.table_rows;
@@ -926,10 +909,11 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
     if (in_place) {
       a.w = w, a.ldw = r.dim, a.w_dim = r.dim;
     } else {
-      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, st);
+      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, r.dtype,
+               st);
       a.w = at(workspace, l.table), a.ldw = l.dim_pad, a.w_dim = l.dim_pad;
     }
-    a.k = r.dtype == 1 ? l.dim_pad : r.dim;
+    a.k = l.dim_pad;
     pick_logits<false>(a, r.m, r.dtype, st);
     rc = last_error();
     if (rc != 0) return rc;
@@ -970,14 +954,14 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   const int64_t e = r.dtype == 1 ? 2 : 4;
   int rc = run_collect(r, l, lse, grad_loss, nullptr, nullptr, workspace, st);
   if (rc != 0) return rc;
-  const bool in_place = r.dtype == 0 || loads_in_place(r.w, r.dim);
+  const bool in_place = loads_in_place(r.w, r.dim, r.dtype);
   // columns of a piece: what the buffer holds, in pieces of one size
-  int64_t most = l.piece_cap / (r.m * e) / 256 * 256;
+  int64_t most = loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride);
   if (!in_place) most = loss_min(most, l.table_rows);
   const int64_t pieces = (r.rows + most - 1) / most;
   const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
   Logits a{};
-  a.x = at(workspace, l.x), a.ldx = l.dim_pad, a.k = r.dtype == 1 ? l.dim_pad : r.dim;
+  a.x = at(workspace, l.x), a.ldx = l.dim_pad, a.k = l.dim_pad;
   a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
   a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
   a.lse = reinterpret_cast<const float *>(at(workspace, l.lse));
@@ -998,7 +982,8 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
     if (in_place) {
       a.w = w, a.ldw = r.dim, a.w_dim = r.dim;
     } else {
-      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, st);
+      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, r.dtype,
+               st);
       a.w = at(workspace, l.table), a.ldw = l.dim_pad, a.w_dim = l.dim_pad;
     }
   };
@@ -1039,14 +1024,14 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
   if (r.m == 0) return zero_table(r, g, st);
   const LossLayout l = loss_layout(kHeadGrad, r.m, r.dim, r.rows, r.dtype);
   const int64_t e = r.dtype == 1 ? 2 : 4;
-  const bool f32 = r.dtype == 0;
-  // d is read in place when its rows take 16-byte loads and end at a multiple
-  // of 8 columns (what lies behind may be anything, a NaN too)
-  const bool d_in_place = f32 || (loads_in_place(d, ld) && r.rows % 8 == 0);
-  const bool w_in_place = f32 || loads_in_place(r.w, r.dim);
-  const bool x_in_place = f32 || loads_in_place(r.x, r.dim);
+  // (d's rows have to end at whole 16 bytes too: what lies behind may be anything,
+  // a NaN as well)
+  const bool d_in_place = loads_in_place(d, ld, r.dtype) && r.rows % (16 / e) == 0;
+  const bool w_in_place = loads_in_place(r.w, r.dim, r.dtype);
+  const bool x_in_place = loads_in_place(r.x, r.dim, r.dtype);
   int64_t most = r.rows;
-  if (!d_in_place) most = loss_min(most, l.piece_cap / (r.m * e) / 256 * 256);
+  if (!d_in_place)
+    most = loss_min(most, loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride));
   if (!w_in_place) most = loss_min(most, l.table_rows);
   const int64_t pieces = (r.rows + most - 1) / most;
   const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
@@ -1059,7 +1044,7 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
   p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
   p.x = r.x, p.ldx = r.dim;
   if (!x_in_place) {
-    run_copy(r.x, r.dim, r.m, r.dim, at(workspace, l.x), l.dim_pad, st);
+    run_copy(r.x, r.dim, r.m, r.dim, at(workspace, l.x), l.dim_pad, r.dtype, st);
     p.x = at(workspace, l.x), p.ldx = l.dim_pad;
   }
   for (int64_t row = 0; row < r.rows; row += step) {
@@ -1067,12 +1052,13 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
     p.cols = cols;
     p.d = static_cast<const char *>(d) + row * e, p.ldd = ld;
     if (!d_in_place) {
-      run_copy(p.d, ld, r.m, cols, at(workspace, l.piece[0]), loss_up(cols, 64), st);
+      run_copy(p.d, ld, r.m, cols, at(workspace, l.piece[0]), loss_up(cols, 64), r.dtype, st);
       p.d = at(workspace, l.piece[0]), p.ldd = loss_up(cols, 64);
     }
     p.w = static_cast<const char *>(r.w) + row * r.dim * e, p.ldw = r.dim;
     if (!w_in_place) {
-      run_copy(p.w, r.dim, cols, r.dim, at(workspace, l.table), l.dim_pad, st);
+      run_copy(p.w, r.dim, cols, r.dim, at(workspace, l.table), l.dim_pad, r.dtype,
+               st);
       p.w = at(workspace, l.table), p.ldw = l.dim_pad;
     }
     p.gw = g.gw == nullptr ? nullptr

@@ -25,11 +25,14 @@ vpe_status launched(int rc) { return rc == 0 ? VPE_OK : VPE_ERR_LAUNCH; }
 // Largest element count of any one tensor (indexes in the kernels are 64-bit).
 constexpr int64_t kMaxElems = int64_t(1) << 39;
 constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
+// Largest number of logits: their tiles are counted in 31 bits.
+constexpr int64_t kMaxLogits = int64_t(1) << 42;
 
 vpe_status check_sizes(int64_t m, int64_t dim, int64_t shard_rows, vpe_dtype dt) {
   if (!known_dtype(dt)) return VPE_ERR_DTYPE;
   if (m < 0 || m > VPE_MAX_LOSS_ROWS || dim < 1 || dim > VPE_MAX_LOSS_DIM || shard_rows < 1 ||
-      shard_rows > kMax31 || shard_rows > kMaxElems / dim)
+      shard_rows > kMax31 || shard_rows > kMaxElems / dim ||
+      (m > 0 && shard_rows > kMaxLogits / m))
     return VPE_ERR_SHAPE;
   return VPE_OK;
 }

@@ -28,6 +28,10 @@ constexpr int64_t kLossMinPiece = 512;
 constexpr int64_t kLossSums = int64_t(1) << 23;
 constexpr int64_t kLossSplitRows = 128;
 
+// Largest stride of rows that the tiles read in place: offsets inside a tile of 256
+// rows fit 31 bits.
+constexpr int64_t kLossMaxStride = int64_t(1) << 22;
+
 constexpr int64_t loss_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 constexpr int64_t loss_min(int64_t a, int64_t b) { return a < b ? a : b; }
 constexpr int64_t loss_max(int64_t a, int64_t b) { return a > b ? a : b; }
@@ -47,7 +51,7 @@ struct LossLayout {
   int64_t piece[2];  // (gradients) [m][columns of a piece] of the type; the second
                      // where there is more than one piece of bf16
   int64_t piece_cap;
-  int64_t table;   // bf16 [table_rows][dim_pad]
+  int64_t table;   // [table_rows][dim_pad] of the type
   int64_t table_rows;
   int64_t dim_pad;
   int64_t bytes;
@@ -75,9 +79,9 @@ inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t sha
   l.count = take(256);
   if (call != kHeadGrad) l.row_of = take(m * 4), l.target = take(m * 4);
   if (call == kLossGrad) l.lse = take(m * 4), l.ratio = take(m * 4), l.place = take(m * 4);
-  if (call != kHeadGrad || dtype == 1) l.x = take(m * l.dim_pad * e);
+  l.x = take(m * l.dim_pad * e);
   l.table_rows = loss_min(loss_up(shard_rows, 256),
-                          loss_max(4096, kLossCopyBytes / (2 * l.dim_pad) / 256 * 256));
+                          loss_max(4096, kLossCopyBytes / (e * l.dim_pad) / 256 * 256));
   if (call == kLossForward) {
     const int64_t tile = loss_tile_rows(dtype);
     l.pairs = take(m * ((shard_rows + tile - 1) / tile) * 8);
@@ -91,7 +95,7 @@ inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t sha
     l.piece[0] = take(l.piece_cap);
     l.piece[1] = call == kLossGrad && dtype == 1 ? take(l.piece_cap) : l.piece[0];
   }
-  if (dtype == 1) l.table = take(l.table_rows * l.dim_pad * 2);
+  l.table = take(l.table_rows * l.dim_pad * e);
   l.bytes = at;
   return l;
 }

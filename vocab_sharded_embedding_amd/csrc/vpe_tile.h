@@ -8,13 +8,13 @@
 // contiguous ("columns": at k ld + n, as a table is for the gradient of the
 // hidden rows, which sums over its rows).  Nothing is ever transposed in memory.
 //
-// bf16: v_mfma_f32_32x32x16_bf16.  Both operands are staged through NS stages of
-// LDS by buffer loads that write LDS directly, BK values of k each.  A lane's
-// fragment is 8 consecutive k of one n or m: an operand in rows gives it in one
-// 16-byte LDS read, one in columns in two transposing 8-byte reads
-// (ds_read_b64_tr_b16: 16 lanes read 4 values of k x 16 columns and get 4 values
-// of k of one column each).
-// fp32: v_mfma_f32_32x32x2_f32 on tiles kept in LDS with k outermost.
+// Both operands are staged through NS stages of LDS by buffer loads that write LDS
+// directly, BK values of k each, and multiplied by v_mfma_f32_32x32x16_bf16 or
+// v_mfma_f32_32x32x2_f32.  A lane's fragment is consecutive values of k of one n or
+// m: an operand in rows gives it in one 16-byte LDS read; one in columns, of bf16 in
+// two transposing 8-byte reads (ds_read_b64_tr_b16: 16 lanes read 4 values of k x 16
+// columns and get 4 values of k of one column each), of fp32 in four 4-byte reads.
+// Rows have to begin at 16 bytes and hold whole 16 bytes.
 #ifndef VPE_TILE_H
 #define VPE_TILE_H
 
@@ -59,8 +59,21 @@ __device__ __forceinline__ int wave_id() {
   return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
 }
 
-// One operand's side of the staging.  `COLS`: it lies in columns.
-template <bool COLS, int SIDE, int BK, int NW>
+// A lane's fragment: bf16, 8 consecutive values of k of one n or m (a round of
+// MFMAs takes 16 values of k, lanes 0-31 the first 8); fp32, 4 of them (8 values a
+// round, in 4 MFMAs that each take one from either half of the lanes).
+template <int E>
+struct Frag {
+  typedef bf16x8 type;
+};
+template <>
+struct Frag<4> {
+  typedef f32x4 type;
+};
+
+// One operand's side of the staging, elements of E bytes.  `COLS`: it lies in
+// columns.  Row strides are at most 2^22 elements: offsets inside a tile fit an int.
+template <bool COLS, int SIDE, int BK, int NW, int E>
 struct Stage;
 
 // In rows: LDS row n holds BK values as pieces of 16 bytes, piece p at slot
@@ -69,124 +82,147 @@ struct Stage;
 // every 256 bytes of rows, so that they meet 16 different groups of 4 banks
 // (counted bank conflicts: half of the LDS's cycles with f changing every 128
 // bytes).
-template <int SIDE, int BK, int NW>
-struct Stage<false, SIDE, BK, NW> {
-  static constexpr int kElems = SIDE * BK;
-  static constexpr int kPieces = BK / 8, kRowsPerLoad = 64 / kPieces;
+template <int SIDE, int BK, int NW, int E>
+struct Stage<false, SIDE, BK, NW, E> {
+  static constexpr int kRowBytes = BK * E, kBytes = SIDE * kRowBytes;
+  static constexpr int kPieces = kRowBytes / 16, kRowsPerLoad = 64 / kPieces;
   static constexpr int kLoads = SIDE / kRowsPerLoad / NW;
+  static constexpr int kReads = 1;  // of the LDS, per fragment
   static_assert(kLoads * kRowsPerLoad * NW == SIDE, "whole loads per wave");
+  typedef typename Frag<E>::type frag_t;
   const char *base;
   int left;  // bytes from base to the operand's end (of SIDE rows: below 2^31)
-  int k_left;
   int voff[kLoads];
-  int piece8[2];  // first k of this lane's piece, by load
-  int rd[BK / 16];
+  int piece_at[2];  // this lane's piece, as bytes into a row's step, by load
+  int rd[kRowBytes / 32];
+  int k_left;  // bytes of a row
 
   static __device__ __forceinline__ int swizzle(int row) {
-    constexpr int kGroup = BK * 2 >= 256 ? 1 : 256 / (BK * 2);
+    constexpr int kGroup = kRowBytes >= 256 ? 1 : 256 / kRowBytes;
     return (row / kGroup) & (kPieces - 1);
   }
-  // `rows` rows from p on exist, of k_limit values (a multiple of 8) each.
-  __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int64_t rows,
-                                       int64_t k_limit, int side_base) {
+  // `rows` rows from p on exist, of k_limit values (whole 16 bytes) each.
+  __device__ __forceinline__ void init(const void *p, int64_t ld, int64_t rows, int64_t k_limit,
+                                       int side_base) {
     const int lane = threadIdx.x & 63, wave = wave_id();
-    base = reinterpret_cast<const char *>(p);
-    left = static_cast<int>(rows > 0 ? ((rows < SIDE ? rows : SIDE) - 1) * ld * 2 + k_limit * 2 : 0);
-    k_left = static_cast<int>(k_limit);
+    base = static_cast<const char *>(p);
+    left = static_cast<int>(rows > 0 ? (((rows < SIDE ? rows : SIDE) - 1) * ld + k_limit) * E : 0);
+    k_left = static_cast<int>(k_limit * E);
     const int lrow = lane / kPieces, slot = lane % kPieces;
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
       const int row = (q * NW + wave) * kRowsPerLoad + lrow;
       const int piece = slot ^ swizzle(row);
-      voff[q] = row < rows ? static_cast<int>(row * ld * 2) + piece * 16 : kLoadMask;
+      voff[q] = row < rows ? static_cast<int>(row * ld * E) + piece * 16 : kLoadMask;
     }
     // (two loads cover whole periods of f)
-    piece8[0] = (slot ^ swizzle(wave * kRowsPerLoad + lrow)) * 8;
-    piece8[1] = (slot ^ swizzle((NW + wave) * kRowsPerLoad + lrow)) * 8;
+    piece_at[0] = (slot ^ swizzle(wave * kRowsPerLoad + lrow)) * 16;
+    piece_at[1] = (slot ^ swizzle((NW + wave) * kRowsPerLoad + lrow)) * 16;
     static_assert(2 * NW * kRowsPerLoad % 16 == 0, "loads two apart take one piece");
     const int row = side_base + (lane & 31);
 #pragma unroll
-    for (int ks = 0; ks < BK / 16; ++ks)
-      rd[ks] = row * BK + (((ks * 2 + (lane >> 5)) ^ swizzle(row)) << 3);
+    for (int ks = 0; ks < kRowBytes / 32; ++ks)
+      rd[ks] = row * kRowBytes + (((ks * 2 + (lane >> 5)) ^ swizzle(row)) << 4);
   }
   // This wave's q-th load of the next BK values of k into the stage at `dst`.
-  __device__ __forceinline__ void load(uint16_t *dst, int q) const {
+  __device__ __forceinline__ void load(char *dst, int q) const {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char *>(base), 0, left > 0 ? left : 0, kRawBuffer);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave_id()) * 512), 16,
-        piece8[q & 1] < k_left ? voff[q] : kLoadMask, 0, 0, 0);
+        rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave_id()) * 1024), 16,
+        piece_at[q & 1] < k_left ? voff[q] : kLoadMask, 0, 0, 0);
   }
   __device__ __forceinline__ void advance() {
-    base += BK * 2;
-    left -= BK * 2;
-    k_left -= BK;
+    base += kRowBytes;
+    left -= kRowBytes;
+    k_left -= kRowBytes;
   }
-  __device__ __forceinline__ bf16x8 frag(const uint16_t *src, int ks, int i) const {
-    return *reinterpret_cast<const bf16x8 *>(src + rd[ks] + i * 32 * BK);
+  __device__ __forceinline__ frag_t frag(const char *src, int ks, int i) const {
+    return *reinterpret_cast<const frag_t *>(src + rd[ks] + i * 32 * kRowBytes);
   }
 };
 
-// In columns: LDS row k holds SIDE values as segments of 32 bytes, segment s at
-// s ^ f(k), f(k) = r ^ 2 r ^ (bit 3 of k), r = k % 4.  A transposing read takes
-// one segment of 4 values of k per 16 lanes: those 4 segments, and the 8 of 32
-// lanes, meet different groups of banks.
-template <int SIDE, int BK, int NW>
-struct Stage<true, SIDE, BK, NW> {
-  static constexpr int kElems = SIDE * BK;
-  static constexpr int kPieces = SIDE / 8, kRowsPerLoad = 64 / kPieces;
+// In columns: LDS row k holds SIDE values.
+//  - bf16: as segments of 32 bytes, segment s at s ^ f(k), f(k) = r ^ 2 r ^ (bit 3
+//    of k), r = k % 4.  A transposing read takes one segment of 4 values of k per
+//    16 lanes: those 4 segments, and the 8 of 32 lanes, meet different banks.
+//  - fp32: the halves of every 64 values change places where bit 2 of k is set, so
+//    that the two halves of the lanes, 4 values of k apart, read different banks.
+template <int SIDE, int BK, int NW, int E>
+struct Stage<true, SIDE, BK, NW, E> {
+  static constexpr int kRowBytes = SIDE * E, kBytes = BK * kRowBytes;
+  static constexpr int kPieces = kRowBytes / 16, kRowsPerLoad = 64 / kPieces;
   static constexpr int kLoads = BK / kRowsPerLoad / NW;
-  static_assert(kLoads * kRowsPerLoad * NW == BK && SIDE >= 128, "whole loads per wave");
+  static constexpr int kReads = E == 2 ? 2 : 4;
+  static_assert(kLoads * kRowsPerLoad * NW == BK && kRowBytes >= 256, "whole loads per wave");
+  typedef typename Frag<E>::type frag_t;
   const char *base;
   int64_t left, step;
   int voff[kLoads];
   int rd[4];
 
   static __device__ __forceinline__ int swizzle(int k) {
-    return ((k & 3) ^ ((k & 3) << 1) ^ ((k >> 3) & 1)) & 7;
+    return E == 2 ? ((k & 3) ^ ((k & 3) << 1) ^ ((k >> 3) & 1)) << 1 : ((k >> 2) & 1) << 3;
   }
-  // Columns from p on, `cols` of them inside a row (which ends at a multiple of 8);
+  // Columns from p on, `cols` of them inside a row (which ends at whole 16 bytes);
   // k_limit rows exist.
-  __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, int64_t cols,
-                                       int64_t k_limit, int side_base) {
+  __device__ __forceinline__ void init(const void *p, int64_t ld, int64_t cols, int64_t k_limit,
+                                       int side_base) {
+    constexpr int kEpp = 16 / E;
     const int lane = threadIdx.x & 63, wave = wave_id();
-    base = reinterpret_cast<const char *>(p);
-    left = k_limit > 0 ? ((k_limit - 1) * ld + (cols + 7) / 8 * 8) * 2 : 0;
-    step = ld * BK * 2;
+    base = static_cast<const char *>(p);
+    left = k_limit > 0 ? ((k_limit - 1) * ld + (cols + kEpp - 1) / kEpp * kEpp) * E : 0;
+    step = ld * BK * E;
     const int lrow = lane / kPieces, slot = lane % kPieces;
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
       const int k = (q * NW + wave) * kRowsPerLoad + lrow;
-      const int seg = (slot >> 1) ^ swizzle(k);
-      // 16 bytes that begin at or past the row's last column are another row's
-      // (or lie past the end): nothing reads them
-      voff[q] = static_cast<int>(k * ld * 2) + (seg * 2 + (slot & 1)) * 16;
+      // (16 bytes that begin at or past the row's last column are another row's,
+      // or lie past the end: nothing reads them)
+      voff[q] = static_cast<int>(k * ld * E) + (slot ^ swizzle(k)) * 16;
     }
-    const int r = (lane & 15) >> 2, hi = lane >> 5, b = (lane >> 4) & 1;
-    const int f = swizzle(r + 8 * hi);
+    const int hi = lane >> 5;
+    if constexpr (E == 2) {
+      const int r = (lane & 15) >> 2, b = (lane >> 4) & 1;
+      const int f = swizzle(r + 8 * hi) >> 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      rd[i] = (8 * hi + r) * SIDE + (((side_base / 16 + 2 * i + b) ^ f) << 4) + (lane & 3) * 4;
+      for (int i = 0; i < 4; ++i)
+        rd[i] = (8 * hi + r) * kRowBytes + (((side_base / 16 + 2 * i + b) ^ f) << 5) +
+                (lane & 3) * 8;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        rd[i] = 4 * hi * kRowBytes + ((((side_base / 32 + i) ^ hi) << 5) + (lane & 31)) * 4;
+    }
   }
-  __device__ __forceinline__ void load(uint16_t *dst, int q) const {
+  __device__ __forceinline__ void load(char *dst, int q) const {
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char *>(base), 0,
         static_cast<int>(left > kLoadMask ? kLoadMask : (left > 0 ? left : 0)), kRawBuffer);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave_id()) * 512), 16,
+        rsrc, (__attribute__((address_space(3))) void *)(dst + (q * NW + wave_id()) * 1024), 16,
         voff[q], 0, 0, 0);
   }
   __device__ __forceinline__ void advance() {
     base += step;
     left -= step;
   }
-  __device__ __forceinline__ bf16x8 frag(const uint16_t *src, int ks, int i) const {
-    typedef __attribute__((address_space(3))) s16x4 lds_v;
-    const uint16_t *p = src + rd[i & 3] + (i >> 2) * 128 + ks * 16 * SIDE;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v *)(p));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v *)(p + 4 * SIDE));
-    return __builtin_bit_cast(bf16x8,
-                              __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  __device__ __forceinline__ frag_t frag(const char *src, int ks, int i) const {
+    if constexpr (E == 2) {
+      typedef __attribute__((address_space(3))) s16x4 lds_v;
+      const char *p = src + rd[i & 3] + (i >> 2) * 256 + ks * 16 * kRowBytes;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v *)(p));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v *)(p + 4 * kRowBytes));
+      return __builtin_bit_cast(bf16x8,
+                                __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      f32x4 f;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        f[s] = *reinterpret_cast<const float *>(src + rd[i & 3] + (i >> 2) * 512 +
+                                                (ks * 8 + s) * kRowBytes);
+      return f;
+    }
   }
 };
 
@@ -194,15 +230,16 @@ struct Stage<true, SIDE, BK, NW> {
 // compiler then sees that a read does not touch the stage that a load in flight
 // fills, and waits for no load on its account (it puts a wait for all of them
 // before every transposing read otherwise: 8192^3 in columns 1091 against 956 us).
-template <class S, bool NCOLS, bool MCOLS>
+template <class S, int E, bool NCOLS, bool MCOLS>
 struct Product {
-  typedef Stage<NCOLS, S::BN, S::BK, S::NW> StageN;
-  typedef Stage<MCOLS, S::BM, S::BK, S::NW> StageM;
-  static constexpr int kStageBytes = (StageN::kElems + StageM::kElems) * 2;
+  typedef Stage<NCOLS, S::BN, S::BK, S::NW, E> StageN;
+  typedef Stage<MCOLS, S::BM, S::BK, S::NW, E> StageM;
+  typedef typename Frag<E>::type frag_t;
+  static constexpr int kStageBytes = StageN::kBytes + StageM::kBytes;
   static constexpr int kLoads = StageN::kLoads + StageM::kLoads;
-  static constexpr int KS = S::BK / 16;
-  static constexpr int kReads = S::FN * (NCOLS ? 2 : 1) + S::FM * (MCOLS ? 2 : 1);
-  static constexpr int kMfma = S::FN * S::FM;
+  static constexpr int KS = S::BK * E / 32;  // rounds per step
+  static constexpr int kReads = S::FN * StageN::kReads + S::FM * StageM::kReads;
+  static constexpr int kMfma = S::FN * S::FM * (E == 2 ? 1 : 4);
   static_assert(KS % 2 == 0, "fragments alternate between two sets of registers");
   static_assert((S::NS - 1) * kLoads <= 63, "outstanding loads fit the counter");
   // The loads of a step go out over kSpread rounds, from the one in which its
@@ -213,12 +250,11 @@ struct Product {
 
   StageN a;
   StageM b;
-  bf16x8 fa[2][S::FN], fb[2][S::FM];
+  frag_t fa[2][S::FN], fb[2][S::FM];
 
   __device__ __forceinline__ void load(char *stage, int q) {
-    uint16_t *dst = reinterpret_cast<uint16_t *>(stage);
-    if (q < StageN::kLoads) a.load(dst, q);
-    else if (q < kLoads) b.load(dst + StageN::kElems, q - StageN::kLoads);
+    if (q < StageN::kLoads) a.load(stage, q);
+    else if (q < kLoads) b.load(stage + StageN::kBytes, q - StageN::kLoads);
   }
   __device__ __forceinline__ void load_parts(char *stage, int from, int to) {
 #pragma unroll
@@ -228,23 +264,29 @@ struct Product {
   // The fragments of round ks of a stage, and (part >= 0) a part of the loads into
   // stage `to` in turn with them.
   __device__ __forceinline__ void frags(int set, const char *stage, int ks, int part, char *to) {
-    const uint16_t *src = reinterpret_cast<const uint16_t *>(stage);
     constexpr int kF = S::FN + S::FM;
 #pragma unroll
     for (int f = 0; f < (kF > kPart ? kF : kPart); ++f) {
-      if (f < S::FM) fb[set][f] = b.frag(src + StageN::kElems, ks, f);
-      else if (f < kF) fa[set][f - S::FM] = a.frag(src, ks, f - S::FM);
+      if (f < S::FM) fb[set][f] = b.frag(stage + StageN::kBytes, ks, f);
+      else if (f < kF) fa[set][f - S::FM] = a.frag(stage, ks, f - S::FM);
       if (part >= 0 && f < kPart) load(to, part * kPart + f);
     }
     if (part == kSpread - 1) a.advance(), b.advance();
   }
   __device__ __forceinline__ void mfma(int set, f32x16 (&acc)[S::FN][S::FM]) const {
 #pragma unroll
-    for (int i = 0; i < S::FN; ++i)
+    for (int v = 0; v < (E == 2 ? 1 : 4); ++v)
 #pragma unroll
-      for (int j = 0; j < S::FM; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j], 0,
-                                                            0, 0);
+      for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+        for (int j = 0; j < S::FM; ++j) {
+          if constexpr (E == 2)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j],
+                                                                0, 0, 0);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[set][i][v], fb[set][j][v],
+                                                             acc[i][j], 0, 0, 0);
+        }
   }
   // Order of a round: the next round's reads and `loads` loads between the MFMAs;
   // nothing crosses a round's end.  (Left to the compiler, reads sink to just
@@ -329,119 +371,6 @@ struct Product {
       cur = next;
       next = S::NS == 2 ? free : prev;
       prev = free;
-    }
-  }
-};
-
-// ---------------------------------------------------------------------------
-// fp32
-// ---------------------------------------------------------------------------
-// One fp32 operand: BK values of k of SIDE rows (or columns) pass through
-// registers into LDS with k outermost, whichever way they lie in memory.  The
-// row stride of SIDE + 4 spreads the transposing writes of an operand in rows.
-template <bool COLS, int SIDE, int BK, int NT>
-struct StageF {
-  static constexpr int kLd = SIDE + 4;
-  static constexpr int kElems = BK * kLd;
-  static constexpr int kVecs = SIDE * BK / 4 / NT;
-  static_assert(kVecs * 4 * NT == SIDE * BK, "whole vectors per thread");
-  const float *base;
-  int64_t ld, limit, k_left, k_at;
-  bool wide;
-  f32x4 v[kVecs];
-
-  // `limit_` rows (columns) from p on exist, k_limit values of k.
-  __device__ __forceinline__ void init(const float *p, int64_t ld_, int64_t limit_,
-                                       int64_t k_limit) {
-    base = p, ld = ld_, limit = limit_, k_left = k_limit, k_at = 0;
-    wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld_ & 3) == 0;
-  }
-  __device__ __forceinline__ void load() {
-#pragma unroll
-    for (int q = 0; q < kVecs; ++q) {
-      const int t = q * NT + static_cast<int>(threadIdx.x);
-      int64_t at, in, left;  // first element, whether its line exists, elements left in it
-      if constexpr (COLS) {
-        const int k = t / (SIDE / 4), i = t % (SIDE / 4) * 4;
-        at = (k_at + k) * ld + i, in = k < k_left, left = limit - i;
-      } else {
-        const int i = t / (BK / 4), k = t % (BK / 4) * 4;
-        at = i * ld + k_at + k, in = i < limit, left = k_left - k;
-      }
-      f32x4 r = f32x4(0.f);
-      if (in && wide && left >= 4) {
-        r = *reinterpret_cast<const f32x4 *>(base + at);
-      } else if (in) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < left) r[e] = base[at + e];
-      }
-      v[q] = r;
-    }
-    k_at += BK;
-    k_left -= BK;
-  }
-  __device__ __forceinline__ void store(float *dst) const {
-#pragma unroll
-    for (int q = 0; q < kVecs; ++q) {
-      const int t = q * NT + static_cast<int>(threadIdx.x);
-      if constexpr (COLS) {
-        const int k = t / (SIDE / 4), i = t % (SIDE / 4) * 4;
-        *reinterpret_cast<f32x4 *>(dst + k * kLd + i) = v[q];
-      } else {
-        const int i = t / (BK / 4), k = t % (BK / 4) * 4;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[(k + e) * kLd + i] = v[q][e];
-      }
-    }
-  }
-};
-
-template <class S, bool NCOLS, bool MCOLS>
-struct ProductF {
-  typedef StageF<NCOLS, S::BN, S::BK, S::NT> StageN;
-  typedef StageF<MCOLS, S::BM, S::BK, S::NT> StageM;
-  static constexpr int kStageBytes = (StageN::kElems + StageM::kElems) * 4;
-
-  StageN a;
-  StageM b;
-
-  __device__ __forceinline__ void run(int nk, char *const (&st)[kStages], int side_n, int side_m,
-                                      f32x16 (&acc)[S::FN][S::FM]) {
-    static_assert(S::NS == 2, "two stages");
-    if (nk <= 0) return;
-    const int lane = threadIdx.x & 63, row = lane & 31, hi = lane >> 5;
-    a.load();
-    b.load();
-    float *even = reinterpret_cast<float *>(st[0]), *odd = reinterpret_cast<float *>(st[1]);
-    a.store(even);
-    b.store(even + StageN::kElems);
-    for (int kt = 0; kt < nk; ++kt) {
-      __syncthreads();
-      float *cur = kt & 1 ? odd : even, *next = kt & 1 ? even : odd;
-      if (kt + 1 < nk) {
-        a.load();
-        b.load();
-      }
-#pragma unroll
-      for (int k = 0; k < S::BK; k += 2) {
-        float fa[S::FN], fb[S::FM];
-#pragma unroll
-        for (int i = 0; i < S::FN; ++i)
-          fa[i] = cur[(k + hi) * StageN::kLd + side_n + i * 32 + row];
-#pragma unroll
-        for (int j = 0; j < S::FM; ++j)
-          fb[j] = cur[StageN::kElems + (k + hi) * StageM::kLd + side_m + j * 32 + row];
-#pragma unroll
-        for (int j = 0; j < S::FM; ++j)
-#pragma unroll
-          for (int i = 0; i < S::FN; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
-      }
-      if (kt + 1 < nk) {
-        a.store(next);
-        b.store(next + StageN::kElems);
-      }
     }
   }
 };
