@@ -17,21 +17,27 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Up to N tensors of a launch: kClipTable, or a few (the arguments of a launch are
+// copied: 2 KB of them cost a small call about 1 us).
+constexpr int kFewTensors = 8;
+template <int N>
 struct Table {
-  const void *g[kClipTable];
-  int64_t count[kClipTable];
-  int32_t first[kClipTable + 1];  // first workgroup of a tensor
-  uint32_t bf16[(kClipTable + 31) / 32];
+  const void *g[N];
+  int64_t count[N];
+  int32_t first[N + 1];  // first workgroup of a tensor
+  uint32_t bf16[(N + 31) / 32];
   int64_t chunk;
   int n;
 };
 
+template <int N>
 struct Outputs {
-  void *out[kClipTable];
+  void *out[N];
 };
 
 // The tensor that workgroup b works on.
-__device__ __forceinline__ int tensor_of(const Table &t, int b) {
+template <int N>
+__device__ __forceinline__ int tensor_of(const Table<N> &t, int b) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -41,6 +47,27 @@ __device__ __forceinline__ int tensor_of(const Table &t, int b) {
   return lo;
 }
 
+// Calls each(i, v) for the vectors of 16 bytes of elements [begin, end) that this
+// thread takes, v the one that begins at element i; kAhead loads are in flight.
+constexpr int kAhead = 4;
+template <bool BF16, class Each>
+__device__ __forceinline__ void vectors(const void *g, int64_t begin, int64_t end, Each each) {
+  constexpr int kEpv = BF16 ? 8 : 4, kRow = kThreads * kEpv;
+  int64_t i = begin + threadIdx.x * kEpv;
+  for (; i + (kAhead - 1) * kRow + kEpv <= end; i += kAhead * kRow) {
+    float v[kAhead][kEpv];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) dev::load_vec<BF16, kEpv>(g, i + k * kRow, end, v[k]);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) each(i + k * kRow, v[k]);
+  }
+  for (; i < end; i += kRow) {
+    float v[kEpv];
+    dev::load_vec<BF16, kEpv>(g, i, end, v);
+    each(i, v);
+  }
+}
+
 // Squares and their sums in fp64: neither the square of a large fp32 gradient
 // nor that of a small one leaves its range, and no bits are lost over 10^10 of
 // them.  Four sums per thread keep the additions apart.
@@ -48,12 +75,10 @@ template <bool BF16>
 __device__ __forceinline__ double squares(const void *g, int64_t begin, int64_t end) {
   constexpr int kEpv = BF16 ? 8 : 4;
   double s[4] = {0., 0., 0., 0.};
-  for (int64_t i = begin + threadIdx.x * kEpv; i < end; i += kThreads * kEpv) {
-    float v[kEpv];
-    dev::load_vec<BF16, kEpv>(g, i, end, v);
+  vectors<BF16>(g, begin, end, [&](int64_t, const float (&v)[kEpv]) {
 #pragma unroll
     for (int e = 0; e < kEpv; ++e) s[e & 3] = fma(double(v[e]), double(v[e]), s[e & 3]);
-  }
+  });
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
@@ -69,7 +94,8 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
-__global__ __launch_bounds__(kThreads) void sumsq_pieces(Table t, double *__restrict__ partial) {
+template <int N>
+__global__ __launch_bounds__(kThreads) void sumsq_pieces(Table<N> t, double *__restrict__ partial) {
   const int at = tensor_of(t, blockIdx.x);
   const int64_t begin = (blockIdx.x - t.first[at]) * t.chunk;
   const int64_t end = begin + t.chunk < t.count[at] ? begin + t.chunk : t.count[at];
@@ -103,60 +129,98 @@ template <bool BF16>
 __device__ __forceinline__ void scale_piece(const void *g, void *out, int64_t begin, int64_t end,
                                             float f) {
   constexpr int kEpv = BF16 ? 8 : 4;
-  for (int64_t i = begin + threadIdx.x * kEpv; i < end; i += kThreads * kEpv) {
-    float v[kEpv];
-    dev::load_vec<BF16, kEpv>(g, i, end, v);
+  vectors<BF16>(g, begin, end, [&](int64_t i, float (&v)[kEpv]) {
 #pragma unroll
     for (int e = 0; e < kEpv; ++e) v[e] *= f;
     dev::store_vec_nt<BF16, kEpv>(out, i, end, v);
-  }
+  });
 }
 
-__global__ __launch_bounds__(kThreads) void clip_pieces(Table t, Outputs o, Norms p,
+// The pieces last to first: what the sum of squares read last may still be in the
+// memory-side cache.
+template <int N>
+__global__ __launch_bounds__(kThreads) void clip_pieces(Table<N> t, Outputs<N> o, Norms p,
                                                         float *__restrict__ norm) {
   const double whole = global_norm(p);
   if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(whole);
   if (t.n == 0) return;
+  const int block = t.first[t.n] - 1 - static_cast<int>(blockIdx.x);
   const double ratio = p.max_norm / (whole + 1e-6);
   const float f = ratio < 1. ? static_cast<float>(ratio) : (ratio != ratio ? __builtin_nanf("") : 1.f);
-  const int at = tensor_of(t, blockIdx.x);
+  const int at = tensor_of(t, block);
   const void *g = t.g[at];
   // (times 1 in place: nothing to write)
   if (f == 1.f && g == o.out[at]) return;
-  const int64_t begin = (blockIdx.x - t.first[at]) * t.chunk;
+  const int64_t begin = (block - t.first[at]) * t.chunk;
   const int64_t end = begin + t.chunk < t.count[at] ? begin + t.chunk : t.count[at];
   if ((t.bf16[at / 32] >> (at % 32)) & 1) scale_piece<true>(g, o.out[at], begin, end, f);
   else scale_piece<false>(g, o.out[at], begin, end, f);
 }
 
-// Calls launch(table, outputs, workgroups) for the tensors that have elements,
-// kClipTable at a time.
-template <class F>
+// Calls launch(table, outputs, workgroups) for the tensors that have elements, N at
+// a time; `last_first`: from the last table to the first.
+template <int N, class F>
 void each_table(const void *const *tensors, const int64_t *counts, const int32_t *dtypes, int n,
-                int64_t total, void *const *out, F launch) {
-  Table t{};
-  Outputs o{};
-  t.chunk = clip_chunk(total);
-  int64_t groups = 0;
-  auto flush = [&]() {
-    if (t.n == 0) return;
-    t.first[t.n] = static_cast<int32_t>(groups);
-    launch(t, o, groups);
-    t = Table{};
+                int64_t total, void *const *out, bool last_first, F launch) {
+  int end = n;
+  for (int at = 0; last_first ? end > 0 : at < n;) {
+    // the tensors of this table: [lo, hi)
+    int lo = at, hi = at, found = 0;
+    if (last_first) {
+      for (lo = hi = end; lo > 0 && found < N; --lo) found += counts[lo - 1] != 0;
+      end = lo;
+    } else {
+      for (; hi < n && found < N; ++hi) found += counts[hi] != 0;
+      at = hi;
+    }
+    if (found == 0) continue;
+    Table<N> t{};
+    Outputs<N> o{};
     t.chunk = clip_chunk(total);
-    groups = 0;
-  };
-  for (int i = 0; i < n; ++i) {
-    if (counts[i] == 0) continue;
-    t.g[t.n] = tensors[i];
-    if (out != nullptr) o.out[t.n] = out[i];
-    t.count[t.n] = counts[i];
+    int64_t groups = 0;
+    for (int i = lo; i < hi; ++i) {
+      if (counts[i] == 0) continue;
+      t.g[t.n] = tensors[i];
+      if (out != nullptr) o.out[t.n] = out[i];
+      t.count[t.n] = counts[i];
+      t.first[t.n] = static_cast<int32_t>(groups);
+      if (dtypes[i] == 1) t.bf16[t.n / 32] |= uint32_t(1) << (t.n % 32);
+      groups += (counts[i] + t.chunk - 1) / t.chunk;
+      ++t.n;
+    }
     t.first[t.n] = static_cast<int32_t>(groups);
-    if (dtypes[i] == 1) t.bf16[t.n / 32] |= uint32_t(1) << (t.n % 32);
-    groups += (counts[i] + t.chunk - 1) / t.chunk;
-    if (++t.n == kClipTable) flush();
+    launch(t, o, static_cast<unsigned>(groups));
   }
-  flush();
+}
+
+template <int N>
+int run_sumsq(const void *const *tensors, const int64_t *counts, const int32_t *dtypes, int n,
+              int64_t total, double *sumsq, double *partial, hipStream_t st) {
+  int64_t pieces = 0;
+  each_table<N>(tensors, counts, dtypes, n, total, nullptr, false,
+                [&](const Table<N> &t, const Outputs<N> &, unsigned groups) {
+                  hipLaunchKernelGGL(sumsq_pieces<N>, dim3(groups), dim3(kThreads), 0, st, t,
+                                     partial + pieces);
+                  pieces += groups;
+                });
+  hipLaunchKernelGGL(sumsq_join, dim3(1), dim3(1024), 0, st, partial, pieces, sumsq);
+  return static_cast<int>(hipGetLastError());
+}
+
+template <int N>
+int run_clip(const void *const *tensors, const int64_t *counts, const int32_t *dtypes, int n,
+             int64_t total, void *const *out, const Norms &p, float *norm, hipStream_t st) {
+  bool first = true;
+  each_table<N>(tensors, counts, dtypes, n, total, out, true,
+                [&](const Table<N> &t, const Outputs<N> &o, unsigned groups) {
+                  hipLaunchKernelGGL(clip_pieces<N>, dim3(groups), dim3(kThreads), 0, st, t, o, p,
+                                     first ? norm : nullptr);
+                  first = false;
+                });
+  if (first)
+    hipLaunchKernelGGL(clip_pieces<N>, dim3(1), dim3(kThreads), 0, st, Table<N>{}, Outputs<N>{}, p,
+                       norm);
+  return static_cast<int>(hipGetLastError());
 }
 
 }  // namespace
@@ -165,15 +229,9 @@ int launch_grad_sumsq(const void *const *tensors, const int64_t *counts, const i
                       int n, int64_t total, double *sumsq, double *partial, void *stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();  // clear a stale error so the status below is this launch's
-  int64_t pieces = 0;
-  each_table(tensors, counts, dtypes, n, total, nullptr,
-             [&](const Table &t, const Outputs &, int64_t groups) {
-               hipLaunchKernelGGL(sumsq_pieces, dim3(static_cast<unsigned>(groups)),
-                                  dim3(kThreads), 0, st, t, partial + pieces);
-               pieces += groups;
-             });
-  hipLaunchKernelGGL(sumsq_join, dim3(1), dim3(1024), 0, st, partial, pieces, sumsq);
-  return static_cast<int>(hipGetLastError());
+  return n <= kFewTensors
+             ? run_sumsq<kFewTensors>(tensors, counts, dtypes, n, total, sumsq, partial, st)
+             : run_sumsq<kClipTable>(tensors, counts, dtypes, n, total, sumsq, partial, st);
 }
 
 int launch_grad_clip(const void *const *tensors, const int64_t *counts, const int32_t *dtypes,
@@ -184,16 +242,9 @@ int launch_grad_clip(const void *const *tensors, const int64_t *counts, const in
   Norms p{};
   for (int r = 0; r < n_parts; ++r) p.sumsq[r] = sumsq[r];
   p.n = n_parts, p.max_norm = max_norm;
-  bool first = true;
-  each_table(tensors, counts, dtypes, n, total, out,
-             [&](const Table &t, const Outputs &o, int64_t groups) {
-               hipLaunchKernelGGL(clip_pieces, dim3(static_cast<unsigned>(groups)),
-                                  dim3(kThreads), 0, st, t, o, p, first ? norm : nullptr);
-               first = false;
-             });
-  if (first)
-    hipLaunchKernelGGL(clip_pieces, dim3(1), dim3(kThreads), 0, st, Table{}, Outputs{}, p, norm);
-  return static_cast<int>(hipGetLastError());
+  return n <= kFewTensors
+             ? run_clip<kFewTensors>(tensors, counts, dtypes, n, total, out, p, norm, st)
+             : run_clip<kClipTable>(tensors, counts, dtypes, n, total, out, p, norm, st);
 }
 
 }  // namespace vpe

@@ -203,10 +203,17 @@ struct RowWriter {
   static constexpr int kLd = kCols + 4, kLd16 = S::TN + 8;
   static constexpr int kWaveBytes = 32 * kLd * 4 > 32 * kLd16 * 2 ? 32 * kLd * 4 : 32 * kLd16 * 2;
 
-  static __device__ __forceinline__ char *region(char *const (&st)[tile::kStages]) {
-    // (half of the waves in each of two stages)
+  // (half of the waves in each of two stages; LDS pointers by type: a choice
+  // between two generic ones would make every access a flat one)
+  typedef __attribute__((address_space(3))) char lds_char;
+  static __device__ __forceinline__ lds_char *region(char *const (&st)[tile::kStages]) {
     const int wave = tile::wave_id();
-    return ((wave & 1) ? st[1] : st[0]) + wave / 2 * kWaveBytes;
+    lds_char *even = (lds_char *)st[0], *odd = (lds_char *)st[1];
+    return ((wave & 1) ? odd : even) + wave / 2 * kWaveBytes;
+  }
+  template <class T>
+  static __device__ __forceinline__ __attribute__((address_space(3))) T *lds(lds_char *p) {
+    return (__attribute__((address_space(3))) T *)p;
   }
   static __device__ __forceinline__ void turn() {
     __builtin_amdgcn_wave_barrier();
@@ -221,14 +228,14 @@ struct RowWriter {
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) {
       if constexpr (BF16) {
-        uint16_t *mine = reinterpret_cast<uint16_t *>(region(st));
+        lds_char *mine = region(st);
         constexpr int kPer = S::TN / 8, kRows = 64 / kPer;
 #pragma unroll
         for (int i = 0; i < S::FN; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f32x16 &f = acc[i][j];
-            *reinterpret_cast<dev::u32x2 *>(mine + row * kLd16 + i * 32 + 8 * q + 4 * hi) =
+            *lds<dev::u32x2>(mine + (row * kLd16 + i * 32 + 8 * q + 4 * hi) * 2) =
                 dev::u32x2{dev::pack_bf16(f[4 * q], f[4 * q + 1]),
                            dev::pack_bf16(f[4 * q + 2], f[4 * q + 3])};
           }
@@ -236,12 +243,12 @@ struct RowWriter {
 #pragma unroll
         for (int t = 0; t < 32 / kRows; ++t) {
           const int r = t * kRows + lane / kPer, n = lane % kPer * 8;
-          const dev::u32x4 v = *reinterpret_cast<const dev::u32x4 *>(mine + r * kLd16 + n);
+          const dev::u32x4 v = *lds<dev::u32x4>(mine + (r * kLd16 + n) * 2);
           put(m0 + j * 32 + r, n0 + n, v);
         }
         turn();
       } else {
-        float *mine = reinterpret_cast<float *>(region(st));
+        lds_char *mine = region(st);
         constexpr int kPer = kCols / 4, kRows = 64 / kPer;
 #pragma unroll
         for (int h = 0; h < S::TN / kCols; ++h) {
@@ -250,14 +257,14 @@ struct RowWriter {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const f32x16 &f = acc[h * (kCols / 32) + i][j];
-              *reinterpret_cast<f32x4 *>(mine + row * kLd + i * 32 + 8 * q + 4 * hi) =
+              *lds<f32x4>(mine + (row * kLd + i * 32 + 8 * q + 4 * hi) * 4) =
                   f32x4{f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]};
             }
           turn();
 #pragma unroll
           for (int t = 0; t < 32 / kRows; ++t) {
             const int r = t * kRows + lane / kPer, n = lane % kPer * 4;
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(mine + r * kLd + n);
+            const f32x4 v = *lds<f32x4>(mine + (r * kLd + n) * 4);
             put(m0 + j * 32 + r, n0 + h * kCols + n, v);
           }
           turn();
@@ -824,13 +831,19 @@ constexpr int64_t kLargeRows = 1025;
 // The two products of a piece.  `splits` is fixed for all pieces of a call.
 void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t st) {
   if (dtype == 0) {
+    const bool small_x = few_tiles(a.dim, a.rows, a.splits), small_w = few_tiles(a.dim, a.cols);
+    if (gx && gw && a.rows > 32 && small_x == small_w) {
+      if (small_x) run_products<SmallF, false, 3>(a, st);
+      else run_products<MediumF, false, 3>(a, st);
+      return;
+    }
     if (gx) {
       if (a.rows <= 32) run_products<LowF, false, 1>(a, st);
-      else if (few_tiles(a.dim, a.rows, a.splits)) run_products<SmallF, false, 1>(a, st);
+      else if (small_x) run_products<SmallF, false, 1>(a, st);
       else run_products<MediumF, false, 1>(a, st);
     }
     if (gw) {
-      if (few_tiles(a.dim, a.cols)) run_products<SmallF, false, 2>(a, st);
+      if (small_w) run_products<SmallF, false, 2>(a, st);
       else run_products<MediumF, false, 2>(a, st);
     }
     return;

@@ -137,11 +137,9 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
 // Tensors per launch: their table travels in the kernel's arguments.
 constexpr int kClipTable = 96;
 
-// Elements per workgroup: a multiple of 2048, so that about 4096 workgroups
-// share the elements, and at least 16384.
-inline int64_t clip_chunk(int64_t total) {
-  return loss_max(loss_up((total + 4095) / 4096, 2048), 16384);
-}
+// Elements per workgroup: a multiple of 4096, so that about 8192 workgroups at most
+// share the elements.
+inline int64_t clip_chunk(int64_t total) { return loss_up((total + 8191) / 8192 + 1, 4096); }
 inline int64_t clip_chunks(const int64_t *counts, int n, int64_t chunk) {
   int64_t chunks = 0;
   for (int i = 0; i < n; ++i) chunks += (counts[i] + chunk - 1) / chunk;
