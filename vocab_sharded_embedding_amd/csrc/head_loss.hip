@@ -290,15 +290,32 @@ struct RowWriter {
 // ---------------------------------------------------------------------------
 // logits
 // ---------------------------------------------------------------------------
+// The targets of rows that were not collected.
+struct Targets {
+  const void *ids;
+  int itype;
+  int64_t vocab_start, vocab, rows;
+
+  __device__ __forceinline__ bool local(int64_t i, int64_t &at) const {
+    const int64_t t = itype == 0 ? static_cast<const int32_t *>(ids)[i]
+                                 : static_cast<const int64_t *>(ids)[i];
+    at = t - vocab_start;
+    if (at < 0 || at >= rows || t >= vocab) at = -1;
+    return t >= 0 && t < vocab;
+  }
+};
+
 struct Logits {
   const void *x;  // live rows, stride ldx
-  int64_t ldx;
+  int64_t ldx, x_dim;  // x_dim, w_dim: values of a row that may be read
   const void *w;  // a piece of the shard's rows, stride ldw
-  int64_t ldw, w_rows, w_dim;  // w_dim: values of a row that may be read
+  int64_t ldw, w_rows, w_dim;
   int64_t k;
-  const int32_t *count;
+  const int32_t *count;  // live rows; nullptr: all m, targets in `any`
+  int64_t m;
   int tiles_n, tiles_m, group_n;
   const int32_t *target;
+  Targets any;
   int64_t row0;  // the piece's first row in the shard
   // loss
   float *pairs;  // [tile][pair_ld] (maximum, sum)
@@ -328,7 +345,7 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
   int tn, tm;
   tile_of(block, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
   const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
-  const int64_t live = *a.count;
+  const int64_t live = a.count != nullptr ? *a.count : a.m;
   if (m0 >= live) return;
   f32x16 acc[S::FN][S::FM];
 #pragma unroll
@@ -337,7 +354,8 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
     for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
   product<S, kSize, false, false>(
       static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
-      static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.k, a.k, st, acc);
+      static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.x_dim, a.k, st,
+      acc);
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
   const int wn = wave % S::WN, wm = wave / S::WN, hi = lane >> 5;
   const int64_t nb = n0 + wn * S::TN;  // this wave's first column
@@ -380,8 +398,9 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
       // the row's target, where this wave has its column
       int64_t rel = -1;
       if (m < live) {
-        const int32_t t = a.target[m];
-        rel = t < 0 ? -1 : t - a.row0 - nb;
+        if (a.count != nullptr) rel = a.target[m];
+        else a.any.local(m, rel);
+        rel = rel < 0 ? -1 : rel - a.row0 - nb;
       }
       if (__any(rel >= 0 && rel < S::TN)) {
         float z = 0.f;
@@ -391,7 +410,8 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
 #pragma unroll
           for (int r = 0; r < 16; ++r)
             if (at == i * 32 + 8 * (r / 4) + 4 * hi + r % 4) z = acc[i][j][r];
-        if (at >= 0 && ((at >> 2) & 1) == hi) a.target_logit[a.row_of[m]] = z;
+        if (at >= 0 && ((at >> 2) & 1) == hi)
+          a.target_logit[a.count != nullptr ? a.row_of[m] : m] = z;
       }
     }
     __syncthreads();
@@ -466,15 +486,18 @@ __global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
 }
 
 // A row's pairs joined: shard_lse[row] = log sum exp.  64 rows per workgroup of
-// 16 waves, each every 16th tile; few rows: a workgroup each.
+// 16 waves, each every 16th tile; few rows: a workgroup each.  Rows that were not
+// collected (count nullptr) get their zeros here.
 template <bool FEW>
 __global__ __launch_bounds__(1024) void join_pairs(const float *__restrict__ pairs, int64_t ld,
                                                    int tiles, const int32_t *__restrict__ count,
+                                                   int64_t m_all, Targets any,
                                                    const int32_t *__restrict__ row_of,
-                                                   float *__restrict__ shard_lse) {
+                                                   float *__restrict__ shard_lse,
+                                                   float *__restrict__ target_logit) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   __shared__ float part[16][64][2];
-  const int64_t live = *count;
+  const int64_t live = count != nullptr ? *count : m_all;
   const int64_t row = FEW ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 64 + lane;
   if ((FEW ? row : static_cast<int64_t>(blockIdx.x) * 64) >= live) return;
   float m = -__builtin_huge_valf(), s = 0.f;
@@ -491,8 +514,14 @@ __global__ __launch_bounds__(1024) void join_pairs(const float *__restrict__ pai
   __syncthreads();
   if (wave == 0 && row < live) {
     for (int w = 1; w < 16; ++w) merge(m, s, part[w][lane][0], part[w][lane][1]);
-    if (!FEW || lane == 0)
-      shard_lse[row_of[row]] = m == -__builtin_huge_valf() ? m : m + logf(s);
+    if (FEW && lane != 0) return;
+    float v = m == -__builtin_huge_valf() ? m : m + logf(s);
+    if (count == nullptr) {
+      int64_t at;
+      if (!any.local(row, at)) v = 0.f;
+      if (at < 0) target_logit[row] = 0.f;
+    }
+    shard_lse[count != nullptr ? row_of[row] : row] = v;
   }
 }
 
@@ -674,6 +703,7 @@ __global__ __launch_bounds__(256) void finish_grad_x(const float *__restrict__ s
   f32x4 v = f32x4(0.f);
   if (from >= 0) {
     const float *p = sums + from * ld_sums + n;
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * split_stride);
     if (scale != nullptr) v *= *scale;
   }
@@ -731,6 +761,12 @@ int run_collect(const LossRows &r, const LossLayout &l, const float *lse, const 
   }
   return last_error();
 }
+
+// Up to this many rows (one tile of them in bf16) the loss reads x in place:
+// leaving rows out saves no tile, and collecting them costs a launch (of 1 row
+// against 151936 x 1024: 66 -> 62 us).  A row only reaches its own results there,
+// whatever it holds.
+constexpr int64_t kWholeRows = 256;
 
 // Rows that the tiles can read in place.
 bool loads_in_place(const void *p, int64_t ld, int dtype) {
@@ -903,11 +939,18 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
   (void)hipGetLastError();  // clear a stale error so the status below is this launch's
   const LossLayout l = loss_layout(kLossForward, r.m, r.dim, r.rows, r.dtype);
   const int64_t e = r.dtype == 1 ? 2 : 4;
-  int rc = run_collect(r, l, nullptr, nullptr, shard_lse, target_logit, workspace, st);
-  if (rc != 0) return rc;
+  int rc = 0;
   Logits a{};
-  a.x = at(workspace, l.x), a.ldx = l.dim_pad;
-  a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
+  a.m = r.m;
+  a.any = Targets{r.targets, r.itype, r.vocab_start, r.vocab, r.rows};
+  if (r.m <= kWholeRows && loads_in_place(r.x, r.dim, r.dtype)) {
+    a.x = r.x, a.ldx = r.dim, a.x_dim = r.dim;
+  } else {
+    rc = run_collect(r, l, nullptr, nullptr, shard_lse, target_logit, workspace, st);
+    if (rc != 0) return rc;
+    a.x = at(workspace, l.x), a.ldx = l.dim_pad, a.x_dim = l.dim_pad;
+    a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
+  }
   a.row_of = reinterpret_cast<const int32_t *>(at(workspace, l.row_of));
   a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
   a.pairs = reinterpret_cast<float *>(at(workspace, l.pairs)), a.pair_ld = r.m;
@@ -934,10 +977,11 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
   const int tiles = blocks(r.rows, tile_rows);
   if (r.m <= 256)
     hipLaunchKernelGGL(join_pairs<true>, dim3(static_cast<unsigned>(r.m)), dim3(1024), 0, st,
-                       a.pairs, a.pair_ld, tiles, a.count, a.row_of, shard_lse);
+                       a.pairs, a.pair_ld, tiles, a.count, a.m, a.any, a.row_of, shard_lse,
+                       target_logit);
   else
     hipLaunchKernelGGL(join_pairs<false>, dim3(blocks(r.m, 64)), dim3(1024), 0, st, a.pairs,
-                       a.pair_ld, tiles, a.count, a.row_of, shard_lse);
+                       a.pair_ld, tiles, a.count, a.m, a.any, a.row_of, shard_lse, target_logit);
   return last_error();
 }
 
@@ -974,7 +1018,7 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   const int64_t pieces = (r.rows + most - 1) / most;
   const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
   Logits a{};
-  a.x = at(workspace, l.x), a.ldx = l.dim_pad, a.k = l.dim_pad;
+  a.x = at(workspace, l.x), a.ldx = a.x_dim = l.dim_pad, a.k = l.dim_pad;
   a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
   a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
   a.lse = reinterpret_cast<const float *>(at(workspace, l.lse));

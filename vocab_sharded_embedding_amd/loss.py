@@ -98,18 +98,23 @@ def vpe_xent_loss(shard_lse: Sequence, target_logit: Sequence, targets, vocab: i
     n, m = len(shard_lse), targets.numel()
     if n == 0 or n != len(target_logit):
         raise ValueError("need one shard_lse and one target_logit per shard")
+    parts = (*shard_lse, *target_logit)
+    for t in parts:
+        float_rows("shard_lse and target_logit each", t, m)
+    given = []
     if loss is None:
         loss = torch.empty(m, dtype=torch.float32, device=targets.device)
+    else:
+        given.append(("loss", loss))
     if lse is None:
         lse = torch.empty(m, dtype=torch.float32, device=targets.device)
-    for t in (*shard_lse, *target_logit, loss, lse):
-        float_rows("shard_lse, target_logit, loss and lse each", t, m)
-    apart("loss", loss, lse, targets)
-    for name, t in (("loss", loss), ("lse", lse)):
-        apart(name, t, targets, *[p for p in (*shard_lse, *target_logit)
-                                  if p.data_ptr() != t.data_ptr()])
-    index = placed("targets loss lse" + " shard_lse" * n + " target_logit" * n, targets, loss, lse,
-                   *shard_lse, *target_logit)
+    else:
+        given.append(("lse", lse))
+    for name, t in given:
+        float_rows(name, t, m)
+        apart(name, t, targets, lse if t is loss else loss,
+              *[p for p in parts if p.data_ptr() != t.data_ptr()])
+    index = placed("targets loss lse" + " part" * len(parts), targets, loss, lse, *parts)
     array = ctypes.c_void_p * n
     enqueue("vpe_xent_loss", index, array(*[t.data_ptr() for t in shard_lse]),
             array(*[t.data_ptr() for t in target_logit]), n, m, int(vocab), targets.data_ptr(),
@@ -213,13 +218,19 @@ def vpe_lmhead_grad(grad_logits, x, weight, col_offset: int = 0, grad_x=None, gr
 # ---------------------------------------------------------------------------
 # clipping
 # ---------------------------------------------------------------------------
-def _tensor_table(tensors: Sequence):
-    """(pointers, counts, dtypes) of `tensors` as C arrays, and their device's index."""
-    n = len(tensors)
-    index = placed("gradient " * n, *tensors)
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int32 * n)(*[dtype_code(t) for t in tensors]), index)
+class _Table:
+    """`tensors` as C arrays of pointers, element counts and dtypes, with the lists
+    they were made of and their device's index."""
+
+    def __init__(self, tensors: Sequence):
+        n = self.n = len(tensors)
+        self.index = placed("gradient " * n, *tensors)
+        self.at = [t.data_ptr() for t in tensors]
+        self.sizes = [t.numel() for t in tensors]
+        kinds = [dtype_code(t) for t in tensors]
+        self.bytes = [c * (2 if k else 4) for c, k in zip(self.sizes, kinds)]
+        self.args = ((ctypes.c_void_p * n)(*self.at), (ctypes.c_int64 * n)(*self.sizes),
+                     (ctypes.c_int32 * n)(*kinds), n)
 
 
 def vpe_grad_sumsq_workspace(counts: Sequence[int]) -> int:
@@ -234,38 +245,46 @@ def vpe_grad_sumsq(tensors: Sequence, sumsq=None, workspace=None):
     tensors = list(tensors)
     if not tensors:
         raise ValueError("need at least one tensor")
-    pointers, counts, dtypes, index = _tensor_table(tensors)
+    table = _Table(tensors)
     device = tensors[0].device
+    given = []
     if sumsq is None:
         sumsq = torch.empty(1, dtype=torch.float64, device=device)
     elif sumsq.dtype != torch.float64 or sumsq.numel() != 1:
         raise ValueError("sumsq must be a float64 tensor of one element")
     else:
         apart("sumsq", sumsq, *tensors)
+        given.append(sumsq)
     if workspace is None:
         need = ctypes.c_int64()
         _check("vpe_grad_sumsq_workspace", load_library().vpe_grad_sumsq_workspace(
-            counts, len(tensors), ctypes.byref(need)))
+            table.args[1], table.n, ctypes.byref(need)))
         workspace = new_workspace(need.value, device)
     else:
         apart("workspace", workspace, sumsq, *tensors)
-    placed("gradient sumsq workspace", tensors[0], sumsq, workspace)
-    enqueue("vpe_grad_sumsq", index, pointers, counts, dtypes, len(tensors), sumsq.data_ptr(),
-            workspace.data_ptr(), nbytes(workspace))
+        given.append(workspace)
+    if given:
+        placed("gradient" + " sumsq_or_workspace" * len(given), tensors[0], *given)
+    enqueue("vpe_grad_sumsq", table.index, *table.args, sumsq.data_ptr(), workspace.data_ptr(),
+            nbytes(workspace))
     return sumsq
 
 
-def _refuse_overlaps(tensors, out, others) -> None:
-    """Refuse an output that shares bytes with another one, with `others`, or with a
-    tensor other than being the whole of its own."""
-    spans = [(o.data_ptr(), o.data_ptr() + nbytes(o), True) for o in out]
-    spans += [(t.data_ptr(), t.data_ptr() + nbytes(t), False)
-              for t, o in zip(tensors, out) if t.data_ptr() != o.data_ptr()]
+def _refuse_overlaps(table, out_at, others) -> None:
+    """Refuse an output (at out_at, as large as its tensor) that shares bytes with
+    another one, with `others`, or with a tensor other than being the whole of its
+    own."""
+    spans = [(o, o + n, True) for o, n in zip(out_at, table.bytes)]
+    if out_at is not table.at:
+        spans += [(t, t + n, False) for t, o, n in zip(table.at, out_at, table.bytes) if t != o]
     spans += [(t.data_ptr(), t.data_ptr() + nbytes(t), False) for t in others]
+    spans.sort()
     # in order of their first bytes: the furthest end of what came before, of the
     # outputs alone and of everything
     written = read = 0
-    for begin, end, is_out in sorted(s for s in spans if s[0] < s[1]):
+    for begin, end, is_out in spans:
+        if begin == end:
+            continue
         if begin < written or (is_out and begin < read):
             raise ValueError("an output of vpe_grad_clip must be its own tensor, or apart from "
                              "the call's other tensors")
@@ -287,27 +306,29 @@ def vpe_grad_clip(tensors: Sequence, sumsq: Sequence, max_norm: float,
     for s in sumsq:
         if s.dtype != torch.float64 or s.numel() != 1:
             raise ValueError("sumsq must be float64 tensors of one element")
-    pointers, counts, dtypes, index = _tensor_table(tensors)
+    table = _Table(tensors)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=tensors[0].device)
+        others = sumsq
     else:
         float_rows("norm", norm, 1)
         apart("norm", norm, *sumsq)
-    if out is None:
-        targets, out = pointers, tensors
-    else:
+        others = (*sumsq, norm)
+    out_at, targets = table.at, table.args[0]
+    if out is not None:
         out = list(out)
-        if len(out) != len(tensors):
+        if len(out) != table.n:
             raise ValueError("out must hold one tensor per gradient")
-        for o, t in zip(out, tensors):
-            if o.dtype != t.dtype or o.numel() != t.numel():
+        for o, t, n in zip(out, tensors, table.sizes):
+            if o.dtype != t.dtype or o.numel() != n:
                 raise ValueError("each of out must have its gradient's dtype and size")
-        placed("out " * len(out), *out)
-        targets = (ctypes.c_void_p * len(out))(*[o.data_ptr() for o in out])
-    _refuse_overlaps(tensors, out, (*sumsq, norm))
+        placed("gradient" + " out" * len(out), tensors[0], *out)
+        out_at = [o.data_ptr() for o in out]
+        targets = (ctypes.c_void_p * table.n)(*out_at)
+    _refuse_overlaps(table, out_at, others)
     n = len(sumsq)
-    placed("gradient norm out" + " sumsq" * n, tensors[0], norm, out[0], *sumsq)
-    enqueue("vpe_grad_clip", index, pointers, counts, dtypes, len(tensors), targets,
+    placed("gradient norm" + " sumsq" * n, tensors[0], norm, *sumsq)
+    enqueue("vpe_grad_clip", table.index, *table.args, targets,
             (ctypes.c_void_p * n)(*[s.data_ptr() for s in sumsq]), n, float(max_norm),
             norm.data_ptr())
     return norm
