@@ -131,10 +131,16 @@ __global__ __launch_bounds__(256) void collect_rows(Collect c) {
   for (int k = wave; k < mine; k += 4) {
     const char *src = x + (row0 + kept[k]) * c.dim * kSize;
     char *dst = xl + static_cast<int64_t>(kept_at[k]) * c.dim_pad * kSize;
-    for (int v = lane; v < vecs; v += 64) {
-      float e[kEpv];
-      dev::load_vec<BF16, kEpv>(src, static_cast<int64_t>(v) * kEpv, c.dim, e);
-      *reinterpret_cast<dev::u32x4 *>(dst + v * 16) = dev::Vec<BF16, kEpv>::narrow(e);
+    for (int v = lane; v < vecs; v += 4 * 64) {
+      float e[4][kEpv];  // four loads in flight
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        dev::load_vec<BF16, kEpv>(src, (static_cast<int64_t>(v) + u * 64) * kEpv, c.dim, e[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (v + u * 64 < vecs)
+          *reinterpret_cast<dev::u32x4 *>(dst + (v + u * 64) * 16) =
+              dev::Vec<BF16, kEpv>::narrow(e[u]);
     }
   }
 }
@@ -736,9 +742,9 @@ int run_collect(const LossRows &r, const LossLayout &l, const float *lse, const 
   c.x = r.x, c.m = r.m, c.dim = r.dim, c.dim_pad = l.dim_pad;
   c.targets = r.targets, c.vocab_start = r.vocab_start, c.vocab = r.vocab, c.rows = r.rows;
   c.lse = lse, c.grad_loss = grad_loss;
-  // 16 rows per workgroup fill the chip from 4096 rows on; past that the
-  // counting of earlier rows is kept in proportion to the copying
-  int64_t per = loss_max(16, loss_min(1024, loss_up(r.m / 256, 16)));
+  // about 1024 workgroups, so that the counting of earlier rows stays small against
+  // the copying; a row per wave at least
+  const int64_t per = loss_max(4, loss_min(1024, loss_up(r.m / 1024, 4)));
   c.rows_per_block = static_cast<int>(per);
   c.count = reinterpret_cast<int32_t *>(at(ws, l.count));
   c.scale = reinterpret_cast<float *>(at(ws, l.count)) + 1;
@@ -861,8 +867,11 @@ int64_t splits_for(int64_t rows, int64_t dim, int64_t cols, int64_t bn, int64_t 
   return loss_max(1, loss_min(s, most));
 }
 
-// Rows from which the bf16 products take 256 x 256 tiles.
-constexpr int64_t kLargeRows = 1025;
+// Whether the bf16 products take 256 x 256 tiles: where at least three quarters of
+// their rows exist.  (The head's backward of 256 rows against 75968 x 1024: 114 us,
+// 136 with 128 x 128; the gradients of 257 rows against 50257 x 999: 110 us, 91 with
+// 128 x 128.)
+bool large_tiles(int64_t rows) { return rows > 128 && rows * 4 >= loss_up(rows, 256) * 3; }
 
 // The two products of a piece.  `splits` is fixed for all pieces of a call.
 void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t st) {
@@ -884,7 +893,7 @@ void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t s
     }
     return;
   }
-  if (a.rows >= kLargeRows) {
+  if (large_tiles(a.rows)) {
     if (gx && gw) run_products<Large, true, 3>(a, st);
     else if (gx) run_products<Large, true, 1>(a, st);
     else run_products<Large, true, 2>(a, st);
@@ -902,7 +911,7 @@ void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t s
 
 int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, int64_t most) {
   const int64_t side = rows <= 32 ? 32 : (rows <= 64 && dtype == 1) ? 64 : 128;
-  if (dtype == 1 && rows >= kLargeRows) return splits_for(rows, dim, cols, 256, 256, 256, most);
+  if (dtype == 1 && large_tiles(rows)) return splits_for(rows, dim, cols, 256, 256, 256, most);
   const int64_t s = splits_for(rows, dim, cols, 128, side, 512, most);
   if (dtype == 1 || rows <= 32 || !few_tiles(dim, rows, s)) return s;
   return splits_for(rows, dim, cols, 64, 64, 512, most);
@@ -1051,7 +1060,7 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
                            : static_cast<char *>(g.gw) + a.row0 * r.dim * (g.gwt == 1 ? 2 : 4);
   };
   // (a copied table leaves no second copy to read beside the products of the first)
-  const bool together = r.dtype == 1 && in_place && r.m >= kLargeRows && g.gx && g.gw;
+  const bool together = r.dtype == 1 && in_place && large_tiles(r.m) && g.gx && g.gw;
   for (int64_t row = 0; row < r.rows; row += step) {
     if (!together || row == 0) {
       piece_logits(row);
