@@ -4,7 +4,8 @@
 // The logits z = x W^T are products for the matrix cores and, at training sizes,
 // far larger than their operands; they are never kept.  Rows without a target
 // are left out first: `collect_rows` copies the live rows of x, so that what a
-// padded row holds is never read and no tile is spent on it.
+// padded row holds reaches no sum over rows and no tile is spent on it (the loss
+// of up to 256 rows, which sums over none, reads x in place).
 //  - Loss: every tile of z becomes one pair (maximum, sum of exponentials) per
 //    row in the workgroup that computed it, and the one logit that is a row's
 //    target; `join_pairs` merges a row's pairs.
@@ -813,6 +814,8 @@ bool few_tiles(int64_t n, int64_t m, int64_t splits = 1) {
   return blocks(n, 128) * static_cast<int64_t>(blocks(m, 128)) * splits < 256;
 }
 
+static_assert(256 * kLossMaxStride * 2 <= kLoadMask && 128 * kLossMaxStride * 4 <= kLoadMask,
+              "a tile's rows lie before the masked loads");
 static_assert(SmallF::BN == loss_tile_rows(0) && Medium::BN == loss_tile_rows(1),
               "the workspace holds a pair per tile");
 

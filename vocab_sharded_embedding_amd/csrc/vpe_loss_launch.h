@@ -28,9 +28,9 @@ constexpr int64_t kLossMinPiece = 512;
 constexpr int64_t kLossSums = int64_t(1) << 23;
 constexpr int64_t kLossSplitRows = 128;
 
-// Largest stride of rows that the tiles read in place: offsets inside a tile of 256
-// rows fit 31 bits.
-constexpr int64_t kLossMaxStride = int64_t(1) << 22;
+// Largest stride of rows, in elements, that the tiles read in place: 256 rows of bf16
+// (128 of fp32) end before the offset of a masked load, kLoadMask.
+constexpr int64_t kLossMaxStride = (int64_t(1) << 22) - 1024;
 
 constexpr int64_t loss_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 constexpr int64_t loss_min(int64_t a, int64_t b) { return a < b ? a : b; }
