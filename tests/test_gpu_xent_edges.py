@@ -200,6 +200,69 @@ def test_unaligned_tensors_and_what_lies_around_them(dtype):
     assert (rest == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m,vocab,dim", [(20, 33001, 37), (60, 34007, 129), (128, 33001, 100),
+                                         (300, 40003, 65), (520, 33001, 63)])
+def test_rows_at_any_element(m, vocab, dim, dtype):
+    """Rows that begin at any element, with what must not count right before the first
+    and right behind the last one."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+
+    def between(n, scale):
+        whole = torch.full((n + 2,), NAN, device="cuda", dtype=dtype)
+        whole[1:-1] = (scale * torch.randn(n, generator=g, device="cuda")).to(dtype)
+        return whole[1:-1]
+
+    x, w = between(m * dim, 1.0).view(m, dim), between(vocab * dim, 0.1).view(vocab, dim)
+    t = torch.randint(0, vocab, (m,), generator=g, device="cuda")
+    t[::9] = -1
+    gl = torch.rand(m, generator=g, device="cuda") + 0.5
+    ref = Reference(x, w, t, vocab, gl)
+    loss, lse = _loss(x, w, t, vocab)
+    assert_within(loss, ref.loss, ref.loss_err, "loss")
+    gx, gw = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab)
+    rx, ex, rw, ew = ref.grads(slice(0, vocab), dtype, dtype)
+    assert_within(gx, rx, ex, "grad_x")
+    assert_within(gw, rw, ew, "grad_weight")
+    d = between(m * vocab, 1.0).view(m, vocab)
+    gx, gw = vpe.vpe_lmhead_grad(d, x, w)
+    dd = d.double()
+    rx, ex, rw, ew = products(dd, torch.zeros_like(dd), x.double(), w.double(), dtype, dtype)
+    assert_within(gx, rx, ex, "grad_x")
+    assert_within(gw, rw, ew, "grad_weight")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_a_small_last_piece_of_a_copied_table(dtype):
+    """32768 (65536) table rows are copied at a time; the last 300 hold the logits that
+    matter."""
+    m, dim, vocab = 640, 1021, (32768 if dtype == F32 else 65536) + 300
+    x, w, t, gl = _case(m, vocab, dim, dtype)
+    w[-300:] *= 4
+    t[::3] = vocab - 1 - torch.arange(t[::3].numel(), device="cuda")
+    ref = Reference(x, w, t, vocab, gl)
+    loss, lse = _loss(x, w, t, vocab)
+    assert_within(loss, ref.loss, ref.loss_err, "loss")
+    assert_within(lse, ref.lse, ref.lse_err, "lse")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("live", [1, 63, 64, 65, 127, 128, 129, 255, 256, 257, 383, 385])
+def test_live_rows_around_a_tile(live, dtype):
+    """The last tile of live rows full, half full and beyond."""
+    m, vocab, dim = 520, 34000, 136
+    x, w, t, gl = _case(m, vocab, dim, dtype, live)
+    order = torch.randperm(m, device="cuda")
+    t[order[live:]] = -100
+    ref = Reference(x, w, t, vocab, gl)
+    loss, lse = _loss(x, w, t, vocab)
+    assert_within(loss, ref.loss, ref.loss_err, "loss")
+    gx, gw = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab)
+    rx, ex, rw, ew = ref.grads(slice(0, vocab), dtype, dtype)
+    assert_within(gx, rx, ex, "grad_x")
+    assert_within(gw, rw, ew, "grad_weight")
+
+
 def _bytes(n):
     return torch.empty(n, dtype=torch.uint8, device="cuda")
 

@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256) void copy_rows(const char *__restrict__ from, 
 #if defined(__HIP_DEVICE_COMPILE__)
 // Adds to acc the tile whose operands begin at a and b: n_left and m_left rows (or
 // columns), ka and kb values of k that may be read, k to sum over.
-template <class S, int E, bool NCOLS, bool MCOLS>
+template <class S, int E, bool NCOLS, bool MCOLS, bool LOOSE>
 __device__ __forceinline__ void product(const void *a, int64_t lda, int64_t n_left, int64_t ka,
                                         const void *b, int64_t ldb, int64_t m_left, int64_t kb,
                                         int64_t k, char *const (&st)[tile::kStages],
@@ -196,7 +196,9 @@ __device__ __forceinline__ void product(const void *a, int64_t lda, int64_t n_le
   tile::Product<S, E, NCOLS, MCOLS> p;
   p.a.init(a, lda, n_left, ka, wave % S::WN * S::TN);
   p.b.init(b, ldb, m_left, kb, wave / S::WN * S::TM);
-  p.run(static_cast<int>((k + S::BK - 1) / S::BK), st, acc);
+  const int steps = static_cast<int>((k + S::BK - 1) / S::BK);
+  if constexpr (LOOSE) p.run_loose(steps, st, acc);
+  else p.run(steps, st, acc);
 }
 
 // A wave's accumulators as rows of m: 32 rows at a time pass through the wave's
@@ -344,22 +346,36 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
   s = a + b;
 }
 
+// A tile's last rows may fill half of it or less: then half a tile is computed, as
+// wide and by as many waves.  (The live rows are known to the device alone.)
+template <class S>
+struct Half {
+  static constexpr bool kExists = false;
+  typedef S type;
+};
+template <>
+struct Half<tile::Shape<256, 256, 2, 4, 64, 2>> {
+  static constexpr bool kExists = true;
+  typedef tile::Shape<256, 128, 4, 2, 64, 2> type;
+};
+template <>
+struct Half<tile::Shape<128, 128, 2, 2, 32, 2>> {
+  static constexpr bool kExists = true;
+  typedef tile::Shape<128, 64, 2, 2, 32, 2> type;
+};
+
 #if defined(__HIP_DEVICE_COMPILE__)
-template <class S, bool BF16, bool GRAD>
-__device__ __forceinline__ void logits_tile(const Logits &a, int block,
-                                            char *const (&st)[tile::kStages]) {
+// Columns n0.. (tile tn) of rows m0.. .
+template <class S, bool BF16, bool GRAD, bool LOOSE>
+__device__ __forceinline__ void logits_of(const Logits &a, int tn, int64_t n0, int64_t m0,
+                                          int64_t live, char *const (&st)[tile::kStages]) {
   constexpr int kSize = BF16 ? 2 : 4;
-  int tn, tm;
-  tile_of(block, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
-  const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
-  const int64_t live = a.count != nullptr ? *a.count : a.m;
-  if (m0 >= live) return;
   f32x16 acc[S::FN][S::FM];
 #pragma unroll
   for (int i = 0; i < S::FN; ++i)
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
-  product<S, kSize, false, false>(
+  product<S, kSize, false, false, LOOSE>(
       static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
       static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.x_dim, a.k, st,
       acc);
@@ -480,48 +496,67 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
     RowWriter<S>::template run<BF16>(acc, st, put);
   }
 }
+
+template <class S, bool BF16, bool GRAD, bool LOOSE>
+__device__ __forceinline__ void logits_tile(const Logits &a, int block,
+                                            char *const (&st)[tile::kStages]) {
+  int tn, tm;
+  tile_of(block, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
+  const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
+  const int64_t live = a.count != nullptr ? *a.count : a.m;
+  if (m0 >= live) return;
+  if (Half<S>::kExists && live - m0 <= S::BM / 2)
+    logits_of<typename Half<S>::type, BF16, GRAD, LOOSE>(a, tn, n0, m0, live, st);
+  else
+    logits_of<S, BF16, GRAD, LOOSE>(a, tn, n0, m0, live, st);
+}
 #endif
 
-template <class S, bool BF16, bool GRAD>
-__global__ __launch_bounds__(S::NT) void logits_tiles(Logits a) {
+template <class S, bool BF16, bool GRAD, bool LOOSE>
+__global__ __launch_bounds__(S::NT, S::NT == 256 ? 2 : 1) void logits_tiles(Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kSize = BF16 ? 2 : 4;
   VPE_STAGES(S, kSize)
   static_assert(kStageBytes >= S::BM * S::WN * 8, "the pairs fit a stage");
-  logits_tile<S, BF16, GRAD>(a, blockIdx.x, st);
+  logits_tile<S, BF16, GRAD, LOOSE>(a, blockIdx.x, st);
 #endif
 }
 
-// A row's pairs joined: shard_lse[row] = log sum exp.  64 rows per workgroup of
-// 16 waves, each every 16th tile; few rows: a workgroup each.  Rows that were not
-// collected (count nullptr) get their zeros here.
-template <bool FEW>
+// A row's pairs joined: shard_lse[row] = log sum exp.  ROWS rows per workgroup of
+// 1024: neighbouring lanes have neighbouring rows, and 1024 / ROWS threads share a
+// row's tiles.  Rows that were not collected (count nullptr) get their zeros here.
+template <int ROWS>
 __global__ __launch_bounds__(1024) void join_pairs(const float *__restrict__ pairs, int64_t ld,
                                                    int tiles, const int32_t *__restrict__ count,
                                                    int64_t m_all, Targets any,
                                                    const int32_t *__restrict__ row_of,
                                                    float *__restrict__ shard_lse,
                                                    float *__restrict__ target_logit) {
+  constexpr int kShare = 1024 / ROWS;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __shared__ float part[16][64][2];
+  __shared__ float part[16][ROWS][2];
   const int64_t live = count != nullptr ? *count : m_all;
-  const int64_t row = FEW ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  if ((FEW ? row : static_cast<int64_t>(blockIdx.x) * 64) >= live) return;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + lane % ROWS;
+  if (static_cast<int64_t>(blockIdx.x) * ROWS >= live) return;
   float m = -__builtin_huge_valf(), s = 0.f;
   if (row < live)
-    for (int t = FEW ? threadIdx.x : wave; t < tiles; t += FEW ? 1024 : 16) {
-      const float *e = pairs + (t * ld + row) * 2;
-      merge(m, s, e[0], e[1]);
-    }
-  if (FEW) {
+    for (int t = threadIdx.x / ROWS; t < tiles; t += 4 * kShare) {
+      dev::f32x2 e[4];  // four loads in flight
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) merge(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
-  }
-  part[wave][lane][0] = m, part[wave][lane][1] = s;
+      for (int u = 0; u < 4; ++u) {
+        e[u] = dev::f32x2{-__builtin_huge_valf(), 0.f};
+        if (t + u * kShare < tiles)
+          e[u] = *reinterpret_cast<const dev::f32x2 *>(pairs + ((t + u * kShare) * ld + row) * 2);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) merge(m, s, e[u][0], e[u][1]);
+    }
+#pragma unroll
+  for (int d = ROWS; d < 64; d *= 2) merge(m, s, __shfl_xor(m, d), __shfl_xor(s, d));
+  if (lane < ROWS) part[wave][lane][0] = m, part[wave][lane][1] = s;
   __syncthreads();
-  if (wave == 0 && row < live) {
+  if (wave == 0 && lane < ROWS && row < live) {
     for (int w = 1; w < 16; ++w) merge(m, s, part[w][lane][0], part[w][lane][1]);
-    if (FEW && lane != 0) return;
     float v = m == -__builtin_huge_valf() ? m : m + logf(s);
     if (count == nullptr) {
       int64_t at;
@@ -584,18 +619,42 @@ struct Products {
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// Parts of the launch: 1 the gradient of x, 2 that of the table, 3 both, the
-// first's workgroups before the second's.
-template <class S, bool BF16, int PARTS>
-__device__ __forceinline__ void products_tile(const Products &a, int b,
-                                              char *const (&st)[tile::kStages]) {
+// sums (+)= columns k0.. (k of them) of d, rows m0.., times the table's columns n0.. .
+template <class S, bool BF16, bool LOOSE>
+__device__ __forceinline__ void grad_x_of(const Products &a, int split, int64_t n0, int64_t m0,
+                                          int64_t live, char *const (&st)[tile::kStages]) {
   constexpr int kSize = BF16 ? 2 : 4;
-  const int64_t live = a.count != nullptr ? *a.count : a.rows;
+  const int64_t k0 = split * a.per_split;
+  int64_t k = a.cols - k0 < a.per_split ? a.cols - k0 : a.per_split;
+  if (k < 0) k = 0;
+  if (k == 0 && !a.first) return;
   f32x16 acc[S::FN][S::FM];
 #pragma unroll
   for (int i = 0; i < S::FN; ++i)
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
+  // (columns of d up to whole 16 bytes: the table's rows end before)
+  constexpr int kEpp = LOOSE ? 1 : 16 / kSize;
+  product<S, kSize, true, false, LOOSE>(
+      static_cast<const char *>(a.w) + (k0 * a.ldw + n0) * kSize, a.ldw, a.dim - n0, k,
+      static_cast<const char *>(a.d) + (m0 * a.ldd + k0) * kSize, a.ldd, live - m0,
+      (k + kEpp - 1) / kEpp * kEpp, k, st, acc);
+  __syncthreads();
+  float *sums = a.sums + split * a.rows * a.ld_sums;
+  RowWriter<S>::template run<false>(acc, st, [&](int m, int n, f32x4 v) {
+    if (m0 + m >= live || n0 + n >= a.ld_sums) return;
+    f32x4 *to = reinterpret_cast<f32x4 *>(sums + (m0 + m) * a.ld_sums + n0 + n);
+    *to = a.first ? v : *to + v;
+  });
+}
+
+// Parts of the launch: 1 the gradient of x, 2 that of the table, 3 both, the
+// first's workgroups before the second's.
+template <class S, bool BF16, int PARTS, bool LOOSE>
+__device__ __forceinline__ void products_tile(const Products &a, int b,
+                                              char *const (&st)[tile::kStages]) {
+  constexpr int kSize = BF16 ? 2 : 4;
+  const int64_t live = a.count != nullptr ? *a.count : a.rows;
   const int x_blocks = (PARTS & 1) ? a.x_tiles_n * a.x_tiles_m * a.splits : 0;
   if constexpr ((PARTS & 1) != 0) {
     if (b < x_blocks) {
@@ -604,23 +663,10 @@ __device__ __forceinline__ void products_tile(const Products &a, int b,
       const int split = t2 / a.x_tiles_m, tm = t2 - split * a.x_tiles_m;
       const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
       if (m0 >= live) return;
-      const int64_t k0 = split * a.per_split;
-      int64_t k = a.cols - k0 < a.per_split ? a.cols - k0 : a.per_split;
-      if (k < 0) k = 0;
-      if (k == 0 && !a.first) return;
-      // (columns of d up to whole 16 bytes: the table's rows end before)
-      constexpr int kEpp = 16 / kSize;
-      product<S, kSize, true, false>(
-          static_cast<const char *>(a.w) + (k0 * a.ldw + n0) * kSize, a.ldw, a.dim - n0, k,
-          static_cast<const char *>(a.d) + (m0 * a.ldd + k0) * kSize, a.ldd, live - m0,
-          (k + kEpp - 1) / kEpp * kEpp, k, st, acc);
-      __syncthreads();
-      float *sums = a.sums + split * a.rows * a.ld_sums;
-      RowWriter<S>::template run<false>(acc, st, [&](int m, int n, f32x4 v) {
-        if (m0 + m >= live || n0 + n >= a.ld_sums) return;
-        f32x4 *to = reinterpret_cast<f32x4 *>(sums + (m0 + m) * a.ld_sums + n0 + n);
-        *to = a.first ? v : *to + v;
-      });
+      if (Half<S>::kExists && live - m0 <= S::BM / 2)
+        grad_x_of<typename Half<S>::type, BF16, LOOSE>(a, split, n0, m0, live, st);
+      else
+        grad_x_of<S, BF16, LOOSE>(a, split, n0, m0, live, st);
       return;
     }
   }
@@ -628,7 +674,12 @@ __device__ __forceinline__ void products_tile(const Products &a, int b,
     int tn, tm;
     tile_of(b - x_blocks, a.w_tiles_n, a.w_tiles_m, a.w_tiles_n, tn, tm);
     const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
-    product<S, kSize, true, true>(
+    f32x16 acc[S::FN][S::FM];
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
+    product<S, kSize, true, true, LOOSE>(
         static_cast<const char *>(a.x) + n0 * kSize, a.ldx, a.dim - n0, live,
         static_cast<const char *>(a.d) + m0 * kSize, a.ldd, a.cols - m0, live, live, st, acc);
     __syncthreads();
@@ -675,12 +726,12 @@ __device__ __forceinline__ void products_tile(const Products &a, int b,
 }
 #endif
 
-template <class S, bool BF16, int PARTS>
+template <class S, bool BF16, int PARTS, bool LOOSE>
 __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kSize = BF16 ? 2 : 4;
   VPE_STAGES(S, kSize)
-  products_tile<S, BF16, PARTS>(a, blockIdx.x, st);
+  products_tile<S, BF16, PARTS, LOOSE>(a, blockIdx.x, st);
 #endif
 }
 
@@ -690,8 +741,8 @@ template <class S>
 __global__ __launch_bounds__(S::NT) void grad_and_logits_tiles(Products p, int n, Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   VPE_STAGES(S, 2)
-  if (static_cast<int>(blockIdx.x) < n) products_tile<S, true, 3>(p, blockIdx.x, st);
-  else logits_tile<S, true, true>(a, blockIdx.x - n, st);
+  if (static_cast<int>(blockIdx.x) < n) products_tile<S, true, 3, false>(p, blockIdx.x, st);
+  else logits_tile<S, true, true, false>(a, blockIdx.x - n, st);
 #endif
 }
 
@@ -781,6 +832,18 @@ bool loads_in_place(const void *p, int64_t ld, int dtype) {
          (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
 
+// Whether rows that cannot be read in place pass through registers, in tiles of at
+// most 128 x 128, rather than be copied first.  Against 50001 x 1001, loose and copied:
+// loss of 16 rows 26 and 60 us, of 257 81 and 89, of 1000 189 and 155; gradients of 128
+// rows 130 and 136 (against 50001 x 3001 306 and 417), of 257 259 and 183; the head's
+// backward of 128 rows 94 and 162, of 257 175 and 194, of 500 255 and 223.  Gradients
+// of 128 rows against 5001 x 3001, whose tiles leave CUs idle: 112 and 84.
+bool loose_rows(LossCall call, int64_t m, int64_t rows, int64_t ld) {
+  if (ld > kLossMaxStride) return false;
+  if (call == kLossGrad) return m <= 128 && blocks(rows, 128) >= 256;
+  return m <= (call == kLossForward ? 512 : 256);
+}
+
 void run_copy(const void *from, int64_t ld, int64_t rows, int64_t cols, void *to, int64_t ld_to,
               int dtype, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(loss_min((rows + 3) / 4, 4096)));
@@ -801,17 +864,20 @@ int set_tiles(Logits &a, int64_t m) {
   return a.tiles_n * a.tiles_m;
 }
 
-template <class S, bool BF16, bool GRAD>
+template <class S, bool BF16, bool GRAD, bool LOOSE>
 void run_logits(Logits a, int64_t m, hipStream_t st) {
   set_tiles<S, GRAD>(a, m);
-  hipLaunchKernelGGL((logits_tiles<S, BF16, GRAD>), dim3(a.tiles_n * a.tiles_m), dim3(S::NT), 0, st,
+  hipLaunchKernelGGL((logits_tiles<S, BF16, GRAD, LOOSE>), dim3(a.tiles_n * a.tiles_m), dim3(S::NT), 0, st,
                      a);
 }
 
-// fp32 products with too few tiles of 128 x 128 to fill the chip (`splits` times)
-// take 64 x 64.
-bool few_tiles(int64_t n, int64_t m, int64_t splits = 1) {
-  return blocks(n, 128) * static_cast<int64_t>(blocks(m, 128)) * splits < 256;
+// fp32 products of n x m (`splits` times) that take tiles of 64 x 64: with too few of
+// 128 x 128 to fill the chip, or where those cover over 1/16 more.  (Forward and
+// gradients of 512 x 32000 x 512: 597 us, 626 with 64 x 64; gradients of 300 x 8000 x
+// 256: 69 us, 55 with 64 x 64; of 100 x 151936 x 64: 171 us, 102 with 64 x 64.)
+bool small_tiles(int64_t n, int64_t m, int64_t splits = 1) {
+  const int64_t area = loss_up(n, 128) * loss_up(m, 128);
+  return area / (128 * 128) * splits < 256 || area / 17 > loss_up(n, 64) * loss_up(m, 64) / 16;
 }
 
 static_assert(256 * kLossMaxStride * 2 <= kLoadMask && 128 * kLossMaxStride * 4 <= kLoadMask,
@@ -819,26 +885,35 @@ static_assert(256 * kLossMaxStride * 2 <= kLoadMask && 128 * kLossMaxStride * 4 
 static_assert(SmallF::BN == loss_tile_rows(0) && Medium::BN == loss_tile_rows(1),
               "the workspace holds a pair per tile");
 
-// Width of the tiles that `pick_logits` takes, as the loss counts its pairs.
-int64_t logits_tile_rows(int64_t m, int64_t rows, int dtype) {
-  if (dtype == 1) return m > 128 ? Large::BN : Medium::BN;
-  return m > 32 && few_tiles(rows, m) ? SmallF::BN : MediumF::BN;
+// Whether the bf16 logits of m rows and `rows` of the table take 256 x 256 tiles: with
+// two for every CU.  (Loss of 600 rows against 151936 x 1024: 201 us, 231 with 128 x
+// 128; of 4000 rows against 5000 x 1024: 71 us, 65 with 128 x 128.)
+bool large_logits(int64_t m, int64_t rows) {
+  return m > 128 && blocks(rows, 256) * static_cast<int64_t>(blocks(m, 256)) >= 512;
 }
 
-template <bool GRAD>
-void pick_logits(const Logits &a, int64_t m, int dtype, hipStream_t st) {
+// Width of the tiles that `pick_logits` takes, as the loss counts its pairs.
+int64_t logits_tile_rows(int64_t m, int64_t rows, int dtype, bool loose) {
+  if (dtype == 1) return !loose && large_logits(m, rows) ? Large::BN : Medium::BN;
+  return m > 32 && small_tiles(rows, m) ? SmallF::BN : MediumF::BN;
+}
+
+// `rows`: the table's rows by which the tiles are chosen, the same for all pieces of
+// a loss.
+template <bool GRAD, bool LOOSE>
+void pick_logits(const Logits &a, int64_t m, int64_t rows, int dtype, hipStream_t st) {
   if (dtype == 0) {
-    if (m <= 32) run_logits<LowF, false, GRAD>(a, m, st);
-    else if (few_tiles(a.w_rows, m)) run_logits<SmallF, false, GRAD>(a, m, st);
-    else run_logits<MediumF, false, GRAD>(a, m, st);
+    if (m <= 32) run_logits<LowF, false, GRAD, LOOSE>(a, m, st);
+    else if (small_tiles(rows, m)) run_logits<SmallF, false, GRAD, LOOSE>(a, m, st);
+    else run_logits<MediumF, false, GRAD, LOOSE>(a, m, st);
   } else if (m <= 32) {
-    run_logits<Low32, true, GRAD>(a, m, st);
+    run_logits<Low32, true, GRAD, LOOSE>(a, m, st);
   } else if (m <= 64) {
-    run_logits<Low64, true, GRAD>(a, m, st);
-  } else if (m <= 128) {
-    run_logits<Medium, true, GRAD>(a, m, st);
-  } else {
-    run_logits<Large, true, GRAD>(a, m, st);
+    run_logits<Low64, true, GRAD, LOOSE>(a, m, st);
+  } else if (LOOSE || !large_logits(m, rows)) {
+    run_logits<Medium, true, GRAD, LOOSE>(a, m, st);
+  } else if constexpr (!LOOSE) {
+    run_logits<Large, true, GRAD, false>(a, m, st);
   }
 }
 
@@ -853,11 +928,11 @@ int set_tiles(Products &a) {
          ((PARTS & 2) ? a.w_tiles_n * a.w_tiles_m : 0);
 }
 
-template <class S, bool BF16, int PARTS>
+template <class S, bool BF16, int PARTS, bool LOOSE>
 void run_products(Products a, hipStream_t st) {
   const int n = set_tiles<S, PARTS>(a);
   if (n > 0)
-    hipLaunchKernelGGL((grad_tiles<S, BF16, PARTS>), dim3(n), dim3(S::NT), 0, st, a);
+    hipLaunchKernelGGL((grad_tiles<S, BF16, PARTS, LOOSE>), dim3(n), dim3(S::NT), 0, st, a);
 }
 
 // Splits of the sum over the vocabulary so that about `want` workgroups of
@@ -871,52 +946,59 @@ int64_t splits_for(int64_t rows, int64_t dim, int64_t cols, int64_t bn, int64_t 
 }
 
 // Whether the bf16 products take 256 x 256 tiles: where at least three quarters of
-// their rows exist.  (The head's backward of 256 rows against 75968 x 1024: 114 us,
-// 136 with 128 x 128; the gradients of 257 rows against 50257 x 999: 110 us, 91 with
-// 128 x 128.)
-bool large_tiles(int64_t rows) { return rows > 128 && rows * 4 >= loss_up(rows, 256) * 3; }
+// their rows and more than half of their columns exist.  (The head's backward of 256
+// rows against 75968 x 1024: 114 us, 136 with 128 x 128; the gradients of 257 rows
+// against 50257 x 999: 110 us, 91 with 128 x 128; of 4000 rows against 151936 x 128:
+// 1330 us, 1220 with 128 x 128.)
+bool large_tiles(int64_t rows, int64_t dim) {
+  return rows > 128 && rows * 4 >= loss_up(rows, 256) * 3 && dim > 128;
+}
 
 // The two products of a piece.  `splits` is fixed for all pieces of a call.
+template <bool LOOSE>
 void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t st) {
   if (dtype == 0) {
-    const bool small_x = few_tiles(a.dim, a.rows, a.splits), small_w = few_tiles(a.dim, a.cols);
+    const bool small_x = small_tiles(a.dim, a.rows, a.splits), small_w = small_tiles(a.dim, a.cols);
     if (gx && gw && a.rows > 32 && small_x == small_w) {
-      if (small_x) run_products<SmallF, false, 3>(a, st);
-      else run_products<MediumF, false, 3>(a, st);
+      if (small_x) run_products<SmallF, false, 3, LOOSE>(a, st);
+      else run_products<MediumF, false, 3, LOOSE>(a, st);
       return;
     }
     if (gx) {
-      if (a.rows <= 32) run_products<LowF, false, 1>(a, st);
-      else if (small_x) run_products<SmallF, false, 1>(a, st);
-      else run_products<MediumF, false, 1>(a, st);
+      if (a.rows <= 32) run_products<LowF, false, 1, LOOSE>(a, st);
+      else if (small_x) run_products<SmallF, false, 1, LOOSE>(a, st);
+      else run_products<MediumF, false, 1, LOOSE>(a, st);
     }
     if (gw) {
-      if (small_w) run_products<SmallF, false, 2>(a, st);
-      else run_products<MediumF, false, 2>(a, st);
+      if (small_w) run_products<SmallF, false, 2, LOOSE>(a, st);
+      else run_products<MediumF, false, 2, LOOSE>(a, st);
     }
     return;
   }
-  if (large_tiles(a.rows)) {
-    if (gx && gw) run_products<Large, true, 3>(a, st);
-    else if (gx) run_products<Large, true, 1>(a, st);
-    else run_products<Large, true, 2>(a, st);
-    return;
+  if constexpr (!LOOSE) {
+    if (large_tiles(a.rows, a.dim)) {
+      if (gx && gw) run_products<Large, true, 3, false>(a, st);
+      else if (gx) run_products<Large, true, 1, false>(a, st);
+      else run_products<Large, true, 2, false>(a, st);
+      return;
+    }
   }
   if (gx && gw && a.rows > 64) {
-    run_products<Medium, true, 3>(a, st);
+    run_products<Medium, true, 3, LOOSE>(a, st);
     return;
   }
-  if (gx && a.rows <= 32) run_products<Low32, true, 1>(a, st);
-  else if (gx && a.rows <= 64) run_products<Low64, true, 1>(a, st);
-  else if (gx) run_products<Medium, true, 1>(a, st);
-  if (gw) run_products<Medium, true, 2>(a, st);
+  if (gx && a.rows <= 32) run_products<Low32, true, 1, LOOSE>(a, st);
+  else if (gx && a.rows <= 64) run_products<Low64, true, 1, LOOSE>(a, st);
+  else if (gx) run_products<Medium, true, 1, LOOSE>(a, st);
+  if (gw) run_products<Medium, true, 2, LOOSE>(a, st);
 }
 
-int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, int64_t most) {
+int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, bool loose, int64_t most) {
   const int64_t side = rows <= 32 ? 32 : (rows <= 64 && dtype == 1) ? 64 : 128;
-  if (dtype == 1 && large_tiles(rows)) return splits_for(rows, dim, cols, 256, 256, 256, most);
+  if (dtype == 1 && !loose && large_tiles(rows, dim))
+    return splits_for(rows, dim, cols, 256, 256, 256, most);
   const int64_t s = splits_for(rows, dim, cols, 128, side, 512, most);
-  if (dtype == 1 || rows <= 32 || !few_tiles(dim, rows, s)) return s;
+  if (dtype == 1 || rows <= 32 || !small_tiles(dim, rows, s)) return s;
   return splits_for(rows, dim, cols, 64, 64, 512, most);
 }
 
@@ -938,8 +1020,8 @@ int zero_table(const LossRows &r, const LossGrads &g, hipStream_t st) {
   Products a{};
   a.dim = r.dim, a.cols = r.rows, a.gw = g.gw, a.gw_bf16 = g.gwt == 1;
   // (no rows: no operand is read)
-  if (r.dtype == 1) run_products<Medium, true, 2>(a, st);
-  else run_products<MediumF, false, 2>(a, st);
+  if (r.dtype == 1) run_products<Medium, true, 2, false>(a, st);
+  else run_products<MediumF, false, 2, false>(a, st);
   return last_error();
 }
 
@@ -955,7 +1037,9 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
   Logits a{};
   a.m = r.m;
   a.any = Targets{r.targets, r.itype, r.vocab_start, r.vocab, r.rows};
-  if (r.m <= kWholeRows && loads_in_place(r.x, r.dim, r.dtype)) {
+  const bool w_in_place = loads_in_place(r.w, r.dim, r.dtype);
+  const bool loose = !w_in_place && loose_rows(kLossForward, r.m, r.rows, r.dim);
+  if (r.m <= kWholeRows && (loose || loads_in_place(r.x, r.dim, r.dtype))) {
     a.x = r.x, a.ldx = r.dim, a.x_dim = r.dim;
   } else {
     rc = run_collect(r, l, nullptr, nullptr, shard_lse, target_logit, workspace, st);
@@ -967,32 +1051,28 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
   a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
   a.pairs = reinterpret_cast<float *>(at(workspace, l.pairs)), a.pair_ld = r.m;
   a.target_logit = target_logit;
-  const bool in_place = loads_in_place(r.w, r.dim, r.dtype);
-  const int64_t tile_rows = logits_tile_rows(r.m, r.rows, r.dtype);
-  const int64_t piece = in_place ? r.rows : l.table_rows / tile_rows * tile_rows;
-  const int64_t step = piece > 0 ? piece : l.table_rows;
+  const int64_t tile_rows = logits_tile_rows(r.m, r.rows, r.dtype, loose);
+  const int64_t step = w_in_place || loose ? r.rows : l.table_rows;  // (whole tiles)
   for (int64_t row = 0; row < r.rows; row += step) {
     const char *w = static_cast<const char *>(r.w) + row * r.dim * e;
     a.w_rows = loss_min(step, r.rows - row), a.row0 = row, a.tile0 = row / tile_rows;
-    if (in_place) {
-      a.w = w, a.ldw = r.dim, a.w_dim = r.dim;
-    } else {
-      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, r.dtype,
-               st);
-      a.w = at(workspace, l.table), a.ldw = l.dim_pad, a.w_dim = l.dim_pad;
+    a.w = w, a.ldw = a.w_dim = a.k = r.dim;
+    if (!w_in_place && !loose) {
+      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, r.dtype, st);
+      a.w = at(workspace, l.table), a.ldw = a.w_dim = l.dim_pad;
     }
-    a.k = l.dim_pad;
-    pick_logits<false>(a, r.m, r.dtype, st);
+    if (loose) pick_logits<false, true>(a, r.m, r.rows, r.dtype, st);
+    else pick_logits<false, false>(a, r.m, r.rows, r.dtype, st);
     rc = last_error();
     if (rc != 0) return rc;
   }
   const int tiles = blocks(r.rows, tile_rows);
   if (r.m <= 256)
-    hipLaunchKernelGGL(join_pairs<true>, dim3(static_cast<unsigned>(r.m)), dim3(1024), 0, st,
+    hipLaunchKernelGGL(join_pairs<1>, dim3(static_cast<unsigned>(r.m)), dim3(1024), 0, st,
                        a.pairs, a.pair_ld, tiles, a.count, a.m, a.any, a.row_of, shard_lse,
                        target_logit);
   else
-    hipLaunchKernelGGL(join_pairs<false>, dim3(blocks(r.m, 64)), dim3(1024), 0, st, a.pairs,
+    hipLaunchKernelGGL(join_pairs<16>, dim3(blocks(r.m, 16)), dim3(1024), 0, st, a.pairs,
                        a.pair_ld, tiles, a.count, a.m, a.any, a.row_of, shard_lse, target_logit);
   return last_error();
 }
@@ -1023,14 +1103,16 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   const int64_t e = r.dtype == 1 ? 2 : 4;
   int rc = run_collect(r, l, lse, grad_loss, nullptr, nullptr, workspace, st);
   if (rc != 0) return rc;
-  const bool in_place = loads_in_place(r.w, r.dim, r.dtype);
+  const bool w_in_place = loads_in_place(r.w, r.dim, r.dtype);
+  const bool loose = !w_in_place && loose_rows(kLossGrad, r.m, r.rows, r.dim);
+  const bool copied = !w_in_place && !loose;
   // columns of a piece: what the buffer holds, in pieces of one size
   int64_t most = loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride);
-  if (!in_place) most = loss_min(most, l.table_rows);
+  if (copied) most = loss_min(most, l.table_rows);
   const int64_t pieces = (r.rows + most - 1) / most;
   const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
   Logits a{};
-  a.x = at(workspace, l.x), a.ldx = a.x_dim = l.dim_pad, a.k = l.dim_pad;
+  a.x = at(workspace, l.x), a.ldx = a.x_dim = l.dim_pad, a.k = r.dim;
   a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
   a.target = reinterpret_cast<const int32_t *>(at(workspace, l.target));
   a.lse = reinterpret_cast<const float *>(at(workspace, l.lse));
@@ -1040,7 +1122,7 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   p.sums = reinterpret_cast<float *>(at(workspace, l.sums)), p.ld_sums = l.dim_pad;
   p.scale = reinterpret_cast<const float *>(at(workspace, l.count)) + 1;
   p.gw_bf16 = g.gwt == 1, p.accumulate = g.accumulate;
-  p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype,
+  p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype, loose,
                                           loss_most_splits(r.m, l.dim_pad, r.rows)));
   p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
   // the piece of d that begins at `row`
@@ -1048,12 +1130,10 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
     const char *w = static_cast<const char *>(r.w) + row * r.dim * e;
     a.w_rows = loss_min(step, r.rows - row), a.row0 = row, a.ldd = loss_up(a.w_rows, 64);
     a.d = at(workspace, l.piece[row / step % 2]);
-    if (in_place) {
-      a.w = w, a.ldw = r.dim, a.w_dim = r.dim;
-    } else {
-      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, r.dtype,
-               st);
-      a.w = at(workspace, l.table), a.ldw = l.dim_pad, a.w_dim = l.dim_pad;
+    a.w = w, a.ldw = a.w_dim = r.dim;
+    if (copied) {
+      run_copy(w, r.dim, a.w_rows, r.dim, at(workspace, l.table), l.dim_pad, r.dtype, st);
+      a.w = at(workspace, l.table), a.ldw = a.w_dim = l.dim_pad;
     }
   };
   // its products, once `a` is it
@@ -1063,11 +1143,13 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
                            : static_cast<char *>(g.gw) + a.row0 * r.dim * (g.gwt == 1 ? 2 : 4);
   };
   // (a copied table leaves no second copy to read beside the products of the first)
-  const bool together = r.dtype == 1 && in_place && large_tiles(r.m) && g.gx && g.gw;
+  const bool together =
+      r.dtype == 1 && w_in_place && large_tiles(r.m, r.dim) && g.gx && g.gw;
   for (int64_t row = 0; row < r.rows; row += step) {
     if (!together || row == 0) {
       piece_logits(row);
-      pick_logits<true>(a, r.m, r.dtype, st);
+      if (loose) pick_logits<true, true>(a, r.m, a.w_rows, r.dtype, st);
+      else pick_logits<true, false>(a, r.m, a.w_rows, r.dtype, st);
     }
     piece_products();
     if (together && row + step < r.rows) {
@@ -1076,7 +1158,8 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
       hipLaunchKernelGGL(grad_and_logits_tiles<Large>, dim3(n + more), dim3(Large::NT), 0, st, p,
                          n, a);
     } else {
-      pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
+      if (loose) pick_products<true>(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
+      else pick_products<false>(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
     }
     rc = last_error();
     if (rc != 0) return rc;
@@ -1095,24 +1178,26 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
   const int64_t e = r.dtype == 1 ? 2 : 4;
   // (d's rows have to end at whole 16 bytes too: what lies behind may be anything,
   // a NaN as well)
-  const bool d_in_place = loads_in_place(d, ld, r.dtype) && r.rows % (16 / e) == 0;
-  const bool w_in_place = loads_in_place(r.w, r.dim, r.dtype);
-  const bool x_in_place = loads_in_place(r.x, r.dim, r.dtype);
+  bool d_copied = !loads_in_place(d, ld, r.dtype) || r.rows % (16 / e) != 0;
+  bool w_copied = !loads_in_place(r.w, r.dim, r.dtype);
+  bool x_copied = !loads_in_place(r.x, r.dim, r.dtype);
+  const bool loose = (d_copied || w_copied || x_copied) &&
+                     loose_rows(kHeadGrad, r.m, r.rows, loss_max(ld, r.dim));
+  if (loose) d_copied = w_copied = x_copied = false;
   int64_t most = r.rows;
-  if (!d_in_place)
-    most = loss_min(most, loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride));
-  if (!w_in_place) most = loss_min(most, l.table_rows);
+  if (d_copied) most = loss_min(most, loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride));
+  if (w_copied) most = loss_min(most, l.table_rows);
   const int64_t pieces = (r.rows + most - 1) / most;
   const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
   Products p{};
   p.rows = r.m, p.dim = r.dim;
   p.sums = reinterpret_cast<float *>(at(workspace, l.sums)), p.ld_sums = l.dim_pad;
   p.gw_bf16 = g.gwt == 1, p.accumulate = g.accumulate;
-  p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype,
+  p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype, loose,
                                           loss_most_splits(r.m, l.dim_pad, r.rows)));
   p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
   p.x = r.x, p.ldx = r.dim;
-  if (!x_in_place) {
+  if (x_copied) {
     run_copy(r.x, r.dim, r.m, r.dim, at(workspace, l.x), l.dim_pad, r.dtype, st);
     p.x = at(workspace, l.x), p.ldx = l.dim_pad;
   }
@@ -1120,12 +1205,12 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
     const int64_t cols = loss_min(step, r.rows - row);
     p.cols = cols;
     p.d = static_cast<const char *>(d) + row * e, p.ldd = ld;
-    if (!d_in_place) {
+    if (d_copied) {
       run_copy(p.d, ld, r.m, cols, at(workspace, l.piece[0]), loss_up(cols, 64), r.dtype, st);
       p.d = at(workspace, l.piece[0]), p.ldd = loss_up(cols, 64);
     }
     p.w = static_cast<const char *>(r.w) + row * r.dim * e, p.ldw = r.dim;
-    if (!w_in_place) {
+    if (w_copied) {
       run_copy(p.w, r.dim, cols, r.dim, at(workspace, l.table), l.dim_pad, r.dtype,
                st);
       p.w = at(workspace, l.table), p.ldw = l.dim_pad;
@@ -1133,7 +1218,8 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
     p.gw = g.gw == nullptr ? nullptr
                            : static_cast<char *>(g.gw) + row * r.dim * (g.gwt == 1 ? 2 : 4);
     p.first = row == 0;
-    pick_products(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
+    if (loose) pick_products<true>(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
+    else pick_products<false>(p, r.dtype, g.gx != nullptr, g.gw != nullptr, st);
     const int rc = last_error();
     if (rc != 0) return rc;
   }

@@ -14,7 +14,8 @@
 // m: an operand in rows gives it in one 16-byte LDS read; one in columns, of bf16 in
 // two transposing 8-byte reads (ds_read_b64_tr_b16: 16 lanes read 4 values of k x 16
 // columns and get 4 values of k of one column each), of fp32 in four 4-byte reads.
-// Rows have to begin at 16 bytes and hold whole 16 bytes.
+// Rows have to begin at 16 bytes and hold whole 16 bytes.  Other rows pass through
+// registers (`run_loose`).
 #ifndef VPE_TILE_H
 #define VPE_TILE_H
 
@@ -57,6 +58,24 @@ constexpr int wait_vm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) 
 
 __device__ __forceinline__ int wave_id() {
   return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+}
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 __attribute__((aligned(2))) loose_u32x4;
+
+// The first `bytes` of 16 at p, elements of E bytes, zeros behind them.
+template <int E>
+__device__ __forceinline__ u32x4 some_of(const char *p, int bytes) {
+  u32x4 v = u32x4(0u);
+#pragma unroll
+  for (int i = 0; i < 16 / E; ++i)
+    if ((i + 1) * E <= bytes) {
+      if constexpr (E == 2)
+        v[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << (i % 2 * 16);
+      else
+        v[i] = reinterpret_cast<const uint32_t *>(p)[i];
+    }
+  return v;
 }
 
 // A lane's fragment: bf16, 8 consecutive values of k of one n or m (a round of
@@ -137,6 +156,19 @@ struct Stage<false, SIDE, BK, NW, E> {
     left -= kRowBytes;
     k_left -= kRowBytes;
   }
+  // Loose rows.  Steps that hold BK values of every row; rows that do not exist give
+  // the first one's values there, which reach no result.
+  __device__ __forceinline__ int whole_steps() const { return k_left / kRowBytes; }
+  template <bool WHOLE>
+  __device__ __forceinline__ u32x4 fetch(int q) const {
+    const bool row = voff[q] != kLoadMask;
+    if constexpr (WHOLE)
+      return *reinterpret_cast<const loose_u32x4 *>(base + (row ? voff[q] : 0));
+    const int bytes = k_left - piece_at[q & 1];
+    if (!row || bytes <= 0) return u32x4(0u);
+    return bytes >= 16 ? *reinterpret_cast<const loose_u32x4 *>(base + voff[q])
+                       : some_of<E>(base + voff[q], bytes);
+  }
   __device__ __forceinline__ frag_t frag(const char *src, int ks, int i) const {
     return *reinterpret_cast<const frag_t *>(src + rd[ks] + i * 32 * kRowBytes);
   }
@@ -160,6 +192,7 @@ struct Stage<true, SIDE, BK, NW, E> {
   int64_t left, step;
   int voff[kLoads];
   int rd[4];
+  int k_rows, row_bytes;  // (loose rows) that exist, up to SIDE of a row
 
   static __device__ __forceinline__ int swizzle(int k) {
     return E == 2 ? ((k & 3) ^ ((k & 3) << 1) ^ ((k >> 3) & 1)) << 1 : ((k >> 2) & 1) << 3;
@@ -173,6 +206,8 @@ struct Stage<true, SIDE, BK, NW, E> {
     base = static_cast<const char *>(p);
     left = k_limit > 0 ? ((k_limit - 1) * ld + (cols + kEpp - 1) / kEpp * kEpp) * E : 0;
     step = ld * BK * E;
+    k_rows = static_cast<int>(k_limit);
+    row_bytes = static_cast<int>(cols < SIDE ? (cols > 0 ? cols : 0) : SIDE) * E;
     const int lrow = lane / kPieces, slot = lane % kPieces;
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
@@ -206,6 +241,20 @@ struct Stage<true, SIDE, BK, NW, E> {
   __device__ __forceinline__ void advance() {
     base += step;
     left -= step;
+    k_rows -= BK;
+  }
+  __device__ __forceinline__ int whole_steps() const {
+    return row_bytes == kRowBytes ? k_rows / BK : 0;
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ u32x4 fetch(int q) const {
+    if constexpr (WHOLE) return *reinterpret_cast<const loose_u32x4 *>(base + voff[q]);
+    const int lane = threadIdx.x & 63;
+    const int k = (q * NW + wave_id()) * kRowsPerLoad + lane / kPieces;
+    const int bytes = row_bytes - ((lane % kPieces) ^ swizzle(k)) * 16;
+    if (k >= k_rows || bytes <= 0) return u32x4(0u);
+    return bytes >= 16 ? *reinterpret_cast<const loose_u32x4 *>(base + voff[q])
+                       : some_of<E>(base + voff[q], bytes);
   }
   __device__ __forceinline__ frag_t frag(const char *src, int ks, int i) const {
     if constexpr (E == 2) {
@@ -320,6 +369,52 @@ struct Product {
     frags(0, next, 0, 0, cur);
     mfma((KS - 1) & 1, acc);
     schedule(kPart);
+  }
+  // Loose rows: 16 bytes per lane and load, from any element on, pass through
+  // registers into the places that `load` fills.  A step's loads begin three steps
+  // before it, through two sets of registers, and are written a step before it.
+  template <class St>
+  static __device__ __forceinline__ void fetch(St &o, u32x4 (&v)[St::kLoads], bool whole) {
+    if (whole) {
+#pragma unroll
+      for (int q = 0; q < St::kLoads; ++q) v[q] = o.template fetch<true>(q);
+    } else {
+#pragma unroll
+      for (int q = 0; q < St::kLoads; ++q) v[q] = o.template fetch<false>(q);
+    }
+    o.advance();
+  }
+  template <int N>
+  static __device__ __forceinline__ void put(char *to, const u32x4 (&v)[N]) {
+    const int at = wave_id() * 1024 + (threadIdx.x & 63) * 16;
+#pragma unroll
+    for (int q = 0; q < N; ++q) *reinterpret_cast<u32x4 *>(to + q * S::NW * 1024 + at) = v[q];
+  }
+  __device__ __forceinline__ void run_loose(int nk, char *const (&st)[kStages],
+                                            f32x16 (&acc)[S::FN][S::FM]) {
+    if (nk <= 0) return;
+    const int whole_a = a.whole_steps(), whole_b = b.whole_steps();
+    u32x4 va[2][StageN::kLoads], vb[2][StageM::kLoads];
+    fetch(a, va[0], whole_a > 0), fetch(b, vb[0], whole_b > 0);
+    put(st[0], va[0]), put(st[0] + StageN::kBytes, vb[0]);
+    if (nk > 1) fetch(a, va[1], whole_a > 1), fetch(b, vb[1], whole_b > 1);
+    if (nk > 2) fetch(a, va[0], whole_a > 2), fetch(b, vb[0], whole_b > 2);
+    __syncthreads();
+    for (int kt = 0; kt < nk; kt += 2) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (kt + u >= nk) break;
+        if (kt + u + 1 < nk) put(st[1 - u], va[1 - u]), put(st[1 - u] + StageN::kBytes, vb[1 - u]);
+        if (kt + u + 3 < nk)
+          fetch(a, va[1 - u], whole_a > kt + u + 3), fetch(b, vb[1 - u], whole_b > kt + u + 3);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          frags(ks & 1, st[u], ks, -1, nullptr);
+          mfma(ks & 1, acc);
+        }
+        __syncthreads();
+      }
+    }
   }
   // acc += the product over nk steps, through the stages st (NS of them).  A wave
   // reads each fragment one round of MFMAs ahead; the loads of a step begin NS - 1
