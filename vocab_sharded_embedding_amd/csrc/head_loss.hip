@@ -19,6 +19,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "vpe_device.h"
 #include "vpe_loss_launch.h"
 #include "vpe_tile.h"
@@ -323,6 +325,7 @@ struct Logits {
   const int32_t *count;  // live rows; nullptr: all m, targets in `any`
   int64_t m;
   int tiles_n, tiles_m, group_n;
+  int round;  // tiles that run at once, where the last round may be cut in two; or 0
   const int32_t *target;
   Targets any;
   int64_t row0;  // the piece's first row in the shard
@@ -497,18 +500,38 @@ __device__ __forceinline__ void logits_of(const Logits &a, int tn, int64_t n0, i
   }
 }
 
+// Whole tiles first; then, where they exist, half ones: those of the last live rows,
+// or the whole tiles that would begin a round of the chip's CUs and leave most of it
+// idle, in two.
 template <class S, bool BF16, bool GRAD, bool LOOSE>
 __device__ __forceinline__ void logits_tile(const Logits &a, int block,
                                             char *const (&st)[tile::kStages]) {
+  const int live = static_cast<int>(a.count != nullptr ? *a.count : a.m);
+  int whole_m = (live + S::BM - 1) / S::BM, halves = 0;
+  if (Half<S>::kExists && whole_m * S::BM - live >= S::BM / 2) whole_m -= 1, halves = a.tiles_n;
+  int whole = a.tiles_n * whole_m, split = 0;
+  if (Half<S>::kExists && halves == 0 && a.round > 0 && whole > a.round &&
+      whole % a.round <= a.round / 2)
+    split = whole % a.round, whole -= split;
   int tn, tm;
-  tile_of(block, a.tiles_n, a.tiles_m, a.group_n, tn, tm);
-  const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
-  const int64_t live = a.count != nullptr ? *a.count : a.m;
-  if (m0 >= live) return;
-  if (Half<S>::kExists && live - m0 <= S::BM / 2)
-    logits_of<typename Half<S>::type, BF16, GRAD, LOOSE>(a, tn, n0, m0, live, st);
-  else
-    logits_of<S, BF16, GRAD, LOOSE>(a, tn, n0, m0, live, st);
+  if (block < whole) {
+    tile_of(block, a.tiles_n, whole_m, a.group_n, tn, tm);  // (of them all)
+    logits_of<S, BF16, GRAD, LOOSE>(a, tn, static_cast<int64_t>(tn) * S::BN,
+                                    static_cast<int64_t>(tm) * S::BM, live, st);
+  } else if constexpr (Half<S>::kExists) {
+    typedef typename Half<S>::type H;
+    const int j = block - whole;
+    if (j >= halves + 2 * split) return;
+    int64_t m0;
+    if (split > 0) {
+      tile_of(whole + j / 2, a.tiles_n, whole_m, a.group_n, tn, tm);
+      m0 = static_cast<int64_t>(tm) * S::BM + j % 2 * H::BM;
+      if (m0 >= live) return;
+    } else {
+      tn = j, m0 = static_cast<int64_t>(whole_m) * S::BM;
+    }
+    logits_of<H, BF16, GRAD, LOOSE>(a, tn, static_cast<int64_t>(tn) * S::BN, m0, live, st);
+  }
 }
 #endif
 
@@ -866,9 +889,10 @@ int set_tiles(Logits &a, int64_t m) {
 
 template <class S, bool BF16, bool GRAD, bool LOOSE>
 void run_logits(Logits a, int64_t m, hipStream_t st) {
-  set_tiles<S, GRAD>(a, m);
-  hipLaunchKernelGGL((logits_tiles<S, BF16, GRAD, LOOSE>), dim3(a.tiles_n * a.tiles_m), dim3(S::NT), 0, st,
-                     a);
+  int n = set_tiles<S, GRAD>(a, m);
+  a.round = std::is_same<S, Large>::value ? 256 : 0;
+  if (a.round > 0) n += a.round / 2;
+  hipLaunchKernelGGL((logits_tiles<S, BF16, GRAD, LOOSE>), dim3(n), dim3(S::NT), 0, st, a);
 }
 
 // fp32 products of n x m (`splits` times) that take tiles of 64 x 64: with too few of
