@@ -368,30 +368,46 @@ struct Half<tile::Shape<128, 128, 2, 2, 32, 2>> {
 };
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// Columns n0.. (tile tn) of rows m0.. .
-template <class S, bool BF16, bool GRAD, bool LOOSE>
-__device__ __forceinline__ void logits_of(const Logits &a, int tn, int64_t n0, int64_t m0,
-                                          int64_t live, char *const (&st)[tile::kStages]) {
+// The loss: column in the shard of the target of this lane's rows, or -1.
+template <class S>
+__device__ __forceinline__ void loss_targets(const Logits &a, int64_t m0, int64_t live,
+                                             int (&target)[S::FM]) {
+#pragma unroll
+  for (int j = 0; j < S::FM; ++j) {
+    const int64_t m = m0 + tile::wave_id() / S::WN * S::TM + j * 32 + (threadIdx.x & 31);
+    target[j] = -1;
+    if (m < live) {
+      if (a.count != nullptr) {
+        target[j] = a.target[m];
+      } else {
+        int64_t at;
+        a.any.local(m, at);
+        target[j] = static_cast<int>(at);
+      }
+    }
+  }
+}
+
+// What becomes of the logits acc: columns n0.. (tile tn) of rows m0.. .  `out`: the
+// loss's [BM][WN] pairs; `st`: free, for the gradients.
+template <class S, bool BF16, bool GRAD>
+__device__ __forceinline__ void logits_done(const Logits &a, int tn, int64_t n0, int64_t m0,
+                                            int64_t live, const int (&target)[S::FM], float *out,
+                                            char *const (&st)[tile::kStages],
+                                            f32x16 (&acc)[S::FN][S::FM]) {
   constexpr int kSize = BF16 ? 2 : 4;
-  f32x16 acc[S::FN][S::FM];
-#pragma unroll
-  for (int i = 0; i < S::FN; ++i)
-#pragma unroll
-    for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
-  product<S, kSize, false, false, LOOSE>(
-      static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
-      static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.x_dim, a.k, st,
-      acc);
-  const int lane = threadIdx.x & 63, wave = tile::wave_id();
+  // (opaque, so that what depends on the lane alone is not kept over a loop of tiles:
+  // there are no registers for it)
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  const int wave = tile::wave_id();
   const int wn = wave % S::WN, wm = wave / S::WN, hi = lane >> 5;
   const int64_t nb = n0 + wn * S::TN;  // this wave's first column
   // this lane's columns nb + c, c = 32 i + 8 (r / 4) + 4 hi + r % 4, exist for
   // c < lim
   const int64_t left = a.w_rows - nb;
   const int lim = left < 0 ? 0 : (left < S::TN ? static_cast<int>(left) : S::TN);
-  __syncthreads();  // every wave is done with the stages
   if constexpr (!GRAD) {
-    float *out = reinterpret_cast<float *>(st[0]);  // [BM][WN] pairs
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) {
       const int64_t m = m0 + wm * S::TM + j * 32 + (lane & 31);
@@ -422,12 +438,7 @@ __device__ __forceinline__ void logits_of(const Logits &a, int tn, int64_t n0, i
         e[0] = top, e[1] = s;
       }
       // the row's target, where this wave has its column
-      int64_t rel = -1;
-      if (m < live) {
-        if (a.count != nullptr) rel = a.target[m];
-        else a.any.local(m, rel);
-        rel = rel < 0 ? -1 : rel - a.row0 - nb;
-      }
+      const int64_t rel = target[j] < 0 ? -1 : target[j] - a.row0 - nb;
       if (__any(rel >= 0 && rel < S::TN)) {
         float z = 0.f;
         const int at = rel >= 0 && rel < lim ? static_cast<int>(rel) : -1;
@@ -500,37 +511,78 @@ __device__ __forceinline__ void logits_of(const Logits &a, int tn, int64_t n0, i
   }
 }
 
-// Whole tiles first; then, where they exist, half ones: those of the last live rows,
-// or the whole tiles that would begin a round of the chip's CUs and leave most of it
-// idle, in two.
 template <class S, bool BF16, bool GRAD, bool LOOSE>
-__device__ __forceinline__ void logits_tile(const Logits &a, int block,
-                                            char *const (&st)[tile::kStages]) {
-  const int live = static_cast<int>(a.count != nullptr ? *a.count : a.m);
-  int whole_m = (live + S::BM - 1) / S::BM, halves = 0;
-  if (Half<S>::kExists && whole_m * S::BM - live >= S::BM / 2) whole_m -= 1, halves = a.tiles_n;
-  int whole = a.tiles_n * whole_m, split = 0;
-  if (Half<S>::kExists && halves == 0 && a.round > 0 && whole > a.round &&
-      whole % a.round <= a.round / 2)
-    split = whole % a.round, whole -= split;
-  int tn, tm;
-  if (block < whole) {
-    tile_of(block, a.tiles_n, whole_m, a.group_n, tn, tm);  // (of them all)
-    logits_of<S, BF16, GRAD, LOOSE>(a, tn, static_cast<int64_t>(tn) * S::BN,
-                                    static_cast<int64_t>(tm) * S::BM, live, st);
-  } else if constexpr (Half<S>::kExists) {
-    typedef typename Half<S>::type H;
-    const int j = block - whole;
-    if (j >= halves + 2 * split) return;
-    int64_t m0;
+__device__ __forceinline__ void logits_of(const Logits &a, int tn, int64_t n0, int64_t m0,
+                                          int64_t live, float *out,
+                                          char *const (&st)[tile::kStages]) {
+  constexpr int kSize = BF16 ? 2 : 4;
+  f32x16 acc[S::FN][S::FM];
+#pragma unroll
+  for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
+  int target[S::FM];
+  if constexpr (!GRAD) loss_targets<S>(a, m0, live, target);
+  product<S, kSize, false, false, LOOSE>(
+      static_cast<const char *>(a.w) + n0 * a.ldw * kSize, a.ldw, a.w_rows - n0, a.w_dim,
+      static_cast<const char *>(a.x) + m0 * a.ldx * kSize, a.ldx, live - m0, a.x_dim, a.k, st,
+      acc);
+  __syncthreads();  // every wave is done with the stages
+  logits_done<S, BF16, GRAD>(a, tn, n0, m0, live, target, out, st, acc);
+}
+
+// The tiles of a launch, with the device's count of live rows: whole ones first;
+// then, where they exist, half ones: those of the last live rows, or the whole tiles
+// that would begin a round of the chip's CUs and leave most of it idle, in two.
+template <class S>
+struct Tiles {
+  typedef typename Half<S>::type H;
+  int live, whole_m, whole, split, halves;
+
+  __device__ __forceinline__ explicit Tiles(const Logits &a) {
+    live = static_cast<int>(a.count != nullptr ? *a.count : a.m);
+    whole_m = (live + S::BM - 1) / S::BM, halves = split = 0;
+    if (Half<S>::kExists && whole_m * S::BM - live >= S::BM / 2) whole_m -= 1, halves = a.tiles_n;
+    whole = a.tiles_n * whole_m;
+    if (Half<S>::kExists && halves == 0 && a.round > 0 && whole > a.round &&
+        whole % a.round <= a.round / 2) {
+      split = whole % a.round;
+      whole -= split, halves = 2 * split;
+    }
+  }
+  // Whole tile t < whole,
+  __device__ __forceinline__ void place(const Logits &a, int t, int &tn, int64_t &m0) const {
+    int tm;
+    tile_of(t, a.tiles_n, whole_m, a.group_n, tn, tm);
+    m0 = static_cast<int64_t>(tm) * S::BM;
+  }
+  // and half tile j < halves.
+  __device__ __forceinline__ void place_half(const Logits &a, int j, int &tn, int64_t &m0) const {
     if (split > 0) {
-      tile_of(whole + j / 2, a.tiles_n, whole_m, a.group_n, tn, tm);
-      m0 = static_cast<int64_t>(tm) * S::BM + j % 2 * H::BM;
-      if (m0 >= live) return;
+      place(a, whole + j / 2, tn, m0);
+      m0 += j % 2 * H::BM;
     } else {
       tn = j, m0 = static_cast<int64_t>(whole_m) * S::BM;
     }
-    logits_of<H, BF16, GRAD, LOOSE>(a, tn, static_cast<int64_t>(tn) * S::BN, m0, live, st);
+  }
+};
+
+template <class S, bool BF16, bool GRAD, bool LOOSE>
+__device__ __forceinline__ void logits_tile(const Logits &a, int block,
+                                            char *const (&st)[tile::kStages]) {
+  const Tiles<S> tiles(a);
+  int tn;
+  int64_t m0;
+  float *out = reinterpret_cast<float *>(st[0]);
+  if (block < tiles.whole) {
+    tiles.place(a, block, tn, m0);
+    logits_of<S, BF16, GRAD, LOOSE>(a, tn, static_cast<int64_t>(tn) * S::BN, m0, tiles.live, out,
+                                    st);
+  } else if constexpr (Half<S>::kExists) {
+    if (block - tiles.whole >= tiles.halves) return;
+    tiles.place_half(a, block - tiles.whole, tn, m0);
+    logits_of<typename Half<S>::type, BF16, GRAD, LOOSE>(
+        a, tn, static_cast<int64_t>(tn) * S::BN, m0, tiles.live, out, st);
   }
 }
 #endif
@@ -542,6 +594,55 @@ __global__ __launch_bounds__(S::NT, S::NT == 256 ? 2 : 1) void logits_tiles(Logi
   VPE_STAGES(S, kSize)
   static_assert(kStageBytes >= S::BM * S::WN * 8, "the pairs fit a stage");
   logits_tile<S, BF16, GRAD, LOOSE>(a, blockIdx.x, st);
+#endif
+}
+
+// The loss in large tiles: a workgroup per CU takes tile after tile, and the loads
+// of the next one are under way while the exponentials of one are taken.
+template <class S>
+__global__ __launch_bounds__(S::NT) void loss_tiles(Logits a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  VPE_STAGES(S, 2)
+  __shared__ float out[S::BM * S::WN * 2];
+  static_assert(Half<S>::type::BM * Half<S>::type::WN <= S::BM * S::WN, "its pairs fit too");
+  const Tiles<S> tiles(a);
+  const int nk = static_cast<int>((a.k + S::BK - 1) / S::BK);
+  tile::Product<S, 2, false, false> p;
+  int t = blockIdx.x, tn = 0;
+  int64_t m0 = 0;
+  auto start = [&]() {
+    tiles.place(a, t, tn, m0);
+    const int64_t n0 = static_cast<int64_t>(tn) * S::BN;
+    p.a.init(static_cast<const char *>(a.w) + n0 * a.ldw * 2, a.ldw, a.w_rows - n0, a.w_dim,
+             tile::wave_id() % S::WN * S::TN);
+    p.b.init(static_cast<const char *>(a.x) + m0 * a.ldx * 2, a.ldx, tiles.live - m0, a.x_dim,
+             tile::wave_id() / S::WN * S::TM);
+    p.start(nk, st);
+  };
+  if (t < tiles.whole) start();
+  while (t < tiles.whole) {
+    int target[S::FM];
+    loss_targets<S>(a, m0, tiles.live, target);
+    f32x16 acc[S::FN][S::FM];
+#pragma unroll
+    for (int i = 0; i < S::FN; ++i)
+#pragma unroll
+      for (int j = 0; j < S::FM; ++j) acc[i][j] = f32x16(0.f);
+    p.go_on(nk, st, acc);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // (all done with the stages)
+    const int tn_now = tn;
+    const int64_t m0_now = m0;
+    t += gridDim.x;
+    if (t < tiles.whole) start();
+    logits_done<S, true, false>(a, tn_now, static_cast<int64_t>(tn_now) * S::BN, m0_now,
+                                tiles.live, target, out, st, acc);
+  }
+  for (int j = t - tiles.whole; j < tiles.halves; j += gridDim.x) {
+    tiles.place_half(a, j, tn, m0);
+    __syncthreads();
+    logits_of<typename Half<S>::type, true, false, false>(
+        a, tn, static_cast<int64_t>(tn) * S::BN, m0, tiles.live, out, st);
+  }
 #endif
 }
 
@@ -936,8 +1037,13 @@ void pick_logits(const Logits &a, int64_t m, int64_t rows, int dtype, hipStream_
     run_logits<Low64, true, GRAD, LOOSE>(a, m, st);
   } else if (LOOSE || !large_logits(m, rows)) {
     run_logits<Medium, true, GRAD, LOOSE>(a, m, st);
+  } else if constexpr (GRAD && !LOOSE) {
+    run_logits<Large, true, true, false>(a, m, st);
   } else if constexpr (!LOOSE) {
-    run_logits<Large, true, GRAD, false>(a, m, st);
+    Logits b = a;
+    const int n = set_tiles<Large, false>(b, m);
+    b.round = 256;
+    hipLaunchKernelGGL(loss_tiles<Large>, dim3(n < b.round ? n : b.round), dim3(Large::NT), 0, st, b);
   }
 }
 

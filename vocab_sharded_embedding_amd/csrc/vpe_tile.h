@@ -422,20 +422,25 @@ struct Product {
   __device__ __forceinline__ void run(int nk, char *const (&st)[kStages],
                                       f32x16 (&acc)[S::FN][S::FM]) {
     if (nk <= 0) return;
-    // (few steps: every stage at once, nothing spread)
-    bool rest = nk >= 2 * S::NS;
+    start(nk, st);
+    go_on(nk, st, acc);
+  }
+  // Its first loads, of the first NS steps (few steps: every stage at once, nothing
+  // spread),
+  __device__ __forceinline__ void start(int nk, char *const (&st)[kStages]) {
 #pragma unroll
     for (int s = 0; s < S::NS - 1; ++s)
       if (s < nk) load_parts(st[s], 0, kSpread);
-    if (rest) {
-      load_parts(st[S::NS - 1], 0, 1);
-      __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 2) * kLoads + kPart));
-    } else if (S::NS - 1 < nk) {
-      load_parts(st[S::NS - 1], 0, kSpread);
-      __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 1) * kLoads));
-    } else {
-      __builtin_amdgcn_s_waitcnt(wait_vm(0));
-    }
+    if (nk >= 2 * S::NS) load_parts(st[S::NS - 1], 0, 1);
+    else if (S::NS - 1 < nk) load_parts(st[S::NS - 1], 0, kSpread);
+  }
+  // and the rest.
+  __device__ __forceinline__ void go_on(int nk, char *const (&st)[kStages],
+                                        f32x16 (&acc)[S::FN][S::FM]) {
+    bool rest = nk >= 2 * S::NS;
+    if (rest) __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 2) * kLoads + kPart));
+    else if (S::NS - 1 < nk) __builtin_amdgcn_s_waitcnt(wait_vm((S::NS - 1) * kLoads));
+    else __builtin_amdgcn_s_waitcnt(wait_vm(0));
     asm volatile("s_barrier" ::: "memory");
     frags(0, st[0], 0, -1, nullptr);
     int kt = 0;
