@@ -94,6 +94,7 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
+// (310 tensors, 600 million elements, a third fp32, on two ranks: 300 us, 5.3 TB/s)
 template <int N>
 __global__ __launch_bounds__(kThreads) void sumsq_pieces(Table<N> t, double *__restrict__ partial) {
   const int at = tensor_of(t, blockIdx.x);
@@ -137,7 +138,8 @@ __device__ __forceinline__ void scale_piece(const void *g, void *out, int64_t be
 }
 
 // The pieces last to first: what the sum of squares read last may still be in the
-// memory-side cache.
+// memory-side cache.  (The same tensors: 660 us, 4.9 TB/s of reads and writes; with
+// the sums 967 us, 1062 first to last and with fewer loads in flight.)
 template <int N>
 __global__ __launch_bounds__(kThreads) void clip_pieces(Table<N> t, Outputs<N> o, Norms p,
                                                         float *__restrict__ norm) {

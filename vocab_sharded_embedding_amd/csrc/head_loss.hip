@@ -59,7 +59,8 @@ __device__ __forceinline__ bool row_lives(const Collect &c, int64_t i) {
   return t >= 0 && t < c.vocab && (c.grad_loss == nullptr || c.grad_loss[i] != 0.f);
 }
 
-// Live rows in order, without a second pass: every workgroup counts the live
+// Live rows in order, without a second pass (8192 x 1024 bf16: 23 us, latency; of 1021
+// rows 7 us): every workgroup counts the live
 // rows before its own (targets are small against x).  The gradients' factors are
 // taken over the largest finite |grad_loss|, so that a loss averaged over its
 // rows has factors of exactly 1 and d is rounded as softmax - onehot.
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(256) void collect_rows(Collect c) {
 }
 
 // `rows` rows of `cols` values at stride ld, any alignment, copied to stride ld_to
-// with zeros up to it.
+// with zeros up to it.  Bound by HBM: 50257 x 999 bf16 33-42 us, 4.8-6.1 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(256) void copy_rows(const char *__restrict__ from, int64_t ld,
                                                  int64_t rows, int64_t cols,
@@ -353,19 +354,20 @@ __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
 // wide and by as many waves.  (The live rows are known to the device alone.)
 template <class S>
 struct Half {
-  static constexpr bool kExists = false;
-  typedef S type;
+  typedef S type;  // none
 };
 template <>
 struct Half<tile::Shape<256, 256, 2, 4, 64, 2>> {
-  static constexpr bool kExists = true;
   typedef tile::Shape<256, 128, 4, 2, 64, 2> type;
 };
 template <>
 struct Half<tile::Shape<128, 128, 2, 2, 32, 2>> {
-  static constexpr bool kExists = true;
   typedef tile::Shape<128, 64, 2, 2, 32, 2> type;
 };
+template <class S>
+constexpr bool has_half() {
+  return !std::is_same<typename Half<S>::type, S>::value;
+}
 
 #if defined(__HIP_DEVICE_COMPILE__)
 // The loss: column in the shard of the target of this lane's rows, or -1.
@@ -542,9 +544,9 @@ struct Tiles {
   __device__ __forceinline__ explicit Tiles(const Logits &a) {
     live = static_cast<int>(a.count != nullptr ? *a.count : a.m);
     whole_m = (live + S::BM - 1) / S::BM, halves = split = 0;
-    if (Half<S>::kExists && whole_m * S::BM - live >= S::BM / 2) whole_m -= 1, halves = a.tiles_n;
+    if (has_half<S>() && whole_m * S::BM - live >= S::BM / 2) whole_m -= 1, halves = a.tiles_n;
     whole = a.tiles_n * whole_m;
-    if (Half<S>::kExists && halves == 0 && a.round > 0 && whole > a.round &&
+    if (has_half<S>() && halves == 0 && a.round > 0 && whole > a.round &&
         whole % a.round <= a.round / 2) {
       split = whole % a.round;
       whole -= split, halves = 2 * split;
@@ -578,7 +580,7 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
     tiles.place(a, block, tn, m0);
     logits_of<S, BF16, GRAD, LOOSE>(a, tn, static_cast<int64_t>(tn) * S::BN, m0, tiles.live, out,
                                     st);
-  } else if constexpr (Half<S>::kExists) {
+  } else if constexpr (has_half<S>()) {
     if (block - tiles.whole >= tiles.halves) return;
     tiles.place_half(a, block - tiles.whole, tn, m0);
     logits_of<typename Half<S>::type, BF16, GRAD, LOOSE>(
@@ -587,6 +589,12 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
 }
 #endif
 
+// One workgroup per tile.  Few rows: bound by reading the table (1 row against 151936 x
+// 1024 bf16: 51 us, 6.05 TB/s).  Loose rows: by the latency of loads that pass through
+// registers (257 rows against 50257 x 999: 60 us, 33 on aligned rows).  fp32: by the
+// matrix cores (448 rows against 32000 x 512: 138-144 us, 102-106 TFLOP/s, two rounds of
+// tiles; 2048 against 32000 x 1024: 0.97 ms, 138).
+// (4 waves: two workgroups per CU)
 template <class S, bool BF16, bool GRAD, bool LOOSE>
 __global__ __launch_bounds__(S::NT, S::NT == 256 ? 2 : 1) void logits_tiles(Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -599,6 +607,14 @@ __global__ __launch_bounds__(S::NT, S::NT == 256 ? 2 : 1) void logits_tiles(Logi
 
 // The loss in large tiles: a workgroup per CU takes tile after tile, and the loads
 // of the next one are under way while the exponentials of one are taken.
+//
+// Bound by the matrix cores and, between two tiles of K = 1024, by the exponentials
+// (a seventh of the cycles: all eight waves take them at once).  8192 rows, 7168 of
+// them live, against 151936 x 1024: 1.79-1.92 ms, 1.16-1.24 PFLOP/s, matrix cores busy
+// 63% at the 1.69 GHz that the power allows; 3584 live rows against 37984 x 4096: 0.92
+// ms, 1.21 PFLOP/s; 896 against 75968 x 1024: 147 us, 0.95 PFLOP/s, four and a half
+// rounds of tiles for the work of four.  A workgroup per tile: 1% slower.  Four stages
+// of 32 values of k: 5% slower.
 template <class S>
 __global__ __launch_bounds__(S::NT) void loss_tiles(Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -648,7 +664,8 @@ __global__ __launch_bounds__(S::NT) void loss_tiles(Logits a) {
 
 // A row's pairs joined: shard_lse[row] = log sum exp.  ROWS rows per workgroup of
 // 1024: neighbouring lanes have neighbouring rows, and 1024 / ROWS threads share a
-// row's tiles.  Rows that were not collected (count nullptr) get their zeros here.
+// row's tiles (297 tiles of 896 rows: 5.8 us; 10.4 with 64 rows per workgroup; 594 of
+// 7168: 11.7 and 23.3).  Rows that were not collected (count nullptr) get their zeros here.
 template <int ROWS>
 __global__ __launch_bounds__(1024) void join_pairs(const float *__restrict__ pairs, int64_t ld,
                                                    int tiles, const int32_t *__restrict__ count,
@@ -774,6 +791,11 @@ __device__ __forceinline__ void grad_x_of(const Products &a, int split, int64_t 
 
 // Parts of the launch: 1 the gradient of x, 2 that of the table, 3 both, the
 // first's workgroups before the second's.
+//
+// With many rows bound by the matrix cores: 4096 rows against 37984 x 4096, fp32
+// gradients, both products 2.15-2.45 ms, 1.04-1.18 PFLOP/s; fp32, 448 rows against
+// 32000 x 512, 265 us, 110 TFLOP/s.  With few by HBM: 256 against 75968 x 1024 bf16, 92-98
+// us, 3.6-3.8 TB/s, the workgroups of either product reading d for themselves.
 template <class S, bool BF16, int PARTS, bool LOOSE>
 __device__ __forceinline__ void products_tile(const Products &a, int b,
                                               char *const (&st)[tile::kStages]) {
@@ -787,7 +809,7 @@ __device__ __forceinline__ void products_tile(const Products &a, int b,
       const int split = t2 / a.x_tiles_m, tm = t2 - split * a.x_tiles_m;
       const int64_t n0 = static_cast<int64_t>(tn) * S::BN, m0 = static_cast<int64_t>(tm) * S::BM;
       if (m0 >= live) return;
-      if (Half<S>::kExists && live - m0 <= S::BM / 2)
+      if (has_half<S>() && live - m0 <= S::BM / 2)
         grad_x_of<typename Half<S>::type, BF16, LOOSE>(a, split, n0, m0, live, st);
       else
         grad_x_of<S, BF16, LOOSE>(a, split, n0, m0, live, st);
@@ -860,7 +882,9 @@ __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
 }
 
 // Both products of one piece, and the logits' gradient of the next: the second
-// fills the CUs that the first, with few and long tiles, leaves idle.
+// fills the CUs that the first, with few and long tiles, leaves idle.  Bound by the
+// matrix cores (7168 live rows, 8192 columns, K = 1024 and 7168: 300-310 us, 1.16-1.20
+// PFLOP/s, busy 61%).
 template <class S>
 __global__ __launch_bounds__(S::NT) void grad_and_logits_tiles(Products p, int n, Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -870,7 +894,7 @@ __global__ __launch_bounds__(S::NT) void grad_and_logits_tiles(Products p, int n
 #endif
 }
 
-// grad_x from its sums: row i's is at place[i] (nullptr: i), 0 where that is -1.
+// grad_x from its sums (4096 x 4096 fp32 of 1 sum: 25 us, 5.3 TB/s): row i's is at place[i] (nullptr: i), 0 where that is -1.
 template <bool BF16>
 __global__ __launch_bounds__(256) void finish_grad_x(const float *__restrict__ sums,
                                                      int64_t ld_sums, int64_t split_stride,
