@@ -611,7 +611,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 256 ? 2 : 1) void logits_tiles(Logi
 // Bound by the matrix cores and, between two tiles of K = 1024, by the exponentials
 // (a seventh of the cycles: all eight waves take them at once).  8192 rows, 7168 of
 // them live, against 151936 x 1024: 1.79-1.92 ms, 1.16-1.24 PFLOP/s, matrix cores busy
-// 63% at the 1.69 GHz that the power allows; 3584 live rows against 37984 x 4096: 0.92
+// 63% at 1.84 GHz; 3584 live rows against 37984 x 4096: 0.92
 // ms, 1.21 PFLOP/s; 896 against 75968 x 1024: 147 us, 0.95 PFLOP/s, four and a half
 // rounds of tiles for the work of four.  A workgroup per tile: 1% slower.  Four stages
 // of 32 values of k: 5% slower.
