@@ -263,6 +263,57 @@ def test_live_rows_around_a_tile(live, dtype):
     assert_within(gw, rw, ew, "grad_weight")
 
 
+@pytest.mark.parametrize("live", [0, 1, 128, 129, 256, 300, 384, 385, 642, 700, 768, 769, 900,
+                                  1024, 1025, 1030])
+def test_live_rows_in_large_tiles(live):
+    """As above where the bf16 logits take 256 x 256 tiles, by workgroups that go from
+    tile to tile: whole, half and divided ones."""
+    m, vocab, dim = 1030, 44000, 72
+    x, w, t, gl = _case(m, vocab, dim, BF16, live)
+    order = torch.randperm(m, device="cuda")
+    t[order[live:]] = -100
+    x[order[live:]] = NAN
+    clean = torch.where(t[:, None] < 0, 0.0, x)
+    ref = Reference(clean, w, t, vocab, gl)
+    loss, lse = _loss(x, w, t, vocab)
+    assert_within(loss, ref.loss, ref.loss_err, "loss")
+    gx, gw = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab)
+    rx, ex, rw, ew = ref.grads(slice(0, vocab), BF16, BF16)
+    assert_within(gx, rx, ex, "grad_x")
+    assert_within(gw, rw, ew, "grad_weight")
+
+
+def test_large_tiles_captured():
+    m, vocab, dim = 1100, 70000, 64
+    x, w, t, gl = _case(m, vocab, dim, BF16)
+    buf = _buffers(m, vocab, dim, BF16)
+    _step(x, w, t, gl, vocab, *buf)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(x, w, t, gl, vocab, *buf)
+    for turn in range(4):
+        fresh = _case(m, vocab, dim, BF16, turn + 1)
+        fresh[2][turn::3] = -100
+        for a, b in zip((x, w, t, gl), fresh):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = _buffers(m, vocab, dim, BF16)
+        _step(*fresh, vocab, *eager)
+        for name, i in (("loss", 0), ("lse", 1), ("grad_x", 4), ("grad_weight", 5), ("norm", 9)):
+            assert torch.equal(buf[i], eager[i]), (turn, name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_hidden_rows_alone_at_any_element(dtype):
+    m, vocab, dim = 150, 640, 64
+    x, w, _, _ = _case(m, vocab, dim, dtype)
+    odd = torch.cat([x.new_zeros(1), x.reshape(-1)])[1:].view(m, dim)
+    d = torch.randn(m, vocab, device="cuda").to(dtype)
+    for a, b in zip(vpe.vpe_lmhead_grad(d, odd, w), vpe.vpe_lmhead_grad(d, x, w)):
+        assert torch.equal(a, b)
+
+
 def _bytes(n):
     return torch.empty(n, dtype=torch.uint8, device="cuda")
 

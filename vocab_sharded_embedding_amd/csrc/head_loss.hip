@@ -1335,8 +1335,9 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
   bool d_copied = !loads_in_place(d, ld, r.dtype) || r.rows % (16 / e) != 0;
   bool w_copied = !loads_in_place(r.w, r.dim, r.dtype);
   bool x_copied = !loads_in_place(r.x, r.dim, r.dtype);
-  const bool loose = (d_copied || w_copied || x_copied) &&
-                     loose_rows(kHeadGrad, r.m, r.rows, loss_max(ld, r.dim));
+  // (x alone is a small copy)
+  const bool loose =
+      (d_copied || w_copied) && loose_rows(kHeadGrad, r.m, r.rows, loss_max(ld, r.dim));
   if (loose) d_copied = w_copied = x_copied = false;
   int64_t most = r.rows;
   if (d_copied) most = loss_min(most, loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride));
