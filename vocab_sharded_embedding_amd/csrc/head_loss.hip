@@ -341,6 +341,19 @@ struct Logits {
   int64_t ldd;  // the piece's columns, zeros after the last
 };
 
+// exp(z - lse), |z - lse| times a rounding closer than the exponential of the rounded
+// product (z - lse) log2(e): what the difference and the product lose is added as a
+// factor 1 + the loss.  (An infinite or NaN difference has no loss to add.)
+__device__ __forceinline__ float exp_of(float z, float lse) {
+  const float t = z - lse, back = t - z;
+  const float lost = (z - (t - back)) - (lse + back);
+  const float hi = t * kLog2e;
+  const float lo = fmaf(t, 1.92596299e-8f, fmaf(t, kLog2e, -hi));  // log2(e) - kLog2e
+  const float p = __builtin_amdgcn_exp2f(hi);
+  const float more = fmaf(lo, 0.693147182f, lost);
+  return fabsf(more) < 1.f ? fmaf(p, more, p) : p;
+}
+
 // (m, s) of two disjoint sets of logits; an empty one is (-inf, 0).
 __device__ __forceinline__ void merge(float &m, float &s, float m2, float s2) {
   const float top = (m != m || m > m2) ? m : m2;
@@ -426,13 +439,15 @@ __device__ __forceinline__ void logits_done(const Logits &a, int tn, int64_t n0,
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
-      const float shift = top == -__builtin_huge_valf() ? 0.f : -top * kLog2e;
+      const float base = top == -__builtin_huge_valf() ? 0.f : top, shift = -base * kLog2e;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, shift));
+          // (fp32: the difference first; `shift` rounds every term alike)
+          s += __builtin_amdgcn_exp2f(BF16 ? fmaf(acc[i][j][r], kLog2e, shift)
+                                           : (acc[i][j][r] - base) * kLog2e);
       if (s != s) top = s;  // a NaN logit, or +inf
       merge(top, s, __shfl_xor(top, 32), __shfl_xor(s, 32));
       if (hi == 0) {
@@ -482,10 +497,8 @@ __device__ __forceinline__ void logits_done(const Logits &a, int tn, int64_t n0,
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          // (fp32: the difference first, whose rounding the exponential does
-          // not magnify)
-          acc[i][j][r] = __builtin_amdgcn_exp2f(BF16 ? fmaf(acc[i][j][r], kLog2e, shift)
-                                                     : (acc[i][j][r] - lse) * kLog2e);
+          acc[i][j][r] = BF16 ? __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, shift))
+                              : exp_of(acc[i][j][r], lse);
       if (__any(at >= 0)) {
 #pragma unroll
         for (int i = 0; i < S::FN; ++i)
