@@ -306,6 +306,10 @@ struct Product {
   StageN a;
   StageM b;
   frag_t fa[2][S::FN], fb[2][S::FM];
+  // fp32, one fragment a wave: every other MFMA adds to a sum of its own, which
+  // halves the chain of roundings.
+  static constexpr bool kTwo = E == 4 && S::FN * S::FM == 1;
+  f32x16 odd;
 
   __device__ __forceinline__ void load(char *stage, int q) {
     if (q < StageN::kLoads) a.load(stage, q);
@@ -328,7 +332,7 @@ struct Product {
     }
     if (part == kSpread - 1) a.advance(), b.advance();
   }
-  __device__ __forceinline__ void mfma(int set, f32x16 (&acc)[S::FN][S::FM]) const {
+  __device__ __forceinline__ void mfma(int set, f32x16 (&acc)[S::FN][S::FM]) {
 #pragma unroll
     for (int v = 0; v < (E == 2 ? 1 : 4); ++v)
 #pragma unroll
@@ -338,6 +342,8 @@ struct Product {
           if constexpr (E == 2)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[set][i], fb[set][j], acc[i][j],
                                                                 0, 0, 0);
+          else if (kTwo && v % 2 == 1)
+            odd = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[set][i][v], fb[set][j][v], odd, 0, 0, 0);
           else
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[set][i][v], fb[set][j][v],
                                                              acc[i][j], 0, 0, 0);
@@ -399,6 +405,7 @@ struct Product {
   __device__ __forceinline__ void run_loose(int nk, char *const (&st)[kStages],
                                             f32x16 (&acc)[S::FN][S::FM]) {
     if (nk <= 0) return;
+    if constexpr (kTwo) odd = f32x16(0.f);
     const int whole_a = a.whole_steps(), whole_b = b.whole_steps();
     u32x4 va[2][StageN::kLoads], vb[2][StageM::kLoads];
     fetch(a, va[0], whole_a > 0), fetch(b, vb[0], whole_b > 0);
@@ -421,6 +428,7 @@ struct Product {
         __syncthreads();
       }
     }
+    if constexpr (kTwo) acc[0][0] += odd;
   }
   // acc += the product over nk steps, through the stages st (NS of them).  A wave
   // reads each fragment one round of MFMAs ahead; the loads of a step begin NS - 1
@@ -429,7 +437,9 @@ struct Product {
                                       f32x16 (&acc)[S::FN][S::FM]) {
     if (nk <= 0) return;
     start(nk, st);
+    if constexpr (kTwo) odd = f32x16(0.f);
     go_on(nk, st, acc);
+    if constexpr (kTwo) acc[0][0] += odd;
   }
   // Its first loads, of the first NS steps (few steps: every stage at once, nothing
   // spread),
