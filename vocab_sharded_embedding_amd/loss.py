@@ -270,14 +270,15 @@ def vpe_grad_sumsq(tensors: Sequence, sumsq=None, workspace=None):
     return sumsq
 
 
-def _refuse_overlaps(table, out_at, others) -> None:
-    """Refuse an output (at out_at, as large as its tensor) that shares bytes with
-    another one, with `others`, or with a tensor other than being the whole of its
-    own."""
+def _refuse_overlaps(table, out_at, sumsq, norm) -> None:
+    """Refuse an output (at out_at, as large as its tensor; or `norm`) that shares
+    bytes with another one, with `sumsq`, or with a tensor other than being the whole
+    of its own."""
     spans = [(o, o + n, True) for o, n in zip(out_at, table.bytes)]
     if out_at is not table.at:
         spans += [(t, t + n, False) for t, o, n in zip(table.at, out_at, table.bytes) if t != o]
-    spans += [(t.data_ptr(), t.data_ptr() + nbytes(t), False) for t in others]
+    spans += [(t.data_ptr(), t.data_ptr() + nbytes(t), False) for t in sumsq]
+    spans.append((norm.data_ptr(), norm.data_ptr() + 4, True))
     spans.sort()
     # in order of their first bytes: the furthest end of what came before, of the
     # outputs alone and of everything
@@ -287,7 +288,7 @@ def _refuse_overlaps(table, out_at, others) -> None:
             continue
         if begin < written or (is_out and begin < read):
             raise ValueError("an output of vpe_grad_clip must be its own tensor, or apart from "
-                             "the call's other tensors")
+                             "the call's other tensors, and norm apart from all of them")
         read = max(read, end)
         if is_out:
             written = max(written, end)
@@ -309,11 +310,8 @@ def vpe_grad_clip(tensors: Sequence, sumsq: Sequence, max_norm: float,
     table = _Table(tensors)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=tensors[0].device)
-        others = sumsq
     else:
         float_rows("norm", norm, 1)
-        apart("norm", norm, *sumsq)
-        others = (*sumsq, norm)
     out_at, targets = table.at, table.args[0]
     if out is not None:
         out = list(out)
@@ -325,7 +323,7 @@ def vpe_grad_clip(tensors: Sequence, sumsq: Sequence, max_norm: float,
         placed("gradient" + " out" * len(out), tensors[0], *out)
         out_at = [o.data_ptr() for o in out]
         targets = (ctypes.c_void_p * table.n)(*out_at)
-    _refuse_overlaps(table, out_at, others)
+    _refuse_overlaps(table, out_at, sumsq, norm)
     n = len(sumsq)
     placed("gradient norm" + " sumsq" * n, tensors[0], norm, *sumsq)
     enqueue("vpe_grad_clip", table.index, *table.args, targets,
