@@ -1047,13 +1047,6 @@ static_assert(256 * kLossMaxStride * 2 <= kLoadMask && 128 * kLossMaxStride * 4 
 static_assert(SmallF::BN == loss_tile_rows(0) && Medium::BN == loss_tile_rows(1),
               "the workspace holds a pair per tile");
 
-// Whether the bf16 logits of m rows and `rows` of the table take 256 x 256 tiles: with
-// two for every CU.  (Loss of 600 rows against 151936 x 1024: 201 us, 231 with 128 x
-// 128; of 4000 rows against 5000 x 1024: 71 us, 65 with 128 x 128.)
-bool large_logits(int64_t m, int64_t rows) {
-  return m > 128 && blocks(rows, 256) * static_cast<int64_t>(blocks(m, 256)) >= 512;
-}
-
 // Width of the tiles that `pick_logits` takes, as the loss counts its pairs.
 int64_t logits_tile_rows(int64_t m, int64_t rows, int dtype, bool loose) {
   if (dtype == 1) return !loose && large_logits(m, rows) ? Large::BN : Medium::BN;
@@ -1112,15 +1105,6 @@ int64_t splits_for(int64_t rows, int64_t dim, int64_t cols, int64_t bn, int64_t 
   return loss_max(1, loss_min(s, most));
 }
 
-// Whether the bf16 products take 256 x 256 tiles: where at least three quarters of
-// their rows and more than half of their columns exist.  (The head's backward of 256
-// rows against 75968 x 1024: 114 us, 136 with 128 x 128; the gradients of 257 rows
-// against 50257 x 999: 110 us, 91 with 128 x 128; of 4000 rows against 151936 x 128:
-// 1330 us, 1220 with 128 x 128.)
-bool large_tiles(int64_t rows, int64_t dim) {
-  return rows > 128 && rows * 4 >= loss_up(rows, 256) * 3 && dim > 128;
-}
-
 // Whether the fp32 products take 64 x 64 tiles: both in one launch by the table's, the
 // larger one.  (Gradients of 771 rows against 8308 x 1024: 338 us, 403 with the hidden
 // rows' in a launch of 64 x 64 of its own.)
@@ -1150,7 +1134,7 @@ void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t s
     return;
   }
   if constexpr (!LOOSE) {
-    if (large_tiles(a.rows, a.dim)) {
+    if (large_products(a.rows, a.dim)) {
       if (gx && gw) run_products<Large, true, 3, false>(a, st);
       else if (gx) run_products<Large, true, 1, false>(a, st);
       else run_products<Large, true, 2, false>(a, st);
@@ -1170,7 +1154,7 @@ void pick_products(const Products &a, int dtype, bool gx, bool gw, hipStream_t s
 int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, bool loose, bool gw,
                     int64_t most) {
   const int64_t side = rows <= 32 ? 32 : (rows <= 64 && dtype == 1) ? 64 : 128;
-  if (dtype == 1 && !loose && large_tiles(rows, dim))
+  if (dtype == 1 && !loose && large_products(rows, dim))
     return splits_for(rows, dim, cols, 256, 256, 256, most);
   const int64_t s = splits_for(rows, dim, cols, 128, side, 512, most);
   if (dtype == 1 || rows <= 32 || !small_products(rows, dim, cols, s, gw)) return s;
@@ -1281,11 +1265,7 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   const bool w_in_place = loads_in_place(r.w, r.dim, r.dtype);
   const bool loose = !w_in_place && loose_rows(kLossGrad, r.m, r.rows, r.dim);
   const bool copied = !w_in_place && !loose;
-  // columns of a piece: what the buffer holds, in pieces of one size
-  int64_t most = loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride);
-  if (copied) most = loss_min(most, l.table_rows);
-  const int64_t pieces = (r.rows + most - 1) / most;
-  const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
+  const int64_t step = grad_piece(l, r.m, r.rows, r.dtype, copied);
   Logits a{};
   a.x = at(workspace, l.x), a.ldx = a.x_dim = l.dim_pad, a.k = r.dim;
   a.count = reinterpret_cast<const int32_t *>(at(workspace, l.count));
@@ -1319,7 +1299,7 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   };
   // (a copied table leaves no second copy to read beside the products of the first)
   const bool together =
-      r.dtype == 1 && w_in_place && large_tiles(r.m, r.dim) && g.gx && g.gw;
+      r.dtype == 1 && w_in_place && large_products(r.m, r.dim) && g.gx && g.gw;
   for (int64_t row = 0; row < r.rows; row += step) {
     if (!together || row == 0) {
       piece_logits(row);

@@ -100,6 +100,32 @@ inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t sha
   return l;
 }
 
+// Columns of a piece of the logits' gradient: what its buffer (`copied`: and that of the
+// copied table) holds, in pieces of one size.
+inline int64_t grad_piece(const LossLayout &l, int64_t m, int64_t rows, int dtype, bool copied) {
+  const int64_t e = dtype == 1 ? 2 : 4;
+  int64_t most = loss_min(l.piece_cap / (m * e) / 256 * 256, kLossMaxStride);
+  if (copied) most = loss_min(most, l.table_rows);
+  const int64_t pieces = (rows + most - 1) / most;
+  return loss_min(most, loss_up((rows + pieces - 1) / pieces, 256));
+}
+
+// Whether the bf16 logits of m rows and `rows` of the table take 256 x 256 tiles: with
+// two for every CU.  (Loss of 600 rows against 151936 x 1024: 201 us, 231 with 128 x
+// 128; of 4000 rows against 5000 x 1024: 71 us, 65 with 128 x 128.)
+constexpr bool large_logits(int64_t m, int64_t rows) {
+  return m > 128 && loss_up(rows, 256) / 256 * (loss_up(m, 256) / 256) >= 512;
+}
+
+// Whether the bf16 products take 256 x 256 tiles: where at least three quarters of
+// their rows and more than half of their columns exist.  (The head's backward of 256
+// rows against 75968 x 1024: 114 us, 136 with 128 x 128; the gradients of 257 rows
+// against 50257 x 999: 110 us, 91 with 128 x 128; of 4000 rows against 151936 x 128:
+// 1330 us, 1220 with 128 x 128.)
+constexpr bool large_products(int64_t rows, int64_t dim) {
+  return rows > 128 && rows * 4 >= loss_up(rows, 256) * 3 && dim > 128;
+}
+
 struct LossRows {  // hidden rows and their targets
   const void *x;
   int64_t m, dim;
