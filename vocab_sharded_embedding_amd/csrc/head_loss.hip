@@ -492,12 +492,14 @@ __device__ __forceinline__ void logits_done(const Logits &a, int tn, int64_t n0,
         const int64_t rel = t < 0 ? -1 : t - a.row0 - nb;
         at = rel >= 0 && rel < lim ? static_cast<int>(rel) : -1;
       }
-      const float shift = -lse * kLog2e;
+      // (the difference first: one fma with a rounded -lse log2(e) would put that rounding
+      // into every entry of the row, as large as lse, and be NaN or 0 for a finite lse
+      // past 2.3e38)
 #pragma unroll
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          acc[i][j][r] = BF16 ? __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], kLog2e, shift))
+          acc[i][j][r] = BF16 ? __builtin_amdgcn_exp2f((acc[i][j][r] - lse) * kLog2e)
                               : exp_of(acc[i][j][r], lse);
       if (__any(at >= 0)) {
 #pragma unroll
