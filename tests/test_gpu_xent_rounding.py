@@ -55,6 +55,57 @@ def test_entries_of_the_gradient(m, vocab, level, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("level", [0.0, -355.9, 355.9, 711.0, 5000.0])
+@pytest.mark.parametrize("m,vocab", SIZES)
+def test_sums_of_the_loss(m, vocab, level, dtype):
+    """The log-sum-exp is its row's maximum, exact, and a logarithm added to it with one
+    rounding.  The logarithm's argument is a sum of exponentials of differences: each
+    off by U (3 |z - max| + 4) of itself, which is at most 4 U on the sum (x exp(-x) <=
+    0.37), n terms added with at most 64 + 16 roundings one behind another in a tile and
+    log2(n) + 24 in the joins, each of them with a factor's 4 U."""
+    w, t, z = _logits(m, vocab, dtype, level, m)
+    want = torch.logsumexp(z, 1)
+    got, at = vpe.vpe_lmhead_xent(_identity(m, dtype), w, t, 0, vocab)
+    assert torch.equal(at.double(), z[torch.arange(m, device="cuda"), t])
+    bound = U * want.abs() + 200 * U + 2 * U * (want - z.max(1).values)
+    assert_within(got, want, bound, "shard_lse")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m,vocab", SIZES)
+def test_logits_next_to_the_largest_float(m, vocab, dtype):
+    """Finite logits whose product with log2(e) is not: 3e38, and all of a row's at
+    -3e38 but one."""
+    w, t, _ = _logits(m, vocab, dtype, 0.0, m)
+    row = torch.arange(m, device="cuda")
+    big = torch.tensor(3e38, device="cuda").to(dtype).float()
+    w[t[::2], row[::2]] = big.to(dtype)
+    if m > 1:
+        w[:, 1] = -big.to(dtype)
+    z = w[:, :m].T.double().contiguous()
+    x = _identity(m, dtype)
+    a, b = vpe.vpe_lmhead_xent(x, w, t, 0, vocab)
+    loss, lse = vpe.vpe_xent_loss([a], [b], t, vocab)
+    assert (lse[::2] == big).all() and (loss[::2] == 0).all()
+    if m > 1:  # (log of vocab is far below a rounding)
+        assert lse[1] == -big and loss[1] == 0
+    rest = torch.arange(m, device="cuda")[3::2]
+    want = torch.logsumexp(z[rest], 1)
+    assert ((lse[rest].double() - want).abs() <= U * want.abs() + 200 * U).all()
+    gl = torch.ones(m, device="cuda")
+    _, gw = vpe.vpe_lmhead_xent_grad(x, w, t, lse, gl, 0, vocab, weight_dtype=F32)
+    d = gw[:, :m].T
+    assert (d[::2] == 0).all()
+    if m > 1:  # every difference is 0
+        one = torch.zeros(vocab, device="cuda")
+        one[t[1]] = 1
+        assert torch.equal(d[1], 1 - one)
+    p = torch.exp(z[rest] - lse[rest].double()[:, None])
+    p[torch.arange(rest.numel(), device="cuda"), t[rest]] -= 1
+    assert ((d[rest].double() - p).abs() <= (HALF[dtype] + 100 * U) * p.abs() + 100 * U).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_infinite_sums_follow_the_formula(dtype):
     """A log-sum-exp of +inf leaves exponentials of 0, one of -inf those of +inf, and
     neither touches another row."""

@@ -439,15 +439,15 @@ __device__ __forceinline__ void logits_done(const Logits &a, int tn, int64_t n0,
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
-      const float base = top == -__builtin_huge_valf() ? 0.f : top, shift = -base * kLog2e;
+      const float base = top == -__builtin_huge_valf() ? 0.f : top;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < S::FN; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          // (fp32: the difference first; `shift` rounds every term alike)
-          s += __builtin_amdgcn_exp2f(BF16 ? fmaf(acc[i][j][r], kLog2e, shift)
-                                           : (acc[i][j][r] - base) * kLog2e);
+          // (the difference first: a rounded shift of base log2(e) would be in every term,
+          // and infinite for a finite base past 2.3e38)
+          s += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * kLog2e);
       if (s != s) top = s;  // a NaN logit, or +inf
       merge(top, s, __shfl_xor(top, 32), __shfl_xor(s, 32));
       if (hi == 0) {
