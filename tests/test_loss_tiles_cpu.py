@@ -59,3 +59,10 @@ def test_large_logits_and_pieces_are_reached():
     # the steady loop of a sum has more than four steps of 64
     assert max(d for _, _, d in PIECES) > 512 and max(d for _, _, d in ONE_PIECE) > 512
     assert max(LIVE) == PIECES[0][0]
+
+
+def test_the_join_of_sums_fits_a_grid():
+    """Fewer than 2^32 work-items at every accepted size."""
+    sizes = [(m, 1, dim) for m in (1, 4096, 1 << 20, 1 << 21) for dim in (1, 4100, 16384, 1 << 16)]
+    groups = _each(sizes, "finish_groups(m, dim)")
+    assert all(0 < n and n * 256 < 1 << 32 for n in groups)

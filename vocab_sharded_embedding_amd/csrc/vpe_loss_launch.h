@@ -100,6 +100,12 @@ inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t sha
   return l;
 }
 
+// Workgroups of 256 that join the sums of [m, dim], four values a thread at a time: some
+// hundred for every CU, and never more than a grid holds.
+constexpr int64_t finish_groups(int64_t m, int64_t dim) {
+  return loss_min((m * ((dim + 3) / 4) + 255) / 256, int64_t(1) << 16);
+}
+
 // Columns of a piece of the logits' gradient: what its buffer (`copied`: and that of the
 // copied table) holds, in pieces of one size.
 inline int64_t grad_piece(const LossLayout &l, int64_t m, int64_t rows, int dtype, bool copied) {
