@@ -8,6 +8,60 @@ from _loss import HALF, U, assert_within
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
+MOST = (1 << 31) - 1
+
+
+def test_the_largest_table_is_cleared():
+    """2^31 - 1 rows of one value: 2^24 tiles of 128 rows."""
+    w = torch.zeros(MOST, 1, device="cuda", dtype=BF16)
+    gw = torch.full_like(w, 7.0)
+    x = torch.empty(0, 1, device="cuda", dtype=BF16)
+    none = torch.empty(0, device="cuda")
+    ids = torch.empty(0, device="cuda", dtype=torch.int64)
+    vpe.vpe_lmhead_xent_grad(x, w, ids, none, none, 0, MOST, grad_weight=gw)
+    assert not gw.any()
+
+
+def test_the_loss_of_the_largest_table():
+    """In pieces, whose last one is ragged.  A tile's sum and 2^14 pairs joined one after
+    another: (64 + 2^14 4) U at most."""
+    w = torch.empty(MOST, 1, device="cuda", dtype=BF16)
+    for c in w.split(1 << 28):
+        c.copy_(torch.randn(c.shape, device="cuda"))
+    x = torch.tensor([[1.0], [-0.5]], device="cuda", dtype=BF16)
+    w[MOST - 1], w[12345] = 9.0, 11.0
+    t = torch.tensor([MOST - 1, 12345], device="cuda")
+    lse, at = vpe.vpe_lmhead_xent(x, w, t, 0, MOST)
+    want = torch.zeros(2, dtype=torch.float64, device="cuda")
+    for c in w.split(1 << 26):
+        want += torch.exp(x.double() * c.double().T).sum(1)
+    assert (lse.double() - want.log()).abs().max() <= (64 + 4 * 2 ** 14) * U
+    assert at.tolist() == [9.0, -5.5]
+
+
+@pytest.mark.parametrize("dtype,vocab,dim", [(F32, 16500, 8), (BF16, 16500, 8)],
+                         ids=["f32", "bf16"])
+def test_the_most_rows(dtype, vocab, dim):
+    """2^21 rows against 16500: 2^35 logits, in three pieces of the table."""
+    m = 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(m, dim, generator=g, device="cuda").to(dtype)
+    w = torch.randn(vocab, dim, generator=g, device="cuda").to(dtype)
+    t = torch.randint(0, vocab, (m,), generator=g, device="cuda", dtype=torch.int32)
+    t[::17] = -1
+    a, b = vpe.vpe_lmhead_xent(x, w, t, 0, vocab)
+    loss, lse = vpe.vpe_xent_loss([a], [b], t, vocab)
+    assert (loss[::17] == 0).all() and (lse[::17] == 0).all()
+    pick = torch.cat([torch.arange(300, device="cuda"), torch.arange(m - 300, m, device="cuda"),
+                      torch.randint(0, m, (3000,), generator=g, device="cuda")])
+    pick = pick[t[pick] >= 0]
+    z = x[pick].double() @ w.double().T
+    size = (x[pick].double().abs() @ w.double().abs().T).max(1).values
+    want = torch.logsumexp(z, 1)
+    bound = (dim + 2) * U * size + 400 * U + 4 * U * want.abs()
+    assert_within(lse[pick], want, bound, "lse")
+    zt = torch.gather(z, 1, t[pick].long()[:, None])[:, 0]
+    assert_within(loss[pick], want - zt, 2 * bound + 4 * U * zt.abs(), "loss")
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])

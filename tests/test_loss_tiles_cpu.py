@@ -66,3 +66,67 @@ def test_the_join_of_sums_fits_a_grid():
     sizes = [(m, 1, dim) for m in (1, 4096, 1 << 20, 1 << 21) for dim in (1, 4100, 16384, 1 << 16)]
     groups = _each(sizes, "finish_groups(m, dim)")
     assert all(0 < n and n * 256 < 1 << 32 for n in groups)
+
+
+def test_launches_fit_a_grid():
+    """At every accepted size a launch has fewer than 2^32 work-items, and its pieces are
+    whole tiles that cover the table and fit their buffers."""
+    out = _run("""
+  const int64_t sides[] = {1, 3, 33, 64, 65, 200, 1000, 8191, 8192, 1 << 16, (1 << 16) + 1, 1 << 20,
+                           (1 << 21) - 63, 1 << 21};
+  const int64_t tables[] = {1, 255, 257, 50257, 151936, (1 << 21) + 1, (1 << 24) + 5,
+                            (int64_t(1) << 30) + 7, (int64_t(1) << 31) - 1};
+  const int64_t limit = int64_t(1) << 32;
+  auto tiles = [](int64_t n, int64_t m, int64_t bn, int64_t bm) {
+    return loss_up(n, bn) / bn * (loss_up(m, bm) / bm);
+  };
+  long bad = 0, cases = 0;
+  auto check = [&](bool ok, const char *what, int64_t m, int64_t dim, int64_t rows) {
+    ++cases;
+    if (!ok && bad++ < 20)
+      printf("%s:%lld:%lld:%lld\\n", what, (long long)m, (long long)dim, (long long)rows);
+  };
+  for (int64_t m : sides)
+    for (int64_t dim : sides)
+      for (int64_t rows : tables) {
+        if (dim > 1 << 16 || rows > (int64_t(1) << 39) / dim || rows > (int64_t(1) << 42) / m)
+          continue;
+        check(launch_rows(dim) >= 256 && launch_rows(dim) % 256 == 0, "rows", m, dim, rows);
+        check(tiles(launch_rows(dim), dim, 64, 64) * 512 < limit, "zeros", m, dim, rows);
+        for (int dt = 0; dt < 2; ++dt)
+          for (int copied = 0; copied < 2; ++copied) {
+            const int64_t e = dt ? 2 : 4;
+            LossLayout l = loss_layout(kLossForward, m, dim, rows, dt);
+            int64_t step = loss_piece(l, m, rows, copied);
+            check(step >= loss_min(rows, 256) && (step >= rows || step % 256 == 0), "loss piece", m,
+                  dim, rows);
+            check((tiles(step, m, 64, 64) + 128) * 512 < limit, "loss", m, dim, rows);
+            check(!copied || step <= l.table_rows, "loss copy", m, dim, rows);
+            for (int call = 0; call < 4; ++call) {
+              const bool given = call > 0, d_copied = call & 1;
+              l = loss_layout(given ? kHeadGrad : kLossGrad, m, dim, rows, dt);
+              step = given ? head_grad_piece(l, m, rows, dt, d_copied, copied)
+                           : grad_piece(l, m, rows, dt, copied);
+              check(step >= 256 && step % 256 == 0, "piece", m, dim, rows);
+              check(!copied || step <= l.table_rows, "copy", m, dim, rows);
+              check((given && !d_copied) || m * loss_min(step, loss_up(rows, 64)) * e <= l.piece_cap,
+                    "buffer", m, dim, rows);
+              const int64_t logits = given ? 0 : tiles(step, m, 64, 32);
+              for (int gw = 0; gw < 2; ++gw) {
+                // the tiles that the products take, and most splits for them
+                const int64_t most = loss_most_splits(m, l.dim_pad, rows);
+                const bool large = dt && large_products(m, dim);
+                const bool small = !dt && small_products(m, dim, step, most, gw);
+                const int64_t b = large ? 256 : small ? 64 : 128;
+                const int64_t bm = m <= 32 ? 32 : dt && m <= 64 ? 64 : b;
+                const int64_t groups = tiles(dim, m, b, bm) * most + (gw ? tiles(dim, step, b, b) : 0);
+                check((groups + (large ? logits : 0)) * (large ? 512 : 256) < limit, "products", m,
+                      dim, rows);
+              }
+              check((logits + 128) * 512 < limit, "logits", m, dim, rows);
+            }
+          }
+      }
+  printf("%ld %s\\n", cases, bad ? "bad" : "good");
+""")
+    assert out[-1] == "good" and int(out[-2]) > 10000, out

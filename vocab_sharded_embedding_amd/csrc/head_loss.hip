@@ -1037,15 +1037,6 @@ void run_logits(Logits a, int64_t m, hipStream_t st) {
   hipLaunchKernelGGL((logits_tiles<S, BF16, GRAD, LOOSE>), dim3(n), dim3(S::NT), 0, st, a);
 }
 
-// fp32 products of n x m (`splits` times) that take tiles of 64 x 64: with too few of
-// 128 x 128 to fill the chip, or where those cover over 1/16 more.  (Forward and
-// gradients of 512 x 32000 x 512: 597 us, 626 with 64 x 64; gradients of 300 x 8000 x
-// 256: 69 us, 55 with 64 x 64; of 100 x 151936 x 64: 171 us, 102 with 64 x 64.)
-bool small_tiles(int64_t n, int64_t m, int64_t splits = 1) {
-  const int64_t area = loss_up(n, 128) * loss_up(m, 128);
-  return area / (128 * 128) * splits < 256 || area / 17 > loss_up(n, 64) * loss_up(m, 64) / 16;
-}
-
 static_assert(256 * kLossMaxStride * 2 <= kLoadMask && 128 * kLossMaxStride * 4 <= kLoadMask,
               "a tile's rows lie before the masked loads");
 static_assert(SmallF::BN == loss_tile_rows(0) && Medium::BN == loss_tile_rows(1),
@@ -1107,13 +1098,6 @@ int64_t splits_for(int64_t rows, int64_t dim, int64_t cols, int64_t bn, int64_t 
   int64_t s = want / tiles;
   s = loss_min(s, (cols + kLossSplitRows - 1) / kLossSplitRows);
   return loss_max(1, loss_min(s, most));
-}
-
-// Whether the fp32 products take 64 x 64 tiles: both in one launch by the table's, the
-// larger one.  (Gradients of 771 rows against 8308 x 1024: 338 us, 403 with the hidden
-// rows' in a launch of 64 x 64 of its own.)
-bool small_products(int64_t rows, int64_t dim, int64_t cols, int64_t splits, bool gw) {
-  return gw ? small_tiles(dim, cols) : small_tiles(dim, rows, splits);
 }
 
 // The two products of a piece.  `splits` is fixed for all pieces of a call.
@@ -1180,12 +1164,18 @@ void run_finish(const Products &a, const LossRows &r, const LossGrads &g, const 
 // The gradients of an empty batch: zeros.
 int zero_table(const LossRows &r, const LossGrads &g, hipStream_t st) {
   if (g.gw == nullptr || g.accumulate) return 0;
-  Products a{};
-  a.dim = r.dim, a.cols = r.rows, a.gw = g.gw, a.gw_bf16 = g.gwt == 1;
-  // (no rows: no operand is read)
-  if (r.dtype == 1) run_products<Medium, true, 2, false>(a, st);
-  else run_products<MediumF, false, 2, false>(a, st);
-  return last_error();
+  const int64_t step = launch_rows(r.dim);
+  for (int64_t row = 0; row < r.rows; row += step) {
+    Products a{};
+    a.dim = r.dim, a.cols = loss_min(step, r.rows - row), a.gw_bf16 = g.gwt == 1;
+    a.gw = static_cast<char *>(g.gw) + row * r.dim * (a.gw_bf16 ? 2 : 4);
+    // (no rows: no operand is read)
+    if (r.dtype == 1) run_products<Medium, true, 2, false>(a, st);
+    else run_products<MediumF, false, 2, false>(a, st);
+    const int rc = last_error();
+    if (rc != 0) return rc;
+  }
+  return 0;
 }
 
 }  // namespace
@@ -1215,7 +1205,7 @@ int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit,
   a.pairs = reinterpret_cast<float *>(at(workspace, l.pairs)), a.pair_ld = r.m;
   a.target_logit = target_logit;
   const int64_t tile_rows = logits_tile_rows(r.m, r.rows, r.dtype, loose);
-  const int64_t step = w_in_place || loose ? r.rows : l.table_rows;  // (whole tiles)
+  const int64_t step = loss_piece(l, r.m, r.rows, !w_in_place && !loose);  // (whole tiles)
   for (int64_t row = 0; row < r.rows; row += step) {
     const char *w = static_cast<const char *>(r.w) + row * r.dim * e;
     a.w_rows = loss_min(step, r.rows - row), a.row0 = row, a.tile0 = row / tile_rows;
@@ -1344,11 +1334,7 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
   const bool loose =
       (d_copied || w_copied) && loose_rows(kHeadGrad, r.m, r.rows, loss_max(ld, r.dim));
   if (loose) d_copied = w_copied = x_copied = false;
-  int64_t most = r.rows;
-  if (d_copied) most = loss_min(most, loss_min(l.piece_cap / (r.m * e) / 256 * 256, kLossMaxStride));
-  if (w_copied) most = loss_min(most, l.table_rows);
-  const int64_t pieces = (r.rows + most - 1) / most;
-  const int64_t step = loss_min(most, loss_up((r.rows + pieces - 1) / pieces, 256));
+  const int64_t step = head_grad_piece(l, r.m, r.rows, r.dtype, d_copied, w_copied);
   Products p{};
   p.rows = r.m, p.dim = r.dim;
   p.sums = reinterpret_cast<float *>(at(workspace, l.sums)), p.ld_sums = l.dim_pad;

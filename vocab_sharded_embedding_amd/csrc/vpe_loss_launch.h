@@ -100,20 +100,69 @@ inline LossLayout loss_layout(LossCall call, int64_t m, int64_t dim, int64_t sha
   return l;
 }
 
+// Most workgroups of a launch over table rows and one other side, in tiles of 64 x 64 and
+// more: a grid holds fewer than 2^32 work-items, 512 or 256 a workgroup.  And how many
+// table rows that leaves one launch (of side 2^21: 8192; whole tiles of any width).
+constexpr int64_t kLossMaxGroups = int64_t(1) << 22;
+constexpr int64_t launch_rows(int64_t side) {
+  return kLossMaxGroups / (loss_up(loss_max(side, 1), 64) / 64) * 64 / 256 * 256;
+}
+
 // Workgroups of 256 that join the sums of [m, dim], four values a thread at a time: some
 // hundred for every CU, and never more than a grid holds.
 constexpr int64_t finish_groups(int64_t m, int64_t dim) {
   return loss_min((m * ((dim + 3) / 4) + 255) / 256, int64_t(1) << 16);
 }
 
+// `rows` in pieces of at most `most`, a multiple of 256, as even as whole tiles allow.
+constexpr int64_t even_pieces(int64_t rows, int64_t most) {
+  return loss_min(most, loss_up((rows + (rows + most - 1) / most - 1) / ((rows + most - 1) / most),
+                                256));
+}
+
+// Table rows per launch of the loss (`copied`: as many as the copied table's buffer
+// holds).
+inline int64_t loss_piece(const LossLayout &l, int64_t m, int64_t rows, bool copied) {
+  return loss_min(loss_min(rows, copied ? l.table_rows : rows), launch_rows(m));
+}
+
 // Columns of a piece of the logits' gradient: what its buffer (`copied`: and that of the
-// copied table) holds, in pieces of one size.
+// copied table) holds.
 inline int64_t grad_piece(const LossLayout &l, int64_t m, int64_t rows, int dtype, bool copied) {
   const int64_t e = dtype == 1 ? 2 : 4;
   int64_t most = loss_min(l.piece_cap / (m * e) / 256 * 256, kLossMaxStride);
+  most = loss_min(most, launch_rows(l.dim_pad));
   if (copied) most = loss_min(most, l.table_rows);
-  const int64_t pieces = (rows + most - 1) / most;
-  return loss_min(most, loss_up((rows + pieces - 1) / pieces, 256));
+  return even_pieces(rows, most);
+}
+
+// The same of a given gradient: all of it, where nothing is copied.
+inline int64_t head_grad_piece(const LossLayout &l, int64_t m, int64_t rows, int dtype,
+                               bool d_copied, bool w_copied) {
+  const int64_t e = dtype == 1 ? 2 : 4;
+  int64_t most = loss_min(loss_up(rows, 256), launch_rows(l.dim_pad));
+  if (d_copied)
+    most = loss_min(most, loss_min(l.piece_cap / (m * e) / 256 * 256, kLossMaxStride));
+  if (w_copied) most = loss_min(most, l.table_rows);
+  return even_pieces(rows, most);
+}
+
+// fp32 products of n x m (`splits` times) that take tiles of 64 x 64: with too few of
+// 128 x 128 to fill the chip, or where those cover over 1/16 more.  (Forward and
+// gradients of 512 x 32000 x 512: 597 us, 626 with 64 x 64; gradients of 300 x 8000 x
+// 256: 69 us, 55 with 64 x 64; of 100 x 151936 x 64: 171 us, 102 with 64 x 64.)
+constexpr bool small_tiles(int64_t n, int64_t m, int64_t splits = 1) {
+  return loss_up(n, 128) * loss_up(m, 128) / (128 * 128) * splits < 256 ||
+         loss_up(n, 128) * loss_up(m, 128) / 17 > loss_up(n, 64) * loss_up(m, 64) / 16;
+}
+
+// Whether the fp32 products take 64 x 64 tiles: both in one launch by the table's, the
+// larger one.  (Gradients of 771 rows against 8308 x 1024: 338 us, 403 with the hidden
+// rows' in a launch of 64 x 64 of its own.)  Not where the hidden rows' alone would be
+// too many for a launch.
+constexpr bool small_products(int64_t rows, int64_t dim, int64_t cols, int64_t splits, bool gw) {
+  return (gw ? small_tiles(dim, cols) : small_tiles(dim, rows, splits)) &&
+         loss_up(rows, 64) / 64 * (loss_up(dim, 64) / 64) * splits <= kLossMaxGroups;
 }
 
 // Whether the bf16 logits of m rows and `rows` of the table take 256 x 256 tiles: with
