@@ -176,3 +176,32 @@ def test_pieces_captured_and_replayed():
         calls(*fresh[:3], new_lse, fresh[3], new_d, eager, torch.empty_like(ws))
         for i, (a, b) in enumerate(zip(out, eager)):
             assert torch.equal(a, b), (turn, i)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shift", ["width", "table", "rows"])
+@pytest.mark.parametrize("m", [20, 60, 128, 200, 300])
+def test_one_gradient_of_unaligned_rows(m, shift, dtype):
+    """The operand that a lone gradient does not read may lie at any element."""
+    rows, dim = 2000, 129 if shift == "width" else 136
+    g = torch.Generator(device="cuda").manual_seed(m)
+
+    def at(first, *shape):
+        n = shape[0] * shape[1]
+        whole = torch.full((n + 16,), float("nan"), device="cuda", dtype=dtype)
+        whole[first:first + n] = torch.randn(n, generator=g, device="cuda").to(dtype)
+        return whole[first:first + n].view(shape)
+
+    d = at(0, m, rows)
+    w, x = at(1 if shift == "table" else 0, rows, dim), at(3 if shift == "rows" else 0, m, dim)
+    dd = d.double()
+    rx, ex, rw, ew = products(dd, torch.zeros_like(dd), x.double(), w.double(), dtype, dtype)
+    gx, _ = vpe.vpe_lmhead_grad(d, x, w, with_weight=False)
+    assert_within(gx, rx, ex, "grad_x alone")
+    _, gw = vpe.vpe_lmhead_grad(d, x, w, with_x=False)
+    assert_within(gw, rw, ew, "grad_weight alone")
+    # an operand that is not read takes no part, whatever it holds and wherever it lies
+    same, _ = vpe.vpe_lmhead_grad(d, torch.full_like(x, float("nan")), w, with_weight=False)
+    assert torch.equal(same, gx)
+    _, same = vpe.vpe_lmhead_grad(d, x, torch.full_like(w, float("nan")), with_x=False)
+    assert torch.equal(same, gw)

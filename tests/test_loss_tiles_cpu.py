@@ -130,3 +130,34 @@ def test_launches_fit_a_grid():
   printf("%ld %s\\n", cases, bad ? "bad" : "good");
 """)
     assert out[-1] == "good" and int(out[-2]) > 10000, out
+
+
+def test_the_heads_backward_prepares_what_it_reads():
+    """An unaligned table is neither copied nor a reason for another path where grad_x is
+    not wanted, nor hidden rows where grad_weight is not."""
+    out = _run("""
+  const auto *even = reinterpret_cast<const char *>(uintptr_t(0x10000)), *odd = even + 4;
+  void *out = reinterpret_cast<void *>(uintptr_t(0x20000));
+  const auto rows = [&](const char *d, const char *w, const char *x, int64_t m, void *gx, void *gw) {
+    const HeadGradRows h = head_grad_rows(
+        d, 2000, LossRows{x, m, 136, w, 2000, 1, 0, 2000, nullptr, 0}, LossGrads{gx, 1, gw, 1, false});
+    printf("%d%d%d%d\\n", h.d_copied, h.w_copied, h.x_copied, h.loose);
+  };
+  const int64_t sizes[] = {128, 300};
+  for (int64_t m : sizes) {
+    rows(even, even, even, m, out, out);
+    rows(even, odd, even, m, out, out);
+    rows(even, odd, even, m, out, nullptr);
+    rows(even, odd, even, m, nullptr, out);
+    rows(even, even, odd, m, out, out);
+    rows(even, even, odd, m, nullptr, out);
+    rows(even, even, odd, m, out, nullptr);
+    rows(odd, odd, odd, m, out, out);
+    rows(odd, odd, odd, m, nullptr, out);
+    rows(odd, odd, odd, m, out, nullptr);
+  }
+""")
+    assert out[:10] == ["0000", "0001", "0001", "0000", "0010", "0010", "0000", "0001", "0001",
+                        "0001"]
+    assert out[10:] == ["0000", "0100", "0100", "0000", "0010", "0010", "0000", "1110", "1010",
+                        "1100"]

@@ -991,24 +991,6 @@ int run_collect(const LossRows &r, const LossLayout &l, const float *lse, const 
 // whatever it holds.
 constexpr int64_t kWholeRows = 256;
 
-// Rows that the tiles can read in place.
-bool loads_in_place(const void *p, int64_t ld, int dtype) {
-  return ld % (dtype == 1 ? 8 : 4) == 0 && ld <= kLossMaxStride &&
-         (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-}
-
-// Whether rows that cannot be read in place pass through registers, in tiles of at
-// most 128 x 128, rather than be copied first.  Against 50001 x 1001, loose and copied:
-// loss of 16 rows 26 and 60 us, of 257 81 and 89, of 1000 189 and 155; gradients of 128
-// rows 130 and 136 (against 50001 x 3001 306 and 417), of 257 259 and 183; the head's
-// backward of 128 rows 94 and 162, of 257 175 and 194, of 500 255 and 223.  Gradients
-// of 128 rows against 5001 x 3001, whose tiles leave CUs idle: 112 and 84.
-bool loose_rows(LossCall call, int64_t m, int64_t rows, int64_t ld) {
-  if (ld > kLossMaxStride) return false;
-  if (call == kLossGrad) return m <= 128 && blocks(rows, 128) >= 256;
-  return m <= (call == kLossForward ? 512 : 256);
-}
-
 void run_copy(const void *from, int64_t ld, int64_t rows, int64_t cols, void *to, int64_t ld_to,
               int dtype, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(loss_min((rows + 3) / 4, 4096)));
@@ -1325,15 +1307,7 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
   if (r.m == 0) return zero_table(r, g, st);
   const LossLayout l = loss_layout(kHeadGrad, r.m, r.dim, r.rows, r.dtype);
   const int64_t e = r.dtype == 1 ? 2 : 4;
-  // (d's rows have to end at whole 16 bytes too: what lies behind may be anything,
-  // a NaN as well)
-  bool d_copied = !loads_in_place(d, ld, r.dtype) || r.rows % (16 / e) != 0;
-  bool w_copied = !loads_in_place(r.w, r.dim, r.dtype);
-  bool x_copied = !loads_in_place(r.x, r.dim, r.dtype);
-  // (x alone is a small copy)
-  const bool loose =
-      (d_copied || w_copied) && loose_rows(kHeadGrad, r.m, r.rows, loss_max(ld, r.dim));
-  if (loose) d_copied = w_copied = x_copied = false;
+  const auto [d_copied, w_copied, x_copied, loose] = head_grad_rows(d, ld, r, g);
   const int64_t step = head_grad_piece(l, r.m, r.rows, r.dtype, d_copied, w_copied);
   Products p{};
   p.rows = r.m, p.dim = r.dim;

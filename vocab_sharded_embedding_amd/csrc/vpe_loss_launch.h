@@ -201,6 +201,43 @@ struct LossGrads {
   bool accumulate;
 };
 
+// Rows that the tiles can read in place.
+inline bool loads_in_place(const void *p, int64_t ld, int dtype) {
+  return ld % (dtype == 1 ? 8 : 4) == 0 && ld <= kLossMaxStride &&
+         (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
+// Whether rows that cannot be read in place pass through registers, in tiles of at
+// most 128 x 128, rather than be copied first.  Against 50001 x 1001, loose and copied:
+// loss of 16 rows 26 and 60 us, of 257 81 and 89, of 1000 189 and 155; gradients of 128
+// rows 130 and 136 (against 50001 x 3001 306 and 417), of 257 259 and 183; the head's
+// backward of 128 rows 94 and 162, of 257 175 and 194, of 500 255 and 223.  Gradients
+// of 128 rows against 5001 x 3001, whose tiles leave CUs idle: 112 and 84.
+constexpr bool loose_rows(LossCall call, int64_t m, int64_t rows, int64_t ld) {
+  if (ld > kLossMaxStride) return false;
+  if (call == kLossGrad) return m <= 128 && loss_up(rows, 128) / 128 >= 256;
+  return m <= (call == kLossForward ? 512 : 256);
+}
+
+// The operands of the head's backward that are copied to aligned rows first, or (`loose`)
+// all pass through registers: of those that a wanted gradient reads, which is the table
+// for grad_x and the hidden rows for grad_weight.
+struct HeadGradRows {
+  bool d_copied, w_copied, x_copied, loose;
+};
+inline HeadGradRows head_grad_rows(const void *d, int64_t ld, const LossRows &r,
+                                   const LossGrads &g) {
+  // (d's rows have to end at whole 16 bytes too: what lies behind may be anything,
+  // a NaN as well)
+  const bool d_apart = !loads_in_place(d, ld, r.dtype) || r.rows % (r.dtype == 1 ? 8 : 4) != 0;
+  const bool w_apart = g.gx != nullptr && !loads_in_place(r.w, r.dim, r.dtype);
+  const bool x_apart = g.gw != nullptr && !loads_in_place(r.x, r.dim, r.dtype);
+  // (x alone is a small copy)
+  if ((d_apart || w_apart) && loose_rows(kHeadGrad, r.m, r.rows, loss_max(ld, r.dim)))
+    return {false, false, false, true};
+  return {d_apart, w_apart, x_apart, false};
+}
+
 int launch_lmhead_xent(const LossRows &r, float *shard_lse, float *target_logit, void *workspace,
                        void *stream);
 int launch_xent_loss(const float *const *shard_lse, const float *const *target_logit, int n_parts,
