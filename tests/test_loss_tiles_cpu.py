@@ -17,7 +17,8 @@ def _run(body):
     """What a C++ program with `body` as its main, over the launchers' header, prints."""
     if shutil.which("g++") is None:
         pytest.skip("no host compiler")
-    src = f'#include <stdio.h>\n#include "{HEADER}"\nusing namespace vpe;\nint main() {{\n{body}\n}}\n'
+    src = (f'#include <stdio.h>\n#include "{HEADER}"\nusing namespace vpe;\n'
+           f'int main() {{\n{body}\n}}\n')
     with tempfile.TemporaryDirectory() as tmp:
         exe = os.path.join(tmp, "rules")
         r = subprocess.run(["g++", "-std=c++17", "-Wall", "-Wextra", "-x", "c++", "-", "-o", exe],
@@ -62,10 +63,14 @@ def test_large_logits_and_pieces_are_reached():
 
 
 def test_the_join_of_sums_fits_a_grid():
-    """Fewer than 2^32 work-items at every accepted size."""
+    """Fewer than 2^32 work-items, and 2^16 workgroups, along either dimension at every
+    accepted size."""
     sizes = [(m, 1, dim) for m in (1, 4096, 1 << 20, 1 << 21) for dim in (1, 4100, 16384, 1 << 16)]
-    groups = _each(sizes, "finish_groups(m, dim)")
-    assert all(0 < n and n * 256 < 1 << 32 for n in groups)
+    wide = _each(sizes, "loss_min(kFinishWidth, finish_groups(m, dim))")
+    rows = _each(sizes, "(finish_groups(m, dim) + kFinishWidth - 1) / kFinishWidth")
+    for (m, _, dim), x, y in zip(sizes, wide, rows):
+        assert 0 < x * 256 < 1 << 32 and 0 < y < 1 << 16
+        assert x * y * 256 * 4 >= m * dim and (y == 1 or x * (y - 1) * 256 * 4 < m * (dim + 3))
 
 
 def test_launches_fit_a_grid():
@@ -109,7 +114,8 @@ def test_launches_fit_a_grid():
                            : grad_piece(l, m, rows, dt, copied);
               check(step >= 256 && step % 256 == 0, "piece", m, dim, rows);
               check(!copied || step <= l.table_rows, "copy", m, dim, rows);
-              check((given && !d_copied) || m * loss_min(step, loss_up(rows, 64)) * e <= l.piece_cap,
+              check((given && !d_copied) ||
+                        m * loss_min(step, loss_up(rows, 64)) * e <= l.piece_cap,
                     "buffer", m, dim, rows);
               const int64_t logits = given ? 0 : tiles(step, m, 64, 32);
               for (int gw = 0; gw < 2; ++gw) {
@@ -119,7 +125,8 @@ def test_launches_fit_a_grid():
                 const bool small = !dt && small_products(m, dim, step, most, gw);
                 const int64_t b = large ? 256 : small ? 64 : 128;
                 const int64_t bm = m <= 32 ? 32 : dt && m <= 64 ? 64 : b;
-                const int64_t groups = tiles(dim, m, b, bm) * most + (gw ? tiles(dim, step, b, b) : 0);
+                const int64_t groups =
+                    tiles(dim, m, b, bm) * most + (gw ? tiles(dim, step, b, b) : 0);
                 check((groups + (large ? logits : 0)) * (large ? 512 : 256) < limit, "products", m,
                       dim, rows);
               }
@@ -138,9 +145,11 @@ def test_the_heads_backward_prepares_what_it_reads():
     out = _run("""
   const auto *even = reinterpret_cast<const char *>(uintptr_t(0x10000)), *odd = even + 4;
   void *out = reinterpret_cast<void *>(uintptr_t(0x20000));
-  const auto rows = [&](const char *d, const char *w, const char *x, int64_t m, void *gx, void *gw) {
+  const auto rows = [&](const char *d, const char *w, const char *x, int64_t m, void *gx,
+                        void *gw) {
     const HeadGradRows h = head_grad_rows(
-        d, 2000, LossRows{x, m, 136, w, 2000, 1, 0, 2000, nullptr, 0}, LossGrads{gx, 1, gw, 1, false});
+        d, 2000, LossRows{x, m, 136, w, 2000, 1, 0, 2000, nullptr, 0},
+        LossGrads{gx, 1, gw, 1, false});
     printf("%d%d%d%d\\n", h.d_copied, h.w_copied, h.x_copied, h.loose);
   };
   const int64_t sizes[] = {128, 300};

@@ -918,21 +918,21 @@ __global__ __launch_bounds__(256) void finish_grad_x(const float *__restrict__ s
                                                      const float *scale, int64_t m, int64_t dim,
                                                      void *gx) {
   const int64_t vecs = (dim + 3) / 4;
-  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < m * vecs;
-       at += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t i = at / vecs, n = (at - i * vecs) * 4;
-    const int64_t from = place != nullptr ? place[i] : i;
-    f32x4 v = f32x4(0.f);
-    if (from >= 0) {
-      const float *p = sums + from * ld_sums + n;
+  const int64_t group = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+  const int64_t at = group * 256 + threadIdx.x;
+  const int64_t i = at / vecs, n = (at - i * vecs) * 4;
+  if (i >= m) return;
+  const int64_t from = place != nullptr ? place[i] : i;
+  f32x4 v = f32x4(0.f);
+  if (from >= 0) {
+    const float *p = sums + from * ld_sums + n;
 #pragma unroll 8
-      for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * split_stride);
-      if (scale != nullptr) v *= *scale;
-    }
-    float e[4] = {v[0], v[1], v[2], v[3]};
-    char *row = static_cast<char *>(gx) + i * dim * (BF16 ? 2 : 4);
-    dev::store_vec_nt<BF16, 4>(row, n, dim, e);
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * split_stride);
+    if (scale != nullptr) v *= *scale;
   }
+  float e[4] = {v[0], v[1], v[2], v[3]};
+  char *row = static_cast<char *>(gx) + i * dim * (BF16 ? 2 : 4);
+  dev::store_vec_nt<BF16, 4>(row, n, dim, e);
 }
 
 // ---------------------------------------------------------------------------
@@ -1133,7 +1133,8 @@ int64_t pick_splits(int64_t rows, int64_t dim, int64_t cols, int dtype, bool loo
 
 void run_finish(const Products &a, const LossRows &r, const LossGrads &g, const int32_t *place,
                 hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(finish_groups(r.m, r.dim)));
+  const int64_t groups = finish_groups(r.m, r.dim), wide = loss_min(groups, kFinishWidth);
+  const dim3 grid(static_cast<unsigned>(wide), static_cast<unsigned>((groups + wide - 1) / wide));
   const int64_t stride = a.rows * a.ld_sums;
   if (g.gxt == 1)
     hipLaunchKernelGGL(finish_grad_x<true>, grid, dim3(256), 0, st, a.sums, a.ld_sums, stride,
