@@ -70,8 +70,8 @@ vpe_status vpe_lmhead_xent_workspace(int64_t m, int64_t dim, int64_t shard_rows,
  * m == 0 is a no-op.
  * Errors: VPE_ERR_NULL, VPE_ERR_DTYPE, VPE_ERR_ALIGN, VPE_ERR_SHAPE (m < 0 or
  * > VPE_MAX_LOSS_ROWS, dim < 1 or > VPE_MAX_LOSS_DIM, shard_rows < 1 or >=
- * 2^31, vocab < 1, more than 2^42 logits, a tensor too large), VPE_ERR_RANGE (the shard does not lie in
- * [0, vocab)), VPE_ERR_WORKSPACE.
+ * 2^31, vocab < 1, more than 2^42 logits, a tensor too large), VPE_ERR_RANGE (the
+ * shard does not lie in [0, vocab)), VPE_ERR_WORKSPACE.
  */
 vpe_status vpe_lmhead_xent(const void *x, int64_t m, int64_t dim, const void *weight,
                            int64_t shard_rows, vpe_dtype dt, int64_t vocab_start, int64_t vocab,
@@ -112,10 +112,13 @@ vpe_status vpe_lmhead_xent_grad_workspace(int64_t m, int64_t dim, int64_t shard_
  *   s[j, :]           = sum_i d[i, j] x[i, :]
  *
  * grad_x is this shard's part: the ranks' parts sum to the whole.  The logits
- * are computed again, a piece of the vocabulary at a time; a piece's d / max |
- * grad_loss| is held in `dt` (bf16: each entry within 2^-8 of its value) and
- * multiplied with sums in fp32.  A row whose grad_loss is 0 counts as one
- * without a target.
+ * are computed again, a piece of the vocabulary at a time; a piece's d / max
+ * |grad_loss| is held in `dt` and multiplied with sums in fp32.  An entry of
+ * exp(z - lse) - [j = t] carries what z and lse do (lse is fp32: 2^-24 of its
+ * size), a few 2^-24 (1 + |z - lse|), both times exp(z - lse), and in bf16 one
+ * rounding more, up to 2^-8 of the entry; at a target of probability close to 1 the
+ * first two are the larger ones.  Entries of d below 2^-126 max |grad_loss| may
+ * count as 0.  A row whose grad_loss is 0 counts as one without a target.
  *
  * lse          device float [m]: over the whole vocabulary (vpe_xent_loss).
  * grad_loss    device float [m].

@@ -148,7 +148,8 @@ __global__ __launch_bounds__(kThreads) void clip_pieces(Table<N> t, Outputs<N> o
   if (t.n == 0) return;
   const int block = t.first[t.n] - 1 - static_cast<int>(blockIdx.x);
   const double ratio = p.max_norm / (whole + 1e-6);
-  const float f = ratio < 1. ? static_cast<float>(ratio) : (ratio != ratio ? __builtin_nanf("") : 1.f);
+  const float f =
+      ratio < 1. ? static_cast<float>(ratio) : (ratio != ratio ? __builtin_nanf("") : 1.f);
   const int at = tensor_of(t, block);
   const void *g = t.g[at];
   // (times 1 in place: nothing to write)

@@ -10,11 +10,14 @@
 //    row in the workgroup that computed it, and the one logit that is a row's
 //    target; `join_pairs` merges a row's pairs.
 //  - Gradients, a piece of the vocabulary at a time: the piece's
-//    d = softmax - onehot goes to a buffer that the caches hold (128 MB), and
-//    feeds two products, grad_x += d W and grad_weight = d^T x, that read d and W
-//    (x) in place, in rows or in columns.  The sum over the vocabulary in grad_x
-//    is kept in fp32 between pieces, split over several sums where there are few
-//    rows; `finish_grad_x` joins and rounds them.
+//    d = softmax - onehot goes to a buffer of 128 MB, and feeds two products,
+//    grad_x += d W and grad_weight = d^T x, that read d and W (x) in place, in rows
+//    or in columns.  d is rounded to the operands' type: the matrix cores take two
+//    operands of one type, and their fp32 rate is a tenth of bf16's (bf16 gradients
+//    are off by 2.0e-3 of their size with it, 1.7e-3 by their own rounding alone).
+//    The sum over the vocabulary in grad_x is kept in fp32 between pieces, split
+//    over several sums where there are few rows; `finish_grad_x` joins and rounds
+//    them.
 //  - The head's backward is the same two products on a given d.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -175,8 +178,8 @@ __global__ __launch_bounds__(256) void copy_rows(const char *__restrict__ from, 
 // in turn; each XCD gets one contiguous run of tiles, ordered in groups of
 // group_n tiles of n, so that the tiles it runs at once share both operands in
 // its own L2.
-[[maybe_unused]] __device__ __forceinline__ void tile_of(int b, int tiles_n, int tiles_m, int group_n, int &tn,
-                                        int &tm) {
+[[maybe_unused]] __device__ __forceinline__ void tile_of(int b, int tiles_n, int tiles_m,
+                                                         int group_n, int &tn, int &tm) {
   const int total = tiles_n * tiles_m;
   const int xcd = b & 7, idx = b >> 3, per = total >> 3, rem = total & 7;
   const int t = xcd < rem ? xcd * (per + 1) + idx : rem * (per + 1) + (xcd - rem) * per + idx;
@@ -607,7 +610,7 @@ __device__ __forceinline__ void logits_tile(const Logits &a, int block,
 // One workgroup per tile.  Few rows: bound by reading the table (1 row against 151936 x
 // 1024 bf16: 51 us, 6.05 TB/s).  Loose rows: by the latency of loads that pass through
 // registers (257 rows against 50257 x 999: 60 us, 33 on aligned rows).  fp32: by the
-// matrix cores (448 rows against 32000 x 512: 138-144 us, 102-106 TFLOP/s, two rounds of
+// matrix cores (448 rows against 32000 x 512: 132-144 us, 102-111 TFLOP/s, two rounds of
 // tiles; 2048 against 32000 x 1024: 0.97 ms, 138).
 // (4 waves: two workgroups per CU)
 template <class S, bool BF16, bool GRAD, bool LOOSE>
@@ -626,8 +629,8 @@ __global__ __launch_bounds__(S::NT, S::NT == 256 ? 2 : 1) void logits_tiles(Logi
 // Bound by the matrix cores and, between two tiles of K = 1024, by the exponentials
 // (a seventh of the cycles: all eight waves take them at once).  8192 rows, 7168 of
 // them live, against 151936 x 1024: 1.79-1.92 ms, 1.16-1.24 PFLOP/s, matrix cores busy
-// 63% at 1.84 GHz; 3584 live rows against 37984 x 4096: 0.92
-// ms, 1.21 PFLOP/s; 896 against 75968 x 1024: 147 us, 0.95 PFLOP/s, four and a half
+// 63% at 1.82-1.84 GHz; 3584 live rows against 37984 x 4096: 0.92
+// ms, 1.21 PFLOP/s; 896 against 75968 x 1024: 142-147 us, 0.95-0.98 PFLOP/s, four and a half
 // rounds of tiles for the work of four.  A workgroup per tile: 1% slower.  Four stages
 // of 32 values of k: 5% slower.
 template <class S>
@@ -809,7 +812,7 @@ __device__ __forceinline__ void grad_x_of(const Products &a, int split, int64_t 
 //
 // With many rows bound by the matrix cores: 4096 rows against 37984 x 4096, fp32
 // gradients, both products 2.15-2.45 ms, 1.04-1.18 PFLOP/s; fp32, 448 rows against
-// 32000 x 512, 265 us, 110 TFLOP/s.  With few by HBM: 256 against 75968 x 1024 bf16, 92-98
+// 32000 x 512, 265-277 us, 106-111 TFLOP/s.  With few by HBM: 256 against 75968 x 1024 bf16, 92-98
 // us, 3.6-3.8 TB/s, the workgroups of either product reading d for themselves.
 template <class S, bool BF16, int PARTS, bool LOOSE>
 __device__ __forceinline__ void products_tile(const Products &a, int b,
@@ -899,7 +902,7 @@ __global__ __launch_bounds__(S::NT) void grad_tiles(Products a) {
 // Both products of one piece, and the logits' gradient of the next: the second
 // fills the CUs that the first, with few and long tiles, leaves idle.  Bound by the
 // matrix cores (7168 live rows, 8192 columns, K = 1024 and 7168: 300-310 us, 1.16-1.20
-// PFLOP/s, busy 61%).
+// PFLOP/s, busy 61%; 355 MB read and 160 written past the L2, 1.7 TB/s).
 template <class S>
 __global__ __launch_bounds__(S::NT) void grad_and_logits_tiles(Products p, int n, Logits a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -1050,7 +1053,8 @@ void pick_logits(const Logits &a, int64_t m, int64_t rows, int dtype, hipStream_
     Logits b = a;
     const int n = set_tiles<Large, false>(b, m);
     b.round = 256;
-    hipLaunchKernelGGL(loss_tiles<Large>, dim3(n < b.round ? n : b.round), dim3(Large::NT), 0, st, b);
+    hipLaunchKernelGGL(loss_tiles<Large>, dim3(n < b.round ? n : b.round), dim3(Large::NT), 0, st,
+                       b);
   }
 }
 
@@ -1255,7 +1259,8 @@ int launch_lmhead_xent_grad(const LossRows &r, const float *lse, const float *gr
   p.scale = reinterpret_cast<const float *>(at(workspace, l.count)) + 1;
   p.gw_bf16 = g.gwt == 1, p.accumulate = g.accumulate;
   p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype, loose,
-                                          g.gw != nullptr, loss_most_splits(r.m, l.dim_pad, r.rows)));
+                                          g.gw != nullptr,
+                                          loss_most_splits(r.m, l.dim_pad, r.rows)));
   p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
   // the piece of d that begins at `row`
   auto piece_logits = [&](int64_t row) {
@@ -1315,7 +1320,8 @@ int launch_lmhead_grad(const void *d, int64_t ld, const LossRows &r, const LossG
   p.sums = reinterpret_cast<float *>(at(workspace, l.sums)), p.ld_sums = l.dim_pad;
   p.gw_bf16 = g.gwt == 1, p.accumulate = g.accumulate;
   p.splits = static_cast<int>(pick_splits(r.m, r.dim, loss_min(step, r.rows), r.dtype, loose,
-                                          g.gw != nullptr, loss_most_splits(r.m, l.dim_pad, r.rows)));
+                                          g.gw != nullptr,
+                                          loss_most_splits(r.m, l.dim_pad, r.rows)));
   p.per_split = loss_up((loss_min(step, r.rows) + p.splits - 1) / p.splits, 64);
   p.x = r.x, p.ldx = r.dim;
   if (x_copied) {

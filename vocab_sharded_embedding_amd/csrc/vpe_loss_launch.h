@@ -20,7 +20,9 @@ constexpr int64_t loss_tile_rows(int dtype) { return dtype == 1 ? 128 : 64; }
 // aligned.
 constexpr int64_t kLossCopyBytes = int64_t(1) << 27;
 // Bytes of one piece of the logits' gradient, where the whole is more; at least
-// kLossMinPiece columns of it.
+// kLossMinPiece columns of it.  (Steps of 8192 rows against 151936 x 1024 and of 2048
+// against two of 75968: 64 MB 8.00 and 2.13 ms, 128 MB 7.58 and 2.06, 256 MB 7.60 and
+// 2.03, 512 MB 7.75 and 2.09.)
 constexpr int64_t kLossPieceBytes = int64_t(1) << 27;
 constexpr int64_t kLossMinPiece = 512;
 // Most fp32 sums for the gradient of the hidden rows where its sum over the
